@@ -45,7 +45,10 @@ typedef enum {
     QNN_ERR_TIMEOUT = 6        /* a device-side bounded wait gave up */
 } qnn_status;
 
-typedef enum { QNN_S8 = 0, QNN_U8 = 1, QNN_S4 = 2, QNN_U4 = 3, QNN_S32 = 4, QNN_F32 = 5 } qnn_dtype;
+/* F16 and BF16 are float types of the weight-only product and the block norm. */
+typedef enum {
+    QNN_S8 = 0, QNN_U8 = 1, QNN_S4 = 2, QNN_U4 = 3, QNN_S32 = 4, QNN_F32 = 5, QNN_F16 = 6, QNN_BF16 = 7
+} qnn_dtype;
 
 /* Quantization schemes [QI 量化模式]:
  *   QNN_SYM : q = clip(rint(x / s))
@@ -485,6 +488,50 @@ qnn_status q_quantize_rows_dynamic(const float *x, int64_t rows, int64_t cols, i
  * dst must not overlap. */
 qnn_status q_layout_nchw64(const void *src, int to_nchw64, int N, int H, int W, int C, qnn_dtype dt, void *dst,
                            qnn_stream_t stream);
+
+/* ---- matrix-vector products with 4-bit weights and group scales ----------------- */
+
+/* 4-bit weights of a Linear layer, [N, K] (output channel n, input channel k),
+ * with one scale, and for U4 one zero point, per output channel and group of
+ * `group` consecutive input channels [QI tensor量化与通道量化, refined to groups;
+ * 反量化算子: w = (q - z) * s].  G = ceil(K / group) groups, the last one ragged
+ * when group does not divide K; group >= K: one scale per channel. */
+typedef struct {
+    int32_t N, K;            /* K even (two codes per byte), at most 2^30 */
+    int32_t group;           /* a positive multiple of 32 */
+    int32_t w_dt;            /* S4 (symmetric codes, z = 0) or U4 (with zero points) */
+    int32_t scale_dt;        /* F32, F16 or BF16: the type the scales are given and kept in */
+} qnn_w4_geom;
+
+/* Size in bytes of the prepacked weights; 0 for an invalid geometry or type. */
+size_t qnn_gemv_w4_packed_bytes(const qnn_w4_geom *g);
+
+/* Prepack once, ahead of inference.  W: packed codes [N, K/2] (element 2i in the
+ * low nibble), as q_quantize writes them; scale: [N, G] of scale_dt;
+ * zero_point: int32 [N, G], each in 0..15 (another value is reported as
+ * QNN_ERR_INVALID_ARG by qnn_check_device_error), for U4, and NULL for S4;
+ * W_packed: qnn_gemv_w4_packed_bytes(g) bytes, 16-byte aligned.  q_quantize makes
+ * such codes from fp32 weights whose K is a multiple of `group` when it is
+ * given them as [N * G, group] with per-channel axis 0. */
+qnn_status qgemv_prepack_w4(const void *W, const void *scale, const int32_t *zero_point, const qnn_w4_geom *g,
+                            void *W_packed, qnn_stream_t stream);
+
+/* y[m][n] = bias[n] + sum_k x[m][k] * (q[n][k] - z[n][k / group]) * s[n][k / group]
+ * for M rows of x, rounded once to y_dt.  Per group the sum of x (q - z) is
+ * formed in fp32 on the tensor cores (q - z is an exact integer there, and fp32 x
+ * enters as three bf16 terms that add up to it exactly, bits below 2^-133 aside),
+ * then multiplied by the scale in fp32 and added in fp32; an unscaled group sum beyond the fp32 range
+ * becomes infinite.  The order of the sums depends on the sizes alone: equal
+ * calls give equal bits.
+ * x: device [M, K] of x_dt (F32, F16, BF16), ldx elements between rows (>= K; 0: K).
+ * y: device [M, N] of y_dt (x_dt or F32), ldy elements between rows (>= N; 0: N).
+ * bias: device fp32 [N] or NULL.  x and y must not overlap.  M = 0 does nothing.
+ * Made for one to a few tens of rows; more are taken 32 columns of the tensor
+ * operand at a time (a row of F32 takes three), the weights read again for each;
+ * QNN_ERR_UNSUPPORTED beyond 65535 such passes.
+ * Rows of x off 16-byte boundaries (ldx) are read with scalar loads. */
+qnn_status qgemv_w4(const void *x, qnn_dtype x_dt, int64_t ldx, const void *W_packed, const qnn_w4_geom *g,
+                    int64_t M, const float *bias, void *y, qnn_dtype y_dt, int64_t ldy, qnn_stream_t stream);
 
 /* ---- status ----------------------------------------------------------------- */
 

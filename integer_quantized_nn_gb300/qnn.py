@@ -18,7 +18,7 @@ from . import build as _build
 # ---- enums (mirror include/qnn.h) ------------------------------------------------
 QNN_OK, QNN_ERR_INVALID_ARG, QNN_ERR_UNSUPPORTED, QNN_ERR_ALIGNMENT = 0, 1, 2, 3
 QNN_ERR_OVERFLOW_RISK, QNN_ERR_CUDA, QNN_ERR_TIMEOUT = 4, 5, 6
-DTYPES = {"s8": 0, "u8": 1, "s4": 2, "u4": 3, "s32": 4, "f32": 5}
+DTYPES = {"s8": 0, "u8": 1, "s4": 2, "u4": 3, "s32": 4, "f32": 5, "f16": 6, "bf16": 7}
 SCHEMES = {"sym": 0, "asym": 1, "pow2": 2}
 EPI_MODES = {"requant": 0, "dequant": 1, "s32": 2}
 ELTWISE_OPS = {"add": 0, "mul": 1, "relu": 2}
@@ -60,6 +60,10 @@ class ConvGeom(ctypes.Structure):
         return (self.W + 2 * self.pad_w - self.FW) // self.stride_w + 1
 
 
+class W4Geom(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("N", "K", "group", "w_dt", "scale_dt")]
+
+
 _lib = None
 _SYMBOLS = {}
 
@@ -97,6 +101,9 @@ def _declare(L):
         "q_layout_nchw64": (c_int, [vp, c_int, c_int, c_int, c_int, c_int, c_int, vp, vp]),
         "qconv_prepack_w_u4": (c_int, [vp, vp, vp, vp, vp, vp]),
         "q_lis_attn_v": (c_int, [vp, f32, vp, i64, c_int, c_int, c_int, c_int, vp, vp]),
+        "qnn_gemv_w4_packed_bytes": (sz, [vp]),
+        "qgemv_prepack_w4": (c_int, [vp, vp, vp, vp, vp, vp]),
+        "qgemv_w4": (c_int, [vp, c_int, i64, vp, vp, i64, vp, vp, c_int, i64, vp]),
         "qnn_status_string": (ctypes.c_char_p, [c_int]),
         "qnn_check_device_error": (c_int, [vp]),
         "qnn_selftest_wait_timeout": (c_int, [ctypes.c_uint64, vp]),
@@ -410,6 +417,32 @@ def q_lis_attn_v(x, S: float, v, batch: int, Lq: int, Lk: int, d: int, bits: int
     load()
     _check(_SYMBOLS["q_lis_attn_v"](_ptr(x), float(S), _ptr(v), int(batch), int(Lq), int(Lk), int(d), int(bits),
                                      _ptr(out), _stream(stream)), "q_lis_attn_v")
+
+
+def w4_geom(N: int, K: int, group: int, w_dt: str = "s4", scale_dt: str = "f32") -> W4Geom:
+    return W4Geom(int(N), int(K), int(group), DTYPES[w_dt], DTYPES[scale_dt])
+
+
+def qnn_gemv_w4_packed_bytes(g: W4Geom) -> int:
+    load()
+    return int(_SYMBOLS["qnn_gemv_w4_packed_bytes"](ctypes.byref(g)))
+
+
+def qgemv_prepack_w4(W, scale, g: W4Geom, W_packed, zero_point=None, stream=None):
+    """W: packed 4-bit codes [N, K/2]; scale: [N, ceil(K / group)] of the geometry's scale
+    type; zero_point: int32 of the same shape for u4, None for s4; W_packed: uint8 device
+    tensor of qnn_gemv_w4_packed_bytes(g) bytes, 16-byte aligned."""
+    load()
+    _check(_SYMBOLS["qgemv_prepack_w4"](_ptr(W), _ptr(scale), _ptr(zero_point), ctypes.byref(g), _ptr(W_packed),
+                                        _stream(stream)), "qgemv_prepack_w4")
+
+
+def qgemv_w4(x, x_dt: str, W_packed, g: W4Geom, M: int, y, y_dt: str, bias=None, ldx: int = 0, ldy: int = 0,
+             stream=None):
+    """y [M, N] = x [M, K] times the 4-bit weights; ldx, ldy: elements between rows (0: packed)."""
+    load()
+    _check(_SYMBOLS["qgemv_w4"](_ptr(x), DTYPES[x_dt], int(ldx), _ptr(W_packed), ctypes.byref(g), int(M),
+                                _ptr(bias), _ptr(y), DTYPES[y_dt], int(ldy), _stream(stream)), "qgemv_w4")
 
 
 def qnn_check_device_error(stream=None) -> int:
