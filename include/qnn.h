@@ -533,6 +533,66 @@ qnn_status qgemv_prepack_w4(const void *W, const void *scale, const int32_t *zer
 qnn_status qgemv_w4(const void *x, qnn_dtype x_dt, int64_t ldx, const void *W_packed, const qnn_w4_geom *g,
                     int64_t M, const float *bias, void *y, qnn_dtype y_dt, int64_t ldy, qnn_stream_t stream);
 
+/* ---- norms after and before a block, with its gate and residual scale ------------ */
+
+/* QNN_NORM_RMS  : x^ = x / sqrt(mean(x^2) + eps)
+ * QNN_NORM_LAYER: x^ = (x - mean(x)) / sqrt(var(x) + eps)   (var: over C, biased)
+ * then gamma x^ + beta (either NULL: left out).  QNN_NORM_NONE: x. */
+typedef enum { QNN_NORM_NONE = 0, QNN_NORM_RMS = 1, QNN_NORM_LAYER = 2 } qnn_norm;
+
+typedef struct {
+    int32_t post, pre;       /* qnn_norm after this block, and before the next */
+    float eps_post, eps_pre; /* >= 0 */
+    float res_scale;         /* a, finite */
+    float block_scale;       /* b, finite */
+    const float *gamma_post, *beta_post, *gamma_pre, *beta_pre; /* device fp32 [C] or NULL */
+    const void *gate;        /* device [ceil(rows / gate_rows), C] of the block's type, or NULL (one) */
+    int64_t gate_rows;       /* consecutive rows that share a gate row; 0: all of them */
+    int64_t ld_r, ld_y, ld_h; /* elements between rows (0: C) of the residual stream and its
+                                gradients, of y and dy, of h and dh */
+} qnn_block_norm;
+
+/* One pass over each of `rows` rows of C columns:
+ *   r' = a r + b gate norm_post(y),   h = norm_pre(r')
+ * in fp32, each result rounded once (h from r' before its rounding).
+ * r, r_out: device, of r_dt; y: device, of y_dt, or NULL (no block yet: r' = a r;
+ * post NONE, no gate); y_dt F32, F16 or BF16; r_dt the same, or F32.
+ * r_out may be NULL (not wanted) or r itself.  h may be NULL when r_out is not; of
+ * h_dt: y_dt, or S8: the codes of q_quantize_rows_dynamic with h_scale (fp32 [rows];
+ * NULL otherwise) = max|h| / 127, for a qgemm_s8 with that row_scale; h must then
+ * be finite.  Outputs overlap no input else.
+ * C <= 32768 (QNN_ERR_UNSUPPORTED beyond).  Rows off 16-byte boundaries or C not a
+ * multiple of 8 are read element by element. */
+qnn_status q_block_norm(const void *r, qnn_dtype r_dt, const void *y, qnn_dtype y_dt, int64_t rows, int C,
+                        const qnn_block_norm *p, void *r_out, void *h, qnn_dtype h_dt, float *h_scale,
+                        qnn_stream_t stream);
+
+/* Size in bytes of the backward call's workspace (for the current device); 0 for
+ * an invalid size or rows = 0. */
+size_t qnn_block_norm_backward_workspace_bytes(int64_t rows, int C, const qnn_block_norm *p);
+
+/* The gradients of q_block_norm at the same parameters (h taken as not quantized).
+ * In: r_out (r' as the forward call wrote it; read if dh is given and pre is a
+ * norm), y, dh (of y_dt, gradient of h) and dr_out (of r_dt, gradient of r');
+ * one of dh and dr_out may be NULL (zero).  With t = b gate G, p = norm_post(y),
+ * x^ and y^ the normalised r' and y:
+ *   G = dr' + D_pre(gamma_pre dh)      dr = a G             dy = D_post(gamma_post t)
+ *   dgate = b sum G p                  dgamma_pre = sum dh x^    dbeta_pre = sum dh
+ *                                      dgamma_post = sum t y^    dbeta_post = sum t
+ * where D(g) = (g - mean(g) [LAYER] - x^ mean(g x^)) / sqrt(.), dgate sums the rows
+ * that share a gate row, the others all rows.  Sums are fp32 in a fixed order: equal
+ * calls give equal bits.  Out: dr (r_dt), dy (y_dt), dgate (y_dt, the gate's shape),
+ * the others fp32 [C]; each may be NULL (not wanted), and none asks for a
+ * parameter that p lacks; dgamma_pre and dbeta_pre need dh.  dr may be dr_out;
+ * else no output overlaps an input.  rows = 0 writes zeros to the sums.
+ * workspace: device scratch of qnn_block_norm_backward_workspace_bytes bytes, 16-byte
+ * aligned, overwritten; needed when a sum is wanted.  Two calls in flight must
+ * not share one. */
+qnn_status q_block_norm_backward(const void *r_out, qnn_dtype r_dt, const void *y, qnn_dtype y_dt, int64_t rows,
+                                 int C, const qnn_block_norm *p, const void *dh, const void *dr_out, void *dr,
+                                 void *dy, void *dgate, float *dgamma_pre, float *dbeta_pre, float *dgamma_post,
+                                 float *dbeta_post, void *workspace, size_t workspace_bytes, qnn_stream_t stream);
+
 /* ---- status ----------------------------------------------------------------- */
 
 const char *qnn_status_string(qnn_status s);

@@ -22,6 +22,7 @@ DTYPES = {"s8": 0, "u8": 1, "s4": 2, "u4": 3, "s32": 4, "f32": 5, "f16": 6, "bf1
 SCHEMES = {"sym": 0, "asym": 1, "pow2": 2}
 EPI_MODES = {"requant": 0, "dequant": 1, "s32": 2}
 ELTWISE_OPS = {"add": 0, "mul": 1, "relu": 2}
+NORMS = {"none": 0, "rms": 1, "layer": 2}
 
 
 class QnnError(RuntimeError):
@@ -64,6 +65,13 @@ class W4Geom(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("N", "K", "group", "w_dt", "scale_dt")]
 
 
+class BlockNorm(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("post", "pre")]
+                + [(n, ctypes.c_float) for n in ("eps_post", "eps_pre", "res_scale", "block_scale")]
+                + [(n, ctypes.c_void_p) for n in ("gamma_post", "beta_post", "gamma_pre", "beta_pre", "gate")]
+                + [(n, ctypes.c_int64) for n in ("gate_rows", "ld_r", "ld_y", "ld_h")])
+
+
 _lib = None
 _SYMBOLS = {}
 
@@ -104,6 +112,9 @@ def _declare(L):
         "qnn_gemv_w4_packed_bytes": (sz, [vp]),
         "qgemv_prepack_w4": (c_int, [vp, vp, vp, vp, vp, vp]),
         "qgemv_w4": (c_int, [vp, c_int, i64, vp, vp, i64, vp, vp, c_int, i64, vp]),
+        "q_block_norm": (c_int, [vp, c_int, vp, c_int, i64, c_int, vp, vp, vp, c_int, vp, vp]),
+        "qnn_block_norm_backward_workspace_bytes": (sz, [i64, c_int, vp]),
+        "q_block_norm_backward": (c_int, [vp, c_int, vp, c_int, i64, c_int] + [vp] * 11 + [sz, vp]),
         "qnn_status_string": (ctypes.c_char_p, [c_int]),
         "qnn_check_device_error": (c_int, [vp]),
         "qnn_selftest_wait_timeout": (c_int, [ctypes.c_uint64, vp]),
@@ -443,6 +454,43 @@ def qgemv_w4(x, x_dt: str, W_packed, g: W4Geom, M: int, y, y_dt: str, bias=None,
     load()
     _check(_SYMBOLS["qgemv_w4"](_ptr(x), DTYPES[x_dt], int(ldx), _ptr(W_packed), ctypes.byref(g), int(M),
                                 _ptr(bias), _ptr(y), DTYPES[y_dt], int(ldy), _stream(stream)), "qgemv_w4")
+
+
+def block_norm(post: str = "none", pre: str = "rms", eps_post: float = 1e-6, eps_pre: float = 1e-6, gamma_post=None,
+               beta_post=None, gamma_pre=None, beta_pre=None, gate=None, gate_rows: int = 0, res_scale: float = 1.0,
+               block_scale: float = 1.0, ld_r: int = 0, ld_y: int = 0, ld_h: int = 0) -> BlockNorm:
+    """Holds the tensors' addresses only: keep the tensors alive as long as the struct is used."""
+    return BlockNorm(NORMS[post], NORMS[pre], float(eps_post), float(eps_pre), float(res_scale), float(block_scale),
+                     _ptr(gamma_post), _ptr(beta_post), _ptr(gamma_pre), _ptr(beta_pre), _ptr(gate), int(gate_rows),
+                     int(ld_r), int(ld_y), int(ld_h))
+
+
+def q_block_norm(r, r_dt: str, y, y_dt: str, rows: int, C: int, params: BlockNorm, r_out=None, h=None,
+                 h_dt: str = None, h_scale=None, stream=None):
+    """r_out = res_scale r + block_scale gate norm_post(y), h = norm_pre(r_out); h_dt: y_dt (the
+    default) or "s8", with h_scale fp32 [rows]."""
+    load()
+    _check(_SYMBOLS["q_block_norm"](_ptr(r), DTYPES[r_dt], _ptr(y), DTYPES[y_dt], int(rows), int(C),
+                                    ctypes.byref(params), _ptr(r_out), _ptr(h), DTYPES[h_dt or y_dt], _ptr(h_scale),
+                                    _stream(stream)), "q_block_norm")
+
+
+def qnn_block_norm_backward_workspace_bytes(rows: int, C: int, params: BlockNorm) -> int:
+    load()
+    return int(_SYMBOLS["qnn_block_norm_backward_workspace_bytes"](int(rows), int(C), ctypes.byref(params)))
+
+
+def q_block_norm_backward(r_out, r_dt: str, y, y_dt: str, rows: int, C: int, params: BlockNorm, dh, dr_out, dr, dy,
+                          workspace=None, dgate=None, dgamma_pre=None, dbeta_pre=None, dgamma_post=None,
+                          dbeta_post=None, stream=None):
+    """Gradients of q_block_norm; workspace: uint8 device tensor of
+    qnn_block_norm_backward_workspace_bytes(rows, C, params) bytes, for the parameters' gradients."""
+    load()
+    _check(_SYMBOLS["q_block_norm_backward"](
+        _ptr(r_out), DTYPES[r_dt], _ptr(y), DTYPES[y_dt], int(rows), int(C), ctypes.byref(params), _ptr(dh),
+        _ptr(dr_out), _ptr(dr), _ptr(dy), _ptr(dgate), _ptr(dgamma_pre), _ptr(dbeta_pre), _ptr(dgamma_post),
+        _ptr(dbeta_post), _ptr(workspace), 0 if workspace is None else _nbytes(workspace), _stream(stream)),
+        "q_block_norm_backward")
 
 
 def qnn_check_device_error(stream=None) -> int:
