@@ -170,7 +170,8 @@ def _stream(stream) -> Optional[int]:
     if stream is not None:
         return int(getattr(stream, "cuda_stream", stream))
     import torch
-    return int(torch.cuda.current_stream().cuda_stream)
+    # the handle alone: a torch.cuda.Stream object for it takes longer than the launch
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _shape(shape):
@@ -442,7 +443,7 @@ def qnn_gemv_w4_packed_bytes(g: W4Geom) -> int:
 def qgemv_prepack_w4(W, scale, g: W4Geom, W_packed, zero_point=None, stream=None):
     """W: packed 4-bit codes [N, K/2]; scale: [N, ceil(K / group)] of the geometry's scale
     type; zero_point: int32 of the same shape for u4, None for s4; W_packed: uint8 device
-    tensor of qnn_gemv_w4_packed_bytes(g) bytes, 16-byte aligned."""
+    tensor of qnn_gemv_w4_packed_bytes(g) bytes, 128-byte aligned."""
     load()
     _check(_SYMBOLS["qgemv_prepack_w4"](_ptr(W), _ptr(scale), _ptr(zero_point), ctypes.byref(g), _ptr(W_packed),
                                         _stream(stream)), "qgemv_prepack_w4")
