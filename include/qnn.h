@@ -510,7 +510,7 @@ size_t qnn_gemv_w4_packed_bytes(const qnn_w4_geom *g);
  * low nibble), as q_quantize writes them; scale: [N, G] of scale_dt;
  * zero_point: int32 [N, G], each in 0..15 (another value is reported as
  * QNN_ERR_INVALID_ARG by qnn_check_device_error), for U4, and NULL for S4;
- * W_packed: qnn_gemv_w4_packed_bytes(g) bytes, 16-byte aligned.  q_quantize makes
+ * W_packed: qnn_gemv_w4_packed_bytes(g) bytes, 128-byte aligned.  q_quantize makes
  * such codes from fp32 weights whose K is a multiple of `group` when it is
  * given them as [N * G, group] with per-channel axis 0. */
 qnn_status qgemv_prepack_w4(const void *W, const void *scale, const int32_t *zero_point, const qnn_w4_geom *g,

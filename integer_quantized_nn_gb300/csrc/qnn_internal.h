@@ -1,5 +1,6 @@
 // qnn_internal.h -- host-side helpers shared by the library's translation units.
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 #include "qnn.h"
@@ -15,6 +16,23 @@ uint32_t *status_word();
 int sm_count();
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Lets `kern` take `bytes` of dynamic shared memory on the current device; `done` keeps
+// the devices on which that was asked for already, so that later calls only look.
+template <typename K>
+bool opt_in_smem(K kern, int bytes, std::atomic<uint64_t> &done)
+{
+    int d = -1;
+    if (cudaGetDevice(&d) != cudaSuccess || d < 0) return false;
+    const uint64_t bit = d < 64 ? 1ull << d : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return false;
+    }
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
 
 // Maps the launch error (if any) of the last kernel launch to a status.
 inline qnn_status launch_status()

@@ -327,6 +327,13 @@ __device__ __forceinline__ uint4 lds_v4(uint32_t addr)
 // Returns at once when the kernel was not launched as a dependent.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// ... and let the grid that depends on this one start launching (its own wait still
+// ends only when this grid has completed).
+__device__ __forceinline__ void grid_dependency_launch()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Instruction descriptor: fp32 accumulator, K-major A and B, M x N tile.
 // a_fmt / b_fmt: kind::f16 -> 0 f16, 1 bf16; kind::f8f6f4 -> 0 e4m3, 1 e5m2,
 // 3 e2m3, 4 e3m2, 5 e2m1.

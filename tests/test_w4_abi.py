@@ -22,31 +22,31 @@ def lib():
 
 def test_image_sizes(lib):
     size = qnn.qnn_gemv_w4_packed_bytes
-    assert size(qnn.w4_geom(4096, 4096, 128)) == 256 * 64 * 512 + 256 * 32 * 16 * 4
-    assert size(qnn.w4_geom(4096, 4096, 128, scale_dt="bf16")) == 256 * 64 * 512 + 256 * 32 * 16 * 2
-    # ragged: 17 channels = 2 tiles, 66 inputs = 2 steps, 3 groups of 32; zero points behind the scales
-    assert size(qnn.w4_geom(17, 66, 32, w_dt="u4", scale_dt="f16")) == 2 * 2 * 512 + 2 * 3 * 16 * 2 + 2 * 3 * 16
+    assert size(qnn.w4_geom(4096, 4096, 128)) == 256 * 32 * 1024 + 256 * 32 * 16 * 4
+    assert size(qnn.w4_geom(4096, 4096, 128, scale_dt="bf16")) == 256 * 32 * 1024 + 256 * 32 * 16 * 2
+    # ragged: 17 channels = 2 tiles, 130 inputs = 2 steps, 5 groups of 32; zero points behind the scales
+    assert size(qnn.w4_geom(17, 130, 32, w_dt="u4", scale_dt="f16")) == 2 * 2 * 1024 + 2 * 5 * 16 * 2 + 2 * 5 * 16
     # one group over all inputs
-    assert size(qnn.w4_geom(16, 64, 1 << 20)) == 512 + 64
+    assert size(qnn.w4_geom(16, 64, 1 << 20)) == 1024 + 64
     for bad in (dict(N=0), dict(K=0), dict(K=63), dict(K=(1 << 30) + 2), dict(group=0), dict(group=48),
                 dict(group=-32), dict(w_dt="s8"), dict(scale_dt="s32")):
         assert size(qnn.w4_geom(**{**dict(N=16, K=64, group=32), **bad})) == 0, bad
 
 
 def test_prepack_refusals(lib):
-    def call(W=16, scale=16, zero=None, out=16, **geom):
+    def call(W=16, scale=16, zero=None, out=128, **geom):
         g = qnn.w4_geom(**{**dict(N=16, K=64, group=32), **geom})
         return lib.qgemv_prepack_w4(W, scale, zero, ctypes.byref(g), out, None)
     for bad in (dict(W=None), dict(scale=None), dict(out=None), dict(zero=16), dict(w_dt="u4"), dict(K=63),
                 dict(group=16), dict(w_dt="u8")):
         assert call(**bad) == qnn.QNN_ERR_INVALID_ARG, bad
-    for bad in (dict(W=20), dict(scale=20), dict(out=24), dict(w_dt="u4", zero=20)):
+    for bad in (dict(W=20), dict(scale=20), dict(out=64), dict(w_dt="u4", zero=20)):
         assert call(**bad) == qnn.QNN_ERR_ALIGNMENT, bad
     assert lib.qgemv_prepack_w4(16, 16, None, None, 16, None) == qnn.QNN_ERR_INVALID_ARG
 
 
 def test_product_refusals(lib):
-    def call(x=16, x_dt="bf16", ldx=0, W=16, M=1, bias=None, y=16, y_dt="bf16", ldy=0, **geom):
+    def call(x=16, x_dt="bf16", ldx=0, W=128, M=1, bias=None, y=16, y_dt="bf16", ldy=0, **geom):
         g = qnn.w4_geom(**{**dict(N=16, K=64, group=32), **geom})
         return lib.qgemv_w4(x, qnn.DTYPES[x_dt], ldx, W, ctypes.byref(g), M, bias, y, qnn.DTYPES[y_dt], ldy, None)
     for bad in (dict(x=None), dict(W=None), dict(y=None), dict(M=-1), dict(ldx=63), dict(ldy=15), dict(ldx=-1),
@@ -54,7 +54,7 @@ def test_product_refusals(lib):
         assert call(**bad) == qnn.QNN_ERR_INVALID_ARG, bad
     for bad in (dict(x_dt="s8"), dict(y_dt="s8"), dict(y_dt="f16"), dict(x_dt="f32"), dict(M=1 << 40)):
         assert call(**bad) == qnn.QNN_ERR_UNSUPPORTED, bad
-    for bad in (dict(x=20), dict(W=24), dict(y=18), dict(bias=20)):
+    for bad in (dict(x=20), dict(W=64), dict(y=18), dict(bias=20)):
         assert call(**bad) == qnn.QNN_ERR_ALIGNMENT, bad
     assert call(M=0, x=None, y=None) == qnn.QNN_OK
     assert lib.qgemv_w4(16, 6, 0, 16, None, 1, None, 16, 6, 0, None) == qnn.QNN_ERR_INVALID_ARG
