@@ -558,9 +558,9 @@ typedef struct {
  * r, r_out: device, of r_dt; y: device, of y_dt, or NULL (no block yet: r' = a r;
  * post NONE, no gate); y_dt F32, F16 or BF16; r_dt the same, or F32.
  * r_out may be NULL (not wanted) or r itself.  h may be NULL when r_out is not; of
- * h_dt: y_dt, or S8: the codes of q_quantize_rows_dynamic with h_scale (fp32 [rows];
- * NULL otherwise) = max|h| / 127, for a qgemm_s8 with that row_scale; h must then
- * be finite.  Outputs overlap no input else.
+ * h_dt: y_dt, or S8: codes rint(h (127 / max|h|)) in -127..127, with h_scale (fp32
+ * [rows]; NULL otherwise) = max|h| / 127, for a qgemm_s8 with that row_scale; a row
+ * of zeros gets scale 0 and codes 0; h must then be finite.  Outputs overlap no input else.
  * C <= 32768 (QNN_ERR_UNSUPPORTED beyond).  Rows off 16-byte boundaries or C not a
  * multiple of 8 are read element by element. */
 qnn_status q_block_norm(const void *r, qnn_dtype r_dt, const void *y, qnn_dtype y_dt, int64_t rows, int C,

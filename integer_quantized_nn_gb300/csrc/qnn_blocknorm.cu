@@ -11,16 +11,22 @@
 //   dgate = b sum G p over the rows that share it;   dgamma = sum upstream x^,
 //   dbeta = sum upstream   (upstream: dh before, t after)
 //
-// Both are bound by the bytes of the rows.  A row lives in registers from its one
-// read to its writes: one warp holds rows of up to 1024 columns, a block holds longer
-// ones.  Statistics are fp32, the variance from the centred values (a second
-// reduction over registers, not over memory).  h is formed from r' before r' is
-// rounded to its own type; the backward pass takes its statistics from r' as stored.
+// Both are bound by the bytes of the rows.  A row is read once and lives in registers
+// to its writes: one warp holds rows of up to 1024 columns, a block longer ones.
+// Statistics are fp32, the variance from the centred values (a second reduction over
+// registers, not over memory).  h is formed from r' before r' is rounded to its own
+// type; the backward pass takes its statistics from r' as stored.
+//
+// Many rows on 16-byte boundaries: the rows to come are on their way to shared memory
+// by bulk copies while one is computed (the copies in flight, not registers, are what
+// covers the memory's latency).  Few rows, and rows off those boundaries: direct loads.
 #include <cuda_runtime.h>
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include "qnn_float.cuh"
 #include "qnn_internal.h"
+#include "qnn_ptx.cuh"
 
 namespace qnn {
 namespace {
@@ -28,6 +34,10 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxC = 32768;
 constexpr int kWarpRows = 4;  // warps (rows) per block where a warp holds a row
+constexpr int kMaxStages = 4;
+// Shared memory of an SM given to rings: what covers the latency twice over; the rest
+// stays L1, which holds the parameters.
+constexpr int kRingSmem = 128 << 10;
 
 struct NormArgs {
     const void *r, *y, *gate;
@@ -37,6 +47,9 @@ struct NormArgs {
     int64_t rows, ld_r, ld_y, ld_h, gate_rows;
     float a, b, eps_post, eps_pre, inv_c;
     int C, post, pre, s8;
+    int small_rows;    // row and gate_rows fit 32 bits
+    int stages;        // of a ring
+    uint32_t *status;  // device status word
 };
 
 // V consecutive elements as fp32 (V = 8: 16-byte accesses; V = 1: any address)
@@ -75,6 +88,15 @@ __device__ __forceinline__ void store_v(T *p, const float *v)
     }
 }
 
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+
+__device__ __forceinline__ float2 warp_sum(float2 v) { return make_float2(warp_sum(v.x), warp_sum(v.y)); }
+
 // Sums (or maxima) over a row's threads: a warp, or the block through shared memory.
 // Two slots used in turn make one barrier per call enough: a slot is written again
 // only behind the barrier that follows its last read.
@@ -85,23 +107,29 @@ struct RowReduce {
     template <bool WARP>
     __device__ __forceinline__ float2 sum(float2 v)
     {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            v.x += __shfl_xor_sync(kFull, v.x, o);
-            v.y += __shfl_xor_sync(kFull, v.y, o);
-        }
+        v = warp_sum(v);
         if constexpr (!WARP) {
             float2 *s = slots[turn];
             turn ^= 1;
             const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
             if (lane == 0) s[threadIdx.x >> 5] = v;
             __syncthreads();
-            v = lane < warps ? s[lane] : make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                v.x += __shfl_xor_sync(kFull, v.x, o);
-                v.y += __shfl_xor_sync(kFull, v.y, o);
-            }
+            v = warp_sum(lane < warps ? s[lane] : make_float2(0.0f, 0.0f));
+        }
+        return v;
+    }
+
+    template <bool WARP>
+    __device__ __forceinline__ float sum(float v)
+    {
+        v = warp_sum(v);
+        if constexpr (!WARP) {
+            float2 *s = slots[turn];
+            turn ^= 1;
+            const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+            if (lane == 0) s[threadIdx.x >> 5].x = v;
+            __syncthreads();
+            v = warp_sum(lane < warps ? s[lane].x : 0.0f);
         }
         return v;
     }
@@ -123,22 +151,51 @@ struct RowReduce {
     }
 };
 
+// rint(t) of |t| <= 128 in the low byte: adding 1.5 2^23 leaves the integer in the low
+// bits of the sum, rounded half to even.
+__device__ __forceinline__ uint32_t low_int(float t) { return __float_as_uint(t + 12582912.0f); }
+
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    return prmt(prmt(a, b, 0x0040), prmt(c, d, 0x0040), 0x5410);
+}
+
 // The columns of thread t of a row: vectors t, t + threads, ...; V elements each.
+// Loads read the row's first vector in place of one beyond C: without a branch for
+// each vector all of a thread's loads are in flight together.
 template <int V, int I>
 struct Span {
     int t, threads, C;
     __device__ __forceinline__ int col(int i) const { return (t + i * threads) * V; }
     __device__ __forceinline__ bool in(int i) const { return col(i) < C; }
     template <typename T>
-    __device__ __forceinline__ void load(const T *row, float *v) const
+    __device__ __forceinline__ void load(const T *row, float *v) const  // anything beyond C
     {
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-            if (in(i)) load_v<V>(row + col(i), v + i * V);
-            else
+        for (int i = 0; i < I; ++i) load_v<V>(row + (in(i) ? col(i) : 0), v + i * V);
+    }
+    // 0 beyond C
+    template <typename T>
+    __device__ __forceinline__ void load0(const T *row, float *v) const
+    {
+        load(row, v);
+        clear(v);
+    }
+    __device__ __forceinline__ void clear(float *v) const
+    {
 #pragma unroll
-                for (int e = 0; e < V; ++e) v[i * V + e] = 0.0f;
-        }
+        for (int i = 0; i < I; ++i)
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[i * V + e] = in(i) ? v[i * V + e] : 0.0f;
+    }
+    // `other` everywhere without a row
+    template <typename T>
+    __device__ __forceinline__ void load_or(const T *row, float *v, float other) const
+    {
+        if (row) load(row, v);
+        else
+#pragma unroll
+            for (int e = 0; e < V * I; ++e) v[e] = other;
     }
     template <typename T>
     __device__ __forceinline__ void store(T *row, const float *v) const
@@ -168,48 +225,156 @@ __device__ __forceinline__ Stats row_stats(const Span<V, I> &sp, const float *v,
     if (kind == QNN_NORM_LAYER) {
 #pragma unroll
         for (int e = 0; e < V * I; ++e) acc += v[e];
-        s.mean = red.sum<WARP>(make_float2(acc, 0.0f)).x * inv_c;
+        s.mean = red.sum<WARP>(acc) * inv_c;
         acc = 0.0f;
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+            if (sp.in(i))
+#pragma unroll
+                for (int e = i * V; e < (i + 1) * V; ++e) {
+                    const float d = v[e] - s.mean;
+                    acc = __fmaf_rn(d, d, acc);
+                }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V * I; ++e) acc = __fmaf_rn(v[e], v[e], acc);
     }
+    s.rstd = rstd_of(red.sum<WARP>(acc), inv_c, eps);
+    return s;
+}
+
+// v = (v - mean) rstd
+template <int V, int I>
+__device__ __forceinline__ void normalise(const Span<V, I> &sp, float *v, const Stats &s)
+{
 #pragma unroll
     for (int i = 0; i < I; ++i)
         if (sp.in(i))
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float d = v[i * V + e] - s.mean;
-                acc = __fmaf_rn(d, d, acc);
-            }
-    s.rstd = rstd_of(red.sum<WARP>(make_float2(acc, 0.0f)).x, inv_c, eps);
-    return s;
+            for (int e = i * V; e < (i + 1) * V; ++e) v[e] = (v[e] - s.mean) * s.rstd;
 }
 
-// v = gamma (v - mean) rstd + beta
+// v = gamma (v - mean) rstd + beta, (v - mean) rstd as one fused operation.
 template <int V, int I>
-__device__ __forceinline__ void normalise(const Span<V, I> &sp, float *v, const Stats &s, const float *gamma,
-                                          const float *beta)
+__device__ __forceinline__ void affine(const Span<V, I> &sp, float *v, const Stats &s, const float *gamma,
+                                       const float *beta)
 {
+    const float c = -s.mean * s.rstd;
+    float p[V * I];
+#pragma unroll
+    for (int e = 0; e < V * I; ++e) v[e] = __fmaf_rn(v[e], s.rstd, c);
+    if (gamma) {
+        sp.load(gamma, p);
+#pragma unroll
+        for (int e = 0; e < V * I; ++e) v[e] *= p[e];
+    }
+    if (beta) {
+        sp.load(beta, p);
+#pragma unroll
+        for (int e = 0; e < V * I; ++e) v[e] += p[e];
+    }
+}
+
+// One row from its pointers (y and g may be null).  EARLY: all loads before the first
+// reduction (few rows: one wait for memory, not three).  release() is called once the
+// row has been read by all its threads, unless EARLY.
+template <typename TR, typename TY, bool WARP, bool EARLY, int V, int I, typename F>
+__device__ __forceinline__ void norm_row(const NormArgs &a, const Span<V, I> &sp, int64_t row, const TR *r,
+                                         const TY *y, const TY *g, RowReduce &red, F release)
+{
+    constexpr int E = V * I, L = EARLY ? E : 1;
+    float v[E], t[E], ge[L], gm[L], bt[L], hm[L], hb[L];
+    sp.load_or(y, v, 0.0f);
+    if constexpr (EARLY) {
+        sp.load(r, t);
+        sp.load_or(g, ge, 1.0f);
+        sp.load_or(a.gamma_post, gm, 1.0f);
+        sp.load_or(a.beta_post, bt, 0.0f);
+        sp.load_or(a.gamma_pre, hm, 1.0f);
+        sp.load_or(a.beta_pre, hb, 0.0f);
+    }
+    if (a.post != QNN_NORM_NONE) {
+        sp.clear(v);
+        const Stats s = row_stats<WARP>(sp, v, a.post, a.eps_post, a.inv_c, red);
+        if constexpr (EARLY) {
+            const float c = -s.mean * s.rstd;
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = __fmaf_rn(__fmaf_rn(v[e], s.rstd, c), gm[e], bt[e]);
+        } else {
+            affine(sp, v, s, a.gamma_post, a.beta_post);
+        }
+    }
+    if constexpr (EARLY) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] *= ge[e];
+    } else {
+        if (g) {
+            sp.load(g, t);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] *= t[e];
+        }
+        sp.load(r, t);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = __fmaf_rn(a.b, v[e], a.a * t[e]);
+    if (a.r_out) sp.store(static_cast<TR *>(a.r_out) + row * a.ld_r, v);
+    if (!EARLY && (WARP || a.pre == QNN_NORM_NONE)) {
+        if constexpr (WARP) __syncwarp();
+        else __syncthreads();
+        release();
+    }
+    if (!a.h) return;
+    sp.clear(v);
+    if (a.pre != QNN_NORM_NONE) {
+        const Stats s = row_stats<WARP>(sp, v, a.pre, a.eps_pre, a.inv_c, red);
+        if (!EARLY && !WARP) release();
+        if constexpr (EARLY) {
+            const float c = -s.mean * s.rstd;
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = __fmaf_rn(__fmaf_rn(v[e], s.rstd, c), hm[e], hb[e]);
+        } else {
+            affine(sp, v, s, a.gamma_pre, a.beta_pre);
+        }
+    }
+    if (!a.s8) {
+        sp.store(static_cast<TY *>(a.h) + row * a.ld_h, v);
+        return;
+    }
+    float m = 0.0f;
+    sp.clear(v);
+#pragma unroll
+    for (int e = 0; e < E; ++e) m = fmaxf(m, fabsf(v[e]));
+    m = red.max_abs<WARP>(m);
+    const float f = m == 0.0f ? 0.0f : __fdiv_rn(127.0f, m);
+    if (sp.t == 0) a.h_scale[row] = __fdiv_rn(m, 127.0f);
+    int8_t *hr = static_cast<int8_t *>(a.h) + row * a.ld_h;
 #pragma unroll
     for (int i = 0; i < I; ++i)
         if (sp.in(i)) {
-            float *x = v + i * V;
-            float p[V];
+            if constexpr (V == 1) {
+                hr[sp.col(i)] = (int8_t)low_int(v[i] * f);
+            } else {
+                uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < V; ++e) x[e] = (x[e] - s.mean) * s.rstd;
-            if (gamma) {
-                load_v<V>(gamma + sp.col(i), p);
-#pragma unroll
-                for (int e = 0; e < V; ++e) x[e] *= p[e];
-            }
-            if (beta) {
-                load_v<V>(beta + sp.col(i), p);
-#pragma unroll
-                for (int e = 0; e < V; ++e) x[e] += p[e];
+                for (int e = 0; e < 8; ++e) w[e] = low_int(v[i * V + e] * f);
+                *reinterpret_cast<uint2 *>(hr + sp.col(i)) =
+                    make_uint2(pack4(w[0], w[1], w[2], w[3]), pack4(w[4], w[5], w[6], w[7]));
             }
         }
 }
 
-template <typename TR, typename TY, int V, int I, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024)
+template <typename TY>
+__device__ __forceinline__ const TY *gate_row(const NormArgs &a, int64_t row)
+{
+    if (!a.gate) return nullptr;
+    const int64_t q = a.gate_rows == 0 ? 0 : a.gate_rows == 1 ? row : a.small_rows
+                          ? (int64_t)((uint32_t)row / (uint32_t)a.gate_rows) : row / a.gate_rows;
+    return static_cast<const TY *>(a.gate) + q * a.C;
+}
+
+// Rows by direct loads.  MAXT: threads at most.
+template <typename TR, typename TY, int V, int I, bool WARP, bool EARLY, int MAXT>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : MAXT)
     block_norm_kernel(const __grid_constant__ NormArgs a)
 {
     __shared__ float2 slots[2][32];
@@ -217,61 +382,62 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024)
     const Span<V, I> sp{(int)(WARP ? threadIdx.x & 31 : threadIdx.x), (int)(WARP ? 32 : blockDim.x), a.C};
     const int64_t first = WARP ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
     const int64_t step = WARP ? (int64_t)gridDim.x * kWarpRows : gridDim.x;
+    grid_dependency_launch();
+    grid_dependency_wait();
     for (int64_t row = first; row < a.rows; row += step) {
-        float v[V * I], r[V * I];
-        if (a.y) sp.load(static_cast<const TY *>(a.y) + row * a.ld_y, v);
-        sp.load(static_cast<const TR *>(a.r) + row * a.ld_r, r);
-        if (a.y && a.post != QNN_NORM_NONE) {
-            const Stats s = row_stats<WARP>(sp, v, a.post, a.eps_post, a.inv_c, red);
-            normalise(sp, v, s, a.gamma_post, a.beta_post);
-        }
-        const TY *gate =
-            a.gate ? static_cast<const TY *>(a.gate) + (a.gate_rows ? row / a.gate_rows : 0) * a.C : nullptr;
-#pragma unroll
-        for (int i = 0; i < I; ++i)
-            if (sp.in(i)) {
-                float g[V];
-                if (gate) load_v<V>(gate + sp.col(i), g);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    float &x = v[i * V + e];
-                    float t = a.a * r[i * V + e];
-                    if (a.y) t = __fmaf_rn(gate ? a.b * g[e] : a.b, x, t);
-                    x = t;
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; ++e) v[i * V + e] = 0.0f;
-            }
-        if (a.r_out) sp.store(static_cast<TR *>(a.r_out) + row * a.ld_r, v);
-        if (!a.h) continue;
-        if (a.pre != QNN_NORM_NONE) {
-            const Stats s = row_stats<WARP>(sp, v, a.pre, a.eps_pre, a.inv_c, red);
-            normalise(sp, v, s, a.gamma_pre, a.beta_pre);
-        }
-        if (!a.s8) {
-            sp.store(static_cast<TY *>(a.h) + row * a.ld_h, v);
-            continue;
-        }
-        // codes as q_quantize_rows_dynamic makes them: scale max|h| / 127, rint(h / scale)
-        float m = 0.0f;
-#pragma unroll
-        for (int e = 0; e < V * I; ++e) m = fmaxf(m, fabsf(v[e]));
-        const float scale = __fdiv_rn(red.max_abs<WARP>(m), 127.0f);
-        if (sp.t == 0) a.h_scale[row] = scale;
-        int8_t *hr = static_cast<int8_t *>(a.h) + row * a.ld_h;
-#pragma unroll
-        for (int i = 0; i < I; ++i)
-            if (sp.in(i)) {
-                uint32_t w[(V + 3) / 4] = {};
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const int q = scale == 0.0f ? 0 : __float2int_rn(__fdiv_rn(v[i * V + e], scale));
-                    w[e / 4] |= (uint32_t)(uint8_t)min(max(q, -128), 127) << (8 * (e % 4));
-                }
-                if constexpr (V == 1) hr[sp.col(i)] = (int8_t)w[0];
-                else *reinterpret_cast<uint2 *>(hr + sp.col(i)) = make_uint2(w[0], w[1]);
-            }
+        norm_row<TR, TY, WARP, EARLY>(a, sp, row, static_cast<const TR *>(a.r) + row * a.ld_r,
+                                      a.y ? static_cast<const TY *>(a.y) + row * a.ld_y : nullptr, gate_row<TY>(a, row),
+                                      red, [] {});
+    }
+}
+
+// Rows through a ring of `stages` in shared memory, each [r][y][gate row, when every
+// row has its own]; a warp (WARP) or a block to a ring.  A stage is asked for again
+// behind the reduction that follows its last reads.
+template <typename TR, typename TY, int I, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 256)
+    block_norm_ring_kernel(const __grid_constant__ NormArgs a)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float2 slots[2][32];
+    __shared__ __align__(8) uint64_t bars[WARP ? kWarpRows : 1][kMaxStages];
+    RowReduce red{slots};
+    const int w = WARP ? threadIdx.x >> 5 : 0;
+    const Span<8, I> sp{(int)(WARP ? threadIdx.x & 31 : threadIdx.x), (int)(WARP ? 32 : blockDim.x), a.C};
+    const int64_t first = WARP ? (int64_t)blockIdx.x * kWarpRows + w : blockIdx.x;
+    const int64_t step = WARP ? (int64_t)gridDim.x * kWarpRows : gridDim.x;
+    const int rb = a.C * (int)sizeof(TR), yb = a.y ? a.C * (int)sizeof(TY) : 0,
+              gb = a.gate && a.gate_rows == 1 ? a.C * (int)sizeof(TY) : 0, bytes = rb + yb + gb;
+    uint8_t *ring = smem + (size_t)w * a.stages * bytes;
+    const uint32_t bar0 = smem_u32(&bars[w][0]);
+    auto ask = [&](int64_t row, int stage) {  // by one thread
+        const uint32_t bar = bar0 + 8 * stage, to = smem_u32(ring + (size_t)stage * bytes);
+        mbar_arrive_expect_tx(bar, bytes);
+        bulk_g2s(to, static_cast<const TR *>(a.r) + row * a.ld_r, rb, bar);
+        if (yb) bulk_g2s(to + rb, static_cast<const TY *>(a.y) + row * a.ld_y, yb, bar);
+        if (gb) bulk_g2s(to + rb + yb, static_cast<const TY *>(a.gate) + row * a.C, gb, bar);
+    };
+    grid_dependency_launch();
+    if (sp.t == 0) {
+        for (int i = 0; i < a.stages; ++i) mbar_init(bar0 + 8 * i, 1);
+        fence_mbar_init();
+        grid_dependency_wait();
+        for (int i = 0; i < a.stages && first + i * step < a.rows; ++i) ask(first + i * step, i);
+    }
+    if constexpr (WARP) __syncwarp();
+    else __syncthreads();
+    grid_dependency_wait();
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int64_t row = first; row < a.rows; row += step) {
+        if (!mbar_wait(bar0 + 8 * stage, phase, a.status)) return;
+        const uint8_t *from = ring + (size_t)stage * bytes;
+        norm_row<TR, TY, WARP, false>(
+            a, sp, row, reinterpret_cast<const TR *>(from), yb ? reinterpret_cast<const TY *>(from + rb) : nullptr,
+            gb ? reinterpret_cast<const TY *>(from + rb + yb) : gate_row<TY>(a, row), red, [&] {
+                if (sp.t == 0 && row + a.stages * step < a.rows) ask(row + a.stages * step, stage);
+            });
+        if (++stage == a.stages) stage = 0, phase ^= 1;
     }
 }
 
@@ -317,16 +483,16 @@ __global__ void __launch_bounds__(1024) block_norm_backward_kernel(const __grid_
     for (int64_t row = row0; row < row1; ++row) {
         const bool fresh = row == row0;
         float G[V * I], x[V * I], d[V * I];
-        if (a.dr_out) sp.load(static_cast<const TR *>(a.dr_out) + row * a.ld_r, G);
+        if (a.dr_out) sp.load0(static_cast<const TR *>(a.dr_out) + row * a.ld_r, G);
         else
 #pragma unroll
             for (int e = 0; e < V * I; ++e) G[e] = 0.0f;
         if (a.dh) {
-            sp.load(static_cast<const TY *>(a.dh) + row * a.ld_h, d);
+            sp.load0(static_cast<const TY *>(a.dh) + row * a.ld_h, d);
             if (a.pre != QNN_NORM_NONE) {
-                sp.load(static_cast<const TR *>(a.r) + row * a.ld_r, x);
+                sp.load0(static_cast<const TR *>(a.r) + row * a.ld_r, x);
                 const Stats s = row_stats<false>(sp, x, a.pre, a.eps_pre, a.inv_c, red);
-                normalise(sp, x, s, nullptr, nullptr);
+                normalise(sp, x, s);
                 add(kBetaPre, fresh, d);
                 float t[V * I];
                 float2 m = make_float2(0.0f, 0.0f);
@@ -364,11 +530,11 @@ __global__ void __launch_bounds__(1024) block_norm_backward_kernel(const __grid_
         }
         if (!a.y) continue;
         // x = y^ (or y), d = t = b gate G, gsum += b G p
-        sp.load(static_cast<const TY *>(a.y) + row * a.ld_y, x);
+        sp.load0(static_cast<const TY *>(a.y) + row * a.ld_y, x);
         Stats s{0.0f, 1.0f};
         if (a.post != QNN_NORM_NONE) {
             s = row_stats<false>(sp, x, a.post, a.eps_post, a.inv_c, red);
-            normalise(sp, x, s, nullptr, nullptr);
+            normalise(sp, x, s);
         }
         const int64_t q = a.gate_rows ? row / a.gate_rows : 0;
         float2 m = make_float2(0.0f, 0.0f);
@@ -517,24 +683,56 @@ void with_types(int r_dt, int y_dt, F fn)
     else fn(__nv_bfloat16{}, __nv_bfloat16{});
 }
 
+// Launch as the programmatic dependent of the grid before on the stream: every thread
+// waits for that grid before it touches global memory.
 template <typename K, typename A>
-void launch_rows(K kern, const A &a, int threads, int rows_per_block, cudaStream_t s)
+qnn_status launch_dependent(K kern, const A &a, int64_t grid, int threads, int smem, cudaStream_t s)
 {
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess || per_sm < 1)
-        per_sm = 1;
-    const int64_t want = (a.rows + rows_per_block - 1) / rows_per_block;
-    kern<<<(int)std::min<int64_t>(want, (int64_t)sm_count() * per_sm), threads, 0, s>>>(a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return QNN_ERR_CUDA;
+    }
+    return launch_status();
 }
 
-template <typename TR, typename TY, int V, int I>
-void launch_norm(const NormArgs &a, cudaStream_t s)
+template <typename TR, typename TY, int V, int I, int MAXT>
+qnn_status launch_norm(const NormArgs &a, cudaStream_t s)
 {
-    const int per = V * I;
-    if (a.C <= 32 * per)
-        launch_rows(block_norm_kernel<TR, TY, V, I, true>, a, 32 * kWarpRows, kWarpRows, s);
-    else
-        launch_rows(block_norm_kernel<TR, TY, V, I, false>, a, (a.C + per * 32 - 1) / (per * 32) * 32, 1, s);
+    constexpr int per = V * I;
+    if (a.C <= 32 * per && MAXT <= 512)
+        return launch_dependent(block_norm_kernel<TR, TY, V, I, true, per <= 8, 512>, a,
+                                std::min<int64_t>((a.rows + kWarpRows - 1) / kWarpRows, 16 * sm_count()),
+                                32 * kWarpRows, 0, s);
+    const int threads = (a.C + per * 32 - 1) / (per * 32) * 32;
+    return launch_dependent(block_norm_kernel<TR, TY, V, I, false, per <= 8, MAXT>, a,
+                            std::min<int64_t>(a.rows, (int64_t)sm_count() * std::max(1024 / threads, 1)), threads, 0, s);
+}
+
+template <typename TR, typename TY, int I, bool WARP>
+qnn_status launch_ring(NormArgs a, cudaStream_t s)
+{
+    const int rows = WARP ? kWarpRows : 1, threads = WARP ? 32 * kWarpRows : (a.C + I * 256 - 1) / (I * 256) * 32;
+    const int stage = rows * a.C * (int)(sizeof(TR) + (a.y ? sizeof(TY) : 0) +
+                                         (a.gate && a.gate_rows == 1 ? sizeof(TY) : 0));
+    // as many blocks on an SM as its registers hold, their rings in what there is for them
+    constexpr int most = I == 1 ? 1280 : I == 2 ? 1024 : I == 3 ? 768 : 640;  // threads
+    const int blocks = std::max(1, std::min(kRingSmem / stage, most / threads));
+    a.stages = std::max(1, std::min(kMaxStages, kRingSmem / (blocks * stage)));
+    auto kern = block_norm_ring_kernel<TR, TY, I, WARP>;
+    static std::atomic<uint64_t> opted_in{0};
+    if (!opt_in_smem(kern, kRingSmem, opted_in, 60)) return QNN_ERR_CUDA;
+    const int64_t want = (a.rows + rows - 1) / rows;
+    return launch_dependent(kern, a, std::min<int64_t>(want, (int64_t)sm_count() * blocks), threads, a.stages * stage, s);
 }
 
 // Rows per block of the backward pass: two blocks' worth of rows for each SM, and no
@@ -575,19 +773,29 @@ extern "C" qnn_status q_block_norm(const void *r, qnn_dtype r_dt, const void *y,
     const int ey = float_bytes(y_dt);
     const bool vec = C % 8 == 0 && rows_aligned(a.ld_r, float_bytes(r_dt)) && (!y || rows_aligned(a.ld_y, ey)) &&
                      (!h || (s8 ? a.ld_h % 8 == 0 : rows_aligned(a.ld_h, ey)));
+    a.small_rows = rows <= INT32_MAX && p->gate_rows <= INT32_MAX;
+    a.status = status_word();
+    if (!a.status) return QNN_ERR_CUDA;
+    // rings from the size on at which every SM has several rows to go through
+    const int row_bytes = C * (float_bytes(r_dt) + (y ? ey : 0) + (p->gate && p->gate_rows == 1 ? ey : 0));
+    const bool many = rows * C >= (int64_t)sm_count() * 16384, ring = many && vec && C <= 8192 && row_bytes <= kRingSmem;
     cudaStream_t s = (cudaStream_t)stream;
+    qnn_status done = QNN_OK;
     with_types(r_dt, y_dt, [&](auto tr, auto ty) {
         using TR = decltype(tr);
         using TY = decltype(ty);
-        if (vec && C <= 256) launch_norm<TR, TY, 8, 1>(a, s);
-        else if (vec && C <= 512) launch_norm<TR, TY, 8, 2>(a, s);
-        else if (vec && C <= 1024) launch_norm<TR, TY, 8, 4>(a, s);
-        else if (vec && C <= 8192) launch_norm<TR, TY, 8, 1>(a, s);
-        else if (vec) launch_norm<TR, TY, 8, 4>(a, s);
-        else if (C <= 8192) launch_norm<TR, TY, 1, 8>(a, s);
-        else launch_norm<TR, TY, 1, 32>(a, s);
+        if (ring && C <= 256) done = launch_ring<TR, TY, 1, true>(a, s);
+        else if (ring && C <= 512) done = launch_ring<TR, TY, 2, true>(a, s);
+        else if (ring && C <= 768) done = launch_ring<TR, TY, 3, true>(a, s);
+        else if (ring && C <= 1024) done = launch_ring<TR, TY, 4, true>(a, s);
+        else if (ring) done = launch_ring<TR, TY, 4, false>(a, s);
+        else if (vec && C <= 4096) done = launch_norm<TR, TY, 8, 1, 512>(a, s);
+        else if (vec) done = launch_norm<TR, TY, 8, 4, 1024>(a, s);
+        else if (C <= 4096 && !many) done = launch_norm<TR, TY, 1, 8, 512>(a, s);
+        else if (C <= 4096) done = launch_norm<TR, TY, 1, 16, 512>(a, s);
+        else done = launch_norm<TR, TY, 1, 32, 1024>(a, s);
     });
-    return launch_status();
+    return done;
 }
 
 extern "C" size_t qnn_block_norm_backward_workspace_bytes(int64_t rows, int C, const qnn_block_norm *p)

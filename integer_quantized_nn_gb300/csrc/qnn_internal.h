@@ -17,16 +17,18 @@ int sm_count();
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Lets `kern` take `bytes` of dynamic shared memory on the current device; `done` keeps
-// the devices on which that was asked for already, so that later calls only look.
+// Lets `kern` take `bytes` of dynamic shared memory on the current device, and asks for
+// `carveout` percent of the SM's memory as shared memory (-1: the driver's choice);
+// `done` keeps the devices on which that was done, so that later calls only look.
 template <typename K>
-bool opt_in_smem(K kern, int bytes, std::atomic<uint64_t> &done)
+bool opt_in_smem(K kern, int bytes, std::atomic<uint64_t> &done, int carveout = -1)
 {
     int d = -1;
     if (cudaGetDevice(&d) != cudaSuccess || d < 0) return false;
     const uint64_t bit = d < 64 ? 1ull << d : 0;
     if (done.load(std::memory_order_relaxed) & bit) return true;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, carveout) != cudaSuccess) {
         (void)cudaGetLastError();
         return false;
     }

@@ -111,6 +111,28 @@ def test_codes(case):
     check_codes(p, h, scale)
 
 
+# enough rows for rings of rows in shared memory: one and several rows to a ring, a ring's
+# end inside the rows, widths up to its limit and beyond
+MANY = [
+    (20000, 136, dict(gate="rows", gate_rows=1)), (9001, 512, dict(gate="rows", gate_rows=700)),
+    (4000, 768, dict(gate="all")), (3100, 1000, dict(gate="rows", gate_rows=1)), (1500, 2040, {}),
+    (650, 4096, dict(gate="rows", gate_rows=1)), (500, 5128, dict(gate="all")), (400, 8192, dict(gate="rows", gate_rows=1)),
+    (9000, 333, dict(gate="rows", gate_rows=40)), (1700, 1601, {}), (700, 5001, dict(gate="all")),
+]
+
+
+@pytest.mark.parametrize("i", range(len(MANY)))
+def test_many_rows(i):
+    rows, C, more = MANY[i]
+    for j in range(2):
+        r_dt, y_dt = PAIRS[(2 * i + j) % 5]
+        post, pre = NORMS[(i + 2 * j) % 5]
+        p = bn.make(21, rows, C, r_dt, y_dt, post, pre, beta=j == 0, a=0.9, b=0.6, **more)
+        r_out, h, _ = run_forward(p)
+        check_forward(p, r_out, h)
+        check_codes(p, *run_forward(p, s8=True)[1:])
+
+
 @pytest.mark.parametrize("pads", [(1, 0, 0), (0, 3, 0), (8, 16, 24), (0, 0, 5), (4, 4, 4)])
 @pytest.mark.parametrize("types", PAIRS)
 def test_pitches(types, pads):
