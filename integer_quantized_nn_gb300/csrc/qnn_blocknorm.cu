@@ -172,7 +172,7 @@ template <typename TR, typename TY, int V, int I, bool WARP, bool EARLY, int MAX
 __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : MAXT)
     block_norm_kernel(const __grid_constant__ NormArgs a)
 {
-    __shared__ float2 slots[2][32];
+    __shared__ float slots[2][64];
     RowReduce red{slots};
     const Span<V, I> sp{(int)(WARP ? threadIdx.x & 31 : threadIdx.x), (int)(WARP ? 32 : blockDim.x), a.C};
     const int64_t first = WARP ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 256)
     block_norm_ring_kernel(const __grid_constant__ NormArgs a)
 {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float2 slots[2][32];
+    __shared__ float slots[2][64];
     __shared__ __align__(8) uint64_t bars[WARP ? kWarpRows : 1][kMaxStages];
     RowReduce red{slots};
     const int w = WARP ? threadIdx.x >> 5 : 0;

@@ -57,6 +57,44 @@ __device__ __forceinline__ void store_v(T *p, const float *v)
     }
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t as_u64(float2 v)
+{
+    uint64_t u;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(u) : "f"(v.x), "f"(v.y));
+    return u;
+}
+
+__device__ __forceinline__ float2 as_f2(uint64_t u)
+{
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(u));
+    return v;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
+    return as_f2(d);
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
+    return as_f2(d);
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
+    return as_f2(d);
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
@@ -64,28 +102,43 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-__device__ __forceinline__ float2 warp_sum(float2 v) { return make_float2(warp_sum(v.x), warp_sum(v.y)); }
+// Two sums at once: the half-warps take one each, after exchanging what the other needs;
+// lanes 0 .. 15 get v.x's, 16 .. 31 v.y's.
+__device__ __forceinline__ float half_sums(float2 v)
+{
+    const bool upper = threadIdx.x & 16;
+    float s = upper ? v.y : v.x;
+    s += __shfl_xor_sync(kFull, upper ? v.x : v.y, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+    return s;
+}
 
 // Sums (or maxima) over a row's threads: a warp, or the block through shared memory.
 // Two slots used in turn make one barrier per call enough: a slot is written again
 // only behind the barrier that follows its last read.
 struct RowReduce {
-    float2 (*slots)[32];
+    float (*slots)[64];
     int turn = 0;
 
     template <bool WARP>
     __device__ __forceinline__ float2 sum(float2 v)
     {
-        v = warp_sum(v);
+        float s = half_sums(v);
+        const int lane = threadIdx.x & 31, l = lane & 15, at = (lane >> 4) * 32;
         if constexpr (!WARP) {
-            float2 *s = slots[turn];
+            float *slot = slots[turn];
             turn ^= 1;
-            const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-            if (lane == 0) s[threadIdx.x >> 5] = v;
+            const int warps = blockDim.x >> 5;
+            if (l == 0) slot[at + (threadIdx.x >> 5)] = s;
             __syncthreads();
-            v = warp_sum(lane < warps ? s[lane] : make_float2(0.0f, 0.0f));
+            s = l < warps ? slot[at + l] : 0.0f;
+            if (l + 16 < warps) s += slot[at + 16 + l];
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
         }
-        return v;
+        const float t = __shfl_xor_sync(kFull, s, 16);
+        return lane & 16 ? make_float2(t, s) : make_float2(s, t);
     }
 
     template <bool WARP>
@@ -93,12 +146,12 @@ struct RowReduce {
     {
         v = warp_sum(v);
         if constexpr (!WARP) {
-            float2 *s = slots[turn];
+            float *slot = slots[turn];
             turn ^= 1;
             const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-            if (lane == 0) s[threadIdx.x >> 5].x = v;
+            if (lane == 0) slot[threadIdx.x >> 5] = v;
             __syncthreads();
-            v = warp_sum(lane < warps ? s[lane].x : 0.0f);
+            v = warp_sum(lane < warps ? slot[lane] : 0.0f);
         }
         return v;
     }
@@ -109,12 +162,12 @@ struct RowReduce {
         // magnitudes: their bit patterns order like the values
         uint32_t u = __reduce_max_sync(kFull, __float_as_uint(m));
         if constexpr (!WARP) {
-            float2 *s = slots[turn];
+            float *slot = slots[turn];
             turn ^= 1;
             const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-            if (lane == 0) s[threadIdx.x >> 5] = make_float2(__uint_as_float(u), 0.0f);
+            if (lane == 0) slot[threadIdx.x >> 5] = __uint_as_float(u);
             __syncthreads();
-            u = __reduce_max_sync(kFull, lane < warps ? __float_as_uint(s[lane].x) : 0u);
+            u = __reduce_max_sync(kFull, lane < warps ? __float_as_uint(slot[lane]) : 0u);
         }
         return __uint_as_float(u);
     }
@@ -170,10 +223,8 @@ struct Stats {
     float mean, rstd;
 };
 
-__device__ __forceinline__ float rstd_of(float ss, float inv_c, float eps)
-{
-    return __frcp_rn(__fsqrt_rn(__fmaf_rn(ss, inv_c, eps)));
-}
+// 1 / sqrt(ss / C + eps) (2 ulp of the fp32 value, beside sums of many roundings)
+__device__ __forceinline__ float rstd_of(float ss, float inv_c, float eps) { return rsqrtf(__fmaf_rn(ss, inv_c, eps)); }
 
 // One row's statistics; columns beyond C (zeros in v) are left out of the variance.
 template <bool WARP, int V, int I>

@@ -37,46 +37,128 @@ struct BackArgs {
 // rows that began in an earlier block's chunk, or that goes on in a later one's.
 enum { kGammaPre, kBetaPre, kGammaPost, kBetaPost, kGateHead, kGateTail, kSlots };
 
-// The statistics of two rows of values (r' and y) in the same reductions.
+// A thread's columns as pairs of fp32, for two operations in one instruction: vectors t,
+// t + threads, ... of V = 8 columns, four pairs each (a "group"), or single columns, two
+// of them a pair and a group.  Loads read column 0 in place of one beyond C; sums leave
+// those groups out (keep).
 template <int V, int I>
-__device__ __forceinline__ void stats_of_two(const Span<V, I> &sp, const float *x, const float *y, bool x_layer,
-                                             bool y_layer, const BackArgs &a, RowReduce &red, Stats &sx, Stats &sy)
-{
-    float2 m = make_float2(0.0f, 0.0f);
-    if (x_layer || y_layer) {
-#pragma unroll
-        for (int e = 0; e < V * I; ++e) m.x += x[e], m.y += y[e];
-        m = red.sum<false>(m);
-        sx.mean = x_layer ? m.x * a.inv_c : 0.0f;
-        sy.mean = y_layer ? m.y * a.inv_c : 0.0f;
+struct PairSpan {
+    static constexpr int N = V * I / 2, GP = V == 8 ? 4 : 1, G = N / GP;  // pairs, pairs of a group, groups
+    int t, threads, C;
+    __device__ __forceinline__ int col(int i) const { return (t + i * threads) * V; }
+    __device__ __forceinline__ bool in(int i) const { return col(i) < C; }
+    template <typename T>
+    __device__ __forceinline__ void load_group(const T *row, int g, float2 *v) const
+    {
+        if constexpr (V == 8) {
+            load_v<8>(row + (in(g) ? col(g) : 0), reinterpret_cast<float *>(v));
+        } else {
+            v[0].x = to_f32(row[in(2 * g) ? col(2 * g) : 0]);
+            v[0].y = to_f32(row[in(2 * g + 1) ? col(2 * g + 1) : 0]);
+        }
     }
-    m = make_float2(0.0f, 0.0f);
+    template <typename T>
+    __device__ __forceinline__ void store_group(T *row, int g, const float2 *v) const
+    {
+        if constexpr (V == 8) {
+            if (in(g)) store_v<8>(row + col(g), reinterpret_cast<const float *>(v));
+        } else {
+            if (in(2 * g)) row[col(2 * g)] = from_f32<T>(v[0].x);
+            if (in(2 * g + 1)) row[col(2 * g + 1)] = from_f32<T>(v[0].y);
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void load(const T *row, float2 *v) const
+    {
 #pragma unroll
-    for (int i = 0; i < I; ++i)
-        if (sp.in(i))
+        for (int g = 0; g < G; ++g) load_group(row, g, v + g * GP);
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(T *row, const float2 *v) const
+    {
 #pragma unroll
-            for (int e = i * V; e < (i + 1) * V; ++e) {
-                const float dx = x[e] - sx.mean, dy = y[e] - sy.mean;
-                m.x = __fmaf_rn(dx, dx, m.x);
-                m.y = __fmaf_rn(dy, dy, m.y);
-            }
-    m = red.sum<false>(m);
+        for (int g = 0; g < G; ++g) store_group(row, g, v + g * GP);
+    }
+    // the sum with group g's part where that is inside the row, without it elsewhere
+    __device__ __forceinline__ float2 keep(int g, float2 with, float2 without) const
+    {
+        const bool a = V == 8 ? in(g) : in(2 * g), b = V == 8 ? a : in(2 * g + 1);
+        return make_float2(a ? with.x : without.x, b ? with.y : without.y);
+    }
+};
+
+__device__ __forceinline__ float across(float2 v) { return v.x + v.y; }
+
+// The statistics of two rows of values (r' and y) in the same reductions.
+template <bool LAYER, int V, int I>
+__device__ __forceinline__ void stats_of_two(const PairSpan<V, I> &sp, const float2 *x, const float2 *y,
+                                             const BackArgs &a, RowReduce &red, Stats &sx, Stats &sy)
+{
+    using S = PairSpan<V, I>;
+    float2 sum_x = both(0.0f), sum_y = both(0.0f);
+    if (LAYER) {
+#pragma unroll
+        for (int g = 0; g < S::G; ++g) {
+            float2 tx = sum_x, ty = sum_y;
+#pragma unroll
+            for (int k = g * S::GP; k < (g + 1) * S::GP; ++k) tx = add2(tx, x[k]), ty = add2(ty, y[k]);
+            sum_x = sp.keep(g, tx, sum_x);
+            sum_y = sp.keep(g, ty, sum_y);
+        }
+        const float2 m = red.sum<false>(make_float2(across(sum_x), across(sum_y)));
+        sx.mean = a.pre == QNN_NORM_LAYER ? m.x * a.inv_c : 0.0f;
+        sy.mean = a.post == QNN_NORM_LAYER ? m.y * a.inv_c : 0.0f;
+        sum_x = sum_y = both(0.0f);
+    }
+    const float2 mx = both(-sx.mean), my = both(-sy.mean);
+#pragma unroll
+    for (int g = 0; g < S::G; ++g) {
+        float2 tx = sum_x, ty = sum_y;
+#pragma unroll
+        for (int k = g * S::GP; k < (g + 1) * S::GP; ++k) {
+            const float2 dx = LAYER ? add2(x[k], mx) : x[k], dy = LAYER ? add2(y[k], my) : y[k];
+            tx = fma2(dx, dx, tx);
+            ty = fma2(dy, dy, ty);
+        }
+        sum_x = sp.keep(g, tx, sum_x);
+        sum_y = sp.keep(g, ty, sum_y);
+    }
+    const float2 m = red.sum<false>(make_float2(across(sum_x), across(sum_y)));
     sx.rstd = rstd_of(m.x, a.inv_c, a.eps_pre);
     sy.rstd = rstd_of(m.y, a.inv_c, a.eps_post);
 }
 
-// RING: rows through the ring (V = 8).  REG: sums over rows in registers; rows too wide
-// for that (C > 8192) add to the workspace as they go.
-template <typename TR, typename TY, int V, int I, bool RING, bool REG, bool BETA>
-__global__ void __launch_bounds__(REG ? 512 : 1024)
+// g = (g - mean(g) [LAYER] - x mean(g x)) rstd, from a thread's parts of the sums.
+template <bool LAYER, int V, int I>
+__device__ __forceinline__ void gradient(const PairSpan<V, I> &, float2 *g, const float2 *x, float2 sg, float2 sgx,
+                                         bool layer, float rstd, float inv_c, RowReduce &red)
+{
+    const float2 rs = both(rstd);
+    if (LAYER) {
+        const float2 m = red.sum<false>(make_float2(across(sg), across(sgx)));
+        const float2 mg = both(layer ? -m.x * inv_c : 0.0f), mx = both(-m.y * inv_c);
+#pragma unroll
+        for (int k = 0; k < V * I / 2; ++k) g[k] = mul2(rs, fma2(x[k], mx, add2(g[k], mg)));
+    } else {
+        const float2 mx = both(-red.sum<false>(across(sgx)) * inv_c);
+#pragma unroll
+        for (int k = 0; k < V * I / 2; ++k) g[k] = mul2(rs, fma2(x[k], mx, g[k]));
+    }
+}
+
+// RING: rows through the ring (V = 8).  FULL: a LAYER norm or a beta takes part; without
+// them half the sums over rows are not there.
+template <typename TR, typename TY, int V, int I, bool RING, bool FULL>
+__global__ void __launch_bounds__(V * I <= 16 ? 512 : 1024)
     block_norm_backward_kernel(const __grid_constant__ BackArgs a)
 {
-    constexpr int E = V * I;
+    using S = PairSpan<V, I>;
+    constexpr int N = S::N, GP = S::GP;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float2 slots[2][32];
+    __shared__ float slots[2][64];
     __shared__ __align__(8) uint64_t bars[kMaxStages];
     RowReduce red{slots};
-    const Span<V, I> sp{(int)threadIdx.x, (int)blockDim.x, a.C};
+    const S sp{(int)threadIdx.x, (int)blockDim.x, a.C};
     const int64_t row0 = blockIdx.x * a.chunk, row1 = min(row0 + a.chunk, a.rows);
     float *part = a.ws + (int64_t)blockIdx.x * kSlots * a.C;
     const bool pre = a.dh && a.pre != QNN_NORM_NONE, post = a.y && a.post != QNN_NORM_NONE;
@@ -109,32 +191,29 @@ __global__ void __launch_bounds__(REG ? 512 : 1024)
     }
     grid_dependency_wait();
 
-    float sum[REG ? 4 : 1][REG ? E : 1], gsum[E] = {};  // gsum: the gate's gradient in the current group
-    if constexpr (REG) {
+    // Sums over the chunk's rows.  A gate that several rows share: post[] are sum G y^ and
+    // sum G over the rows of its group, and at the group's end give its gradient, b (gamma
+    // sum G y^ + beta sum G), and their parts of dgamma_post and dbeta_post, b gate times
+    // them.  Else post[] are those gradients themselves.
+    const bool shared = a.gate && a.gate_rows != 1;
+    constexpr int SUMS = FULL ? 2 : 1;
+    float2 pre_sum[SUMS][N], post_sum[SUMS][N];
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-            for (int e = 0; e < E; ++e) sum[s][e] = 0.0f;
-    } else {
-        const float zero[E] = {};
-        for (int s = 0; s < 4; ++s)
-            if (a.wants >> s & 1) sp.store(part + (int64_t)s * a.C, zero);
+    for (int k = 0; k < N; ++k) {
+        pre_sum[0][k] = post_sum[0][k] = both(0.0f);
+        if constexpr (FULL) pre_sum[1][k] = post_sum[1][k] = both(0.0f);
     }
-    // sum[slot] += u w over this thread's vector i
-    auto add = [&](int slot, int i, const float *u, const float *w) {
-        if (!BETA && !w) return;
-        if constexpr (REG) {
+    if (shared) {
+        if (a.wants >> kGammaPost & 1) sp.store(part + (int64_t)kGammaPost * a.C, post_sum[0]);
+        if (a.wants >> kBetaPost & 1) sp.store(part + (int64_t)kBetaPost * a.C, post_sum[0]);
+    }
+    auto add = [](float2 *to, const float2 *u, const float2 *w) {
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                sum[slot][i * V + e] = w ? __fmaf_rn(u[e], w[e], sum[slot][i * V + e]) : sum[slot][i * V + e] + u[e];
-        } else {
-            if (!(a.wants >> slot & 1) || !sp.in(i)) return;
-            float *p = part + (int64_t)slot * a.C + sp.col(i), o[V];
-            load_v<V>(p, o);
+        for (int e = 0; e < GP; ++e) to[e] = fma2(u[e], w[e], to[e]);
+    };
+    auto add1 = [](float2 *to, const float2 *u) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) o[e] = w ? __fmaf_rn(u[e], w[e], o[e]) : o[e] + u[e];
-            store_v<V>(p, o);
-        }
+        for (int e = 0; e < GP; ++e) to[e] = add2(u[e], to[e]);
     };
 
     int64_t q = a.gate_rows ? row0 / a.gate_rows : 0;  // the current group, and the row after it
@@ -160,92 +239,100 @@ __global__ void __launch_bounds__(REG ? 512 : 1024)
             o_row = static_cast<const TR *>(a.dr_out) + row * a.ld_r;
             g_row = static_cast<const TY *>(a.gate) + q * a.C;
         }
-        float x[E], g[E];  // r', then x^; dh, then G
+        constexpr bool KEEP = V * I <= 8 && !FULL;  // y stays in registers
+        float2 x[N], g[N], yv[N];  // r', then x^; dh, then G, then t's and dy; y, then y^
         Stats sx{0.0f, 1.0f}, sy{0.0f, 1.0f};
-        if (pre) sp.load0(r_row, x);
+#pragma unroll
+        for (int k = 0; k < N; ++k) x[k] = yv[k] = both(0.0f);
+        if (pre) sp.load(r_row, x);
+        if (a.y) sp.load(y_row, yv);
+        if (pre || post) stats_of_two<FULL>(sp, x, yv, a, red, sx, sy);
+        if (a.dh) sp.load(h_row, g);
         else
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = 0.0f;
-        if (pre || post) {
-            if (post) sp.load0(y_row, g);
-            else
-#pragma unroll
-                for (int e = 0; e < E; ++e) g[e] = 0.0f;
-            stats_of_two(sp, x, g, pre && a.pre == QNN_NORM_LAYER, post && a.post == QNN_NORM_LAYER, a, red, sx, sy);
-        }
-        if (a.dh) sp.load0(h_row, g);
-        else
-#pragma unroll
-            for (int e = 0; e < E; ++e) g[e] = 0.0f;
+            for (int k = 0; k < N; ++k) g[k] = both(0.0f);
         if (pre) {
-            const float c = -sx.mean * sx.rstd;
-            float2 m = make_float2(0.0f, 0.0f);
+            const float2 rs = both(sx.rstd), c = both(-sx.mean * sx.rstd);
+            float2 sg = both(0.0f), sgx = both(0.0f);
 #pragma unroll
-            for (int i = 0; i < I; ++i) {
-                float *xv = x + i * V, *gv = g + i * V, gm[V];
-                if (a.gamma_pre) load_v<V>(a.gamma_pre + (sp.in(i) ? sp.col(i) : 0), gm);
+            for (int i = 0; i < S::G; ++i) {
+                float2 *xv = x + i * GP, *gv = g + i * GP, gm[GP], tg = sg, tx = sgx;
+                if (a.gamma_pre) sp.load_group(a.gamma_pre, i, gm);
 #pragma unroll
-                for (int e = 0; e < V; ++e) xv[e] = __fmaf_rn(xv[e], sx.rstd, c);
-                add(kBetaPre, i, gv, nullptr);
-                add(kGammaPre, i, gv, xv);
+                for (int e = 0; e < GP; ++e) xv[e] = fma2(xv[e], rs, c);
+                add(pre_sum[0] + i * GP, gv, xv);
+                if constexpr (FULL) add1(pre_sum[1] + i * GP, gv);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    if (a.gamma_pre) gv[e] *= gm[e];
-                    m.x += gv[e];
-                    m.y = __fmaf_rn(gv[e], xv[e], m.y);
+                for (int e = 0; e < GP; ++e) {
+                    if (a.gamma_pre) gv[e] = mul2(gv[e], gm[e]);
+                    if (FULL) tg = add2(tg, gv[e]);
+                    tx = fma2(gv[e], xv[e], tx);
                 }
+                if (FULL) sg = sp.keep(i, tg, sg);
+                sgx = sp.keep(i, tx, sgx);
             }
-            m = red.sum<false>(m);
-            const float mg = a.pre == QNN_NORM_LAYER ? m.x * a.inv_c : 0.0f, mx = m.y * a.inv_c;
-#pragma unroll
-            for (int e = 0; e < E; ++e) g[e] = sx.rstd * __fmaf_rn(-x[e], mx, g[e] - mg);
+            gradient<FULL>(sp, g, x, sg, sgx, a.pre == QNN_NORM_LAYER, sx.rstd, a.inv_c, red);
         }
         if (a.dr_out) {
             sp.load(o_row, x);
 #pragma unroll
-            for (int e = 0; e < E; ++e) g[e] += x[e];
+            for (int k = 0; k < N; ++k) g[k] = add2(g[k], x[k]);
         }
-        sp.clear(g);  // columns beyond C take no part in the sums to come
         if (a.dr) {
+            const float2 f = both(a.a);
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = a.a * g[e];
+            for (int k = 0; k < N; ++k) x[k] = mul2(f, g[k]);
             sp.store(static_cast<TR *>(a.dr) + row * a.ld_r, x);
         }
         if (a.y) {
-            sp.load(y_row, x);
-            const float c = -sy.mean * sy.rstd;
-            float2 m = make_float2(0.0f, 0.0f);
+            if (!KEEP) sp.load(y_row, yv);
+            const float2 rs = both(sy.rstd), c = both(-sy.mean * sy.rstd), f = both(a.b);
+            float2 sg = both(0.0f), sgx = both(0.0f);
+            TY *gate_out = a.dgate && a.gate_rows == 1 ? static_cast<TY *>(a.dgate) + row * a.C : nullptr;
 #pragma unroll
-            for (int i = 0; i < I; ++i) {
-                const int col = sp.in(i) ? sp.col(i) : 0;
-                float *xv = x + i * V, *gv = g + i * V, gm[V], w[V], p[V];
-                if (a.gamma_post) load_v<V>(a.gamma_post + col, gm);
-                if (a.beta_post) load_v<V>(a.beta_post + col, p);
-                if (a.gate) load_v<V>(g_row + col, w);
+            for (int i = 0; i < S::G; ++i) {
+                float2 *xv = yv + i * GP, *gv = g + i * GP, gm[GP], w[GP], tg = sg, tx = sgx;
+                if (a.gamma_post) sp.load_group(a.gamma_post, i, gm);
+                if (a.gate) sp.load_group(g_row, i, w);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    if (post) xv[e] = __fmaf_rn(xv[e], sy.rstd, c);
-                    float t = a.gamma_post ? xv[e] * gm[e] : xv[e];
-                    if (a.beta_post) t += p[e];
-                    gv[e] *= a.b;
-                    gsum[i * V + e] = __fmaf_rn(gv[e], t, gsum[i * V + e]);
-                    if (a.gate) gv[e] *= w[e];
+                for (int e = 0; e < GP; ++e)
+                    if (post) xv[e] = fma2(xv[e], rs, c);
+                if (shared) {
+                    add(post_sum[0] + i * GP, gv, xv);
+                    if constexpr (FULL) add1(post_sum[1] + i * GP, gv);
                 }
-                add(kBetaPost, i, gv, nullptr);
-                add(kGammaPost, i, gv, xv);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    if (a.gamma_post) gv[e] *= gm[e];
-                    m.x += gv[e];
-                    m.y = __fmaf_rn(gv[e], xv[e], m.y);
+                for (int e = 0; e < GP; ++e) gv[e] = mul2(gv[e], f);
+                if (gate_out) {  // b G p
+                    float2 t[GP], p[GP];
+                    if (FULL && a.beta_post) sp.load_group(a.beta_post, i, p);
+#pragma unroll
+                    for (int e = 0; e < GP; ++e) {
+                        t[e] = a.gamma_post ? mul2(xv[e], gm[e]) : xv[e];
+                        if (FULL && a.beta_post) t[e] = add2(t[e], p[e]);
+                        t[e] = mul2(t[e], gv[e]);
+                    }
+                    sp.store_group(gate_out, i, t);
+                }
+                if (a.gate)
+#pragma unroll
+                    for (int e = 0; e < GP; ++e) gv[e] = mul2(gv[e], w[e]);
+                if (post) {
+                    if (!shared) {
+                        add(post_sum[0] + i * GP, gv, xv);
+                        if constexpr (FULL) add1(post_sum[1] + i * GP, gv);
+                    }
+#pragma unroll
+                    for (int e = 0; e < GP; ++e) {
+                        if (a.gamma_post) gv[e] = mul2(gv[e], gm[e]);
+                        if (FULL) tg = add2(tg, gv[e]);
+                        tx = fma2(gv[e], xv[e], tx);
+                    }
+                    if (FULL) sg = sp.keep(i, tg, sg);
+                    sgx = sp.keep(i, tx, sgx);
                 }
             }
-            if (post) {
-                m = red.sum<false>(m);
-                const float mg = a.post == QNN_NORM_LAYER ? m.x * a.inv_c : 0.0f, mx = m.y * a.inv_c;
-#pragma unroll
-                for (int e = 0; e < E; ++e) g[e] = sy.rstd * __fmaf_rn(-x[e], mx, g[e] - mg);
-            }
+            if (post) gradient<FULL>(sp, g, yv, sg, sgx, a.post == QNN_NORM_LAYER, sy.rstd, a.inv_c, red);
         }
         if constexpr (RING) {
             // all threads have read the stage: behind the last reduction, or a barrier for it
@@ -254,23 +341,64 @@ __global__ void __launch_bounds__(REG ? 512 : 1024)
             if (++stage == a.stages) stage = 0, phase ^= 1;
         }
         if (a.dy) sp.store(static_cast<TY *>(a.dy) + row * a.ld_y, g);
-        if (a.dgate && (row + 1 == q_end || row + 1 == row1)) {
-            // the group ends with this row, or the chunk does
-            const bool began = q * a.gate_rows >= row0;
-            if (began && row + 1 == q_end) sp.store(static_cast<TY *>(a.dgate) + q * a.C, gsum);
-            else sp.store(part + (int64_t)(began ? kGateTail : kGateHead) * a.C, gsum);
+        if (shared && (row + 1 == q_end || row + 1 == row1)) {  // the group ends with this row, or the chunk does
+            const bool began = q * a.gate_rows >= row0, whole = began && row + 1 == q_end;
+            float *edge = part + (int64_t)(began ? kGateTail : kGateHead) * a.C;
+            const TY *gate = static_cast<const TY *>(a.gate) + q * a.C;
+            const float2 f = both(a.b);
 #pragma unroll
-            for (int e = 0; e < E; ++e) gsum[e] = 0.0f;
+            for (int i = 0; i < S::G; ++i) {
+                float2 w[GP], t[GP], o[GP], *s0 = post_sum[0] + i * GP;
+                sp.load_group(gate, i, w);
+#pragma unroll
+                for (int e = 0; e < GP; ++e) w[e] = mul2(w[e], f);
+                if (a.wants >> kGammaPost & 1) {
+                    float *to = part + (int64_t)kGammaPost * a.C;
+                    sp.load_group(to, i, o);
+                    add(o, s0, w);
+                    sp.store_group(to, i, o);
+                }
+                if constexpr (FULL)
+                    if (a.wants >> kBetaPost & 1) {
+                        float *to = part + (int64_t)kBetaPost * a.C;
+                        sp.load_group(to, i, o);
+                        add(o, post_sum[1] + i * GP, w);
+                        sp.store_group(to, i, o);
+                    }
+                if (a.dgate) {
+                    if (a.gamma_post) sp.load_group(a.gamma_post, i, w);
+#pragma unroll
+                    for (int e = 0; e < GP; ++e) t[e] = a.gamma_post ? mul2(s0[e], w[e]) : s0[e];
+                    if constexpr (FULL)
+                        if (a.beta_post) {
+                            sp.load_group(a.beta_post, i, w);
+                            add(t, post_sum[1] + i * GP, w);
+                        }
+#pragma unroll
+                    for (int e = 0; e < GP; ++e) t[e] = mul2(t[e], f);
+                    if (whole) sp.store_group(static_cast<TY *>(a.dgate) + q * a.C, i, t);
+                    else sp.store_group(edge, i, t);
+                }
+#pragma unroll
+                for (int e = 0; e < GP; ++e) {
+                    s0[e] = both(0.0f);
+                    if constexpr (FULL) post_sum[1][i * GP + e] = both(0.0f);
+                }
+            }
         }
         if (row + 1 == q_end) {
             ++q;
             q_end = min(q_end + a.gate_rows, a.rows);
         }
     }
-    if constexpr (REG) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-            if (a.wants >> s & 1) sp.store(part + (int64_t)s * a.C, sum[s]);
+    auto put = [&](int slot, const float2 *v) {
+        if (a.wants >> slot & 1) sp.store(part + (int64_t)slot * a.C, v);
+    };
+    put(kGammaPre, pre_sum[0]);
+    if constexpr (FULL) put(kBetaPre, pre_sum[1]);
+    if (!shared) {
+        put(kGammaPost, post_sum[0]);
+        if constexpr (FULL) put(kBetaPost, post_sum[1]);
     }
 }
 
@@ -330,25 +458,28 @@ __global__ void __launch_bounds__(kFinishWarps * 32) block_norm_finish_kernel(co
 
 // ---- launch --------------------------------------------------------------------------
 
-#ifndef EIGHT
-#define EIGHT 4096
-#endif
-#ifndef THR8
-#define THR8 512
-#endif
-// Threads that hold a row: 8 columns each up to 2048, 16 up to 8192, 32 beyond.
-int back_threads(int C)
+// Whether a LAYER norm or a beta takes part: the kernel with all the sums.
+bool back_full(const qnn_block_norm *p)
 {
-    const int per = 32 * (C <= EIGHT ? 8 : C <= 8192 ? 16 : 32);
+    return p->pre == QNN_NORM_LAYER || p->post == QNN_NORM_LAYER || p->beta_pre || p->beta_post;
+}
+
+// Columns of a thread.  16 spread the fixed work of a row (reductions, addresses) over
+// more of them, where their sums fit the registers (4096 bf16 columns, RMS: 59 us with
+// 16, 70 with 8; LAYER with betas: 116 and 84).
+int back_columns(int C, bool full) { return C <= (full ? 4096 : 1024) ? 8 : C <= 8192 ? 16 : 32; }
+
+int back_threads(int C, bool full)
+{
+    const int per = 32 * back_columns(C, full);
     return (C + per - 1) / per * 32;
 }
 
-// Blocks that an SM's registers hold (about 80, 128 and 64 a thread), 8 at most: more
-// blocks are more sums to add.
-int back_blocks_per_sm(int C)
+// Blocks that an SM's registers hold (up to 128 a thread, 64 beyond 8192 columns), 8 at
+// most: more blocks are more sums to add.
+int back_blocks_per_sm(int C, bool full)
 {
-    const int threads = C <= EIGHT ? THR8 : C <= 8192 ? 512 : 1024;
-    return std::max(1, std::min(8, threads / back_threads(C)));
+    return std::max(1, std::min(8, (C <= 8192 ? 512 : 1024) / back_threads(C, full)));
 }
 
 struct BackPlan {
@@ -356,10 +487,10 @@ struct BackPlan {
     int blocks, stages;
 };
 
-BackPlan back_plan(int64_t rows, int C, int stage)
+BackPlan back_plan(int64_t rows, int C, bool full, int stage)
 {
     BackPlan p;
-    int per_sm = back_blocks_per_sm(C);
+    int per_sm = back_blocks_per_sm(C, full);
     // two stages for each block where that leaves half the blocks or more
     p.stages = 1;
     if (stage > 0) {
@@ -373,16 +504,16 @@ BackPlan back_plan(int64_t rows, int C, int stage)
     return p;
 }
 
-template <typename TR, typename TY, int V, int I, bool RING, bool REG, bool BETA>
-qnn_status launch_back(BackArgs a, const BackPlan &p, int stage, cudaStream_t s)
+template <typename TR, typename TY, int V, int I, bool RING, bool FULL>
+qnn_status launch_back(BackArgs a, const BackPlan &p, int threads, int stage, cudaStream_t s)
 {
-    auto kern = block_norm_backward_kernel<TR, TY, V, I, RING, REG, BETA>;
+    auto kern = block_norm_backward_kernel<TR, TY, V, I, RING, FULL>;
     a.stages = p.stages;
     if (RING) {
         static std::atomic<uint64_t> opted_in{0};
         if (!opt_in_smem(kern, kMaxRing, opted_in, kRingCarveout)) return QNN_ERR_CUDA;
     }
-    return launch_dependent(kern, a, p.blocks, back_threads(a.C), RING ? p.stages * stage : 0, s);
+    return launch_dependent(kern, a, p.blocks, threads, RING ? p.stages * stage : 0, s);
 }
 
 }  // namespace
@@ -393,7 +524,7 @@ extern "C" size_t qnn_block_norm_backward_workspace_bytes(int64_t rows, int C, c
     using namespace qnn;
     if (!p || rows < 0 || C <= 0 || C > kMaxC) return 0;
     // the most blocks that any types lead to
-    return (size_t)std::min<int64_t>(rows, (int64_t)sm_count() * back_blocks_per_sm(C)) * kSlots * C * sizeof(float);
+    return (size_t)std::min<int64_t>(rows, (int64_t)sm_count() * back_blocks_per_sm(C, back_full(p))) * kSlots * C * sizeof(float);
 }
 
 extern "C" qnn_status q_block_norm_backward(const void *r_out, qnn_dtype r_dt, const void *y, qnn_dtype y_dt,
@@ -437,8 +568,9 @@ extern "C" qnn_status q_block_norm_backward(const void *r_out, qnn_dtype r_dt, c
     const int stage = C * ((dh && p->pre != QNN_NORM_NONE ? er : 0) + (y ? ey : 0) + (dh ? ey : 0) + (dr_out ? er : 0) +
                            (p->gate && p->gate_rows == 1 ? ey : 0));
     const bool ring = vec && C <= 8192 && stage <= kMaxRing;
-    const bool beta = dbeta_pre || dbeta_post;
-    const BackPlan plan = back_plan(rows, C, ring ? stage : 0);
+    const bool full = back_full(p), eight = back_columns(C, full) == 8;
+    const int threads = back_threads(C, full);
+    const BackPlan plan = back_plan(rows, C, full, ring ? stage : 0);
     a.chunk = plan.chunk;
     cudaStream_t s = (cudaStream_t)stream;
     if (rows > 0) {
@@ -446,12 +578,16 @@ extern "C" qnn_status q_block_norm_backward(const void *r_out, qnn_dtype r_dt, c
         with_types(r_dt, y_dt, [&](auto tr, auto ty) {
             using TR = decltype(tr);
             using TY = decltype(ty);
-            if (ring && C <= EIGHT) done = beta ? launch_back<TR, TY, 8, 1, true, true, true>(a, plan, stage, s) : launch_back<TR, TY, 8, 1, true, true, false>(a, plan, stage, s);
-            else if (ring) done = beta ? launch_back<TR, TY, 8, 2, true, true, true>(a, plan, stage, s) : launch_back<TR, TY, 8, 2, true, true, false>(a, plan, stage, s);
-            else if (C <= EIGHT) done = launch_back<TR, TY, 1, 8, false, true, true>(a, plan, 0, s);
-            else if (C <= 8192) done = launch_back<TR, TY, 1, 16, false, true, true>(a, plan, 0, s);
-            else if (vec) done = launch_back<TR, TY, 8, 4, false, false, true>(a, plan, 0, s);
-            else done = launch_back<TR, TY, 1, 32, false, false, true>(a, plan, 0, s);
+            if (ring && eight)
+                done = full ? launch_back<TR, TY, 8, 1, true, true>(a, plan, threads, stage, s)
+                            : launch_back<TR, TY, 8, 1, true, false>(a, plan, threads, stage, s);
+            else if (ring)
+                done = full ? launch_back<TR, TY, 8, 2, true, true>(a, plan, threads, stage, s)
+                            : launch_back<TR, TY, 8, 2, true, false>(a, plan, threads, stage, s);
+            else if (eight) done = launch_back<TR, TY, 1, 8, false, true>(a, plan, threads, 0, s);
+            else if (C <= 8192) done = launch_back<TR, TY, 1, 16, false, true>(a, plan, threads, 0, s);
+            else if (vec) done = launch_back<TR, TY, 8, 4, false, true>(a, plan, threads, 0, s);
+            else done = launch_back<TR, TY, 1, 32, false, true>(a, plan, threads, 0, s);
         });
         if (done != QNN_OK || !sums) return done;
     }
