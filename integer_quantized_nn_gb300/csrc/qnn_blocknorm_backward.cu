@@ -475,11 +475,11 @@ int back_threads(int C, bool full)
     return (C + per - 1) / per * 32;
 }
 
-// Blocks that an SM's registers hold (up to 128 a thread, 64 beyond 8192 columns), 8 at
+// Blocks that an SM's registers hold (up to 128 a thread, 64 beyond 8192 columns), 16 at
 // most: more blocks are more sums to add.
 int back_blocks_per_sm(int C, bool full)
 {
-    return std::max(1, std::min(8, (C <= 8192 ? 512 : 1024) / back_threads(C, full)));
+    return std::max(1, std::min(16, (C <= 8192 ? 512 : 1024) / back_threads(C, full)));
 }
 
 struct BackPlan {

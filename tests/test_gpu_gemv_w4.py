@@ -65,6 +65,16 @@ CASES = [
     (1, 4096, 1024, 128, "bf16", "s4", "f32", False),
     (1, 24, 32768, 128, "f16", "u4", "f32", False),
     (2, 5000, 64, 32, "bf16", "s4", "f32", True),
+    # more columns than one tile of 8, or x too long for shared memory
+    (8, 40, 8192, 128, "bf16", "s4", "bf16", True),
+    (1, 33, 60002, 64, "f16", "u4", "f32", False),
+    (3, 300, 1024, 64, "f32", "u4", "f16", True),
+    (12, 2500, 512, 128, "f16", "s4", "f16", False),
+    (20, 130, 4096, 32, "bf16", "u4", "bf16", True),
+    (32, 5000, 384, 64, "bf16", "u4", "f32", True),
+    (65, 257, 130, 32, "f16", "u4", "f32", True),
+    (9, 20000, 256, 128, "bf16", "s4", "f32", False),
+    (31, 1030, 3000, 96, "f32", "s4", "f32", True),
 ]
 
 
@@ -75,11 +85,12 @@ def test_product(case):
     check(p, product(p, x_dt, x_dt, scale_dt), x_dt)
 
 
+@pytest.mark.parametrize("M", [2, 5, 21])
 @pytest.mark.parametrize("x_dt", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("pad_x,pad_y", [(0, 1), (1, 3), (8, 0), (24, 8)])
-def test_pitches_and_fp32_results(x_dt, pad_x, pad_y):
+@pytest.mark.parametrize("pad_x,pad_y", [(0, 1), (1, 3), (2, 1), (4, 0), (8, 0), (24, 8)])
+def test_pitches_and_fp32_results(x_dt, pad_x, pad_y, M):
     """Rows apart, on and off 16-byte boundaries, NaN between them; y in fp32."""
-    p = _w4.make(np.random.default_rng(5), 5, 37, 328, 64, x_dt, "u4", "f32", True)
+    p = _w4.make(np.random.default_rng(5), M, 37, 328, 64, x_dt, "u4", "f32", True)
     check(p, product(p, x_dt, "f32", "f32", pad_x, pad_y), "f32")
 
 
@@ -115,10 +126,11 @@ def test_fp32_rows_keep_their_24_bits():
     assert (np.abs(y - ref) <= np.abs(ref) * 2.0 ** -22).all()
 
 
+@pytest.mark.parametrize("M", [4, 13])
 @pytest.mark.parametrize("x_dt", ["f32", "f16", "bf16"])
-def test_infinities_and_nan_stay_in_their_row(x_dt):
+def test_infinities_and_nan_stay_in_their_row(x_dt, M):
     t = torch()
-    p = _w4.make(np.random.default_rng(7), 4, 40, 192, 64, x_dt, "s4", "f32", True)
+    p = _w4.make(np.random.default_rng(7), M, 40, 192, 64, x_dt, "s4", "f32", True)
     p["q"][:] |= 1  # no zero weights: inf * 0 would be NaN
     p["W"] = t.from_numpy(((p["q"][:, 0::2] & 15) | ((p["q"][:, 1::2] & 15) << 4)).astype(np.uint8))
     p["x"][1, 70] = float("inf")
@@ -126,8 +138,9 @@ def test_infinities_and_nan_stay_in_their_row(x_dt):
     y = product(p, x_dt, "f32", "f32")
     assert np.array_equal(y[1], np.where(p["q"][:, 70] > 0, np.inf, -np.inf))
     assert np.isnan(y[2]).all()
-    p["x"] = p["x"][[0, 3]]
-    check(p, y[[0, 3]], "f32")
+    fine = [m for m in range(M) if m not in (1, 2)]
+    p["x"] = p["x"][fine]
+    check(p, y[fine], "f32")
 
 
 def test_zero_rows_and_zero_scales():
@@ -166,7 +179,7 @@ def test_codes_from_q_quantize():
     check(p, product(p, "bf16", "bf16", "f32"), "bf16")
 
 
-@pytest.mark.parametrize("case", [CASES[6], CASES[9], CASES[16]], ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("case", [CASES[6], CASES[9], CASES[16], CASES[27]], ids=lambda c: "-".join(map(str, c)))
 def test_equal_calls_give_equal_bits(case):
     M, N, K, group, x_dt, w_dt, scale_dt, bias = case
     p = _w4.make(np.random.default_rng(1), *case)
@@ -175,25 +188,26 @@ def test_equal_calls_give_equal_bits(case):
         assert np.array_equal(product(p, x_dt, "f32", scale_dt), first)
 
 
-def test_side_stream_and_graph():
+@pytest.mark.parametrize("M", [4, 18])
+def test_side_stream_and_graph(M):
     """On a stream of the caller's, then captured and replayed on new activations."""
     t = torch()
-    case = (4, 512, 1024, 128, "bf16", "u4", "f32", True)
+    case = (M, 512, 1024, 128, "bf16", "u4", "f32", True)
     p = _w4.make(np.random.default_rng(12), *case)
     g, W = packed(p, "f32")
-    x, y = p["x"].cuda(), t.zeros(4, 512, dtype=t.bfloat16, device="cuda")
+    x, y = p["x"].cuda(), t.zeros(M, 512, dtype=t.bfloat16, device="cuda")
     bias = p["bias"].cuda()
     side = t.cuda.Stream()
     side.wait_stream(t.cuda.current_stream())
     with t.cuda.stream(side):
-        qnn.qgemv_w4(x, "bf16", W, g, 4, y, "bf16", bias=bias)
+        qnn.qgemv_w4(x, "bf16", W, g, M, y, "bf16", bias=bias)
     t.cuda.current_stream().wait_stream(side)
     check(p, y.double().cpu().numpy(), "bf16")
     graph = t.cuda.CUDAGraph()
     with t.cuda.graph(graph):
         for _ in range(3):
-            qnn.qgemv_w4(x, "bf16", W, g, 4, y, "bf16", bias=bias)
-    p["x"] = t.from_numpy(np.random.default_rng(13).normal(0, 1, size=(4, 1024))).bfloat16()
+            qnn.qgemv_w4(x, "bf16", W, g, M, y, "bf16", bias=bias)
+    p["x"] = t.from_numpy(np.random.default_rng(13).normal(0, 1, size=(M, 1024))).bfloat16()
     x.copy_(p["x"])
     y.zero_()
     graph.replay()
