@@ -113,7 +113,7 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const Span<V, I> &sp
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = __fmaf_rn(a.b, v[e], a.a * t[e]);
     if (a.r_out) sp.store(static_cast<TR *>(a.r_out) + row * a.ld_r, v);
-    if (!EARLY && (WARP || a.pre == QNN_NORM_NONE)) {
+    if (!EARLY && (WARP || a.pre == QNN_NORM_NONE || !a.h)) {  // no reduction follows whose barrier would do
         if constexpr (WARP) __syncwarp();
         else __syncthreads();
         release();
@@ -225,7 +225,10 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 256)
     int stage = 0;
     uint32_t phase = 0;
     for (int64_t row = first; row < a.rows; row += step) {
-        if (!mbar_wait(bar0 + 8 * stage, phase, a.status)) return;
+        if (!mbar_wait(bar0 + 8 * stage, phase, a.status)) {
+            drain_ring(bar0, a.stages, stage, phase, (a.rows - row + step - 1) / step, a.status);
+            return;
+        }
         const uint8_t *from = ring + (size_t)stage * bytes;
         norm_row<TR, TY, WARP, false>(
             a, sp, row, reinterpret_cast<const TR *>(from), yb ? reinterpret_cast<const TY *>(from + rb) : nullptr,

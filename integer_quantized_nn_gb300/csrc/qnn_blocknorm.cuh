@@ -254,6 +254,17 @@ __device__ __forceinline__ Stats row_stats(const Span<V, I> &sp, const float *v,
     return s;
 }
 
+// After a wait that gave up: waits, each with its limit, for the ring's other copies in
+// flight, `left` rows from `stage` on at most, so that none writes to memory given back.
+__device__ __forceinline__ void drain_ring(uint32_t bar0, int stages, int stage, uint32_t phase, int64_t left,
+                                           uint32_t *status)
+{
+    for (int i = 0; i < stages && i < left; ++i) {
+        (void)mbar_wait(bar0 + 8 * stage, phase, status);
+        if (++stage == stages) stage = 0, phase ^= 1;
+    }
+}
+
 // ---- host ----------------------------------------------------------------------------
 
 

@@ -149,7 +149,7 @@ __device__ __forceinline__ void gradient(const PairSpan<V, I> &, float2 *g, cons
 // RING: rows through the ring (V = 8).  FULL: a LAYER norm or a beta takes part; without
 // them half the sums over rows are not there.
 template <typename TR, typename TY, int V, int I, bool RING, bool FULL>
-__global__ void __launch_bounds__(V * I <= 16 ? 512 : 1024)
+__global__ void __launch_bounds__(V * I <= 16 ? 512 : 1024, 1)
     block_norm_backward_kernel(const __grid_constant__ BackArgs a)
 {
     using S = PairSpan<V, I>;
@@ -224,7 +224,10 @@ __global__ void __launch_bounds__(V * I <= 16 ? 512 : 1024)
         const TR *r_row, *o_row;
         const TY *y_row, *h_row, *g_row;
         if constexpr (RING) {
-            if (!mbar_wait(bar0 + 8 * stage, phase, a.status)) return;
+            if (!mbar_wait(bar0 + 8 * stage, phase, a.status)) {
+                drain_ring(bar0, a.stages, stage, phase, row1 - row, a.status);
+                return;
+            }
             const uint8_t *from = smem + (size_t)stage * bytes;
             r_row = reinterpret_cast<const TR *>(from);
             y_row = reinterpret_cast<const TY *>(from + rb);
@@ -427,6 +430,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32) block_norm_finish_kernel(co
     int b0 = 0, b1 = a.blocks;
     int64_t q = 0;
     grid_dependency_launch();
+    grid_dependency_wait();  // by blocks without a job too: a grid that waited for nothing could end before the rows'
     if (!param) {
         if (a.by_group) q = job;
         else q = (job + 1) * a.chunk / a.gate_rows;  // the group of the first row behind the boundary
@@ -435,7 +439,6 @@ __global__ void __launch_bounds__(kFinishWarps * 32) block_norm_finish_kernel(co
         b1 = (int)((r1 - 1) / a.chunk) + 1;
         if (b1 - b0 == 1 || (!a.by_group && b0 != job)) return;  // one block's alone, or another boundary's
     }
-    grid_dependency_wait();
     float v = 0.0f;
     if (col < a.C)
 #pragma unroll 8

@@ -131,6 +131,24 @@ def test_many_rows(i):
         r_out, h, _ = run_forward(p)
         check_forward(p, r_out, h)
         check_codes(p, *run_forward(p, s8=True)[1:])
+        check_backward(p, stored(p), run_backward(p, stored(p)))
+
+
+@pytest.mark.parametrize("rows,C", [(20000, 136), (5000, 768), (1500, 2048), (400, 8192)])
+def test_many_rows_with_parts_left_out(rows, C):
+    """No h, no r', in place, no block, no norm before: each leaves out a barrier or an array."""
+    p = bn.make(22, rows, C, "f32", "bf16", gate="all", beta=False)
+    check_forward(p, *run_forward(p, want_h=False)[:2])
+    check_forward(p, *run_forward(p, want_r=False)[:2])
+    check_forward(p, *run_forward(p, in_place=True)[:2])
+    for post, pre, with_y in (("layer", "none", True), ("none", "none", True), ("none", "rms", False)):
+        p = bn.make(23, rows, C, "bf16", "bf16", post, pre, gate="all" if with_y else "none", with_y=with_y)
+        r_out, h, _ = run_forward(p)
+        check_forward(p, r_out, h)
+        check_forward(p, *run_forward(p, want_h=False)[:2])
+        check_backward(p, stored(p), run_backward(p, stored(p)))
+        check_backward(p, stored(p), run_backward(p, stored(p), in_place=True))
+    check_backward(p, stored(p), run_backward(p, stored(p), use_dr_out=False), use_dr_out=False)
 
 
 @pytest.mark.parametrize("pads", [(1, 0, 0), (0, 3, 0), (8, 16, 24), (0, 0, 5), (4, 4, 4)])
