@@ -254,6 +254,35 @@ __device__ __forceinline__ Stats row_stats(const Span<V, I> &sp, const float *v,
     return s;
 }
 
+// Rows come to shared memory in whole 16-byte pieces: the window around a row, which
+// starts `off` bytes into it (V = 8: rows on such boundaries, off = 0).  A window reaches
+// up to 15 bytes past its row; rows whose windows could leave the tensor, the last ones,
+// are not copied (ring_rows).
+template <int V>
+__host__ __device__ inline int window_room(int C, int elem)
+{
+    return V == 8 ? C * elem : (C * elem + 30) & ~15;
+}
+
+struct Window {
+    const uint8_t *src;
+    uint32_t off, bytes;
+};
+
+template <int V, typename T>
+__device__ __forceinline__ Window window(const void *base, int64_t row, int64_t ld, int C)
+{
+    const int64_t at = row * ld * (int)sizeof(T);
+    const uint32_t off = V == 8 ? 0 : (uint32_t)at & 15u;
+    return {static_cast<const uint8_t *>(base) + (at - off), off, (off + (uint32_t)C * (uint32_t)sizeof(T) + 15u) & ~15u};
+}
+
+// Leading rows of `rows` whose windows stay inside a tensor of pitch ld.
+inline int64_t ring_rows(int64_t rows, int64_t ld, int elem)
+{
+    return std::max<int64_t>(0, rows - (15 + ld * elem - 1) / (ld * elem));
+}
+
 // After a wait that gave up: waits, each with its limit, for the ring's other copies in
 // flight, `left` rows from `stage` on at most, so that none writes to memory given back.
 __device__ __forceinline__ void drain_ring(uint32_t bar0, int stages, int stage, uint32_t phase, int64_t left,

@@ -30,6 +30,7 @@ struct BackArgs {
     float a, b, eps_post, eps_pre, inv_c;
     int C, post, pre;
     int stages;        // of the ring
+    int64_t ring_rows; // the rows that come through it
     uint32_t *status;  // device status word
 };
 
@@ -146,7 +147,7 @@ __device__ __forceinline__ void gradient(const PairSpan<V, I> &, float2 *g, cons
     }
 }
 
-// RING: rows through the ring (V = 8).  FULL: a LAYER norm or a beta takes part; without
+// RING: rows through the ring.  FULL: a LAYER norm or a beta takes part; without
 // them half the sums over rows are not there.
 template <typename TR, typename TY, int V, int I, bool RING, bool FULL>
 __global__ void __launch_bounds__(V * I <= 16 ? 512 : 1024, 1)
@@ -164,20 +165,26 @@ __global__ void __launch_bounds__(V * I <= 16 ? 512 : 1024, 1)
     const bool pre = a.dh && a.pre != QNN_NORM_NONE, post = a.y && a.post != QNN_NORM_NONE;
 
     // a stage: [r'][y][dh][dr'][gate row], those that every row has
-    const int rb = pre ? a.C * (int)sizeof(TR) : 0, yb = a.y ? a.C * (int)sizeof(TY) : 0,
-              hb = a.dh ? a.C * (int)sizeof(TY) : 0, ob = a.dr_out ? a.C * (int)sizeof(TR) : 0,
-              gb = a.gate && a.gate_rows == 1 ? a.C * (int)sizeof(TY) : 0, bytes = rb + yb + hb + ob + gb;
+    const bool own_gate = a.gate && a.gate_rows == 1;
+    const int rr = window_room<V>(a.C, sizeof(TR)), yr = window_room<V>(a.C, sizeof(TY));
+    const int rb = pre ? rr : 0, yb = a.y ? yr : 0, hb = a.dh ? yr : 0, ob = a.dr_out ? rr : 0, gb = own_gate ? yr : 0,
+              bytes = rb + yb + hb + ob + gb;
     const uint32_t bar0 = smem_u32(bars);
     auto ask = [&](int64_t row, int stage) {  // by one thread
+        if (V == 1 && row >= a.ring_rows) return;
         const uint32_t bar = bar0 + 8 * stage;
         uint32_t to = smem_u32(smem + (size_t)stage * bytes);
-        mbar_arrive_expect_tx(bar, bytes);
-        if (rb) bulk_g2s(to, static_cast<const TR *>(a.r) + row * a.ld_r, rb, bar);
-        if (yb) bulk_g2s(to + rb, static_cast<const TY *>(a.y) + row * a.ld_y, yb, bar);
-        if (hb) bulk_g2s(to + rb + yb, static_cast<const TY *>(a.dh) + row * a.ld_h, hb, bar);
+        const Window r = window<V, TR>(a.r, row, a.ld_r, a.C), y = window<V, TY>(a.y, row, a.ld_y, a.C),
+                     h = window<V, TY>(a.dh, row, a.ld_h, a.C), o = window<V, TR>(a.dr_out, row, a.ld_r, a.C),
+                     g = window<V, TY>(a.gate, row, a.C, a.C);
+        mbar_arrive_expect_tx(bar, (rb ? r.bytes : 0) + (yb ? y.bytes : 0) + (hb ? h.bytes : 0) + (ob ? o.bytes : 0) +
+                                       (gb ? g.bytes : 0));
+        if (rb) bulk_g2s(to, r.src, r.bytes, bar);
+        if (yb) bulk_g2s(to + rb, y.src, y.bytes, bar);
+        if (hb) bulk_g2s(to + rb + yb, h.src, h.bytes, bar);
         to += rb + yb + hb;
-        if (ob) bulk_g2s(to, static_cast<const TR *>(a.dr_out) + row * a.ld_r, ob, bar);
-        if (gb) bulk_g2s(to + ob, static_cast<const TY *>(a.gate) + row * a.C, gb, bar);
+        if (ob) bulk_g2s(to, o.src, o.bytes, bar);
+        if (gb) bulk_g2s(to + ob, g.src, g.bytes, bar);
     };
     grid_dependency_launch();
     if constexpr (RING) {
@@ -221,26 +228,25 @@ __global__ void __launch_bounds__(V * I <= 16 ? 512 : 1024, 1)
     int stage = 0;
     uint32_t phase = 0;
     for (int64_t row = row0; row < row1; ++row) {
-        const TR *r_row, *o_row;
-        const TY *y_row, *h_row, *g_row;
-        if constexpr (RING) {
+        const TR *r_row = static_cast<const TR *>(a.r) + row * a.ld_r,
+                 *o_row = static_cast<const TR *>(a.dr_out) + row * a.ld_r;
+        const TY *y_row = static_cast<const TY *>(a.y) + row * a.ld_y,
+                 *h_row = static_cast<const TY *>(a.dh) + row * a.ld_h,
+                 *g_row = static_cast<const TY *>(a.gate) + q * a.C;
+        if (RING && (V == 8 || row < a.ring_rows)) {
             if (!mbar_wait(bar0 + 8 * stage, phase, a.status)) {
-                drain_ring(bar0, a.stages, stage, phase, row1 - row, a.status);
+                drain_ring(bar0, a.stages, stage, phase, min(row1, a.ring_rows) - row, a.status);
                 return;
             }
             const uint8_t *from = smem + (size_t)stage * bytes;
-            r_row = reinterpret_cast<const TR *>(from);
-            y_row = reinterpret_cast<const TY *>(from + rb);
-            h_row = reinterpret_cast<const TY *>(from + rb + yb);
-            o_row = reinterpret_cast<const TR *>(from + rb + yb + hb);
-            g_row = gb ? reinterpret_cast<const TY *>(from + rb + yb + hb + ob)
-                       : static_cast<const TY *>(a.gate) + q * a.C;
-        } else {
-            r_row = static_cast<const TR *>(a.r) + row * a.ld_r;
-            y_row = static_cast<const TY *>(a.y) + row * a.ld_y;
-            h_row = static_cast<const TY *>(a.dh) + row * a.ld_h;
-            o_row = static_cast<const TR *>(a.dr_out) + row * a.ld_r;
-            g_row = static_cast<const TY *>(a.gate) + q * a.C;
+            r_row = reinterpret_cast<const TR *>(from + window<V, TR>(a.r, row, a.ld_r, a.C).off);
+            from += rb;
+            y_row = reinterpret_cast<const TY *>(from + window<V, TY>(a.y, row, a.ld_y, a.C).off);
+            from += yb;
+            h_row = reinterpret_cast<const TY *>(from + window<V, TY>(a.dh, row, a.ld_h, a.C).off);
+            from += hb;
+            o_row = reinterpret_cast<const TR *>(from + window<V, TR>(a.dr_out, row, a.ld_r, a.C).off);
+            if (gb) g_row = reinterpret_cast<const TY *>(from + ob + window<V, TY>(a.gate, row, a.C, a.C).off);
         }
         constexpr bool KEEP = V * I <= 8 && !FULL;  // y stays in registers
         float2 x[N], g[N], yv[N];  // r', then x^; dh, then G, then t's and dy; y, then y^
@@ -568,9 +574,17 @@ extern "C" qnn_status q_block_norm_backward(const void *r_out, qnn_dtype r_dt, c
     const int er = float_bytes(r_dt), ey = float_bytes(y_dt);
     const bool vec = C % 8 == 0 && rows_aligned(a.ld_r, er) && (!y || rows_aligned(a.ld_y, ey)) &&
                      (!dh || rows_aligned(a.ld_h, ey));
-    const int stage = C * ((dh && p->pre != QNN_NORM_NONE ? er : 0) + (y ? ey : 0) + (dh ? ey : 0) + (dr_out ? er : 0) +
-                           (p->gate && p->gate_rows == 1 ? ey : 0));
-    const bool ring = vec && C <= 8192 && stage <= kMaxRing;
+    const int rr = vec ? window_room<8>(C, er) : window_room<1>(C, er), yr = vec ? window_room<8>(C, ey) : window_room<1>(C, ey);
+    const bool own_gate = p->gate && p->gate_rows == 1, needs_r = dh && p->pre != QNN_NORM_NONE;
+    const int stage = (needs_r ? rr : 0) + (y ? yr : 0) + (dh ? yr : 0) + (dr_out ? rr : 0) + (own_gate ? yr : 0);
+    const bool ring = C <= 8192 && stage <= kMaxRing;
+    a.ring_rows = rows;
+    if (!vec) {
+        a.ring_rows = ring_rows(rows, a.ld_r, er);
+        if (y) a.ring_rows = std::min(a.ring_rows, ring_rows(rows, a.ld_y, ey));
+        if (dh) a.ring_rows = std::min(a.ring_rows, ring_rows(rows, a.ld_h, ey));
+        if (own_gate) a.ring_rows = std::min(a.ring_rows, ring_rows(rows, C, ey));
+    }
     const bool full = back_full(p), eight = back_columns(C, full) == 8;
     const int threads = back_threads(C, full);
     const BackPlan plan = back_plan(rows, C, full, ring ? stage : 0);
@@ -581,13 +595,16 @@ extern "C" qnn_status q_block_norm_backward(const void *r_out, qnn_dtype r_dt, c
         with_types(r_dt, y_dt, [&](auto tr, auto ty) {
             using TR = decltype(tr);
             using TY = decltype(ty);
-            if (ring && eight)
+            if (ring && vec && eight)
                 done = full ? launch_back<TR, TY, 8, 1, true, true>(a, plan, threads, stage, s)
                             : launch_back<TR, TY, 8, 1, true, false>(a, plan, threads, stage, s);
-            else if (ring)
+            else if (ring && vec)
                 done = full ? launch_back<TR, TY, 8, 2, true, true>(a, plan, threads, stage, s)
                             : launch_back<TR, TY, 8, 2, true, false>(a, plan, threads, stage, s);
-            else if (eight) done = launch_back<TR, TY, 1, 8, false, true>(a, plan, threads, 0, s);
+            else if (ring && eight) done = launch_back<TR, TY, 1, 8, true, true>(a, plan, threads, stage, s);
+            else if (ring)
+                done = full ? launch_back<TR, TY, 1, 16, true, true>(a, plan, threads, stage, s)
+                            : launch_back<TR, TY, 1, 16, true, false>(a, plan, threads, stage, s);
             else if (C <= 8192) done = launch_back<TR, TY, 1, 16, false, true>(a, plan, threads, 0, s);
             else if (vec) done = launch_back<TR, TY, 8, 4, false, true>(a, plan, threads, 0, s);
             else done = launch_back<TR, TY, 1, 32, false, true>(a, plan, threads, 0, s);
