@@ -157,21 +157,26 @@ def _check(status: int, what: str):
 
 
 def _ptr(t) -> Optional[int]:
-    if t is None:
-        return None
-    return int(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _nbytes(t) -> int:
     return int(t.numel()) * int(t.element_size())
 
 
+_current_stream = None
+
+
 def _stream(stream) -> Optional[int]:
+    global _current_stream
     if stream is not None:
         return int(getattr(stream, "cuda_stream", stream))
-    import torch
-    # the handle alone: a torch.cuda.Stream object for it takes longer than the launch
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if _current_stream is None:
+        import torch
+        # the handle alone: a torch.cuda.Stream object for it takes longer than the launch
+        handle, device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+        _current_stream = lambda: handle(device())  # noqa: E731
+    return _current_stream()
 
 
 def _shape(shape):
