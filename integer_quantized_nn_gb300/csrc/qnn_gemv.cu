@@ -440,6 +440,8 @@ extern "C" qnn_status qgemv_w4(const void *x, qnn_dtype x_dt, int64_t ldx, const
     if (!x || !W_packed || !y) return QNN_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned_image(W_packed) || !aligned16(y) || (bias && !aligned16(bias)))
         return QNN_ERR_ALIGNMENT;
+    // the passes are a grid's y; ahead of the products of M below, which it keeps in range
+    if (M > 65535 * (int64_t)(kMaxCols / (x_dt == QNN_F32 ? Cols<QNN_F32>::kParts : 1))) return QNN_ERR_UNSUPPORTED;
     const uint8_t *w = static_cast<const uint8_t *>(W_packed);
     GemvArgs a{};
     a.x = x;

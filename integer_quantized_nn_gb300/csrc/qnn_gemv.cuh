@@ -88,6 +88,9 @@ struct Cols {
     static constexpr int kParts = XT == QNN_F32 ? 3 : 1;
 };
 
+// columns of the B operand that one pass over the weights takes at most
+constexpr int kMaxCols = 32;
+
 __device__ __forceinline__ void bf16_parts(float v, uint32_t (&p)[3])
 {
     const uint32_t u = __float_as_uint(v);

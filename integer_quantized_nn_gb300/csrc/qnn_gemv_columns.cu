@@ -381,7 +381,6 @@ qnn_status launch(const GemvArgs &a, cudaStream_t s)
 {
     constexpr int TOK = NC / Cols<XT>::kParts;
     const int64_t by = (a.M + TOK - 1) / TOK, bx = (a.tiles + 7) / 8;
-    if (by > 65535) return QNN_ERR_UNSUPPORTED;
     // K split over a cluster while the blocks still run all at once and keep two steps each
     int splits = 1;
     while (splits < 4 && bx * by * splits * 2 <= sm_count() && a.steps >= 4 * splits) splits *= 2;
@@ -424,7 +423,7 @@ qnn_status launch_type(const GemvArgs &a, int group, cudaStream_t s)
 {
     const int64_t cols = a.M * Cols<XT>::kParts;
     if (cols <= 16) return a.zero ? launch_group<XT, 16, true>(a, group, s) : launch_group<XT, 16, false>(a, group, s);
-    return a.zero ? launch_group<XT, 32, true>(a, group, s) : launch_group<XT, 32, false>(a, group, s);
+    return a.zero ? launch_group<XT, kMaxCols, true>(a, group, s) : launch_group<XT, kMaxCols, false>(a, group, s);
 }
 
 }  // namespace

@@ -60,6 +60,15 @@ def test_product_refusals(lib):
     assert lib.qgemv_w4(16, 6, 0, 16, None, 1, None, 16, 6, 0, None) == qnn.QNN_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("x_dt, rows", [("bf16", 32), ("f16", 32), ("f32", 10)])
+def test_more_rows_than_a_grid_has_passes(lib, x_dt, rows):
+    """Refused before the rows are multiplied by anything: 3 M of fp32 rows passes 64 bits."""
+    g = qnn.w4_geom(N=16, K=64, group=32)
+    for M in (65535 * rows + 1, 1 << 40, (1 << 62) + 1, (1 << 63) - 1):
+        assert lib.qgemv_w4(16, qnn.DTYPES[x_dt], 0, 128, ctypes.byref(g), M, None, 16, qnn.DTYPES["f32"], 0,
+                            None) == qnn.QNN_ERR_UNSUPPORTED, M
+
+
 def test_integer_calls_refuse_the_float_types(lib):
     shape = (ctypes.c_int64 * 2)(4, 8)
     p = qnn.qparams("sym")
