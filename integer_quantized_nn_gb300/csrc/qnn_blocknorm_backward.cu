@@ -560,6 +560,7 @@ extern "C" qnn_status q_block_norm_backward(const void *r_out, qnn_dtype r_dt, c
     if (!sums && !dr && !dy) return QNN_ERR_INVALID_ARG;
     if (sums && rows > 0 && (!workspace || workspace_bytes < qnn_block_norm_backward_workspace_bytes(rows, C, p)))
         return QNN_ERR_INVALID_ARG;
+    if (rows == 0 && !sums) return QNN_OK;
     BackArgs a{};
     a.r = r_out, a.y = y, a.gate = p->gate, a.dh = dh, a.dr_out = dr_out, a.dr = dr, a.dy = dy, a.dgate = dgate;
     a.gamma_post = p->gamma_post, a.beta_post = p->beta_post, a.gamma_pre = p->gamma_pre;
