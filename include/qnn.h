@@ -529,7 +529,7 @@ qnn_status qgemv_prepack_w4(const void *W, const void *scale, const int32_t *zer
  * Made for one to a few tens of rows; more are taken 32 columns of the tensor
  * operand at a time (a row of F32 takes three), the weights read again for each;
  * QNN_ERR_UNSUPPORTED beyond 65535 such passes.
- * Rows of x off 16-byte boundaries (ldx) are read with scalar loads. */
+ * Rows of x off 16-byte boundaries (ldx) are read in narrower pieces. */
 qnn_status qgemv_w4(const void *x, qnn_dtype x_dt, int64_t ldx, const void *W_packed, const qnn_w4_geom *g,
                     int64_t M, const float *bias, void *y, qnn_dtype y_dt, int64_t ldy, qnn_stream_t stream);
 

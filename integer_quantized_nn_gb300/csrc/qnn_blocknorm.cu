@@ -20,6 +20,12 @@
 // Many rows on 16-byte boundaries: the rows to come are on their way to shared memory
 // by bulk copies while one is computed (the copies in flight, not registers, are what
 // covers the memory's latency).  Few rows, and rows off those boundaries: direct loads.
+//
+// Measured: 8192 x 4096 bf16 to s8 codes 40.4 us, 5.8 TB/s (0.86 of a copy's bandwidth);
+// 12608 x 768, fp32 stream, LAYER norms with betas, a gate per 197 rows: 28.4 us, 4.1 TB/s
+// (issue 46 %, the stalls waits on global and shared loads); 777 x 1003 f16 5.8 us; one row
+// of 4096 2.3 us.  Odd widths load element by element: 8192 x 2003 bf16 70 us, 1.9 TB/s;
+// through a ring 92 us.
 #include "qnn_blocknorm.cuh"
 
 namespace qnn {

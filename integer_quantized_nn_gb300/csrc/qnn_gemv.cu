@@ -12,6 +12,12 @@
 // for one row of x alone.  This kernel is for up to 8 columns; qnn_gemv_columns.cu has
 // the one for more.
 //
+// Measured (one row, groups of 128): 8192 x 8192 bf16 9.0 us, 4.0 TB/s, 0.58 of a copy's
+// bandwidth; 4096 x 4096 f16 3.75 us; 1024 x 1024 (groups of 64) 2.1 us.  That is 2 to 4 us
+// beyond the bytes.  8192 x 8192 makes 256 blocks for 152 SMs: an SM's issue is 24 to 49 %
+// busy, by how many blocks it has.  Shifting codes on the multiplier pipe (mul.hi) was
+// slower (13.4 us to 10.9 at that stage).
+//
 // The image (prepack): per tile of 16 output channels and step of 128 input
 // channels, 1024 bytes, 32 a lane.  A 32-bit word of lane (g, j) (g = lane / 4, j =
 // lane % 4) holds channels n = g and g + 8 at four consecutive k: nibbles at bits
