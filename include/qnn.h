@@ -560,7 +560,9 @@ typedef struct {
  * r_out may be NULL (not wanted) or r itself.  h may be NULL when r_out is not; of
  * h_dt: y_dt, or S8: codes rint(h (127 / max|h|)) in -127..127, with h_scale (fp32
  * [rows]; NULL otherwise) = max|h| / 127, for a qgemm_s8 with that row_scale; a row
- * of zeros gets scale 0 and codes 0; h must then be finite.  Outputs overlap no input else.
+ * of zeros gets scale 0 and codes 0 (the codes of every other row reach 127 or -127,
+ * although below max|h| of 2^-119 the scale is subnormal and may round to zero); h must
+ * then be finite.  Outputs overlap no input else.
  * C <= 32768 (QNN_ERR_UNSUPPORTED beyond).  Rows off 16-byte boundaries or C not a
  * multiple of 8 are read element by element. */
 qnn_status q_block_norm(const void *r, qnn_dtype r_dt, const void *y, qnn_dtype y_dt, int64_t rows, int C,

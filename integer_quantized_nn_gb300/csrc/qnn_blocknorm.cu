@@ -146,8 +146,13 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const Span<V, I> &sp
 #pragma unroll
     for (int e = 0; e < E; ++e) m = fmaxf(m, fabsf(v[e]));
     m = red.max_abs<WARP>(m);
-    const float f = m == 0.0f ? 0.0f : __fdiv_rn(127.0f, m);
     if (sp.t == 0) a.h_scale[row] = __fdiv_rn(m, 127.0f);
+    if (m < 0x1p-100f) {  // 127 / m could pass the fp32 range: both sides of h / m times a power of two, exactly
+        m *= 0x1p100f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] *= 0x1p100f;
+    }
+    const float f = m == 0.0f ? 0.0f : __fdiv_rn(127.0f, m);
     int8_t *hr = static_cast<int8_t *>(a.h) + row * a.ld_h;
 #pragma unroll
     for (int i = 0; i < I; ++i)

@@ -1,0 +1,30 @@
+"""q_block_norm and q_block_norm_backward at the edges of their ranges of values and sizes."""
+import numpy as np
+import pytest
+import torch
+
+import _blocknorm as bn
+from test_gpu_blocknorm import check_backward, check_forward, run_backward, run_forward, stored
+
+pytestmark = pytest.mark.gpu
+
+
+# a warp and a block a row, by direct loads and through rings, whole vectors and single elements
+@pytest.mark.parametrize("rows,C", [(60, 96), (60, 101), (60, 2048), (60, 5001), (60, 8200), (20000, 136), (1500, 2040)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_codes_of_tiny_rows(dt, rows, C):
+    """max|h| from 2^-90 down to the smallest values, where 127 / max|h| passes the fp32 range."""
+    p = bn.make(31, rows, C, dt, dt, post="none", pre="none", with_y=False)
+    r = p["r"].double() * torch.exp2(-90.0 - torch.arange(rows, dtype=torch.float64) % 60)[:, None]
+    r[:, ::5] = 0
+    p["r"] = r.to(bn.TORCH[dt])
+    codes, scale = run_forward(p, s8=True)[1:]
+    v = p["r"].double()
+    top = v.abs().max(1).values
+    assert bool((scale.cpu().numpy() == top.float().numpy() / np.float32(127)).all())
+    codes, some = codes.double().cpu(), top > 0
+    assert 0 < int(some.sum()) and bool((codes[~some] == 0).all())
+    # two roundings of at most 127, then the nearest integer
+    off = (codes[some] - v[some] * (127 / top[some])[:, None]).abs()
+    assert float(off.max()) <= 0.5 + 127 * 2 * bn.U * 1.01
+    assert bool((codes[some].abs().max(1).values == 127).all())
