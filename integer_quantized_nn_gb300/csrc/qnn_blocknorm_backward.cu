@@ -571,7 +571,10 @@ extern "C" qnn_status q_block_norm_backward(const void *r_out, qnn_dtype r_dt, c
     a.r = r_out, a.y = y, a.gate = p->gate, a.dh = dh, a.dr_out = dr_out, a.dr = dr, a.dy = dy, a.dgate = dgate;
     a.gamma_post = p->gamma_post, a.beta_post = p->beta_post, a.gamma_pre = p->gamma_pre;
     a.ws = static_cast<float *>(workspace);
-    a.rows = rows, a.gate_rows = p->gate_rows, a.C = C, a.post = p->post, a.pre = p->pre;
+    // a group reaches no further than the rows, and sums of the two stay in 64 bits (a single
+    // row's group keeps the form of shared ones)
+    const int64_t gate_rows = std::min(p->gate_rows, std::max<int64_t>(rows, 2));
+    a.rows = rows, a.gate_rows = gate_rows, a.C = C, a.post = p->post, a.pre = p->pre;
     a.ld_r = p->ld_r ? p->ld_r : C, a.ld_y = p->ld_y ? p->ld_y : C, a.ld_h = p->ld_h ? p->ld_h : C;
     a.a = p->res_scale, a.b = p->block_scale, a.eps_post = p->eps_post, a.eps_pre = p->eps_pre, a.inv_c = 1.0f / C;
     a.wants = (dgamma_pre ? 1u << kGammaPre : 0) | (dbeta_pre ? 1u << kBetaPre : 0) |
@@ -628,13 +631,13 @@ extern "C" qnn_status q_block_norm_backward(const void *r_out, qnn_dtype r_dt, c
     float *const out[4] = {dgamma_pre, dbeta_pre, dgamma_post, dbeta_post};
     for (int i = 0; i < 4; ++i)
         if (out[i]) f.slot[f.sums] = i, f.out[f.sums++] = out[i];
-    f.dgate = dgate, f.gate_dt = y_dt, f.rows = rows, f.gate_rows = p->gate_rows, f.chunk = a.chunk, f.C = C;
+    f.dgate = dgate, f.gate_dt = y_dt, f.rows = rows, f.gate_rows = gate_rows, f.chunk = a.chunk, f.C = C;
     f.blocks = plan.blocks;
     int64_t jobs = 0;
     if (dgate && f.blocks > 1) {
-        const int64_t groups = p->gate_rows ? (rows + p->gate_rows - 1) / p->gate_rows : 1;
+        const int64_t groups = gate_rows ? (rows + gate_rows - 1) / gate_rows : 1;
         f.by_group = groups < f.blocks;
-        jobs = p->gate_rows == 1 ? 0 : f.by_group ? groups : f.blocks - 1;
+        jobs = gate_rows == 1 ? 0 : f.by_group ? groups : f.blocks - 1;
     }
     const dim3 grid((C + 31) / 32, (unsigned)(f.sums + jobs));
     if (grid.y == 0) return QNN_OK;

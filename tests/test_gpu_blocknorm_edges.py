@@ -28,3 +28,12 @@ def test_codes_of_tiny_rows(dt, rows, C):
     off = (codes[some] - v[some] * (127 / top[some])[:, None]).abs()
     assert float(off.max()) <= 0.5 + 127 * 2 * bn.U * 1.01
     assert bool((codes[some].abs().max(1).values == 127).all())
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 2000])
+@pytest.mark.parametrize("gate_rows", [1 << 31, 1 << 62, (1 << 63) - 1])
+def test_a_gate_group_longer_than_any_tensor(gate_rows, rows):
+    """One group, of all rows, whatever its length is beyond them."""
+    p = bn.make(32, rows, 64, "f32", "bf16", post="layer", gate="rows", gate_rows=gate_rows)
+    check_forward(p, *run_forward(p)[:2])
+    check_backward(p, stored(p), run_backward(p, stored(p)))
