@@ -55,15 +55,14 @@ __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, ui
     return prmt(prmt(a, b, 0x0040), prmt(c, d, 0x0040), 0x5410);
 }
 
-// v = gamma (v - mean) rstd + beta, (v - mean) rstd as one fused operation.
+// v = gamma (v - mean) rstd + beta.
 template <int V, int I>
 __device__ __forceinline__ void affine(const Span<V, I> &sp, float *v, const Stats &s, const float *gamma,
                                        const float *beta)
 {
-    const float c = -s.mean * s.rstd;
     float p[V * I];
 #pragma unroll
-    for (int e = 0; e < V * I; ++e) v[e] = __fmaf_rn(v[e], s.rstd, c);
+    for (int e = 0; e < V * I; ++e) v[e] = normalised(v[e], s);
     if (gamma) {
         sp.load(gamma, p);
 #pragma unroll
@@ -98,9 +97,8 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const Span<V, I> &sp
         sp.clear(v);
         const Stats s = row_stats<WARP>(sp, v, a.post, a.eps_post, a.inv_c, red);
         if constexpr (EARLY) {
-            const float c = -s.mean * s.rstd;
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = __fmaf_rn(__fmaf_rn(v[e], s.rstd, c), gm[e], bt[e]);
+            for (int e = 0; e < E; ++e) v[e] = __fmaf_rn(normalised(v[e], s), gm[e], bt[e]);
         } else {
             affine(sp, v, s, a.gamma_post, a.beta_post);
         }
@@ -130,9 +128,8 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const Span<V, I> &sp
         const Stats s = row_stats<WARP>(sp, v, a.pre, a.eps_pre, a.inv_c, red);
         if (!EARLY && !WARP) release();
         if constexpr (EARLY) {
-            const float c = -s.mean * s.rstd;
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = __fmaf_rn(__fmaf_rn(v[e], s.rstd, c), hm[e], hb[e]);
+            for (int e = 0; e < E; ++e) v[e] = __fmaf_rn(normalised(v[e], s), hm[e], hb[e]);
         } else {
             affine(sp, v, s, a.gamma_pre, a.beta_pre);
         }

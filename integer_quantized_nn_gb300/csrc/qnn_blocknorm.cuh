@@ -223,6 +223,10 @@ struct Stats {
     float mean, rstd;
 };
 
+// The mean first: as v rstd - mean rstd, one fused operation, the rounding of mean rstd would
+// stay where the two terms cancel (up to 0.016 on rows of equal values of 1000, eps 1e-5).
+__device__ __forceinline__ float normalised(float v, const Stats &s) { return (v - s.mean) * s.rstd; }
+
 // 1 / sqrt(ss / C + eps) (2 ulp of the fp32 value, beside sums of many roundings)
 __device__ __forceinline__ float rstd_of(float ss, float inv_c, float eps) { return rsqrtf(__fmaf_rn(ss, inv_c, eps)); }
 

@@ -267,14 +267,14 @@ __global__ void __launch_bounds__(V * I <= 16 ? 512 : 1024, 1)
 #pragma unroll
             for (int k = 0; k < N; ++k) g[k] = both(0.0f);
         if (pre) {
-            const float2 rs = both(sx.rstd), c = both(-sx.mean * sx.rstd);
+            const float2 rs = both(sx.rstd), mean = both(-sx.mean);
             float2 sg = both(0.0f), sgx = both(0.0f);
 #pragma unroll
             for (int i = 0; i < S::G; ++i) {
                 float2 *xv = x + i * GP, *gv = g + i * GP, gm[GP], tg = sg, tx = sgx;
                 if (a.gamma_pre) sp.load_group(a.gamma_pre, i, gm);
 #pragma unroll
-                for (int e = 0; e < GP; ++e) xv[e] = fma2(xv[e], rs, c);
+                for (int e = 0; e < GP; ++e) xv[e] = mul2(FULL ? add2(xv[e], mean) : xv[e], rs);
                 add(pre_sum[0] + i * GP, gv, xv);
                 if constexpr (FULL) add1(pre_sum[1] + i * GP, gv);
 #pragma unroll
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(V * I <= 16 ? 512 : 1024, 1)
         }
         if (a.y) {
             if (!KEEP) sp.load(y_row, yv);
-            const float2 rs = both(sy.rstd), c = both(-sy.mean * sy.rstd), f = both(a.b);
+            const float2 rs = both(sy.rstd), mean = both(-sy.mean), f = both(a.b);
             float2 sg = both(0.0f), sgx = both(0.0f);
             TY *gate_out = a.dgate && a.gate_rows == 1 ? static_cast<TY *>(a.dgate) + row * a.C : nullptr;
 #pragma unroll
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(V * I <= 16 ? 512 : 1024, 1)
                 if (a.gate) sp.load_group(g_row, i, w);
 #pragma unroll
                 for (int e = 0; e < GP; ++e)
-                    if (post) xv[e] = fma2(xv[e], rs, c);
+                    if (post) xv[e] = mul2(FULL ? add2(xv[e], mean) : xv[e], rs);
                 if (shared) {
                     add(post_sum[0] + i * GP, gv, xv);
                     if constexpr (FULL) add1(post_sum[1] + i * GP, gv);

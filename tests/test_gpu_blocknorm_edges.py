@@ -37,3 +37,35 @@ def test_a_gate_group_longer_than_any_tensor(gate_rows, rows):
     p = bn.make(32, rows, 64, "f32", "bf16", post="layer", gate="rows", gate_rows=gate_rows)
     check_forward(p, *run_forward(p)[:2])
     check_backward(p, stored(p), run_backward(p, stored(p)))
+
+
+def equal_values(rows, C, dt, **k):
+    """Rows of 1000 (1000 C is an integer below 2^24: its fp32 sum is exact in any order)."""
+    assert 1000 * C < 1 << 24
+    p = bn.make(33, rows, C, dt, dt, **k)
+    for name in ("r", "y"):
+        if p[name] is not None:
+            p[name][:] = 1000
+    return p
+
+
+def check_equal_values(rows, C, dt):
+    """A LAYER row of equal values is exactly zero once its mean is taken off."""
+    p = equal_values(rows, C, dt, post="layer", pre="none", gate="all", beta=False)
+    assert bool((run_forward(p)[0] == 1000).all())
+    got = run_backward(p, p["r"])
+    assert bool((got["dgamma_post"] == 0).all()) and bool((got["dgate"] == 0).all())
+    p = equal_values(rows, C, dt, post="none", pre="layer", with_y=False)
+    h = run_forward(p)[1]
+    assert bool((h.cpu() == p["beta_pre"].to(h.dtype)).all())
+    assert bool((run_backward(p, p["r"])["dgamma_pre"] == 0).all())
+
+
+SPANS = [(5, 64), (5, 101), (5, 768), (5, 2048), (5, 5001), (5, 8192), (5, 9001), (5, 16384), (20000, 136),
+         (5000, 768), (9000, 333), (400, 8192)]
+
+
+@pytest.mark.parametrize("rows,C", SPANS)
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_layer_rows_of_equal_values(dt, rows, C):
+    check_equal_values(rows, C, dt)
