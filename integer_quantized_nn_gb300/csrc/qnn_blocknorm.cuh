@@ -223,6 +223,15 @@ struct Stats {
     float mean, rstd;
 };
 
+// sum / C: the product with the rounded 1 / C, put right by its remainder (exact where the
+// quotient is a float), so that rows of equal values whose sum is exact are centred to zero at
+// every width.  A division's branches cost 12608 x 768 6 us of 28.6.
+__device__ __forceinline__ float mean_of(float sum, int C, float inv_c)
+{
+    const float q = sum * inv_c;
+    return __fmaf_rn(__fmaf_rn(-q, (float)C, sum), inv_c, q);
+}
+
 // The mean first: as v rstd - mean rstd, one fused operation, the rounding of mean rstd would
 // stay where the two terms cancel (up to 0.016 on rows of equal values of 1000, eps 1e-5).
 __device__ __forceinline__ float normalised(float v, const Stats &s) { return (v - s.mean) * s.rstd; }
@@ -240,7 +249,7 @@ __device__ __forceinline__ Stats row_stats(const Span<V, I> &sp, const float *v,
     if (kind == QNN_NORM_LAYER) {
 #pragma unroll
         for (int e = 0; e < V * I; ++e) acc += v[e];
-        s.mean = red.sum<WARP>(acc) * inv_c;
+        s.mean = mean_of(red.sum<WARP>(acc), sp.C, inv_c);
         acc = 0.0f;
 #pragma unroll
         for (int i = 0; i < I; ++i)

@@ -113,8 +113,8 @@ __device__ __forceinline__ void stats_of_two(const PairSpan<V, I> &sp, const flo
             sum_y = sp.keep(g, ty, sum_y);
         }
         const float2 m = red.sum<false>(make_float2(across(sum_x), across(sum_y)));
-        sx.mean = a.pre == QNN_NORM_LAYER ? m.x * a.inv_c : 0.0f;
-        sy.mean = a.post == QNN_NORM_LAYER ? m.y * a.inv_c : 0.0f;
+        sx.mean = a.pre == QNN_NORM_LAYER ? mean_of(m.x, a.C, a.inv_c) : 0.0f;
+        sy.mean = a.post == QNN_NORM_LAYER ? mean_of(m.y, a.C, a.inv_c) : 0.0f;
         sum_x = sum_y = both(0.0f);
     }
     const float2 mx = both(-sx.mean), my = both(-sy.mean);

@@ -69,3 +69,10 @@ SPANS = [(5, 64), (5, 101), (5, 768), (5, 2048), (5, 5001), (5, 8192), (5, 9001)
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_layer_rows_of_equal_values(dt, rows, C):
     check_equal_values(rows, C, dt)
+
+
+# 1000 C (1 / C) in fp32 is not 1000 at these widths
+@pytest.mark.parametrize("rows,C", [(5, 41), (5, 1000), (5, 2040), (5, 5017), (5, 8560), (4000, 1000), (1500, 2040)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_the_mean_of_equal_values_is_their_value(dt, rows, C):
+    check_equal_values(rows, C, dt)
