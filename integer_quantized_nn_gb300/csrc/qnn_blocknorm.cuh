@@ -293,7 +293,8 @@ __device__ __forceinline__ Window window(const void *base, int64_t row, int64_t 
 // Leading rows of `rows` whose windows stay inside a tensor of pitch ld.
 inline int64_t ring_rows(int64_t rows, int64_t ld, int elem)
 {
-    return std::max<int64_t>(0, rows - (15 + ld * elem - 1) / (ld * elem));
+    const int64_t pitch = std::min<int64_t>(ld, 16) * elem;  // from 15 bytes on, the last row alone
+    return std::max<int64_t>(0, rows - (15 + pitch - 1) / pitch);
 }
 
 // After a wait that gave up: waits, each with its limit, for the ring's other copies in
