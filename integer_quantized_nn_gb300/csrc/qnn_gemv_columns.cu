@@ -332,6 +332,9 @@ __global__ void __launch_bounds__(kThreads<NC>, 1) gemv_w4_columns_kernel(const 
             if (t + kStages < n) ask(t + kStages);
         }
     } else {
+        // the grid before reads and writes nothing of this role's: so that its time is not taken
+        // by polls, nor counted by their limit
+        grid_dependency_wait();
         if (lane == 0 && warp < kMmaWarp0 + kMmaWarps) {
             // a serial bottleneck: all that an MMA needs is a constant away from a few
             // registers (descriptor addresses count 16 bytes)

@@ -1,0 +1,32 @@
+"""What the kernels of qgemv_w4 must do on ways that no run takes on purpose, read from their
+source (no GPU needed): they start before the grid ahead of them has ended, and their waits are
+bounded."""
+import os
+import re
+
+import pytest
+
+from integer_quantized_nn_gb300 import build as _build
+
+pytestmark = pytest.mark.cpu
+
+
+def source(name):
+    with open(os.path.join(_build.CSRC, name)) as f:
+        return f.read()
+
+
+def roles():
+    """The branches of the columns kernel: codes, sums, x, MMA."""
+    s = source("qnn_gemv_columns.cu")
+    body = s[s.index("    if (warp < kCodeWarps) {"):s.index("    if (warp == kMmaWarp0) tmem_dealloc")]
+    parts = re.split(r"\n    \} else (?:if \(warp < \w+\) )?\{\n", body)
+    assert len(parts) == 4
+    return parts
+
+
+def test_every_role_waits_for_the_grid_before():
+    """Ahead of its first bounded wait, whose limit would else count the time of that grid."""
+    for part in roles():
+        first = re.search(r"\b(?:mbar_)?wait\((?:done|full)", part)
+        assert "grid_dependency_wait();" in part[:first.start()], part[:200]
