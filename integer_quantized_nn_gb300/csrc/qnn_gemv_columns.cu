@@ -331,6 +331,7 @@ __global__ void __launch_bounds__(kThreads<NC>, 1) gemv_w4_columns_kernel(const 
             if (lane == 0) mbar_arrive(full + 8 * first);
             if (t + kStages < n) ask(t + kStages);
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");  // none in flight, after a wait that gave up either
     } else {
         // the grid before reads and writes nothing of this role's: so that its time is not taken
         // by polls, nor counted by their limit

@@ -30,3 +30,12 @@ def test_every_role_waits_for_the_grid_before():
     for part in roles():
         first = re.search(r"\b(?:mbar_)?wait\((?:done|full)", part)
         assert "grid_dependency_wait();" in part[:first.start()], part[:200]
+
+
+def test_x_copies_have_landed_when_their_role_ends():
+    """Also after a wait that gave up: nothing writes to shared memory that was given back."""
+    part = roles()[2]
+    loop = part.index("for (int t = first; t < n; t += kStages)")
+    end = part.index("\n        }\n", loop)  # of the loop
+    assert "break;" in part[loop:end]
+    assert "cp.async.wait_group 0;" in part[end:]
