@@ -160,8 +160,8 @@ __device__ __forceinline__ void stage_x(const GemvArgs &a, int64_t row, int col,
 #pragma unroll 4
     for (int i = i0 + lane; i < whole; i += 32) {
         const uint4 *v = reinterpret_cast<const uint4 *>(p) + (int64_t)i * W;
-        const uint4 u = __ldg(v);
-        put_piece<XT>(u, W == 2 ? __ldg(v + W - 1) : u, xs + ((i >> 2) * cols + col) * 4 + (i & 3));
+        const uint4 u = load_input(v);
+        put_piece<XT>(u, W == 2 ? load_input(v + W - 1) : u, xs + ((i >> 2) * cols + col) * 4 + (i & 3));
     }
     // rows off 16-byte boundaries and the ragged end: value by value
 #pragma unroll 8
@@ -169,11 +169,11 @@ __device__ __forceinline__ void stage_x(const GemvArgs &a, int64_t row, int col,
         uint16_t *out = reinterpret_cast<uint16_t *>(xs + ((e >> 5) * cols + col) * 4 + (e >> 3 & 3)) + (e & 7);
         if constexpr (W == 2) {
             uint32_t v[3];
-            bf16_parts(e < end ? __ldg(reinterpret_cast<const float *>(p) + e) : 0.0f, v);
+            bf16_parts(e < end ? load_input(reinterpret_cast<const float *>(p) + e) : 0.0f, v);
 #pragma unroll
             for (int q = 0; q < 3; ++q) out[32 * q] = (uint16_t)v[q];
         } else {
-            *out = e < end ? __ldg(reinterpret_cast<const uint16_t *>(p) + e) : (uint16_t)0;
+            *out = e < end ? load_input(reinterpret_cast<const uint16_t *>(p) + e) : (uint16_t)0;
         }
     }
 }
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_w4_kernel(const __grid_co
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 h[r].s[q] = load_scales(sp[r], a.scale_dt);
-                if constexpr (ZERO) h[r].z[q] = __ldg(reinterpret_cast<const uint16_t *>(zp[r]));
+                if constexpr (ZERO) h[r].z[q] = load_input(reinterpret_cast<const uint16_t *>(zp[r]));
             }
             if (--left == 0) {
                 left = a.per_scale;
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_w4_kernel(const __grid_co
         // the bias of this thread's outputs: kWarps * 32 is a multiple of ROWS
         const int row = threadIdx.x % ROWS;
         const int64_t n = (int64_t)set * ROWS + row;
-        const float bias = a.bias && n < a.N ? __ldg(a.bias + n) : 0.0f;
+        const float bias = a.bias && n < a.N ? load_input(a.bias + n) : 0.0f;
         float *part = parts + turn * (kPartBytes<R> / 4);
         turn ^= 1;
 #pragma unroll

@@ -106,11 +106,46 @@ __device__ __forceinline__ void bf16_parts(float v, uint32_t (&p)[3])
     p[2] = __float_as_uint(r2) >> 16;
 }
 
+// Global loads that stay behind grid_dependency_wait.  The grid before may write what they read
+// while this one has already begun, so that it is no constant of this grid (__ldg).
+__device__ __forceinline__ uint32_t load_input(const uint32_t *p)
+{
+    uint32_t v;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint16_t load_input(const uint16_t *p)
+{
+    uint16_t v;
+    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ float load_input(const float *p)
+{
+    return __uint_as_float(load_input(reinterpret_cast<const uint32_t *>(p)));
+}
+
+__device__ __forceinline__ uint2 load_input(const uint2 *p)
+{
+    uint2 v;
+    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint4 load_input(const uint4 *p)
+{
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
 // One scale as it is kept, and its value: apart, so that nothing waits for the load.
 __device__ __forceinline__ uint32_t load_scale(const uint8_t *p, int dt, int64_t i)
 {
-    return dt == QNN_F32 ? __ldg(reinterpret_cast<const uint32_t *>(p) + i)
-                         : (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(p) + i);
+    return dt == QNN_F32 ? load_input(reinterpret_cast<const uint32_t *>(p) + i)
+                         : (uint32_t)load_input(reinterpret_cast<const uint16_t *>(p) + i);
 }
 
 __device__ __forceinline__ float scale_f32(uint32_t s, int dt)
@@ -129,8 +164,8 @@ __device__ __forceinline__ void store_y(const GemvArgs &a, int64_t at, float v)
 // A lane's two scales as they are kept: fp32 in both words, 16-bit types in the first.
 __device__ __forceinline__ uint2 load_scales(const uint8_t *p, int dt)
 {
-    return dt == QNN_F32 ? __ldg(reinterpret_cast<const uint2 *>(p))
-                         : make_uint2(__ldg(reinterpret_cast<const uint32_t *>(p)), 0u);
+    return dt == QNN_F32 ? load_input(reinterpret_cast<const uint2 *>(p))
+                         : make_uint2(load_input(reinterpret_cast<const uint32_t *>(p)), 0u);
 }
 
 __device__ __forceinline__ float2 scales_f32(uint2 s, int dt)

@@ -102,7 +102,7 @@ __device__ __forceinline__ void ask_unit(const GemvArgs &a, int64_t row, int k, 
     else
         for (int i = 0; i < 16; ++i) {  // rows on odd 16-bit addresses
             const uint16_t *q = reinterpret_cast<const uint16_t *>(p) + k + 2 * i;
-            const uint32_t lo = k + 2 * i < a.K ? __ldg(q) : 0, hi = k + 2 * i + 1 < a.K ? __ldg(q + 1) : 0;
+            const uint32_t lo = k + 2 * i < a.K ? load_input(q) : 0, hi = k + 2 * i + 1 < a.K ? load_input(q + 1) : 0;
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 512 * (i / 4) + 4 * (i % 4)), "r"(lo | hi << 16) : "memory");
         }
 }
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads<NC>, 1) gemv_w4_columns_kernel(const 
             for (int q = 0; q < NS; ++q) {
                 if constexpr (ZERO) {
                     const int g = (uint32_t)((b0 + t) * NS + q) / (uint32_t)a.per_scale;
-                    z[u][q] = __ldg(reinterpret_cast<const uint16_t *>(zp + (int64_t)min(g, a.groups - 1) * 16));
+                    z[u][q] = load_input(reinterpret_cast<const uint16_t *>(zp + (int64_t)min(g, a.groups - 1) * 16));
                 } else {
                     z[u][q] = 0x0808u;
                 }
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kThreads<NC>, 1) gemv_w4_columns_kernel(const 
     if (warp < kCodeWarps) {
         const int ch = threadIdx.x & 127;
         const int64_t nn = (int64_t)blockIdx.x * 128 + ch;
-        const float bias = a.bias && nn < a.N ? __ldg(a.bias + nn) : 0.0f;
+        const float bias = a.bias && nn < a.N ? load_input(a.bias + nn) : 0.0f;
         for (int tok = (threadIdx.x >> 7) + 4 * rank; tok < toks && nn < a.N; tok += 4 * splits) {
             float v = 0.0f;
             for (int q = 0; q < splits; ++q) {

@@ -39,3 +39,11 @@ def test_x_copies_have_landed_when_their_role_ends():
     end = part.index("\n        }\n", loop)  # of the loop
     assert "break;" in part[loop:end]
     assert "cp.async.wait_group 0;" in part[end:]
+
+
+@pytest.mark.parametrize("name", ["qnn_gemv.cuh", "qnn_gemv.cu", "qnn_gemv_columns.cu"])
+def test_nothing_is_loaded_as_a_constant(name):
+    """The grid before may still be writing x, the bias or the image when this one has begun, and
+    __ldg is for what no one writes meanwhile (and may be moved ahead of the wait)."""
+    code = re.sub(r"//.*", "", source(name))
+    assert not re.findall(r"__ldg\(.*|\.nc\b.*", code)
