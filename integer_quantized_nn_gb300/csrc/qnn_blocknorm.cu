@@ -1,21 +1,16 @@
-// qnn_blocknorm.cu -- q_block_norm and q_block_norm_backward: the norm after a block,
-// its gate and residual scale, the residual add and the norm before the next block,
-// row by row in one pass.
+// qnn_blocknorm.cu -- q_block_norm: the norm after a block, its gate and residual scale, the
+// residual add and the norm before the next block, row by row in one pass.
 //
 //   p  = norm_post(y)      r' = a r + b gate p      h = norm_pre(r')
 //
 // norm: x^ = x / sqrt(mean(x^2) + eps)  (RMS)  or  (x - mean) / sqrt(var + eps)
-// (LAYER), then gamma x^ + beta.  Backward, with G the gradient at r':
-//   G   = dr' + D_pre(gamma_pre dh),   dr = a G,   t = b gate G,   dy = D_post(gamma_post t)
-//   D(g) = (g - mean(g) [LAYER only] - x^ mean(g x^)) / sqrt(...)
-//   dgate = b sum G p over the rows that share it;   dgamma = sum upstream x^,
-//   dbeta = sum upstream   (upstream: dh before, t after)
+// (LAYER), then gamma x^ + beta.
 //
-// Both are bound by the bytes of the rows.  A row is read once and lives in registers
-// to its writes: one warp holds rows of up to 1024 columns, a block longer ones.
-// Statistics are fp32, the variance from the centred values (a second reduction over
-// registers, not over memory).  h is formed from r' before r' is rounded to its own
-// type; the backward pass takes its statistics from r' as stored.
+// Bound by the bytes of the rows.  A row is read once and lives in registers to its
+// writes: one warp holds rows of up to 1024 columns (through a ring; 256 by direct loads,
+// 512 where many rows are off 16-byte boundaries), a block longer ones.  Statistics are
+// fp32, the variance from the centred values (a second reduction over registers, not over
+// memory).  h is formed from r' before r' is rounded to its own type.
 //
 // Many rows on 16-byte boundaries: the rows to come are on their way to shared memory
 // by bulk copies while one is computed (the copies in flight, not registers, are what
@@ -253,10 +248,12 @@ template <typename TR, typename TY, int V, int I, int MAXT>
 qnn_status launch_norm(const NormArgs &a, cudaStream_t s)
 {
     constexpr int per = V * I;
-    if (a.C <= 32 * per && MAXT <= 512)
-        return launch_dependent(block_norm_kernel<TR, TY, V, I, true, per <= 8, 512>, a,
-                                dim3((unsigned)std::min<int64_t>((a.rows + kWarpRows - 1) / kWarpRows, 16 * sm_count())),
-                                32 * kWarpRows, 0, s);
+    if constexpr (MAXT <= 512)
+        if (a.C <= 32 * per)
+            return launch_dependent(
+                block_norm_kernel<TR, TY, V, I, true, per <= 8, 512>, a,
+                dim3((unsigned)std::min<int64_t>((a.rows + kWarpRows - 1) / kWarpRows, 16 * sm_count())),
+                32 * kWarpRows, 0, s);
     const int threads = (a.C + per * 32 - 1) / (per * 32) * 32;
     return launch_dependent(block_norm_kernel<TR, TY, V, I, false, per <= 8, MAXT>, a,
                             dim3((unsigned)std::min<int64_t>(a.rows, (int64_t)sm_count() * std::max(1024 / threads, 1))), threads, 0, s);
@@ -308,8 +305,8 @@ extern "C" qnn_status q_block_norm(const void *r, qnn_dtype r_dt, const void *y,
     a.status = status_word();
     if (!a.status) return QNN_ERR_CUDA;
     // rings from the size on at which every SM has several rows to go through
-    const int row_bytes = C * (float_bytes(r_dt) + (y ? ey : 0) + (p->gate && p->gate_rows == 1 ? ey : 0));
-    const bool many = rows * C >= (int64_t)sm_count() * 16384, ring = many && vec && C <= 8192 && row_bytes <= kRingSmem;
+    static_assert(3 * kMaxRingC * 4 <= kRingSmem, "a stage of three fp32 rows has to fit");
+    const bool many = rows * C >= (int64_t)sm_count() * 16384, ring = many && vec && C <= kMaxRingC;
     cudaStream_t s = (cudaStream_t)stream;
     qnn_status done = QNN_OK;
     with_types(r_dt, y_dt, [&](auto tr, auto ty) {

@@ -20,6 +20,7 @@ constexpr int kMaxStages = 4;
 constexpr int kRingSmem = 128 << 10;
 constexpr int kRingCarveout = 60;  // percent of the SM's memory
 constexpr int kMaxRing = 200 << 10;  // a single block's ring at most
+constexpr int kMaxRingC = 8192;      // columns of the rows that go through rings, at most
 
 // V consecutive elements as fp32 (V = 8: 16-byte accesses; V = 1: any address)
 template <int V, typename T>
@@ -188,12 +189,6 @@ struct Span {
         for (int i = 0; i < I; ++i) load_v<V>(row + (in(i) ? col(i) : 0), v + i * V);
     }
     // 0 beyond C
-    template <typename T>
-    __device__ __forceinline__ void load0(const T *row, float *v) const
-    {
-        load(row, v);
-        clear(v);
-    }
     __device__ __forceinline__ void clear(float *v) const
     {
 #pragma unroll

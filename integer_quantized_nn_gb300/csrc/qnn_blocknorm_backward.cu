@@ -587,7 +587,8 @@ extern "C" qnn_status q_block_norm_backward(const void *r_out, qnn_dtype r_dt, c
     const int rr = vec ? window_room<8>(C, er) : window_room<1>(C, er), yr = vec ? window_room<8>(C, ey) : window_room<1>(C, ey);
     const bool own_gate = p->gate && p->gate_rows == 1, needs_r = dh && p->pre != QNN_NORM_NONE;
     const int stage = (needs_r ? rr : 0) + (y ? yr : 0) + (dh ? yr : 0) + (dr_out ? rr : 0) + (own_gate ? yr : 0);
-    const bool ring = C <= 8192 && stage <= kMaxRing;
+    const bool ring = C <= kMaxRingC;
+    static_assert(5 * ((kMaxRingC * 4 + 30) & ~15) <= kMaxRing, "a stage of five fp32 windows has to fit");
     a.ring_rows = rows;
     if (!vec) {
         a.ring_rows = ring_rows(rows, a.ld_r, er);
@@ -615,7 +616,6 @@ extern "C" qnn_status q_block_norm_backward(const void *r_out, qnn_dtype r_dt, c
             else if (ring)
                 done = full ? launch_back<TR, TY, 1, 16, true, true>(a, plan, threads, stage, s)
                             : launch_back<TR, TY, 1, 16, true, false>(a, plan, threads, stage, s);
-            else if (C <= 8192) done = launch_back<TR, TY, 1, 16, false, true>(a, plan, threads, 0, s);
             else if (vec) done = launch_back<TR, TY, 8, 4, false, true>(a, plan, threads, 0, s);
             else done = launch_back<TR, TY, 1, 32, false, true>(a, plan, threads, 0, s);
         });
