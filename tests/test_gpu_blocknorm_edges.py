@@ -3,14 +3,16 @@ import numpy as np
 import pytest
 import torch
 
+from integer_quantized_nn_gb300 import qnn
 import _blocknorm as bn
-from test_gpu_blocknorm import check_backward, check_forward, run_backward, run_forward, stored
+from test_gpu_blocknorm import block_norm, check_backward, check_codes, check_forward, run_backward, run_forward, stored
 
 pytestmark = pytest.mark.gpu
 
 
 # a warp and a block a row, by direct loads and through rings, whole vectors and single elements
-@pytest.mark.parametrize("rows,C", [(60, 96), (60, 101), (60, 2048), (60, 5001), (60, 8200), (20000, 136), (1500, 2040)])
+@pytest.mark.parametrize("rows,C", [(60, 96), (60, 101), (60, 2048), (60, 5001), (60, 8200), (20000, 136),
+                                    (1500, 2040)])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_codes_of_tiny_rows(dt, rows, C):
     """max|h| from 2^-90 down to the smallest values, where 127 / max|h| passes the fp32 range."""
@@ -76,3 +78,37 @@ def test_layer_rows_of_equal_values(dt, rows, C):
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_the_mean_of_equal_values_is_their_value(dt, rows, C):
     check_equal_values(rows, C, dt)
+
+
+# more rows than blocks, at widths that a block holds without a ring
+@pytest.mark.parametrize("rows,C,r_dt,y_dt,post,pre,gate", [
+    (400, 8200, "bf16", "bf16", "rms", "rms", dict(gate="all")),
+    (330, 9001, "f32", "f16", "layer", "rms", dict(gate="rows", gate_rows=7)),
+    (320, 16384, "f16", "f16", "layer", "layer", dict(gate="rows", gate_rows=1)),
+    (310, 16385, "f32", "f32", "none", "layer", dict(gate="rows", gate_rows=200)),
+    (310, 32768, "f32", "bf16", "layer", "layer", {}),
+])
+def test_many_rows_beyond_the_rings(rows, C, r_dt, y_dt, post, pre, gate):
+    p = bn.make(35, rows, C, r_dt, y_dt, post, pre, beta=pre == "layer", a=0.9, b=0.6, **gate)
+    check_forward(p, *run_forward(p)[:2])
+    codes, scale = run_forward(p, s8=True, want_r=False)[1:]
+    check_codes(p, codes, scale)
+    check_backward(p, stored(p), run_backward(p, stored(p)))
+
+
+@pytest.mark.parametrize("C", [64, 101])
+def test_the_pitch_of_one_row_is_not_used(C):
+    p = bn.make(34, 1, C, post="layer", gate="all")
+    r, y, dh, dr_out = (p[k].cuda() for k in ("r", "y", "dh", "dr_out"))
+
+    def run(ld):
+        q = block_norm(p)
+        q.ld_r = q.ld_y = q.ld_h = ld
+        out = [torch.zeros_like(r) for _ in range(4)] + [torch.zeros(C, device="cuda") for _ in range(4)]
+        qnn.q_block_norm(r, "f32", y, "f32", 1, C, q, r_out=out[0], h=out[1])
+        ws = torch.empty(qnn.qnn_block_norm_backward_workspace_bytes(1, C, q), dtype=torch.uint8, device="cuda")
+        qnn.q_block_norm_backward(out[0], "f32", y, "f32", 1, C, q, dh, dr_out, out[2], out[3], ws,
+                                  dgamma_pre=out[4], dbeta_pre=out[5], dgamma_post=out[6], dbeta_post=out[7])
+        assert qnn.qnn_check_device_error() == qnn.QNN_OK
+        return out
+    assert all(torch.equal(a, b) for a, b in zip(run(0), run(1 << 62)))
