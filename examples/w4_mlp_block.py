@@ -8,7 +8,8 @@ held as 4-bit codes with a scale per group of input channels.  Three steps:
 1. decode: qgemv_w4 for the two linears and q_block_norm for everything between them, a
    stack of such blocks captured in one CUDA graph, against fp32 torch on the same codes;
 2. prompt: q_block_norm leaves h as int8 codes with a scale per row, which qgemm_s8 takes
-   through its row_scale epilogue;
+   through its row_scale epilogue (a linear with int8 weights of its own: the 4-bit product
+   is made for few rows);
 3. tune: q_block_norm_backward gives the gradients of the gate and the norms' weights, and
    plain gradient steps on them lower a loss.
 """

@@ -520,8 +520,9 @@ qnn_status qgemv_prepack_w4(const void *W, const void *scale, const int32_t *zer
  * for M rows of x, rounded once to y_dt.  Per group the sum of x (q - z) is
  * formed in fp32 on the tensor cores (q - z is an exact integer there, and fp32 x
  * enters as three bf16 terms that add up to it exactly, bits below 2^-133 aside),
- * then multiplied by the scale in fp32 and added in fp32; an unscaled group sum beyond the fp32 range
- * becomes infinite.  The order of the sums depends on the sizes alone: equal
+ * in parts of at most 128 channels; each part is multiplied by the scale and added in
+ * fp32.  An unscaled part beyond the fp32 range becomes infinite; an infinite scale
+ * gives infinities or NaN.  The order of the sums depends on the sizes alone: equal
  * calls give equal bits.
  * x: device [M, K] of x_dt (F32, F16, BF16), ldx elements between rows (>= K; 0: K).
  * y: device [M, N] of y_dt (x_dt or F32), ldy elements between rows (>= N; 0: N).

@@ -16,11 +16,12 @@
 // by bulk copies while one is computed (the copies in flight, not registers, are what
 // covers the memory's latency).  Few rows, and rows off those boundaries: direct loads.
 //
-// Measured: 8192 x 4096 bf16 to s8 codes 40.4 us, 5.8 TB/s (0.86 of a copy's bandwidth);
-// 12608 x 768, fp32 stream, LAYER norms with betas, a gate per 197 rows: 28.4 us, 4.1 TB/s
-// (issue 46 %, the stalls waits on global and shared loads); 777 x 1003 f16 5.8 us; one row
-// of 4096 2.3 us.  Odd widths load element by element: 8192 x 2003 bf16 70 us, 1.9 TB/s;
-// through a ring 92 us.
+// Measured, over data that L2 cannot hold: 8192 x 4096 bf16 to s8 codes 41.3 us, 5.7 TB/s
+// (0.84 of a copy's bandwidth); 12608 x 768, fp32 stream, LAYER norms with betas, a gate per
+// 197 rows: 28.6 us, 4.1 TB/s (issue 49 %, the stalls waits on global and shared loads); 777 x
+// 1003 f16 7.7 us (5.9 out of L2); one row of 4096 2.4 us; 2048 x 16384 bf16 61 us, 4.4 TB/s
+// (no ring, 100 bytes of spills a thread).  Odd widths load element by element: 8192 x 2003
+// bf16 71 us, 1.9 TB/s (through a ring 92); 2048 x 16385 207 us, 1.3 TB/s.
 #include "qnn_blocknorm.cuh"
 
 namespace qnn {

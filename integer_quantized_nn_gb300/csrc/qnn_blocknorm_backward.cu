@@ -16,11 +16,14 @@
 // registers) rather than read: the rows are here anyway.  Rows come through a ring of
 // stages in shared memory, filled by bulk copies while rows are computed.
 //
-// Measured: 4096 x 4096 bf16, RMS norms, one gate: 60 us, 3.3 TB/s (0.49 of a copy's
-// bandwidth); 12608 x 1024 fp32, LAYER norms with betas: 80 us, 3.9 TB/s; 8192 x 2003 bf16
-// 105 us (158 without the ring, which cost 4096 x 4096 1 us); 65 x 1003 9.4 us.  At 4096 x 4096 no unit is at its limit:
-// 58 instructions an element, issue 49 %, 15 warps an SM (128 registers), the stalls spread
-// over fixed latencies, shared memory, global loads and barriers.
+// Measured, over data that L2 cannot hold: 4096 x 4096 bf16, RMS norms, one gate: 59 us, 3.4
+// TB/s (0.50 of a copy's bandwidth); 12608 x 1024 fp32, LAYER norms with betas: 80 us, 3.9
+// TB/s; 8192 x 2003 bf16 104 us (158 without the ring, which cost 4096 x 4096 1 us); 65 x 1003
+// 12.0 us (9.6 out of L2).  At 4096 x 4096 no unit is at its limit: 58 instructions an
+// element, issue 50 %, 15 warps an SM (128 registers), the stalls spread over fixed latencies,
+// shared memory, global loads and barriers.  Beyond 8192 columns a thread holds 32 of them in
+// 64 registers and spills (by the compiler's count 7 KB a thread, 4 KB at odd widths): 2048 x
+// 16384 bf16 766 us, 0.5 TB/s, with LAYER norms 787; 2048 x 16385 1034 us.
 #include "qnn_blocknorm.cuh"
 
 namespace qnn {
@@ -481,7 +484,8 @@ bool back_full(const qnn_block_norm *p)
 
 // Columns of a thread.  16 spread the fixed work of a row (reductions, addresses) over
 // more of them, where their sums fit the registers (4096 bf16 columns, RMS: 59 us with
-// 16, 70 with 8; LAYER with betas: 116 and 84).
+// 16, 70 with 8; LAYER with betas: 116 and 84).  LAYER beyond 4096 columns spills about
+// 430 bytes a thread with its 16.
 int back_columns(int C, bool full) { return C <= (full ? 4096 : 1024) ? 8 : C <= 8192 ? 16 : 32; }
 
 int back_threads(int C, bool full)

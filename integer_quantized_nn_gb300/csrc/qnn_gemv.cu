@@ -12,11 +12,13 @@
 // for one row of x alone.  This kernel is for up to 8 columns; qnn_gemv_columns.cu has
 // the one for more.
 //
-// Measured (one row, groups of 128): 8192 x 8192 bf16 9.0 us, 4.0 TB/s, 0.58 of a copy's
-// bandwidth; 4096 x 4096 f16 3.75 us; 1024 x 1024 (groups of 64) 2.1 us.  That is 2 to 4 us
-// beyond the bytes.  8192 x 8192 makes 256 blocks for 152 SMs: an SM's issue is 24 to 49 %
-// busy, by how many blocks it has.  Shifting codes on the multiplier pipe (mul.hi) was
-// slower (13.4 us to 10.9 at that stage).
+// Measured (one row, groups of 128), over weights that L2 cannot hold and, in brackets, over
+// three copies in turn, of which it can keep some or all: 8192 x 8192 bf16 9.8 us [9.1], 3.7
+// TB/s, 0.54 of a copy's bandwidth; 4096 x 4096 f16 4.3 [3.8]; 1024 x 1024 (groups of 64) 2.4
+// [2.2]; 131072 x 4096 bf16 64 us, 4.3 TB/s.  That is 2 to 5 us beyond the bytes, at 131072
+// channels 23.  8192 x 8192 makes 256 blocks for 152 SMs: an SM's issue is 24 to 49 % busy, by
+// how many blocks it has.  Shifting codes on the multiplier pipe (mul.hi) was slower (13.4 us
+// to 10.9 at that stage).
 //
 // The image (prepack): per tile of 16 output channels and step of 128 input
 // channels, 1024 bytes, 32 a lane.  A 32-bit word of lane (g, j) (g = lane / 4, j =
@@ -378,7 +380,8 @@ template <int XT>
 qnn_status launch_gemv_type(const GemvArgs &a, int group, cudaStream_t s)
 {
     constexpr int P = Cols<XT>::kParts;
-    // x has to fit beside the sums; 8 rows of 8192 bf16 do not, and take 16 us by columns
+    // x has to fit beside the sums; 8 rows of 8192 bf16 do not, and take 17.5 us by columns (4
+    // rows take 10.5 here, both 1 to 2 us less with some of the weights in L2)
     if (a.M * P > 8 || gemv_smem<2>(a, P) > kMaxSmem) return launch_gemv_columns(a, XT, group, s);
     // two tiles a warp share the loads of x and a set's fixed costs, as soon as they leave
     // every SM two blocks (bf16, one row: 8192 x 8192 takes 9.2 us with two, 10.9 with one;

@@ -20,9 +20,10 @@
 // are stored as they come: word f of a lane makes columns 8 f .. 8 f + 7 of the step's 64
 // (two f16 a column), and x is put down in the order of K that this gives.
 //
-// Measured: 32 rows, 16384 x 4096, bf16, groups of 128: 17.6 us (2.0 TB/s, 0.30 of
-// a copy's bandwidth; mma.sync forms took 33 and 37 us), about 800 cycles a step where its
-// 8 KB at 23 bytes a clock would take 350.  Issuing half the MMAs changed nothing, so it is
+// Measured: 32 rows, 16384 x 4096, bf16, groups of 128: 20.0 us over weights that L2 cannot
+// hold (1.8 TB/s, 0.27 of a copy's bandwidth), 17.6 over three copies in turn (mma.sync forms
+// took 33 and 37 there), about 800 cycles a step where its 8 KB at 23 bytes a clock would
+// take 350.  Issuing half the MMAs changed nothing, so it is
 // the latency of the hand-overs between the roles and not the tensor core that bounds it.
 #include <cooperative_groups.h>
 #include <type_traits>
@@ -395,7 +396,8 @@ qnn_status launch(const GemvArgs &a, cudaStream_t s)
     while (splits < 4 && bx * by * splits * 2 <= sm_count() && a.steps >= 4 * splits) splits *= 2;
     // One block on an SM, whatever it needs: two could each hold the tensor memory that the
     // other's cluster waits for.
-    constexpr int NEED = 1024 + kStages * (NC * 256 + (TOK * 4 + 31) / 32 * 512 * kUnitChunks<XT>) + 128 * (NC + 1) * 4, SMEM = NEED > (120 << 10) ? NEED : 120 << 10;
+    constexpr int NEED = 1024 + kStages * (NC * 256 + (TOK * 4 + 31) / 32 * 512 * kUnitChunks<XT>) + 128 * (NC + 1) * 4,
+                  SMEM = NEED > (120 << 10) ? NEED : 120 << 10;
     auto kern = gemv_w4_columns_kernel<XT, NC, ZERO, NS>;
     static std::atomic<uint64_t> opted_in{0};
     if (!opt_in_smem(kern, SMEM, opted_in)) return QNN_ERR_CUDA;
