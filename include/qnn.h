@@ -45,7 +45,8 @@ typedef enum {
     QNN_ERR_TIMEOUT = 6        /* a device-side bounded wait gave up */
 } qnn_status;
 
-/* F16 and BF16 are float types of the weight-only product and the block norm. */
+/* F16 and BF16 are float types of the weight-only product, the block norm and the cache of
+ * keys and values. */
 typedef enum {
     QNN_S8 = 0, QNN_U8 = 1, QNN_S4 = 2, QNN_U4 = 3, QNN_S32 = 4, QNN_F32 = 5, QNN_F16 = 6, QNN_BF16 = 7
 } qnn_dtype;
@@ -596,6 +597,104 @@ qnn_status q_block_norm_backward(const void *r_out, qnn_dtype r_dt, const void *
                                  void *dy, void *dgate, float *dgamma_pre, float *dbeta_pre, float *dgamma_post,
                                  float *dbeta_post, void *workspace, size_t workspace_bytes, qnn_stream_t stream);
 
+/* ---- a quantised cache of keys and values --------------------------------------- */
+
+/* The cache is made of pages.  A page holds, for each of `heads` heads, the K and the V
+ * codes of `page` tokens, D channels each, and a 32-bit word for each token, of K and of V
+ * [QI tensor量化与通道量化, refined to a token and head]:
+ *   QNN_S8: the word is the scale s (fp32); value = q * s
+ *   QNN_U4: the word's upper half is the scale s (bf16), its lowest four bits are the zero
+ *           point z; value = (q - z) * s
+ * (q is a code; the order inside a page is the library's own; a page can be copied whole). */
+typedef struct {
+    int32_t heads;           /* of keys and values, at most 1024 */
+    int32_t D;               /* channels of a head: a multiple of 32, 32..256 */
+    int32_t page;            /* tokens of a page: a multiple of 16, 16..256 */
+    int32_t kv_dt;           /* S8 or U4 */
+} qnn_kv_geom;
+
+/* Size in bytes of a page, a multiple of 128; 0 for an invalid geometry or type. */
+size_t qnn_kv_page_bytes(const qnn_kv_geom *g);
+
+/* The sequences of a call.  Sequence b has lens[b] tokens; token i of it lies in page
+ * table[b * ld_table + i / page].  A call is about the newest tokens of each: T[b] of them,
+ * T[b] = starts[b + 1] - starts[b] with `starts`, else `tokens`.  Their data are rows
+ * starts[b] .. starts[b + 1] - 1 (b * tokens ..) of the call's token tensors, in order; row t
+ * is the token at position lens[b] - T[b] + t.  Rows behind the last sequence's are not
+ * touched.  A row whose position is negative (lens[b] < T[b], such as an empty sequence that
+ * pads a batch) has no token: nothing is written for it, and what is read for it is zero.
+ * lens, starts and table are read on the device.  There a length below 0 or beyond
+ * ld_table * page, starts that descend, pass `rows` or hold more than `tokens`, or, where a
+ * token is in use, a page outside 0..num_pages - 1 are reported as QNN_ERR_INVALID_ARG by
+ * qnn_check_device_error; a sequence of such a length or such starts is left out (its rows
+ * are not touched), a token of such a page is not there (as above). */
+typedef struct {
+    void *pages;             /* device [num_pages][qnn_kv_page_bytes], 128-byte aligned */
+    int64_t num_pages;       /* at most 2^31 - 1 */
+    const int32_t *table;    /* device [batch][ld_table] */
+    int64_t ld_table;        /* entries between sequences, and the most pages of one */
+    const int32_t *lens;     /* device [batch] */
+    const int32_t *starts;   /* device [batch + 1], or NULL: `tokens` rows each */
+    int64_t rows;            /* of the token tensors, at most 2^31 - 1 (no starts: batch * tokens) */
+    int32_t batch;           /* at most 4096 */
+    int32_t tokens;          /* each sequence's newest tokens; with starts, the most of one */
+} qnn_kv_seqs;
+
+/* Quantize the newest tokens' keys and values into the cache.  k, v: device [rows][heads][D]
+ * of x_dt (F32, F16, BF16), ld_k and ld_v elements between rows (>= heads * D; 0: that), as
+ * columns of a fused projection have them.  For each token and head, over its finite values,
+ * every operation rounded to fp32:
+ *   S8: s = max|x| / 127;  q = clip(rint(x / s), -127, 127)
+ *   U4: lo = min(0, min x), hi = max(0, max x), s = bf16(hi / 15 - lo / 15);
+ *       z = clip(rint(-lo / s), 0, 15);  q = clip(rint(x / s) + z, 0, 15)
+ * NaN becomes the code of real zero, infinities saturate [as q_quantize]; s = 0: codes of
+ * zero (z = 0).  No two of the call's tokens may share a place in the cache (a page that
+ * several sequences share may hold none of their newest tokens). */
+qnn_status q_kv_write(const void *k, const void *v, qnn_dtype x_dt, int64_t ld_k, int64_t ld_v,
+                      const qnn_kv_geom *g, const qnn_kv_seqs *seqs, qnn_stream_t stream);
+
+/* The newest tokens' keys and values back: the fp32 product q * s or (q - z) * s, rounded to
+ * x_dt (a code stands for a value up to half a step beyond the largest that was written: at the
+ * end of a type's range that may be an infinity).  k, v as above, written; either may be NULL (not
+ * wanted). */
+qnn_status q_kv_read(void *k, void *v, qnn_dtype x_dt, int64_t ld_k, int64_t ld_v, const qnn_kv_geom *g,
+                     const qnn_kv_seqs *seqs, qnn_stream_t stream);
+
+/* Keep some of the newest tokens, such as the accepted path of a drafted tree: for i in
+ * 0 .. n_keep[b] - 1 the newest token keep[b * ld_keep + i] of sequence b takes the place of
+ * the newest token i (its codes and words move as they are).  The caller then shortens
+ * lens[b] by T[b] - n_keep[b].  keep: device int32 [batch][ld_keep], each sequence's entries
+ * ascending, within 0..T[b] - 1; n_keep: device int32 [batch], 0..min(T[b], ld_keep).  Others are
+ * reported as QNN_ERR_INVALID_ARG by qnn_check_device_error, and that sequence's tokens stay.
+ * ld_keep at most 1024. */
+qnn_status q_kv_keep(const qnn_kv_geom *g, const qnn_kv_seqs *seqs, const int32_t *keep, int64_t ld_keep,
+                     const int32_t *n_keep, qnn_stream_t stream);
+
+/* Size in bytes of the attention's workspace (for the current device); 0 for invalid arguments. */
+size_t qnn_kv_attn_workspace_bytes(const qnn_kv_geom *g, const qnn_kv_seqs *seqs, int heads_q);
+
+/* Attention of the newest tokens over the cache.  q: device [rows][heads_q][D] of x_dt (F16 or
+ * BF16), ld_q elements between rows; heads_q a multiple of heads, and head h of q reads head
+ * h / (heads_q / heads) of the cache.  Row t of sequence b sees every position before the newest
+ * tokens, and of those the newest token j if bit j % 32 of mask[row * mask_words + j / 32] is
+ * set (a tree of drafted tokens: itself and its ancestors), or without a mask if j <= t.  Bits
+ * beyond T[b] do not count; newest tokens beyond 32 * mask_words are not seen.  Over the
+ * visible positions j
+ *   x_j = scale * sum_d q_d k_jd,  out = sum_j e^(x_j - max x) v_j / sum_j e^(x_j - max x)
+ * (k, v: the cache's values), lse = max x + ln sum_j e^(x_j - max x).  A row that sees nothing
+ * gets zeros and -inf.  out: of x_dt, ld_out elements between rows (0: packed, for both); lse:
+ * fp32 [rows][heads_q] or NULL.  scale finite.
+ * q enters the products as f16, each row scaled by a power of two that brings its largest value
+ * near f16's, so that bf16 keeps its 8 bits (values beyond 2^-30 of the row's largest lose
+ * some); weights e^x, with V's scales in them, are f16 too; all sums are fp32, their order set
+ * by the sizes and lengths: equal calls give equal bits.
+ * q's rows must start on multiples of 16 bytes (ld_q a multiple of 8), out's too.
+ * workspace: device scratch of qnn_kv_attn_workspace_bytes bytes, 16-byte aligned,
+ * overwritten.  Two calls in flight must not share one. */
+qnn_status q_kv_attn(const void *q, qnn_dtype x_dt, int64_t ld_q, int heads_q, const qnn_kv_geom *g,
+                     const qnn_kv_seqs *seqs, float scale, const uint32_t *mask, int mask_words, void *out,
+                     int64_t ld_out, float *lse, void *workspace, size_t workspace_bytes, qnn_stream_t stream);
+
 /* ---- status ----------------------------------------------------------------- */
 
 const char *qnn_status_string(qnn_status s);
@@ -603,7 +702,8 @@ const char *qnn_status_string(qnn_status s);
 /* Synchronises `stream`, then reports and clears the device status word that
  * kernels set when a bounded wait gives up (QNN_ERR_TIMEOUT) or a device-side
  * argument check fails (QNN_ERR_INVALID_ARG: a Power-of-Two-Factor shift above
- * its stated bound; a GEMM weight image whose trailer does not match its K, or
+ * its stated bound; a zero point of 4-bit weights, a length, page or kept token of the
+ * cache out of range; a GEMM weight image whose trailer does not match its K, or
  * whose values need more exact runs than the kernel was launched for), or
  * QNN_ERR_CUDA if the stream holds a CUDA error. */
 qnn_status qnn_check_device_error(qnn_stream_t stream);

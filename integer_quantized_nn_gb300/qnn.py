@@ -72,6 +72,16 @@ class BlockNorm(ctypes.Structure):
                 + [(n, ctypes.c_int64) for n in ("gate_rows", "ld_r", "ld_y", "ld_h")])
 
 
+class KvGeom(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("heads", "D", "page", "kv_dt")]
+
+
+class KvSeqs(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("table", ctypes.c_void_p),
+                ("ld_table", ctypes.c_int64), ("lens", ctypes.c_void_p), ("starts", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("batch", ctypes.c_int32), ("tokens", ctypes.c_int32)]
+
+
 _lib = None
 _SYMBOLS = {}
 
@@ -115,6 +125,12 @@ def _declare(L):
         "q_block_norm": (c_int, [vp, c_int, vp, c_int, i64, c_int, vp, vp, vp, c_int, vp, vp]),
         "qnn_block_norm_backward_workspace_bytes": (sz, [i64, c_int, vp]),
         "q_block_norm_backward": (c_int, [vp, c_int, vp, c_int, i64, c_int] + [vp] * 11 + [sz, vp]),
+        "qnn_kv_page_bytes": (sz, [vp]),
+        "q_kv_write": (c_int, [vp, vp, c_int, i64, i64, vp, vp, vp]),
+        "q_kv_read": (c_int, [vp, vp, c_int, i64, i64, vp, vp, vp]),
+        "q_kv_keep": (c_int, [vp, vp, vp, i64, vp, vp]),
+        "qnn_kv_attn_workspace_bytes": (sz, [vp, vp, c_int]),
+        "q_kv_attn": (c_int, [vp, c_int, i64, c_int, vp, vp, f32, vp, c_int, vp, i64, vp, vp, sz, vp]),
         "qnn_status_string": (ctypes.c_char_p, [c_int]),
         "qnn_check_device_error": (c_int, [vp]),
         "qnn_selftest_wait_timeout": (c_int, [ctypes.c_uint64, vp]),
@@ -497,6 +513,61 @@ def q_block_norm_backward(r_out, r_dt: str, y, y_dt: str, rows: int, C: int, par
         _ptr(dr_out), _ptr(dr), _ptr(dy), _ptr(dgate), _ptr(dgamma_pre), _ptr(dbeta_pre), _ptr(dgamma_post),
         _ptr(dbeta_post), _ptr(workspace), 0 if workspace is None else _nbytes(workspace), _stream(stream)),
         "q_block_norm_backward")
+
+
+def kv_geom(heads: int, D: int, page: int, kv_dt: str = "s8") -> KvGeom:
+    return KvGeom(int(heads), int(D), int(page), DTYPES[kv_dt])
+
+
+def qnn_kv_page_bytes(g: KvGeom) -> int:
+    load()
+    return int(_SYMBOLS["qnn_kv_page_bytes"](ctypes.byref(g)))
+
+
+def kv_seqs(pages, table, lens, rows: int, tokens: int, starts=None) -> KvSeqs:
+    """The sequences of a call: pages uint8 [num_pages, qnn_kv_page_bytes(g)], table int32
+    [batch, most pages], lens int32 [batch], starts int32 [batch + 1] or None (`tokens` rows
+    each).  Holds the tensors' addresses only: keep the tensors alive as long as it is used."""
+    return KvSeqs(_ptr(pages), int(pages.shape[0]), _ptr(table), int(table.shape[1]), _ptr(lens), _ptr(starts),
+                  int(rows), int(table.shape[0]), int(tokens))
+
+
+def q_kv_write(k, v, x_dt: str, g: KvGeom, seqs: KvSeqs, ld_k: int = 0, ld_v: int = 0, stream=None):
+    """Quantizes k, v [rows, heads, D] into the cache; ld_k, ld_v: elements between rows (0: packed)."""
+    load()
+    _check(_SYMBOLS["q_kv_write"](_ptr(k), _ptr(v), DTYPES[x_dt], int(ld_k), int(ld_v), ctypes.byref(g),
+                                  ctypes.byref(seqs), _stream(stream)), "q_kv_write")
+
+
+def q_kv_read(k, v, x_dt: str, g: KvGeom, seqs: KvSeqs, ld_k: int = 0, ld_v: int = 0, stream=None):
+    """The newest tokens' values into k, v [rows, heads, D]; either may be None."""
+    load()
+    _check(_SYMBOLS["q_kv_read"](_ptr(k), _ptr(v), DTYPES[x_dt], int(ld_k), int(ld_v), ctypes.byref(g),
+                                 ctypes.byref(seqs), _stream(stream)), "q_kv_read")
+
+
+def q_kv_keep(g: KvGeom, seqs: KvSeqs, keep, n_keep, stream=None):
+    """keep: int32 [batch, most], ascending newest tokens of each sequence; n_keep: int32 [batch]."""
+    load()
+    _check(_SYMBOLS["q_kv_keep"](ctypes.byref(g), ctypes.byref(seqs), _ptr(keep), int(keep.shape[1]), _ptr(n_keep),
+                                 _stream(stream)), "q_kv_keep")
+
+
+def qnn_kv_attn_workspace_bytes(g: KvGeom, seqs: KvSeqs, heads_q: int) -> int:
+    load()
+    return int(_SYMBOLS["qnn_kv_attn_workspace_bytes"](ctypes.byref(g), ctypes.byref(seqs), int(heads_q)))
+
+
+def q_kv_attn(q, x_dt: str, heads_q: int, g: KvGeom, seqs: KvSeqs, scale: float, out, workspace, mask=None, lse=None,
+              ld_q: int = 0, ld_out: int = 0, stream=None):
+    """Attention of q [rows, heads_q, D] over the cache into out; mask: int32 [rows, words], bits of
+    the newest tokens that a row sees (None: up to itself); workspace: uint8 device tensor of
+    qnn_kv_attn_workspace_bytes(g, seqs, heads_q) bytes; lse: fp32 [rows, heads_q] or None."""
+    load()
+    _check(_SYMBOLS["q_kv_attn"](_ptr(q), DTYPES[x_dt], int(ld_q), int(heads_q), ctypes.byref(g), ctypes.byref(seqs),
+                                 float(scale), _ptr(mask), 0 if mask is None else int(mask.shape[-1]), _ptr(out),
+                                 int(ld_out), _ptr(lse), _ptr(workspace), _nbytes(workspace), _stream(stream)),
+           "q_kv_attn")
 
 
 def qnn_check_device_error(stream=None) -> int:
