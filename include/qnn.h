@@ -624,7 +624,7 @@ size_t qnn_kv_page_bytes(const qnn_kv_geom *g);
  * touched.  A row whose position is negative (lens[b] < T[b], such as an empty sequence that
  * pads a batch) has no token: nothing is written for it, and what is read for it is zero.
  * lens, starts and table are read on the device.  There a length below 0 or beyond
- * ld_table * page, starts that descend, pass `rows` or hold more than `tokens`, or, where a
+ * ld_table * page or 2^30, starts that descend, pass `rows` or hold more than `tokens`, or, where a
  * token is in use, a page outside 0..num_pages - 1 are reported as QNN_ERR_INVALID_ARG by
  * qnn_check_device_error; a sequence of such a length or such starts is left out (its rows
  * are not touched), a token of such a page is not there (as above). */

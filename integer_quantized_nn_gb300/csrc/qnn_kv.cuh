@@ -11,7 +11,7 @@
 
 namespace qnn {
 
-constexpr int kKvMaxBatch = 4096, kKvMaxHeads = 1024;
+constexpr int kKvMaxBatch = 4096, kKvMaxHeads = 1024, kKvMaxLen = 1 << 30;
 
 // A head of a page: K codes [page][row], V codes [page][row], K words [page], V words [page].
 // A row is D codes (s8 as q + 128, which a magic number turns into an f16; u4 two a byte, the
@@ -46,7 +46,7 @@ __device__ __forceinline__ void kv_bad(const KvArgs &a) { atomicOr(a.status, kSt
 __device__ __forceinline__ KvSeq kv_seq(const KvArgs &a, int b)
 {
     KvSeq s;
-    const int64_t cap = a.ld_table * a.page;
+    const int64_t cap = min(a.ld_table * a.page, (int64_t)kKvMaxLen);
     s.len = *reinterpret_cast<const volatile int32_t *>(a.lens + b);
     s.first = (int64_t)b * a.tokens;
     s.T = a.tokens;

@@ -1,88 +1,61 @@
-// qnn_kv_attn.cu -- q_kv_attn: attention of the newest tokens over the quantised cache.
-#include "qnn_kv.cuh"
+// qnn_kv_attn.cu -- q_kv_attn: attention of the newest tokens over the quantised cache.  The
+// entry, the choice of the kernel, and the kernel that joins the parts of items that several
+// blocks had.
+#include "qnn_kv_attn.cuh"
 
 namespace qnn {
 namespace {
 
-struct KvAttnArgs {
-    KvArgs c;
-    const void *q;
-    void *out;
-    float *lse;
-    const uint32_t *mask;
-    int64_t ld_q, ld_out;
-    float scale_log2;  // scale * log2(e)
-    int heads_q, group, mask_words;
-};
+constexpr int kJoinThreads = 128, kJoinRows = 8;
 
-constexpr int kThreads = 128;
-
-// One block for a row and head, a token to a warp at a time.
-template <typename T, bool U4>
-__global__ void __launch_bounds__(kThreads) kv_attn_kernel(const __grid_constant__ KvAttnArgs a)
+// A block joins kJoinRows rows of the item that begins in block blockIdx.x's share and ends in a
+// later one's, if there is one.
+__global__ void __launch_bounds__(kJoinThreads) kv_attn_join_kernel(const __grid_constant__ KvAttnArgs a, int rows,
+                                                                    int channels, float weight_unit)
 {
-    const KvArgs &c = a.c;
-    __shared__ float part[4][256 + 2];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = c.D / 32;
-    const int64_t row = blockIdx.x;
-    const int hq = blockIdx.y, h = hq / a.group;
+    __shared__ float factor[kJoinRows][kAttnMaxBlocks], tops[kJoinRows], totals[kJoinRows], unit_of[kJoinRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = blockIdx.x, r0 = blockIdx.y * kJoinRows;
     grid_dependency_launch();
     grid_dependency_wait();
-    int b = 0;
-    if (c.starts) while (b < c.batch && c.starts[b + 1] <= row) ++b;
-    else b = (int)(row / c.tokens);
-    if (b >= c.batch) return;
-    const KvSeq s = kv_seq(c, b);
-    const int64_t t = row - s.first;
-    if (s.T < 0 || t < 0 || t >= s.T) return;
-    float q[8], acc[8], m = -INFINITY, l = 0.0f;
-    for (int e = 0; e < n; ++e) {
-        q[e] = to_f32(static_cast<const T *>(a.q)[row * a.ld_q + (int64_t)hq * c.D + lane * n + e]);
-        acc[e] = 0.0f;
-    }
-    for (int pos = warp; pos < s.len; pos += 4) {
-        const int j = pos - (s.len - s.T);
-        if (j >= 0) {
-            if (!a.mask) {
-                if (j > t) continue;
-            } else if (j >= 32 * a.mask_words || !(a.mask[row * a.mask_words + j / 32] >> (j % 32) & 1u)) {
-                continue;
-            }
+    const volatile int *record = reinterpret_cast<const int *>(a.ws) + block * kAttnRecord;
+    if (!record[0]) return;
+    const int b = record[1], rt = record[2], head = record[3], n = record[4] - block + 1;
+    const KvSeq s = kv_seq(a.c, b);
+    const int width = (int)min((int64_t)rows, (int64_t)s.T * a.group - (int64_t)rt * rows);
+    if (r0 >= width) return;
+    auto slot = [&](int k) { return attn_slot(a, block + k, k == 0 ? 1 : 0, rows, channels); };
+    for (int r = warp; r < kJoinRows && r0 + r < width; r += kJoinThreads / 32) {
+        const int64_t stat = (int64_t)rows * channels + 2 * (r0 + r);
+        float top = -INFINITY, unit = 0.0f, total = 0.0f;
+        for (int k = lane; k < n; k += 32) {
+            top = fmaxf(top, slot(k)[stat]);
+            unit = fmaxf(unit, slot(k)[(int64_t)rows * (channels + 2)]);
         }
-        const int pg = kv_page(c, b, pos / c.page), slot = pos % c.page;
-        if (pg < 0) continue;
-        const uint8_t *head = c.pages + pg * c.page_bytes + (int64_t)h * c.head_bytes;
-        const uint32_t *words = reinterpret_cast<const uint32_t *>(head + 2 * c.page * c.row_bytes);
-        const uint32_t wk = words[slot], wv = words[c.page + slot];
-        auto code = [&](const uint8_t *r, int d) {
-            if constexpr (U4) return (float)(r[16 * kv_chunk(c.chunks, slot, d / 32) + d % 32 / 2] >> (4 * (d & 1)) & 15);
-            else return (float)r[16 * kv_chunk(c.chunks, slot, d / 16) + d % 16];
-        };
-        const float zk = U4 ? (float)(wk & 15u) : 128.0f, zv = U4 ? (float)(wv & 15u) : 128.0f;
-        const float sk = __uint_as_float(U4 ? wk & 0xffff0000u : wk), sv = __uint_as_float(U4 ? wv & 0xffff0000u : wv);
-        float x = 0.0f;
-        for (int e = 0; e < n; ++e) x = __fmaf_rn(q[e], code(head + slot * c.row_bytes, lane * n + e) - zk, x);
-        for (int d = 16; d > 0; d /= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
-        x *= sk * a.scale_log2;
-        const float up = fmaxf(m, x), f = m == -INFINITY ? 0.0f : exp2f(m - up), p = exp2f(x - up);
-        m = up;
-        l = l * f + p;
-        for (int e = 0; e < n; ++e)
-            acc[e] = acc[e] * f + p * (code(head + (c.page + slot) * c.row_bytes, lane * n + e) - zv) * sv;
+        for (int d = 16; d > 0; d /= 2) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            unit = fmaxf(unit, __shfl_xor_sync(0xffffffffu, unit, d));
+        }
+        for (int k = lane; k < n; k += 32) {
+            const float m = slot(k)[stat], f = m == top ? 1.0f : ex2(m - top);
+            total = __fmaf_rn(slot(k)[stat + 1], f, total);
+            // units are powers of two: the quotient by a reciprocal is exact
+            factor[r][k] = f * (slot(k)[(int64_t)rows * (channels + 2)] * __uint_as_float(0x7f000000u - __float_as_uint(unit)));
+        }
+        for (int d = 16; d > 0; d /= 2) total += __shfl_xor_sync(0xffffffffu, total, d);
+        if (lane == 0) tops[r] = top, totals[r] = total, unit_of[r] = unit;
     }
-    for (int e = 0; e < n; ++e) part[warp][lane * n + e] = acc[e];
-    if (lane == 0) part[warp][256] = m, part[warp][257] = l;
     __syncthreads();
-    float top = -INFINITY, sum = 0.0f;
-    for (int w = 0; w < 4; ++w) top = fmaxf(top, part[w][256]);
-    for (int w = 0; w < 4; ++w) sum += part[w][257] * (part[w][256] == top ? 1.0f : exp2f(part[w][256] - top));
-    for (int d = threadIdx.x; d < c.D; d += kThreads) {
-        float o = 0.0f;
-        for (int w = 0; w < 4; ++w) o += part[w][d] * (part[w][256] == top ? 1.0f : exp2f(part[w][256] - top));
-        static_cast<T *>(a.out)[row * a.ld_out + (int64_t)hq * c.D + d] = from_f32<T>(sum == 0.0f ? 0.0f : o / sum);
+    for (int i = threadIdx.x; i < kJoinRows * a.c.D / 2; i += kJoinThreads) {
+        const int r = i / (a.c.D / 2), d = 2 * (i - r * (a.c.D / 2));
+        if (r0 + r >= width) break;
+        float v0 = 0.0f, v1 = 0.0f;
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float2 v = *reinterpret_cast<const float2 *>(slot(k) + (int64_t)(r0 + r) * channels + d);
+            v0 = __fmaf_rn(v.x, factor[r][k], v0), v1 = __fmaf_rn(v.y, factor[r][k], v1);
+        }
+        attn_store(a, s.first, head, rt * rows + r0 + r, d, v0, v1, tops[r], totals[r], unit_of[r] * weight_unit);
     }
-    if (a.lse && threadIdx.x == 0)
-        a.lse[row * a.heads_q + hq] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 bool heads_ok(const qnn_kv_geom *g, int heads_q)
@@ -97,7 +70,8 @@ extern "C" size_t qnn_kv_attn_workspace_bytes(const qnn_kv_geom *g, const qnn_kv
 {
     qnn::KvArgs c;
     if (qnn::kv_args(g, seqs, &c) != QNN_OK || !qnn::heads_ok(g, heads_q)) return 0;
-    return 16;
+    const qnn::AttnPlan p = qnn::attn_few_plan(c, heads_q / g->heads);
+    return 4 * (size_t)(p.blocks * (qnn::kAttnRecord + 2 * qnn::attn_slot_floats(p.rows, p.channels)));
 }
 
 extern "C" qnn_status q_kv_attn(const void *q, qnn_dtype x_dt, int64_t ld_q, int heads_q, const qnn_kv_geom *g,
@@ -130,11 +104,14 @@ extern "C" qnn_status q_kv_attn(const void *q, qnn_dtype x_dt, int64_t ld_q, int
     a.heads_q = heads_q;
     a.group = heads_q / g->heads;
     if (!(a.c.status = status_word())) return QNN_ERR_CUDA;
-    const dim3 grid((unsigned)a.c.rows, (unsigned)heads_q);
-    const bool u4 = g->kv_dt == QNN_U4;
-    if (x_dt == QNN_F16)
-        return u4 ? kv_launch(kv_attn_kernel<__half, true>, grid, kThreads, 0, (cudaStream_t)stream, a)
-                  : kv_launch(kv_attn_kernel<__half, false>, grid, kThreads, 0, (cudaStream_t)stream, a);
-    return u4 ? kv_launch(kv_attn_kernel<__nv_bfloat16, true>, grid, kThreads, 0, (cudaStream_t)stream, a)
-              : kv_launch(kv_attn_kernel<__nv_bfloat16, false>, grid, kThreads, 0, (cudaStream_t)stream, a);
+    const AttnPlan p = attn_few_plan(a.c, a.group);
+    a.blocks = p.blocks;
+    a.bf16 = x_dt == QNN_BF16;
+    a.ws = static_cast<float *>(workspace);
+    a.per16 = g->page / 16;
+    a.magic16 = (int)(((1ull << 32) + a.per16 - 1) / a.per16);
+    const qnn_status sent = launch_attn_few(a, p, g->kv_dt == QNN_U4, (cudaStream_t)stream);
+    if (sent != QNN_OK) return sent;
+    return kv_launch(kv_attn_join_kernel, dim3((unsigned)p.blocks, (unsigned)(p.rows / kJoinRows)), kJoinThreads, 0,
+                     (cudaStream_t)stream, a, p.rows, p.channels, kAttnWeightUnit);
 }

@@ -1,0 +1,243 @@
+// qnn_kv_attn.cuh -- what the kernels of q_kv_attn share: the arguments, how the work is
+// divided, and the workspace in which parts of a row's sum meet.
+#pragma once
+#include "qnn_kv.cuh"
+
+namespace qnn {
+
+struct KvAttnArgs {
+    KvArgs c;
+    const void *q;
+    void *out;
+    float *lse;
+    const uint32_t *mask;
+    float *ws;
+    int64_t ld_q, ld_out;
+    float scale_log2;  // scale * log2(e)
+    int heads_q, group, mask_words, bf16;
+    int blocks;        // of the attention's grid
+    int stages;        // of a ring
+    int per16, magic16;  // 16-token tiles of a page, and 2^32 / per16 rounded up
+};
+
+// The work: an item is a sequence's tile of rows (rows t * group + g, t a newest token, g one of
+// the heads of q that share a head of the cache) with one head of the cache; its units are chunks
+// of 128 tokens, as far as the tile sees.  All units stand in one line, by sequence, row tile,
+// head and position, and each block has an equal part of it, whatever the lengths: an item that
+// lies in one block is finished there; one that goes on behind a block's end is finished by the
+// joining kernel, from one part of each block.
+//
+// Workspace: for each block a record of 8 ints (of the item that its part of the line ends
+// inside: whether there is one, sequence, row tile, head, the block that it ends in), then two
+// slots of parts: slot 0 for an item that began in an earlier block, slot 1 for one that begins
+// here and goes on.  A slot: [rows][channels] sums, then for each row the maximum and the sum of
+// weights, then the unit of V's scales.
+constexpr int kAttnRecord = 8, kAttnChunk = 128;
+
+// Weights are p * (scale of V / unit) * 2^kAttnRoom in f16: p <= 2^kAttnSlack, as maxima move only when a
+// score passes them by more, and scale <= unit, so that they stay below 2^16; the unit is a power
+// of two no smaller than any scale so far.
+constexpr int kAttnSlack = 8, kAttnRoom = 7;
+constexpr float kAttnWeightUnit = 1.0f / (1 << kAttnRoom);
+
+__host__ __device__ inline int64_t attn_slot_floats(int rows, int channels) { return (int64_t)rows * (channels + 2) + 16; }
+
+__device__ __forceinline__ float *attn_slot(const KvAttnArgs &a, int block, int slot, int rows, int channels)
+{
+    return a.ws + (int64_t)a.blocks * kAttnRecord + (2 * (int64_t)block + slot) * attn_slot_floats(rows, channels);
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 2^k as fp32, -126 <= k <= 127
+__device__ __forceinline__ float pow2i(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
+
+// The units that a tile of `width` rows, number rt, sees of a sequence; one at least, so that
+// rows that see nothing are written too.
+__device__ __forceinline__ int attn_units(const KvAttnArgs &a, int T, int len, int rt, int width)
+{
+    int seen = len;
+    if (!a.mask) {
+        const int64_t last = min((int64_t)(rt + 1) * width, (int64_t)T * a.group) - 1;
+        seen = len - T + (int)(last / a.group) + 1;
+    }
+    return max(1, (int)(((int64_t)seen + kAttnChunk - 1) / kAttnChunk));
+}
+
+__device__ __forceinline__ int attn_row_tiles(const KvAttnArgs &a, int T, int width)
+{
+    return (int)(((int64_t)T * a.group + width - 1) / width);
+}
+
+// A sequence's units.
+__device__ __forceinline__ int64_t attn_weight(const KvAttnArgs &a, const KvSeq &s, int width)
+{
+    if (s.T <= 0) return 0;
+    const int tiles = attn_row_tiles(a, s.T, width);
+    int64_t n = 0;
+    if (a.mask || tiles == 1) n = (int64_t)tiles * attn_units(a, s.T, s.len, tiles - 1, width);
+    else
+        for (int rt = 0; rt < tiles; ++rt) n += attn_units(a, s.T, s.len, rt, width);
+    return n * a.c.heads;
+}
+
+// Where a unit stands; next() goes along the line.
+struct AttnCursor {
+    int b, rt, h, chunk, units, tiles, T, len;
+    int64_t first;
+
+    __device__ __forceinline__ void sequence(const KvAttnArgs &a, int width)
+    {
+        const KvSeq s = kv_seq(a.c, b);
+        T = max(s.T, 0);
+        len = s.len;
+        first = s.first;
+        tiles = attn_row_tiles(a, T, width);
+    }
+    // unit x of the line, whose sums up to each sequence are `sums`
+    __device__ __forceinline__ void find(const KvAttnArgs &a, const int64_t *sums, int64_t x, int width)
+    {
+        int lo = 0, hi = a.c.batch - 1;  // the last sequence that begins at or before x
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (sums[mid] <= x) lo = mid;
+            else hi = mid - 1;
+        }
+        b = lo;
+        sequence(a, width);
+        x -= sums[b];
+        for (rt = 0;; ++rt) {
+            units = attn_units(a, T, len, rt, width);
+            const int64_t n = (int64_t)units * a.c.heads;
+            if (x < n || rt + 1 >= tiles) break;
+            x -= n;
+        }
+        h = (int)(x / units);
+        chunk = (int)(x - (int64_t)h * units);
+    }
+    __device__ __forceinline__ void next(const KvAttnArgs &a, int width)
+    {
+        if (++chunk < units) return;
+        chunk = 0;
+        if (++h < a.c.heads) return;
+        h = 0;
+        if (++rt >= tiles) {
+            rt = 0;
+            do {
+                if (++b >= a.c.batch) return;
+                sequence(a, width);
+            } while (T <= 0);
+        }
+        units = attn_units(a, T, len, rt, width);
+    }
+};
+
+// sums[i]: the units of sequences 0 .. i - 1, by all threads of a block; returns all of them.
+template <int THREADS>
+__device__ __forceinline__ int64_t attn_sums(const KvAttnArgs &a, int64_t *sums, int width)
+{
+    __shared__ int64_t part[THREADS / 32];
+    const int per = (a.c.batch + THREADS - 1) / THREADS, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int b0 = min((int)threadIdx.x * per, a.c.batch), b1 = min(b0 + per, a.c.batch);
+    int64_t own = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int64_t w = attn_weight(a, kv_seq(a.c, b), width);
+        sums[b] = own;
+        own += w;
+    }
+    int64_t upto = own;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += v;
+    }
+    if (lane == 31) part[warp] = upto;
+    __syncthreads();
+    int64_t before = upto - own, all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += part[w];
+        all += part[w];
+    }
+    for (int b = b0; b < b1; ++b) sums[b] += before;
+    if (threadIdx.x == 0) sums[a.c.batch] = all;
+    __syncthreads();
+    return all;
+}
+
+// A block's part of the line: [from, to), of `all` units over `active` blocks.
+struct AttnShare {
+    int64_t all, from, to;
+    int active;
+    __device__ __forceinline__ AttnShare(int64_t n, int blocks, int block) : all(n)
+    {
+        active = (int)min((int64_t)blocks, n);
+        from = block < active ? n * block / active : n;
+        to = block < active ? n * (block + 1) / active : n;
+    }
+    __device__ __forceinline__ int block_of(int64_t x) const { return (int)(((x + 1) * active - 1) / all); }
+};
+
+// The page of 16-token tile `tile` of sequence b, or -1.
+__device__ __forceinline__ int attn_page(const KvAttnArgs &a, int b, int tile, int *in_page)
+{
+    const int index = a.per16 == 1 ? tile : (int)__umulhi((uint32_t)tile, (uint32_t)a.magic16);
+    *in_page = tile - index * a.per16;
+    return kv_page(a.c, b, index);
+}
+
+// Whether newest token t's row sees position p.
+__device__ __forceinline__ bool attn_sees(const KvAttnArgs &a, const AttnCursor &c, int t, int p)
+{
+    if (p >= c.len) return false;
+    const int j = p - (c.len - c.T);
+    if (j < 0) return true;
+    if (!a.mask) return j <= t;
+    if ((j >> 5) >= a.mask_words) return false;
+    return (a.mask[(c.first + t) * a.mask_words + (j >> 5)] >> (j & 31)) & 1u;
+}
+
+__device__ __forceinline__ uint32_t attn_pack(const KvAttnArgs &a, float x, float y)
+{
+    if (a.bf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    const __half2 v = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ float attn_lse(float m, float total)
+{
+    return total == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(m, log2f(total)), 0.6931471805599453f);
+}
+
+// Row r of an item (of a sequence whose newest tokens begin at row `first`), channels d and d + 1
+// of it, from sums of weights and codes in units of `unit`; with d = 0, its logarithm.
+__device__ __forceinline__ void attn_store(const KvAttnArgs &a, int64_t first, int head, int r, int d, float v0, float v1,
+                                           float m, float total, float unit)
+{
+    const int t = r / a.group;
+    const int64_t row = first + t;
+    const int hq = head * a.group + (r - t * a.group);
+    const float o0 = total == 0.0f ? 0.0f : v0 / total * unit, o1 = total == 0.0f ? 0.0f : v1 / total * unit;
+    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + row * a.ld_out + (int64_t)hq * a.c.D + d) =
+        attn_pack(a, o0, o1);
+    if (d == 0 && a.lse) a.lse[row * a.heads_q + hq] = attn_lse(m, total);
+}
+
+// The row tile, channels and blocks of a call's kernel.
+constexpr int kAttnMaxBlocks = 320;
+struct AttnPlan {
+    int rows, channels, blocks;
+};
+
+AttnPlan attn_few_plan(const KvArgs &c, int group);
+qnn_status launch_attn_few(const KvAttnArgs &a, const AttnPlan &p, bool u4, cudaStream_t s);
+
+}  // namespace qnn

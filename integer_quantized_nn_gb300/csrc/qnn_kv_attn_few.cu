@@ -1,0 +1,596 @@
+// qnn_kv_attn_few.cu -- q_kv_attn for few rows of a head of the cache (up to 32 at a time: the
+// heads of q that share it, times the newest tokens): decoding.
+//
+//   S^T = K Q^T,  P^T = e^(S^T - m),  O^T = V^T P^T
+// on mma.sync m16n8k16 with the codes as the A operand (16 tokens, or 16 channels) and 8 rows as
+// N: codes go from shared memory to A fragments in registers, no value twice, and P^T's fragment
+// is S^T's transposed 8 x 8 by 8 x 8 (movmatrix).  A code becomes an f16 integer by a magic number and
+// one subtraction; the products are exact, scales of K multiply the scores, scales of V the weights.
+//
+// It is bound by the stream of codes.  Each warp has a ring of its own in shared memory, stages
+// of 16 tokens (their K and V rows and words), filled by bulk copies that its first lanes issue;
+// warps meet only where an item ends.  Maxima move only when a score passes the warp's by 2^8 (the
+// weights have that room), which one vote a tile finds.
+#include "qnn_kv_attn.cuh"
+
+namespace qnn {
+namespace {
+
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+static_assert(kAttnChunk == 16 * kWarps, "a unit is a tile for each warp");
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transposed(uint32_t v)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic)
+{
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "r"(mask), "r"(magic));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t at)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
+}
+
+// N words from shared memory, aligned to their size (16 bytes at most at a time)
+template <int N>
+__device__ __forceinline__ void lds(uint32_t at, uint32_t *w)
+{
+    if constexpr (N == 1) w[0] = lds32(at);
+    else if constexpr (N == 2) {
+        const uint2 v = lds64(at);
+        w[0] = v.x, w[1] = v.y;
+    } else {
+        const uint4 v = lds_v4(at);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    }
+}
+
+// f16 magic numbers: 0x6400 | u is 1024 + u; for the upper half of a byte 1024 + 16 u, of which
+// a sixteenth is 64 + u.
+constexpr uint32_t kMagic = 0x64006400u, kOne = 0x3c003c00u, kSixteenth = 0x2c002c00u;
+constexpr uint32_t k1152 = 0x64806480u;
+
+// Four s8 codes (as q + 128) of a row to two registers of neighbouring pairs.
+__device__ __forceinline__ void s8_pairs(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    lo = hsub2_u32(prmt(w, kMagic, 0x7150), k1152);
+    hi = hsub2_u32(prmt(w, kMagic, 0x7352), k1152);
+}
+
+struct Zero {
+    uint32_t lo, hi;  // -(1024 + z), -(64 + z)
+};
+
+__device__ __forceinline__ Zero zero_of(uint32_t z0, uint32_t z1)
+{
+    const uint32_t z = z0 | z1 << 16;
+    return {0xe400e400u + z, 0xd400d400u + (z << 4)};
+}
+
+// The halves' four 4-bit codes each, less their zero points, as four registers.
+__device__ __forceinline__ void u4_pairs(uint32_t w, const Zero &z, uint32_t (&r)[4])
+{
+    const uint32_t v = w >> 8;
+    r[0] = fma2(and_or(w, 0x000f000fu, kMagic), kOne, z.lo);
+    r[1] = fma2(and_or(w, 0x00f000f0u, kMagic), kSixteenth, z.hi);
+    r[2] = fma2(and_or(v, 0x000f000fu, kMagic), kOne, z.lo);
+    r[3] = fma2(and_or(v, 0x00f000f0u, kMagic), kSixteenth, z.hi);
+}
+
+// DP: channels, D rounded up to 64, 128 or 256.  NT: tiles of 8 rows.
+template <bool U4, int DP, int NT>
+struct Shape {
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kKWords = DP / (U4 ? 32 : 16);   // of a token's K that a lane has
+    static constexpr int kVWords = DP / (U4 ? 64 : 32);   // of a token's V
+    static constexpr int kSteps = DP / 16;                // of K, and tiles of 16 channels of V
+    static constexpr bool kQRegs = NT * DP <= 256;        // q's fragments in registers
+    static constexpr int kMinBlocks = NT * DP <= 128 ? 2 : 1;
+    static constexpr int kPitch = DP + 4;                 // of a row where warps join
+};
+
+// The chunk, and the byte in it, at which a lane's words from w on begin: K's words of lane j (0..3),
+// V's of lane g (0..7).
+template <bool U4, int DP>
+__device__ __forceinline__ int k_chunk(int j, int w) { return U4 && DP == 64 ? j / 2 : 4 * (w / 4) + j; }
+template <bool U4, int DP>
+__device__ __forceinline__ int k_byte(int j) { return U4 && DP == 64 ? 8 * (j % 2) : 0; }
+template <bool U4, int DP>
+__device__ __forceinline__ int v_byte(int g)  // in the row, before the order of chunks
+{
+    constexpr int bytes = U4 ? DP / 16 : DP == 64 ? 8 : 16;
+    return bytes * g;
+}
+
+// Channel of value e of the lane's words of K (in fragment order: two for each register), and of
+// element (tile i, half) of the sums.
+template <bool U4, int DP>
+__device__ __forceinline__ int k_channel(int j, int step, int e)  // e: k = 2j, 2j+1, 2j+8, 2j+9
+{
+    if constexpr (U4) {
+        const int w = step / 2, n = (step % 2) * 2 + (e / 2) + 4 * (e % 2);  // nibbles n, n + 4
+        if (DP == 64) return 16 * j + 8 * w + n;
+        return 128 * (w / 4) + 32 * j + 8 * (w % 4) + n;
+    } else {
+        return 64 * (step / 4) + 16 * j + 4 * (step % 4) + e;
+    }
+}
+template <bool U4, int DP>
+__device__ __forceinline__ int sum_channel(int g, int i, int half)
+{
+    if constexpr (U4) return DP / 8 * g + 2 * i + half;
+    else return DP == 64 ? 8 * g + 2 * i + half : 128 * (i / 8) + 16 * g + 2 * (i % 8) + half;
+}
+
+// A stage: K rows, V rows, K words, V words of 16 tokens.
+__host__ __device__ inline int stage_bytes(int row_bytes) { return 16 * (2 * row_bytes + 8); }
+
+template <bool U4, int DP, int NT>
+__global__ void __launch_bounds__(kThreads, Shape<U4, DP, NT>::kMinBlocks)
+kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
+{
+    using S = Shape<U4, DP, NT>;
+    const KvArgs &c = a.c;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bars[kWarps][8];
+    __shared__ float stats[kWarps][S::kRows][2], units_of[kWarps];
+    __shared__ uint2 q_smem[S::kQRegs ? 1 : NT * S::kSteps * 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, j = lane & 3;
+    const int stage_b = stage_bytes(c.row_bytes), ST = a.stages;
+    float *join = reinterpret_cast<float *>(smem);  // [warps][8][kPitch]
+    uint8_t *ring = smem + kWarps * 8 * S::kPitch * 4 + warp * ST * stage_b;
+    int64_t *sums = reinterpret_cast<int64_t *>(smem + kWarps * (8 * S::kPitch * 4 + ST * stage_b) + 128);
+    const uint32_t ring_at = smem_u32(ring), bar = smem_u32(bars[warp]);
+
+    if (lane == 0) {
+        for (int i = 0; i < ST; ++i) mbar_init(bar + 8 * i, 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    grid_dependency_launch();
+    grid_dependency_wait();
+    const AttnShare share(attn_sums<kThreads>(a, sums, S::kRows), a.blocks, blockIdx.x);
+    int *record = reinterpret_cast<int *>(a.ws) + blockIdx.x * kAttnRecord;
+    if (share.from >= share.to) {
+        if (threadIdx.x == 0) record[0] = 0;
+        return;
+    }
+
+    // the copies' side: `ahead` is the unit whose page has been looked up
+    AttnCursor ahead, at;
+    ahead.find(a, sums, share.from, S::kRows);
+    at = ahead;
+    int64_t asked = share.from;  // units whose copies have been issued
+    int page, in_page;
+    auto look_up = [&]() {
+        const int tile = ahead.chunk * kWarps + warp;
+        page = -2;  // nothing to copy
+        if (tile * 16 < ahead.len) page = attn_page(a, ahead.b, tile, &in_page);
+    };
+    uint32_t absent = 0;  // stages whose tile is not there
+    auto ask = [&](int stage) {
+        const bool there = page >= 0;
+        absent = there ? absent & ~(1u << stage) : absent | 1u << stage;
+        const uint32_t to = ring_at + stage * stage_b, b = bar + 8 * stage;
+        if (lane == 0) mbar_arrive_expect_tx(b, there ? stage_b : 0);
+        __syncwarp();
+        if (there && lane < 4) {
+            const uint8_t *head = c.pages + page * c.page_bytes + (int64_t)ahead.h * c.head_bytes;
+            const int rows = 16 * c.row_bytes, all = c.page * c.row_bytes;
+            if (lane < 2) bulk_g2s(to + lane * rows, head + lane * all + in_page * rows, rows, b);
+            else bulk_g2s(to + 2 * rows + (lane - 2) * 64, head + 2 * all + (lane - 2) * 4 * c.page + in_page * 64, 64, b);
+        }
+        ++asked;
+        if (asked < share.to) {
+            ahead.next(a, S::kRows);
+            look_up();
+        }
+    };
+    look_up();
+    for (int i = 0; i < ST && asked < share.to; ++i) ask(i);
+
+    bool ok = true;
+    int64_t waiting = share.from;  // units whose copies have been waited for
+    int stage = 0;
+    uint32_t phase = 0;
+    int64_t x = share.from;
+    while (x < share.to) {
+        // one item, or the part of it that is this block's
+        const int64_t item_first = x - at.chunk;  // its place in the line
+        const int64_t item_end = item_first + at.units, end = min(item_end, share.to), first = at.first;
+        const int row0 = at.rt * S::kRows, head = at.h;
+        const int width = (int)min((int64_t)S::kRows, (int64_t)at.T * a.group - row0);
+        const int t_first = row0 / a.group, t_last = (row0 + width - 1) / a.group;
+        const bool starts_here = item_first >= share.from, ends_here = item_end <= share.to;
+        if (threadIdx.x == 0 && end == share.to) {
+            record[0] = starts_here && !ends_here;
+            record[1] = at.b, record[2] = at.rt, record[3] = at.h;
+            if (!ends_here) record[4] = share.block_of(item_end - 1);
+        }
+
+        // q's fragments: B of m16n8k16, column g, each row scaled to f16's range
+        uint32_t qf[S::kQRegs ? NT : 1][S::kQRegs ? S::kSteps : 1][2];
+        float cq[NT][2];  // of rows 2j, 2j + 1
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = row0 + 8 * nt + g;
+            const bool live = 8 * nt + g < width;
+            const int64_t qat = (first + r / a.group) * a.ld_q + (int64_t)(head * a.group + r % a.group) * c.D;
+            const uint16_t *qp = static_cast<const uint16_t *>(a.q) + qat;
+            if (S::kQRegs || warp == nt % kWarps) {
+                float top = 0.0f;
+                float v[S::kSteps][4];
+#pragma unroll
+                for (int s = 0; s < S::kSteps; ++s)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int d = k_channel<U4, DP>(j, s, e);
+                        uint16_t raw = 0;
+                        if (live && d < c.D) asm volatile("ld.global.u16 %0, [%1];" : "=h"(raw) : "l"(qp + d));
+                        v[s][e] = a.bf16 ? __uint_as_float((uint32_t)raw << 16) : __half2float(__ushort_as_half(raw));
+                        top = fmaxf(top, fabsf(v[s][e]));
+                    }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int e2 = (int)(__float_as_uint(top) >> 23);
+                const int k = top == 0.0f || e2 == 255 ? 0 : max(-126, min(126, 14 + 127 - e2));
+                const float up = pow2i(k);
+#pragma unroll
+                for (int s = 0; s < S::kSteps; ++s) {
+                    const __half2 lo = __floats2half2_rn(v[s][0] * up, v[s][1] * up);
+                    const __half2 hi = __floats2half2_rn(v[s][2] * up, v[s][3] * up);
+                    const uint32_t b0 = *reinterpret_cast<const uint32_t *>(&lo);
+                    const uint32_t b1 = *reinterpret_cast<const uint32_t *>(&hi);
+                    if constexpr (S::kQRegs) qf[nt][s][0] = b0, qf[nt][s][1] = b1;
+                    else q_smem[(nt * S::kSteps + s) * 32 + lane] = make_uint2(b0, b1);
+                }
+                const float cr = a.scale_log2 * pow2i(-k);
+                if constexpr (S::kQRegs) {
+                    cq[nt][0] = __shfl_sync(0xffffffffu, cr, 8 * j);
+                    cq[nt][1] = __shfl_sync(0xffffffffu, cr, 8 * j + 4);
+                } else if (j == 0) {
+                    stats[0][8 * nt + g][0] = cr;
+                }
+            }
+        }
+        if constexpr (!S::kQRegs) {
+            __syncthreads();
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) cq[nt][0] = stats[0][8 * nt + 2 * j][0], cq[nt][1] = stats[0][8 * nt + 2 * j + 1][0];
+            __syncthreads();
+        }
+
+        float acc[NT][S::kSteps][4], m[NT][2], ref[NT][2], l[NT][2];
+        float unit = pow2i(-126), per_unit = pow2i(126);  // V's scales are taken in units of 2^k
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int s = 0; s < S::kSteps; ++s)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nt][s][e] = 0.0f;
+            m[nt][0] = m[nt][1] = -INFINITY;
+            ref[nt][0] = ref[nt][1] = l[nt][0] = l[nt][1] = 0.0f;
+        }
+
+        for (; x < end && ok; ++x, at.next(a, S::kRows)) {
+            const int pos0 = (at.chunk * kWarps + warp) * 16;
+            ok = __all_sync(0xffffffffu, mbar_wait_idle(bar + 8 * stage, phase, c.status));
+            if (!ok) break;
+            ++waiting;
+            const int seen_by_all = a.mask ? at.len - at.T : min(at.len, at.len - at.T + t_first + 1);
+            const int seen_by_any = a.mask ? at.len : at.len - at.T + t_last + 1;
+            if (!(absent >> stage & 1u) && pos0 < seen_by_any) {
+                const uint32_t k_at = ring_at + stage * stage_b, v_at = k_at + 16 * c.row_bytes,
+                               w_at = v_at + 16 * c.row_bytes;
+                // scales of K and V of tokens g and g + 8
+                const uint32_t wk0 = lds32(w_at + 4 * g), wk1 = lds32(w_at + 4 * g + 32);
+                const uint32_t wv0 = lds32(w_at + 64 + 4 * g), wv1 = lds32(w_at + 64 + 4 * g + 32);
+                float s[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+                {
+                    uint32_t k0[S::kKWords], k1[S::kKWords];
+                    constexpr int step_w = S::kKWords < 4 ? S::kKWords : 4;
+#pragma unroll
+                    for (int w = 0; w < S::kKWords; w += step_w) {
+                        const int ch = k_chunk<U4, DP>(j, w);
+                        lds<step_w>(k_at + g * c.row_bytes + 16 * kv_chunk(c.chunks, g, ch) + k_byte<U4, DP>(j), k0 + w);
+                        lds<step_w>(k_at + (g + 8) * c.row_bytes + 16 * kv_chunk(c.chunks, g + 8, ch) + k_byte<U4, DP>(j),
+                                    k1 + w);
+                    }
+                    const Zero z0 = zero_of(wk0 & 15u, wk0 & 15u), z1 = zero_of(wk1 & 15u, wk1 & 15u);
+#pragma unroll
+                    for (int w = 0; w < S::kKWords; ++w) {
+                        uint32_t f[U4 ? 2 : 1][4];
+                        if constexpr (U4) {
+                            uint32_t r0[4], r1[4];
+                            u4_pairs(k0[w], z0, r0);
+                            u4_pairs(k1[w], z1, r1);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                f[e][0] = r0[2 * e], f[e][1] = r1[2 * e], f[e][2] = r0[2 * e + 1], f[e][3] = r1[2 * e + 1];
+                            }
+                        } else {
+                            s8_pairs(k0[w], f[0][0], f[0][2]);
+                            s8_pairs(k1[w], f[0][1], f[0][3]);
+                        }
+#pragma unroll
+                        for (int e = 0; e < (U4 ? 2 : 1); ++e) {
+                            const int st = w * (U4 ? 2 : 1) + e;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                if constexpr (S::kQRegs) mma16816(s[nt], f[e], qf[nt][st][0], qf[nt][st][1]);
+                                else {
+                                    const uint2 b = q_smem[(nt * S::kSteps + st) * 32 + lane];
+                                    mma16816(s[nt], f[e], b.x, b.y);
+                                }
+                            }
+                        }
+                    }
+                }
+                // scores in units of log2; s[.][0, 1]: token g, rows 2j, 2j + 1; [2, 3]: token g + 8
+                const float sk0 = __uint_as_float(U4 ? wk0 & 0xffff0000u : wk0);
+                const float sk1 = __uint_as_float(U4 ? wk1 & 0xffff0000u : wk1);
+                float sv0 = __uint_as_float(U4 ? wv0 & 0xffff0000u : wv0);
+                float sv1 = __uint_as_float(U4 ? wv1 & 0xffff0000u : wv1);
+                bool over = false;
+                const bool whole = pos0 + 16 <= seen_by_all;
+                if (!whole) {  // words beyond the sequence hold anything
+                    if (pos0 + g >= at.len) sv0 = 0.0f;
+                    if (pos0 + g + 8 >= at.len) sv1 = 0.0f;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    s[nt][0] = s[nt][0] * (cq[nt][0] * sk0), s[nt][1] = s[nt][1] * (cq[nt][1] * sk0);
+                    s[nt][2] = s[nt][2] * (cq[nt][0] * sk1), s[nt][3] = s[nt][3] * (cq[nt][1] * sk1);
+                    if (!whole) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int t = min((row0 + 8 * nt + 2 * j + (e & 1)) / a.group, at.T - 1);
+                            if (!attn_sees(a, at, t, pos0 + g + 8 * (e >> 1))) s[nt][e] = -INFINITY;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) over = over || s[nt][e] > m[nt][e & 1] + kAttnSlack;
+                }
+                over = over || sv0 > unit || sv1 > unit;
+                if (__any_sync(0xffffffffu, over)) {
+                    // new maxima of rows 2j, 2j + 1 (over the lanes of all tokens), a new unit
+                    uint32_t su = max(__float_as_uint(sv0), __float_as_uint(sv1));
+                    su = __reduce_max_sync(0xffffffffu, su);
+                    su = (su + 0x7fffffu) & 0xff800000u;  // a power of two, 2^126 at most: scales stay below
+                    const float grown = fmaxf(unit, __uint_as_float(su));
+                    const float ratio = unit * __uint_as_float(0x7f000000u - __float_as_uint(grown));  // unit / grown
+                    unit = grown;
+                    per_unit = __uint_as_float(0x7f000000u - __float_as_uint(grown));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float f[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float v = fmaxf(s[nt][e], s[nt][e + 2]);
+#pragma unroll
+                            for (int d = 4; d < 32; d *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+                            const float top = fmaxf(m[nt][e], v);
+                            f[e] = m[nt][e] == -INFINITY ? 0.0f : ex2(m[nt][e] - top);
+                            m[nt][e] = top;
+                            ref[nt][e] = top == -INFINITY ? 0.0f : top;
+                            l[nt][e] *= f[e];
+                            f[e] *= ratio;
+                        }
+#pragma unroll
+                        for (int st = 0; st < S::kSteps; ++st)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[nt][st][e] *= f[e & 1];
+                    }
+                }
+                const float w0 = sv0 * per_unit * (float)(1 << kAttnRoom), w1 = sv1 * per_unit * (float)(1 << kAttnRoom);
+                uint32_t p[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float p0 = ex2(s[nt][0] - ref[nt][0]), p1 = ex2(s[nt][1] - ref[nt][1]);
+                    const float p2 = ex2(s[nt][2] - ref[nt][0]), p3 = ex2(s[nt][3] - ref[nt][1]);
+                    l[nt][0] += p0 + p2, l[nt][1] += p1 + p3;
+                    const __half2 lo = __floats2half2_rn(p0 * w0, p1 * w0), hi = __floats2half2_rn(p2 * w1, p3 * w1);
+                    p[nt][0] = transposed(*reinterpret_cast<const uint32_t *>(&lo));
+                    p[nt][1] = transposed(*reinterpret_cast<const uint32_t *>(&hi));
+                }
+                // V of tokens 2j, 2j + 1, 2j + 8, 2j + 9, the lane's channels
+                uint32_t vw[4][S::kVWords];
+                constexpr int step_v = S::kVWords < 4 ? S::kVWords : 4;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 2 * j + (e & 1) + 8 * (e >> 1);
+#pragma unroll
+                    for (int w = 0; w < S::kVWords; w += step_v) {
+                        const int byte = v_byte<U4, DP>(g) + (w / 4) * 128;
+                        lds<step_v>(v_at + t * c.row_bytes + 16 * kv_chunk(c.chunks, t, byte / 16) + byte % 16, vw[e] + w);
+                    }
+                }
+                Zero za, zb;
+                if constexpr (U4) {
+                    const uint2 ta = lds64(w_at + 64 + 8 * j), tb = lds64(w_at + 64 + 8 * j + 32);
+                    za = zero_of(ta.x & 15u, ta.y & 15u);
+                    zb = zero_of(tb.x & 15u, tb.y & 15u);
+                }
+#pragma unroll
+                for (int w = 0; w < S::kVWords; ++w) {
+                    if constexpr (U4) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t ra[4], rb[4];
+                            u4_pairs(prmt(vw[0][w], vw[1][w], half ? 0x7632 : 0x5410), za, ra);
+                            u4_pairs(prmt(vw[2][w], vw[3][w], half ? 0x7632 : 0x5410), zb, rb);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const uint32_t f[4] = {ra[2 * e], ra[2 * e + 1], rb[2 * e], rb[2 * e + 1]};
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt][4 * w + 2 * half + e], f, p[nt][0], p[nt][1]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            // the tokens' codes of a channel side by side: a0 b0 a1 b1
+                            const uint32_t ta = prmt(vw[0][w], vw[1][w], half ? 0x7362 : 0x5140);
+                            const uint32_t tb = prmt(vw[2][w], vw[3][w], half ? 0x7362 : 0x5140);
+                            uint32_t f[4];
+                            s8_pairs(ta, f[0], f[1]);
+                            s8_pairs(tb, f[2], f[3]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt][2 * w + half], f, p[nt][0], p[nt][1]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();  // the stage has been read
+            if (asked < share.to) ask(stage);
+            if (++stage == ST) stage = 0, phase ^= 1u;
+        }
+        // a wait that gave up: this warp goes on in step with the others, without its tiles, and
+        // lets the copies that it has asked for land
+        if (!ok) {
+            for (; waiting < asked; ++waiting) {
+                (void)mbar_wait_idle(bar + 8 * stage, phase, c.status);
+                if (++stage == ST) stage = 0, phase ^= 1u;
+            }
+            for (; x < end; ++x) at.next(a, S::kRows);
+        }
+
+        // the warps' parts meet
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
+                if (g == 0) stats[warp][8 * nt + 2 * j + e][0] = m[nt][e], stats[warp][8 * nt + 2 * j + e][1] = l[nt][e];
+            }
+        if (lane == 0) units_of[warp] = unit;
+        __syncthreads();
+        float top_unit = units_of[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) top_unit = fmaxf(top_unit, units_of[w]);
+        const bool done = starts_here && ends_here;
+        float *slot = attn_slot(a, blockIdx.x, starts_here ? 1 : 0, S::kRows, DP);
+        const float shrink = unit * __uint_as_float(0x7f000000u - __float_as_uint(top_unit));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * nt + 2 * j + e;
+                float top = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[w][r][0]);
+                const float f = (m[nt][e] == top ? 1.0f : ex2(m[nt][e] - top)) * shrink;
+                float *to = join + (warp * 8 + 2 * j + e) * S::kPitch + g;
+#pragma unroll
+                for (int s = 0; s < S::kSteps; ++s)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) to[(2 * s + half) * 8] = acc[nt][s][2 * half + e] * f;
+            }
+            __syncthreads();
+            // pairs of channels of a row, in the order of (step, half, g)
+            for (int i = threadIdx.x; i < 8 * DP / 2; i += kThreads) {
+                const int r = i / (DP / 2), p = i % (DP / 2), row = 8 * nt + r;
+                if (row >= width) break;
+                const int step = p / 8, pg = p % 8;
+                float v0 = 0.0f, v1 = 0.0f, top = -INFINITY, total = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float *from = join + (w * 8 + r) * S::kPitch + 16 * step + pg;
+                    v0 += from[0], v1 += from[8];
+                    top = fmaxf(top, stats[w][row][0]);
+                }
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    total += stats[w][row][1] * (stats[w][row][0] == top ? 1.0f : ex2(stats[w][row][0] - top));
+                const int d = sum_channel<U4, DP>(pg, step, 0);
+                if (!done) {
+                    *reinterpret_cast<float2 *>(slot + row * DP + d) = make_float2(v0, v1);
+                    if (p == 0) {
+                        slot[S::kRows * DP + 2 * row] = top, slot[S::kRows * DP + 2 * row + 1] = total;
+                        if (row == 0) slot[S::kRows * (DP + 2)] = top_unit;
+                    }
+                } else if (d < c.D) {
+                    attn_store(a, first, head, row0 + row, d, v0, v1, top, total, top_unit * kAttnWeightUnit);
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+template <bool U4, int DP, int NT>
+qnn_status launch(KvAttnArgs a, cudaStream_t s)
+{
+    using S = Shape<U4, DP, NT>;
+    auto kern = kv_attn_few_kernel<U4, DP, NT>;
+    static std::atomic<uint64_t> opted_in{0};
+    // of an SM's 228 KB: 1 KB a block for the system, and the static part
+    constexpr int kMost = (S::kMinBlocks == 2 ? 112 : 224) << 10, kStatic = 12 << 10;
+    const int join = kWarps * 8 * S::kPitch * 4, sums = (a.c.batch + 1) * 8 + 128, stage = kWarps * stage_bytes(a.c.row_bytes);
+    a.stages = std::min(8, (kMost - kStatic - join - sums) / stage);
+    if (!opt_in_smem(kern, kMost - kStatic, opted_in, 100)) return QNN_ERR_CUDA;
+    return kv_launch(kern, dim3((unsigned)a.blocks), kThreads, join + sums + a.stages * stage, s, a);
+}
+
+template <bool U4>
+qnn_status launch_channels(const KvAttnArgs &a, const AttnPlan &p, cudaStream_t s)
+{
+    if (p.channels == 64)
+        return p.rows == 8 ? launch<U4, 64, 1>(a, s) : p.rows == 16 ? launch<U4, 64, 2>(a, s) : launch<U4, 64, 4>(a, s);
+    if (p.channels == 128)
+        return p.rows == 8 ? launch<U4, 128, 1>(a, s) : p.rows == 16 ? launch<U4, 128, 2>(a, s) : launch<U4, 128, 4>(a, s);
+    return p.rows == 8 ? launch<U4, 256, 1>(a, s) : launch<U4, 256, 2>(a, s);
+}
+
+}  // namespace
+
+AttnPlan attn_few_plan(const KvArgs &c, int group)
+{
+    AttnPlan p;
+    p.channels = c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256;
+    const int64_t rows = (int64_t)c.tokens * group;
+    p.rows = rows <= 8 ? 8 : rows <= 16 || p.channels == 256 ? 16 : 32;
+    p.blocks = std::min(kAttnMaxBlocks, sm_count() * (p.rows * p.channels <= 1024 ? 2 : 1));
+    return p;
+}
+
+qnn_status launch_attn_few(const KvAttnArgs &a, const AttnPlan &p, bool u4, cudaStream_t s)
+{
+    return u4 ? launch_channels<true>(a, p, s) : launch_channels<false>(a, p, s);
+}
+
+}  // namespace qnn
