@@ -58,6 +58,13 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attn_join_kernel(const __grid
     }
 }
 
+bool many_rows(const KvArgs &c, int group) { return c.D <= 128 && (int64_t)c.tokens * group > 32; }
+
+AttnPlan attn_plan(const KvArgs &c, int group)
+{
+    return many_rows(c, group) ? attn_rows_plan(c, group) : attn_few_plan(c, group);
+}
+
 bool heads_ok(const qnn_kv_geom *g, int heads_q)
 {
     return heads_q > 0 && heads_q % g->heads == 0 && heads_q / g->heads <= 1024;
@@ -70,7 +77,7 @@ extern "C" size_t qnn_kv_attn_workspace_bytes(const qnn_kv_geom *g, const qnn_kv
 {
     qnn::KvArgs c;
     if (qnn::kv_args(g, seqs, &c) != QNN_OK || !qnn::heads_ok(g, heads_q)) return 0;
-    const qnn::AttnPlan p = qnn::attn_few_plan(c, heads_q / g->heads);
+    const qnn::AttnPlan p = qnn::attn_plan(c, heads_q / g->heads);
     return 4 * (size_t)(p.blocks * (qnn::kAttnRecord + 2 * qnn::attn_slot_floats(p.rows, p.channels)));
 }
 
@@ -104,13 +111,14 @@ extern "C" qnn_status q_kv_attn(const void *q, qnn_dtype x_dt, int64_t ld_q, int
     a.heads_q = heads_q;
     a.group = heads_q / g->heads;
     if (!(a.c.status = status_word())) return QNN_ERR_CUDA;
-    const AttnPlan p = attn_few_plan(a.c, a.group);
+    const AttnPlan p = attn_plan(a.c, a.group);
     a.blocks = p.blocks;
     a.bf16 = x_dt == QNN_BF16;
     a.ws = static_cast<float *>(workspace);
     a.per16 = g->page / 16;
     a.magic16 = (int)(((1ull << 32) + a.per16 - 1) / a.per16);
-    const qnn_status sent = launch_attn_few(a, p, g->kv_dt == QNN_U4, (cudaStream_t)stream);
+    const qnn_status sent = (many_rows(a.c, a.group) ? launch_attn_rows : launch_attn_few)(a, p, g->kv_dt == QNN_U4,
+                                                                                          (cudaStream_t)stream);
     if (sent != QNN_OK) return sent;
     return kv_launch(kv_attn_join_kernel, dim3((unsigned)p.blocks, (unsigned)(p.rows / kJoinRows)), kJoinThreads, 0,
                      (cudaStream_t)stream, a, p.rows, p.channels, kAttnWeightUnit);

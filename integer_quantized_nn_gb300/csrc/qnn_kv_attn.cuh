@@ -54,6 +54,52 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic)
+{
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "r"(mask), "r"(magic));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+// f16 magic numbers: 0x6400 | u is 1024 + u; for the upper half of a byte 1024 + 16 u, of which
+// a sixteenth is 64 + u.
+constexpr uint32_t kMagic = 0x64006400u, kOne = 0x3c003c00u, kSixteenth = 0x2c002c00u;
+constexpr uint32_t k1152 = 0x64806480u;
+
+// Four s8 codes (as q + 128) of a row to two registers of neighbouring pairs.
+__device__ __forceinline__ void s8_pairs(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    lo = hsub2_u32(prmt(w, kMagic, 0x7150), k1152);
+    hi = hsub2_u32(prmt(w, kMagic, 0x7352), k1152);
+}
+
+struct Zero {
+    uint32_t lo, hi;  // -(1024 + z), -(64 + z)
+};
+
+__device__ __forceinline__ Zero zero_of(uint32_t z0, uint32_t z1)
+{
+    const uint32_t z = z0 | z1 << 16;
+    return {0xe400e400u + z, 0xd400d400u + (z << 4)};
+}
+
+// The halves' four 4-bit codes each, less their zero points, as four registers.
+__device__ __forceinline__ void u4_pairs(uint32_t w, const Zero &z, uint32_t (&r)[4])
+{
+    const uint32_t v = w >> 8;
+    r[0] = fma2(and_or(w, 0x000f000fu, kMagic), kOne, z.lo);
+    r[1] = fma2(and_or(w, 0x00f000f0u, kMagic), kSixteenth, z.hi);
+    r[2] = fma2(and_or(v, 0x000f000fu, kMagic), kOne, z.lo);
+    r[3] = fma2(and_or(v, 0x00f000f0u, kMagic), kSixteenth, z.hi);
+}
+
 // 2^k as fp32, -126 <= k <= 127
 __device__ __forceinline__ float pow2i(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
 
@@ -238,6 +284,8 @@ struct AttnPlan {
 };
 
 AttnPlan attn_few_plan(const KvArgs &c, int group);
+AttnPlan attn_rows_plan(const KvArgs &c, int group);
+qnn_status launch_attn_rows(const KvAttnArgs &a, const AttnPlan &p, bool u4, cudaStream_t s);
 qnn_status launch_attn_few(const KvAttnArgs &a, const AttnPlan &p, bool u4, cudaStream_t s);
 
 }  // namespace qnn

@@ -1,0 +1,594 @@
+// qnn_kv_attn_rows.cu -- q_kv_attn for many rows of a head of the cache: trees of drafted tokens
+// and chunks of prompts, 128 rows (the heads of q that share a head of the cache, times newest
+// tokens) at a time on the 5th-generation tensor cores.
+//
+//   S = Q K^T,  P = e^(S - m),  O += P V
+// for chunks of 128 tokens.  Even and odd chunks are two streams with a maximum, a sum and an O of
+// their own (S and O of both fill tensor memory), which meet where an item ends: while the rows'
+// warps of one stream make P of a chunk, the tensor cores work on the other's.
+//
+// Roles of a block's warps:
+//   0       copies: codes of K and V of 128 tokens at a time, page by page, to a ring
+//   1       MMA: S of a chunk, then O of the same stream's chunk before ... in order
+//   2       scales: of K for the scores, of V over a unit for the weights
+//   4..7    codes: a token's row each, codes -> f16 integers -> the swizzled operand tiles, for K
+//           (K-major) and V (N-major) the same image
+//   8..15   rows: a row of S each, in tensor memory -> weights as f16 over it; the other way for O
+//           when a maximum has moved by more than 2^8 or the unit has grown
+#include "qnn_kv_attn.cuh"
+
+namespace qnn {
+namespace {
+
+constexpr int kRows = 128, kTokens = kAttnChunk, kThreads = 512, kInfos = 4, kMaxStages = 6;
+constexpr int kCodeWarp0 = 4, kCodeWarps = 4, kRowWarp0 = 8, kRowWarps = 8;
+constexpr uint32_t kTmemCols = 512, kOCol = 256;  // S of both streams, then O
+
+// Of a chunk: scales of K, and of V over the stream's unit, for each token.
+struct Info {
+    float k[kTokens], v[kTokens];
+    float ratio, unit;  // the unit before over this one; this one
+    uint32_t present;   // 16-token tiles that are there
+    uint32_t pad;
+};
+
+// f16 operands, A from tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// The tile image as an operand whose rows are K: 64 of N (128 bytes) a row, 8 rows an atom of the
+// 128-byte swizzle; the next 8 rows follow, the next 64 of N are `panel` bytes on.
+__device__ __forceinline__ uint64_t sdesc_n_major(uint32_t addr, uint32_t panel)
+{
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)((panel >> 4) & 0x3FFFu) << 16 | (uint64_t)(1024u >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// the lowest n bits, n from 0 (or below) to 32 (or above)
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; }
+
+// Which of positions p0 .. p0 + 31 the row of newest token t sees.
+__device__ __forceinline__ uint32_t seen_bits(const KvAttnArgs &a, const AttnCursor &c, int t, int p0)
+{
+    const int base = c.len - c.T;
+    if (!a.mask) return low_bits(min(c.len, base + t + 1) - p0);
+    const int j0 = p0 - base, w = j0 >> 5;
+    const uint32_t *m = a.mask + (c.first + t) * a.mask_words;
+    const uint32_t lo = w >= 0 && w < a.mask_words ? m[w] : 0u, hi = w + 1 >= 0 && w + 1 < a.mask_words ? m[w + 1] : 0u;
+    return (low_bits(-j0) | __funnelshift_r(lo, hi, j0 & 31)) & low_bits(c.len - p0);
+}
+
+template <bool U4, int DP>
+__global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_constant__ KvAttnArgs a)
+{
+    constexpr uint32_t PANEL = kTokens * 128, TILE = PANEL * (DP / 64);
+    const KvArgs &c = a.c;
+    extern __shared__ __align__(16) uint8_t raw[];
+    __shared__ __align__(8) uint64_t code_full[kMaxStages], code_empty[kMaxStages], tile_full[4], tile_empty[4],
+        info_full[kInfos], info_empty[kInfos], s_full[2], p_ready[2], q_full, o_full, mma_end;
+    __shared__ __align__(16) Info infos[kInfos];
+    __shared__ float row_m[2][kRows], row_l[2][kRows], row_top[2][kRows], stream_unit[2];
+    __shared__ uint32_t present[kMaxStages], tmem_slot;
+    uint8_t *smem = raw + (-smem_u32(raw) & 1023u);  // the swizzle's atoms
+    // tiles: K of even and odd chunks, V of both; q; codes; the sums of the line
+    const uint32_t tiles = smem_u32(smem), q_tile = tiles + 4 * TILE, codes = q_tile + TILE;
+    const int ST = a.stages, code_bytes = kTokens * (c.row_bytes + 4);
+    int64_t *sums = reinterpret_cast<int64_t *>(smem + 5 * TILE + ST * code_bytes);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(smem_u32(&code_full[i]), 1);
+            mbar_init(smem_u32(&code_empty[i]), kCodeWarps + 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(smem_u32(&tile_full[i]), kCodeWarps);
+            mbar_init(smem_u32(&tile_empty[i]), 1);
+        }
+        for (int i = 0; i < kInfos; ++i) {
+            mbar_init(smem_u32(&info_full[i]), 1);
+            mbar_init(smem_u32(&info_empty[i]), kRowWarps / 2);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&s_full[i]), 1);
+            mbar_init(smem_u32(&p_ready[i]), kRowWarps / 2);
+        }
+        mbar_init(smem_u32(&q_full), kRowWarps);
+        mbar_init(smem_u32(&o_full), 1);
+        mbar_init(smem_u32(&mma_end), 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    // only now: a block of the next grid that took tensor memory first and waited for this grid
+    // would keep it from blocks of this one
+    grid_dependency_launch();
+    grid_dependency_wait();
+
+    const AttnShare share(attn_sums<kThreads>(a, sums, kRows), a.blocks, blockIdx.x);
+    int *record = reinterpret_cast<int *>(a.ws) + blockIdx.x * kAttnRecord;
+    if (threadIdx.x == 0 && share.from >= share.to) record[0] = 0;
+    const int chunks = (int)(share.to - share.from);
+
+    bool ok = true;
+    auto wait = [&](uint64_t &bar, int use) {  // the use-th phase of a barrier, by a whole warp
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_idle(smem_u32(&bar), (uint32_t)use & 1u, c.status));
+        return ok;
+    };
+
+    AttnCursor at;
+    if (chunks > 0) at.find(a, sums, share.from, kRows);
+    if (chunks <= 0) {
+    } else if (warp == 0) {
+        int page = -1, in_page = 0, asked = 0;
+        auto look_up = [&]() {
+            const int tile = at.chunk * (kTokens / 16) + lane;
+            page = -1;
+            if (lane < kTokens / 16 && tile * 16 < at.len) page = attn_page(a, at.b, tile, &in_page);
+        };
+        look_up();
+        for (int n = 0; n < chunks && ok; ++n) {
+            const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+            const int rows = 16 * c.row_bytes, all = c.page * c.row_bytes;
+            const uint8_t *head = c.pages + page * c.page_bytes + (int64_t)at.h * c.head_bytes;
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                const int stage = asked % ST, use = asked / ST;
+                if (use > 0 && !wait(code_empty[stage], use - 1)) break;
+                const uint32_t to = codes + stage * code_bytes, bar = smem_u32(&code_full[stage]);
+                if (lane == 0) {
+                    present[stage] = there;
+                    mbar_arrive_expect_tx(bar, __popc(there) * (rows + 64));
+                }
+                __syncwarp();
+                if (page >= 0) {
+                    bulk_g2s(to + lane * rows, head + o * all + in_page * rows, rows, bar);
+                    bulk_g2s(to + kTokens * c.row_bytes + lane * 64, head + 2 * all + o * 4 * c.page + in_page * 64, 64, bar);
+                }
+                ++asked;
+            }
+            if (n + 1 < chunks) {
+                at.next(a, kRows);
+                look_up();
+            }
+        }
+        // nothing that was asked for is in flight when the block ends
+        for (int s = 0; s < min(ST, asked); ++s)
+            (void)mbar_wait_idle(smem_u32(&code_full[s]), (uint32_t)((asked - 1 - s) / ST) & 1u, c.status);
+    } else if (warp == 1) {
+        const uint32_t idesc_s = idesc_f32acc(0, 0, kRows, kTokens);
+        const uint32_t idesc_o = idesc_f32acc(0, 0, kRows, 0) | (uint32_t)(c.D >> 3) << 17 | 1u << 16;  // B is N-major
+        const int steps = c.D / 16;
+        auto scores = [&](int n) {
+            const int slot = n & 1;
+            if (!wait(tile_full[slot], n >> 1)) return;
+            tc_fence_after();
+            if (lane == 0) {
+                const uint64_t qd = sdesc_sw128(q_tile), kd = sdesc_sw128(tiles + slot * TILE);
+                for (int s = 0; s < steps; ++s) {
+                    const uint64_t off = (uint64_t)((s >> 2) * (PANEL >> 4) + (s & 3) * 2);
+                    mma_f16_ss(tmem + slot * kTokens, qd + off, kd + off, idesc_s, s > 0);
+                }
+                mma_commit(smem_u32(&tile_empty[slot]));
+                mma_commit(smem_u32(&s_full[slot]));
+            }
+            __syncwarp();
+        };
+        int n = 0, item = 0;
+        while (n < chunks && ok) {
+            const int count = min(at.units - at.chunk, chunks - n);
+            if (!wait(q_full, item)) break;
+            for (int i = 0; i < 2 && i < count; ++i) scores(n + i);
+            for (int i = 0; i < count && ok; ++i) {
+                const int m = n + i, slot = m & 1;
+                if (!wait(p_ready[slot], m >> 1) || !wait(tile_full[2 + slot], m >> 1)) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t vd = sdesc_n_major(tiles + (2 + slot) * TILE, PANEL);
+                    const uint32_t p = tmem + slot * kTokens, o = tmem + kOCol + slot * 128;
+#pragma unroll
+                    for (int s = 0; s < kTokens / 16; ++s)
+                        mma_ts(o, p + 8 * s, vd + (uint64_t)s * (2048 >> 4), idesc_o, i >= 2 || s > 0);
+                    mma_commit(smem_u32(&tile_empty[2 + slot]));
+                }
+                __syncwarp();
+                if (i + 2 < count) scores(m + 2);
+            }
+            if (ok && lane == 0) mma_commit(smem_u32(&o_full));
+            __syncwarp();
+            n += count;
+            ++item;
+            at.chunk = at.units - 1;
+            at.next(a, kRows);
+        }
+        // nothing of this thread's is in flight when the block ends
+        if (lane == 0) {
+            mma_commit(smem_u32(&mma_end));
+            (void)mbar_wait_idle(smem_u32(&mma_end), 0, c.status);
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        float unit[2] = {0.0f, 0.0f};
+        for (int n = 0; n < chunks && ok; ++n) {
+            if (n == 0 || at.chunk == 0) unit[0] = unit[1] = pow2i(-126);
+            Info &info = infos[n % kInfos];
+            if (n >= kInfos && !wait(info_empty[n % kInfos], n / kInfos - 1)) break;
+            const int pos = at.chunk * kTokens + 4 * lane;
+            uint32_t there = 0;
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                const int q = 2 * n + o, stage = q % ST;
+                if (!wait(code_full[stage], q / ST)) break;
+                there = *reinterpret_cast<volatile uint32_t *>(&present[stage]);
+                const uint4 w = lds_v4(codes + stage * code_bytes + kTokens * c.row_bytes + 16 * lane);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&code_empty[stage]));
+                float s[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (U4) s[e] = __uint_as_float(__float_as_uint(s[e]) & 0xffff0000u);
+                    // beyond the sequence the words are anything
+                    if (!(there >> (lane / 4) & 1u) || pos + e >= at.len) s[e] = 0.0f;
+                }
+                if (o == 0) {
+                    *reinterpret_cast<float4 *>(info.k + 4 * lane) = make_float4(s[0], s[1], s[2], s[3]);
+                } else {
+                    uint32_t top = __float_as_uint(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])));
+                    top = __reduce_max_sync(0xffffffffu, top);
+                    const float old = n & 1 ? unit[1] : unit[0];
+                    const float now = fmaxf(old, __uint_as_float((top + 0x7fffffu) & 0xff800000u));
+                    const float per = __uint_as_float(0x7f000000u - __float_as_uint(now));
+                    if (n & 1) unit[1] = now;
+                    else unit[0] = now;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[e] = s[e] * per * (float)(1 << kAttnRoom);
+                    *reinterpret_cast<float4 *>(info.v + 4 * lane) = make_float4(s[0], s[1], s[2], s[3]);
+                    if (lane == 0) info.ratio = old * per, info.unit = now, info.present = there;
+                }
+            }
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(smem_u32(&info_full[n % kInfos]));
+            if (n + 1 < chunks) at.next(a, kRows);
+        }
+    } else if (warp >= kCodeWarp0 && warp < kCodeWarp0 + kCodeWarps) {
+        const int t = threadIdx.x - kCodeWarp0 * 32;
+        for (int n = 0; n < chunks && ok; ++n) {
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                const int q = 2 * n + o, stage = q % ST, slot = 2 * o + (n & 1);
+                if (n >= 2 && !wait(tile_empty[slot], (n >> 1) - 1)) break;
+                if (!wait(code_full[stage], q / ST)) break;
+                const uint32_t from = codes + stage * code_bytes, row = from + t * c.row_bytes;
+                const uint32_t to = tiles + slot * TILE + t * 128;
+                auto put = [&](int chunk, const uint32_t (&f)[4]) {  // chunk of 8 f16
+                    sts_v4(to + (chunk >> 3) * PANEL + (((chunk & 7) ^ (t & 7)) << 4), f[0], f[1], f[2], f[3]);
+                };
+                if constexpr (U4) {
+                    uint32_t word;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(word) : "r"(from + kTokens * c.row_bytes + 4 * t) : "memory");
+                    const Zero z = zero_of(word & 15u, word & 15u);
+#pragma unroll 2
+                    for (int ch = 0; ch < c.chunks; ++ch) {
+                        const uint4 w = lds_v4(row + 16 * kv_chunk(c.chunks, t, ch));
+                        uint32_t f[4];
+                        u4_pairs(w.x, z, f), put(4 * ch, f);
+                        u4_pairs(w.y, z, f), put(4 * ch + 1, f);
+                        u4_pairs(w.z, z, f), put(4 * ch + 2, f);
+                        u4_pairs(w.w, z, f), put(4 * ch + 3, f);
+                    }
+                } else {
+#pragma unroll 4
+                    for (int ch = 0; ch < c.chunks; ++ch) {
+                        const uint4 w = lds_v4(row + 16 * kv_chunk(c.chunks, t, ch));
+                        uint32_t f[4];
+                        s8_pairs(w.x, f[0], f[1]), s8_pairs(w.y, f[2], f[3]), put(2 * ch, f);
+                        s8_pairs(w.z, f[0], f[1]), s8_pairs(w.w, f[2], f[3]), put(2 * ch + 1, f);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&tile_full[slot]));
+                    mbar_arrive(smem_u32(&code_empty[stage]));
+                }
+            }
+        }
+    } else if (warp >= kRowWarp0) {
+        const int stream = (warp - kRowWarp0) >> 2, r = (threadIdx.x - kRowWarp0 * 32) & 127;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        auto meet = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+        int n = 0, item = 0;
+        while (n < chunks) {
+            const int count = min(at.units - at.chunk, chunks - n), row0 = at.rt * kRows;
+            const int width = (int)min((int64_t)kRows, (int64_t)at.T * a.group - row0);
+            const int rr = row0 + r, t = min(rr / a.group, at.T - 1);
+            const int t_first = row0 / a.group;
+            const bool live = r < width, starts_here = n > 0 || at.chunk == 0, ends_here = at.chunk + count == at.units;
+            if (threadIdx.x == kRowWarp0 * 32 && n + count == chunks) {
+                record[0] = starts_here && !ends_here;
+                record[1] = at.b, record[2] = at.rt, record[3] = at.h;
+                if (!ends_here) record[4] = share.block_of(share.from + n - at.chunk + at.units - 1);
+            }
+            const int64_t out_row = at.first + rr / a.group;
+            const int hq = at.h * a.group + rr % a.group;
+
+            // q: half a row for each thread; a row's largest value is brought near f16's by a power of two
+            float cq;
+            {
+                const int half = c.D / 2;  // a multiple of 16
+                const uint16_t *qp = static_cast<const uint16_t *>(a.q) + out_row * a.ld_q + (int64_t)hq * c.D + stream * half;
+                uint4 w[DP / 16];
+                float top = 0.0f;
+#pragma unroll
+                for (int i = 0; i < DP / 16; ++i) {
+                    w[i] = make_uint4(0, 0, 0, 0);
+                    if (live && 8 * i < half)
+                        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                                     : "l"(qp + 8 * i));
+                }
+                auto value = [&](uint32_t v, int hi) {
+                    const uint32_t h = hi ? v >> 16 : v & 0xffffu;
+                    return a.bf16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((uint16_t)h));
+                };
+#pragma unroll
+                for (int i = 0; i < DP / 16; ++i) {
+                    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(value(u[e / 2], e & 1)));
+                }
+                row_top[stream][r] = top;
+                meet();
+                top = fmaxf(row_top[0][r], row_top[1][r]);
+                const int e2 = (int)(__float_as_uint(top) >> 23);
+                const int k = top == 0.0f || e2 == 255 ? 0 : max(-126, min(126, 14 + 127 - e2));
+                const float up = a.scale_log2 < 0.0f ? -pow2i(k) : pow2i(k);  // cq >= 0
+                cq = fabsf(a.scale_log2) * pow2i(-k);
+#pragma unroll
+                for (int i = 0; i < DP / 16; ++i) {
+                    if (8 * i >= half) break;
+                    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                    uint32_t f[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        // the order in which codes are unpacked: u4 0 4, 1 5, 2 6, 3 7
+                        const float lo = U4 ? value(u[e / 2], e & 1) : value(u[e], 0);
+                        const float hi = U4 ? value(u[2 + e / 2], e & 1) : value(u[e], 1);
+                        const __half2 h = __floats2half2_rn(lo * up, hi * up);
+                        f[e] = *reinterpret_cast<const uint32_t *>(&h);
+                    }
+                    const int chunk = stream * (half / 8) + i;
+                    sts_v4(q_tile + (chunk >> 3) * PANEL + r * 128 + (((chunk & 7) ^ (r & 7)) << 4), f[0], f[1], f[2], f[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&q_full));
+            }
+
+            float m = -INFINITY, ref = 0.0f, l = 0.0f, unit = pow2i(-126);
+            bool first = true;
+            const int seen_by_all = a.mask ? at.len - at.T : min(at.len, at.len - at.T + t_first + 1);
+            for (int i = (n ^ stream) & 1; i < count; i += 2) {
+                const int x = n + i, slot = x % kInfos;
+                const Info &info = infos[slot];
+                if (!wait(info_full[slot], x / kInfos) || !wait(s_full[stream], x >> 1)) break;
+                tc_fence_after();
+                const uint32_t s_at = lanes + stream * kTokens;
+                const int pos0 = (at.chunk + i) * kTokens;
+                const uint32_t there = info.present;
+                const bool whole = pos0 + kTokens <= seen_by_all && there == 0xffu;
+                const float ratio = info.ratio;
+                unit = info.unit;
+                uint32_t bits[4];
+                if (!whole) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        bits[b] = seen_bits(a, at, t, pos0 + 32 * b) &
+                                  ((there >> (2 * b) & 1u ? 0xffffu : 0u) | (there >> (2 * b + 1) & 1u ? 0xffff0000u : 0u));
+                    __syncwarp();
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t v[32];
+                    tmem_ld32(s_at + 32 * b, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 k = *reinterpret_cast<const float4 *>(info.k + 32 * b + e);
+                        const float y[4] = {__uint_as_float(v[e]) * k.x, __uint_as_float(v[e + 1]) * k.y,
+                                            __uint_as_float(v[e + 2]) * k.z, __uint_as_float(v[e + 3]) * k.w};
+#pragma unroll
+                        for (int d = 0; d < 4; ++d)
+                            if (whole || (bits[b] >> (e + d) & 1u)) top = fmaxf(top, y[d]);
+                    }
+                }
+                top = top == -INFINITY ? top : top * cq;
+                if (__any_sync(0xffffffffu, top > m + kAttnSlack || ratio != 1.0f)) {
+                    const float up = fmaxf(m, top), f = m == -INFINITY ? 0.0f : ex2(m - up);
+                    m = up;
+                    ref = up == -INFINITY ? 0.0f : up;
+                    l *= f;
+                    if (!first) {
+                        const uint32_t o_at = lanes + kOCol + stream * 128;
+                        const float g = f * ratio;
+                        for (int b = 0; b < DP / 32; ++b) {
+                            uint32_t v[32];
+                            tmem_ld32(o_at + 32 * b, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * g);
+                            tmem_st32(o_at + 32 * b, v);
+                        }
+                    }
+                }
+                first = false;
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t v[32], p[16];
+                    tmem_ld32(s_at + 32 * b, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 k = *reinterpret_cast<const float4 *>(info.k + 32 * b + e);
+                        const float4 w = *reinterpret_cast<const float4 *>(info.v + 32 * b + e);
+                        const float ks[4] = {k.x, k.y, k.z, k.w}, ws[4] = {w.x, w.y, w.z, w.w};
+                        float y[4];
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) {
+                            y[d] = ex2(__fmaf_rn(__uint_as_float(v[e + d]) * ks[d], cq, -ref));
+                            if (!whole && !(bits[b] >> (e + d) & 1u)) y[d] = 0.0f;
+                            sum[d] += y[d];
+                            y[d] *= ws[d];
+                        }
+                        const __half2 lo = __floats2half2_rn(y[0], y[1]), hi = __floats2half2_rn(y[2], y[3]);
+                        p[e / 2] = *reinterpret_cast<const uint32_t *>(&lo);
+                        p[e / 2 + 1] = *reinterpret_cast<const uint32_t *>(&hi);
+                    }
+                    tmem_st16(s_at + 16 * b, p);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&p_ready[stream]));
+                    mbar_arrive(smem_u32(&info_empty[slot]));
+                }
+            }
+
+            // the two streams meet
+            row_m[stream][r] = m;
+            row_l[stream][r] = l;
+            if (r == 0) stream_unit[stream] = unit;
+            (void)wait(o_full, item);
+            tc_fence_after();
+            meet();
+            {
+                const float m0 = row_m[0][r], m1 = row_m[1][r], up = fmaxf(m0, m1);
+                const float f0 = m0 == up ? 1.0f : ex2(m0 - up), f1 = m1 == up ? 1.0f : ex2(m1 - up);
+                const float total = __fmaf_rn(row_l[0][r], f0, row_l[1][r] * f1);
+                const float top_unit = fmaxf(stream_unit[0], stream_unit[1]);
+                const float per = __uint_as_float(0x7f000000u - __float_as_uint(top_unit));
+                const bool has0 = count > 1 || !(n & 1), has1 = count > 1 || (n & 1);
+                const float g0 = f0 * (stream_unit[0] * per), g1 = f1 * (stream_unit[1] * per);
+                const bool done = starts_here && ends_here;
+                float *slot = attn_slot(a, blockIdx.x, starts_here ? 1 : 0, kRows, DP);
+                uint16_t *out = static_cast<uint16_t *>(a.out) + out_row * a.ld_out + (int64_t)hq * c.D;
+                const float weight = top_unit * kAttnWeightUnit;
+                // blocks of 32 channels, in turn for the two streams' threads
+                for (int b = stream; b < c.D / 32; b += 2) {
+                    float o[32];
+                    __syncwarp();
+                    {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+                        if (has0) {
+                            tmem_ld32(lanes + kOCol + 32 * b, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(v[e]) * g0;
+                        }
+                        if (has1) {
+                            tmem_ld32(lanes + kOCol + 128 + 32 * b, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __fmaf_rn(__uint_as_float(v[e]), g1, o[e]);
+                        }
+                    }
+                    if (!live || !ok) continue;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = o[8 * i + (U4 ? 2 * (e & 3) + (e >> 2) : e)];
+                        const int d = 32 * b + 8 * i;
+                        if (done) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[e] = total == 0.0f ? 0.0f : v[e] / total * weight;
+                            *reinterpret_cast<uint4 *>(out + d) = make_uint4(attn_pack(a, v[0], v[1]), attn_pack(a, v[2], v[3]),
+                                                                            attn_pack(a, v[4], v[5]), attn_pack(a, v[6], v[7]));
+                        } else {
+                            float4 *to = reinterpret_cast<float4 *>(slot + r * DP + d);
+                            to[0] = make_float4(v[0], v[1], v[2], v[3]);
+                            to[1] = make_float4(v[4], v[5], v[6], v[7]);
+                        }
+                    }
+                }
+                if (live && ok && stream == 0) {
+                    if (done) {
+                        if (a.lse) a.lse[out_row * a.heads_q + hq] = attn_lse(up, total);
+                    } else {
+                        slot[kRows * DP + 2 * r] = up, slot[kRows * DP + 2 * r + 1] = total;
+                        if (r == 0) slot[kRows * (DP + 2)] = top_unit;
+                    }
+                }
+            }
+            tc_fence_before();  // O has been read before q_full says so
+            meet();
+            n += count;
+            ++item;
+            at.chunk = at.units - 1;
+            at.next(a, kRows);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <bool U4, int DP>
+qnn_status launch(KvAttnArgs a, cudaStream_t s)
+{
+    auto kern = kv_attn_rows_kernel<U4, DP>;
+    static std::atomic<uint64_t> opted_in{0};
+    constexpr int kStatic = 9 << 10, kMost = (227 << 10) - kStatic;
+    const int fixed = 1024 + 5 * kTokens * DP * 2 + (a.c.batch + 1) * 8, stage = kTokens * (a.c.row_bytes + 4);
+    a.stages = std::min(kMaxStages, (kMost - fixed) / stage);
+    if (!opt_in_smem(kern, kMost, opted_in, 100)) return QNN_ERR_CUDA;
+    return kv_launch(kern, dim3((unsigned)a.blocks), kThreads, fixed + a.stages * stage, s, a);
+}
+
+}  // namespace
+
+AttnPlan attn_rows_plan(const KvArgs &c, int)
+{
+    return {kRows, c.D <= 64 ? 64 : 128, std::min(kAttnMaxBlocks, sm_count())};
+}
+
+qnn_status launch_attn_rows(const KvAttnArgs &a, const AttnPlan &p, bool u4, cudaStream_t s)
+{
+    if (p.channels == 64) return u4 ? launch<true, 64>(a, s) : launch<false, 64>(a, s);
+    return u4 ? launch<true, 128>(a, s) : launch<false, 128>(a, s);
+}
+
+}  // namespace qnn
