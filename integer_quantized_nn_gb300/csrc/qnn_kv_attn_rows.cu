@@ -43,16 +43,60 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b_d
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
+// Tensor memory as fragments: 16 lanes; registers 4 i .. 4 i + 3 of thread 4 g + j are row g, columns
+// 8 i + 2 j and + 1, then the same of row g + 8 (16x256b); register 2 i + h is row g + 8 h, column
+// 4 i + j (16x128b): two f16 of the first are one word of the second.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[64])
 {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "tcgen05.ld.sync.aligned.16x256b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 "
+        "[%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+          "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_pairs(uint32_t taddr, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x16.b32 "
+        "[%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
         "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+          "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+          "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+          "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
 
@@ -76,6 +120,95 @@ __device__ __forceinline__ uint32_t seen_bits(const KvAttnArgs &a, const AttnCur
     const uint32_t *m = a.mask + (c.first + t) * a.mask_words;
     const uint32_t lo = w >= 0 && w < a.mask_words ? m[w] : 0u, hi = w + 1 >= 0 && w + 1 < a.mask_words ? m[w + 1] : 0u;
     return (low_bits(-j0) | __funnelshift_r(lo, hi, j0 & 31)) & low_bits(c.len - p0);
+}
+
+// A warp's 32 rows of S of a chunk -> P over it.  A thread has 4 rows and the columns 8 i + 2 j and + 1 of each:
+// with a row to a thread each would read all scales of the chunk from shared memory, 1500 cycles
+// of its bandwidth a chunk; so it is a quarter.  ks, vs: scales of the thread's columns; bits: lane
+// t has those of the positions that row t sees.
+template <bool MASKED, int DP>
+__device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, const float *ks, const float *vs,
+                                        const uint32_t (&bits)[4], int j, bool first, float ratio, const float (&cr)[4],
+                                        float (&m)[4], float (&ref)[4], float (&l)[4])
+{
+    const int g = (threadIdx.x & 31) >> 2;
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+        const uint32_t down = (uint32_t)(16 * half) << 16;
+        uint32_t v[64];
+        tmem_ld_frag(s_at + down, v);
+        tmem_ld_wait();
+        // by selection and not by index: the arrays stay in registers
+        const float c0 = half ? cr[2] : cr[0], c1 = half ? cr[3] : cr[1];
+        float m0 = half ? m[2] : m[0], m1 = half ? m[3] : m[1], r0 = half ? ref[2] : ref[0], r1 = half ? ref[3] : ref[1];
+        float l0 = half ? l[2] : l[0], l1 = half ? l[3] : l[1], top0 = -INFINITY, top1 = -INFINITY;
+        uint32_t b0[4], b1[4];
+        if constexpr (MASKED) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                b0[b] = __shfl_sync(0xffffffffu, bits[b], 16 * half + g) >> (2 * j);
+                b1[b] = __shfl_sync(0xffffffffu, bits[b], 16 * half + 8 + g) >> (2 * j);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 k = *reinterpret_cast<const float2 *>(ks + 8 * i);
+            float2 y0 = mul2(as_f2(v[4 * i], v[4 * i + 1]), k), y1 = mul2(as_f2(v[4 * i + 2], v[4 * i + 3]), k);
+            if constexpr (MASKED) {
+                const uint32_t bit = 1u << (8 * (i & 3));
+                y0.x = b0[i >> 2] & bit ? y0.x : -INFINITY, y0.y = b0[i >> 2] & (2 * bit) ? y0.y : -INFINITY;
+                y1.x = b1[i >> 2] & bit ? y1.x : -INFINITY, y1.y = b1[i >> 2] & (2 * bit) ? y1.y : -INFINITY;
+            }
+            top0 = max3(top0, y0.x, y0.y), top1 = max3(top1, y1.x, y1.y);
+            v[4 * i] = __float_as_uint(y0.x), v[4 * i + 1] = __float_as_uint(y0.y);
+            v[4 * i + 2] = __float_as_uint(y1.x), v[4 * i + 3] = __float_as_uint(y1.y);
+        }
+        top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 1)), top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
+        top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 2)), top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 2));
+        if (top0 != -INFINITY) top0 *= c0;
+        if (top1 != -INFINITY) top1 *= c1;
+        if (__any_sync(0xffffffffu, top0 > m0 + kAttnSlack || top1 > m1 + kAttnSlack || ratio != 1.0f)) {
+            const float u0 = fmaxf(m0, top0), u1 = fmaxf(m1, top1);
+            float f0 = m0 == -INFINITY ? 0.0f : ex2(m0 - u0), f1 = m1 == -INFINITY ? 0.0f : ex2(m1 - u1);
+            m0 = u0, m1 = u1;
+            r0 = u0 == -INFINITY ? 0.0f : u0, r1 = u1 == -INFINITY ? 0.0f : u1;
+            l0 *= f0, l1 *= f1, f0 *= ratio, f1 *= ratio;
+            if (!first) {
+#pragma unroll 1
+                for (int b = 0; b < DP / 32; ++b) {
+                    uint32_t o[16];
+                    tmem_ld_frag(o_at + down + 32 * b, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (e & 2 ? f1 : f0));
+                    tmem_st_frag(o_at + down + 32 * b, o);
+                }
+            }
+        }
+        uint32_t p[32];
+        float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
+        const float2 cc0 = make_float2(c0, c0), cc1 = make_float2(c1, c1), n0 = make_float2(-r0, -r0), n1 = make_float2(-r1, -r1);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 w = *reinterpret_cast<const float2 *>(vs + 8 * i);
+            float2 y0 = fma2(as_f2(v[4 * i], v[4 * i + 1]), cc0, n0), y1 = fma2(as_f2(v[4 * i + 2], v[4 * i + 3]), cc1, n1);
+            y0.x = ex2(y0.x), y0.y = ex2(y0.y), y1.x = ex2(y1.x), y1.y = ex2(y1.y);
+            if constexpr (MASKED) {  // -inf times a scale of zero is not
+                const uint32_t bit = 1u << (8 * (i & 3));
+                y0.x = b0[i >> 2] & bit ? y0.x : 0.0f, y0.y = b0[i >> 2] & (2 * bit) ? y0.y : 0.0f;
+                y1.x = b1[i >> 2] & bit ? y1.x : 0.0f, y1.y = b1[i >> 2] & (2 * bit) ? y1.y : 0.0f;
+            }
+            s0 = add2(s0, y0), s1 = add2(s1, y1);
+            y0 = mul2(y0, w), y1 = mul2(y1, w);
+            const __half2 h0 = __floats2half2_rn(y0.x, y0.y), h1 = __floats2half2_rn(y1.x, y1.y);
+            p[2 * i] = *reinterpret_cast<const uint32_t *>(&h0);
+            p[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&h1);
+        }
+        tmem_st_pairs(s_at + down, p);
+        l0 += s0.x + s0.y, l1 += s1.x + s1.y;
+        if (half) m[2] = m0, m[3] = m1, ref[2] = r0, ref[3] = r1, l[2] = l0, l[3] = l1;
+        else m[0] = m0, m[1] = m1, ref[0] = r0, ref[1] = r1, l[0] = l0, l[1] = l1;
+    }
 }
 
 template <bool U4, int DP>
@@ -142,6 +275,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         return ok;
     };
 
+    // 128 registers a thread at the launch, and as many after: 80 + 80 + 2 * 176 = 4 * 128
+    if (warp < kCodeWarp0) {
+    regs_dec<80>();
     AttnCursor at;
     if (chunks > 0) at.find(a, sums, share.from, kRows);
     if (chunks <= 0) {
@@ -276,7 +412,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             if (ok && lane == 0) mbar_arrive(smem_u32(&info_full[n % kInfos]));
             if (n + 1 < chunks) at.next(a, kRows);
         }
-    } else if (warp >= kCodeWarp0 && warp < kCodeWarp0 + kCodeWarps) {
+    }
+    } else if (warp < kRowWarp0) {
+        regs_dec<80>();
         const int t = threadIdx.x - kCodeWarp0 * 32;
         for (int n = 0; n < chunks && ok; ++n) {
 #pragma unroll
@@ -319,8 +457,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 }
             }
         }
-    } else if (warp >= kRowWarp0) {
+    } else {
+        regs_inc<176>();
+        AttnCursor at;
+        if (chunks > 0) at.find(a, sums, share.from, kRows);
         const int stream = (warp - kRowWarp0) >> 2, r = (threadIdx.x - kRowWarp0 * 32) & 127;
+        const int g = lane >> 2, j = lane & 3;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         auto meet = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
         int n = 0, item = 0;
@@ -391,90 +533,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 if (lane == 0) mbar_arrive(smem_u32(&q_full));
             }
 
-            float m = -INFINITY, ref = 0.0f, l = 0.0f, unit = pow2i(-126);
+            // rows of this thread: of q = 0 .. 3, 16 (q / 2) + 8 (q % 2) + g of the warp's 32
+            float cr[4], m[4], ref[4], l[4], unit = pow2i(-126);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                cr[q] = __shfl_sync(0xffffffffu, cq, 16 * (q >> 1) + 8 * (q & 1) + g);
+                m[q] = -INFINITY;
+                ref[q] = l[q] = 0.0f;
+            }
             bool first = true;
             const int seen_by_all = a.mask ? at.len - at.T : min(at.len, at.len - at.T + t_first + 1);
             for (int i = (n ^ stream) & 1; i < count; i += 2) {
                 const int x = n + i, slot = x % kInfos;
-                const Info &info = infos[slot];
                 if (!wait(info_full[slot], x / kInfos) || !wait(s_full[stream], x >> 1)) break;
                 tc_fence_after();
-                const uint32_t s_at = lanes + stream * kTokens;
                 const int pos0 = (at.chunk + i) * kTokens;
-                const uint32_t there = info.present;
-                const bool whole = pos0 + kTokens <= seen_by_all && there == 0xffu;
-                const float ratio = info.ratio;
-                unit = info.unit;
-                uint32_t bits[4];
-                if (!whole) {
+                const uint32_t there = infos[slot].present;
+                const float ratio = infos[slot].ratio;
+                unit = infos[slot].unit;
+                const float *ks = infos[slot].k + 2 * j, *vs = infos[slot].v + 2 * j;
+                const uint32_t s_at = lanes + stream * kTokens, o_at = lanes + kOCol + stream * 128;
+                if (pos0 + kTokens <= seen_by_all && there == 0xffu) {
+                    const uint32_t none[4] = {};
+                    weights<false, DP>(s_at, o_at, ks, vs, none, j, first, ratio, cr, m, ref, l);
+                } else {
+                    uint32_t bits[4];
 #pragma unroll
                     for (int b = 0; b < 4; ++b)
                         bits[b] = seen_bits(a, at, t, pos0 + 32 * b) &
                                   ((there >> (2 * b) & 1u ? 0xffffu : 0u) | (there >> (2 * b + 1) & 1u ? 0xffff0000u : 0u));
                     __syncwarp();
-                }
-                float top = -INFINITY;
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    uint32_t v[32];
-                    tmem_ld32(s_at + 32 * b, v);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 k = *reinterpret_cast<const float4 *>(info.k + 32 * b + e);
-                        const float y[4] = {__uint_as_float(v[e]) * k.x, __uint_as_float(v[e + 1]) * k.y,
-                                            __uint_as_float(v[e + 2]) * k.z, __uint_as_float(v[e + 3]) * k.w};
-#pragma unroll
-                        for (int d = 0; d < 4; ++d)
-                            if (whole || (bits[b] >> (e + d) & 1u)) top = fmaxf(top, y[d]);
-                    }
-                }
-                top = top == -INFINITY ? top : top * cq;
-                if (__any_sync(0xffffffffu, top > m + kAttnSlack || ratio != 1.0f)) {
-                    const float up = fmaxf(m, top), f = m == -INFINITY ? 0.0f : ex2(m - up);
-                    m = up;
-                    ref = up == -INFINITY ? 0.0f : up;
-                    l *= f;
-                    if (!first) {
-                        const uint32_t o_at = lanes + kOCol + stream * 128;
-                        const float g = f * ratio;
-                        for (int b = 0; b < DP / 32; ++b) {
-                            uint32_t v[32];
-                            tmem_ld32(o_at + 32 * b, v);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * g);
-                            tmem_st32(o_at + 32 * b, v);
-                        }
-                    }
+                    weights<true, DP>(s_at, o_at, ks, vs, bits, j, first, ratio, cr, m, ref, l);
                 }
                 first = false;
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    uint32_t v[32], p[16];
-                    tmem_ld32(s_at + 32 * b, v);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 k = *reinterpret_cast<const float4 *>(info.k + 32 * b + e);
-                        const float4 w = *reinterpret_cast<const float4 *>(info.v + 32 * b + e);
-                        const float ks[4] = {k.x, k.y, k.z, k.w}, ws[4] = {w.x, w.y, w.z, w.w};
-                        float y[4];
-#pragma unroll
-                        for (int d = 0; d < 4; ++d) {
-                            y[d] = ex2(__fmaf_rn(__uint_as_float(v[e + d]) * ks[d], cq, -ref));
-                            if (!whole && !(bits[b] >> (e + d) & 1u)) y[d] = 0.0f;
-                            sum[d] += y[d];
-                            y[d] *= ws[d];
-                        }
-                        const __half2 lo = __floats2half2_rn(y[0], y[1]), hi = __floats2half2_rn(y[2], y[3]);
-                        p[e / 2] = *reinterpret_cast<const uint32_t *>(&lo);
-                        p[e / 2 + 1] = *reinterpret_cast<const uint32_t *>(&hi);
-                    }
-                    tmem_st16(s_at + 16 * b, p);
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -485,8 +576,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             }
 
             // the two streams meet
-            row_m[stream][r] = m;
-            row_l[stream][r] = l;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                l[q] += __shfl_xor_sync(0xffffffffu, l[q], 1);
+                l[q] += __shfl_xor_sync(0xffffffffu, l[q], 2);
+                const int own = 32 * (warp & 3) + 16 * (q >> 1) + 8 * (q & 1) + g;
+                if (j == 0) row_m[stream][own] = m[q], row_l[stream][own] = l[q];
+            }
             if (r == 0) stream_unit[stream] = unit;
             (void)wait(o_full, item);
             tc_fence_after();
