@@ -24,6 +24,23 @@ constexpr int kRows = 128, kTokens = kAttnChunk, kThreads = 512, kInfos = 4, kMa
 constexpr int kCodeWarp0 = 4, kCodeWarps = 4, kRowWarp0 = 8, kRowWarps = 8;
 constexpr uint32_t kTmemCols = 512, kOCol = 256;  // S of both streams, then O
 
+// An item, or the part of one that is this block's, as the copies' warp leaves it to the others.
+struct Item {
+    int64_t first;              // row of the sequence's first newest token
+    int b, rt, h, chunk;        // chunk: the first
+    int count, units, T, len;   // count: of chunks here; units: of the item
+};
+constexpr int kItems = 4;
+
+// A place in the ring of codes, and how often the ring has come round to it.
+struct Ring {
+    int stage = 0, use = 0;
+    __device__ __forceinline__ void next(int stages)
+    {
+        if (++stage == stages) stage = 0, ++use;
+    }
+};
+
 // Of a chunk: scales of K, and of V over the stream's unit, for each token.
 struct Info {
     float k[kTokens], v[kTokens];
@@ -100,6 +117,15 @@ __device__ __forceinline__ void tmem_st_pairs(uint32_t taddr, const uint32_t (&r
         : "memory");
 }
 
+// a lane's row, 8 columns
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
 // The tile image as an operand whose rows are K: 64 of N (128 bytes) a row, 8 rows an atom of the
 // 128-byte swizzle; the next 8 rows follow, the next 64 of N are `panel` bytes on.
 __device__ __forceinline__ uint64_t sdesc_n_major(uint32_t addr, uint32_t panel)
@@ -112,7 +138,7 @@ __device__ __forceinline__ uint64_t sdesc_n_major(uint32_t addr, uint32_t panel)
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; }
 
 // Which of positions p0 .. p0 + 31 the row of newest token t sees.
-__device__ __forceinline__ uint32_t seen_bits(const KvAttnArgs &a, const AttnCursor &c, int t, int p0)
+__device__ __forceinline__ uint32_t seen_bits(const KvAttnArgs &a, const Item &c, int t, int p0)
 {
     const int base = c.len - c.T;
     if (!a.mask) return low_bits(min(c.len, base + t + 1) - p0);
@@ -218,8 +244,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
     const KvArgs &c = a.c;
     extern __shared__ __align__(16) uint8_t raw[];
     __shared__ __align__(8) uint64_t code_full[kMaxStages], code_empty[kMaxStages], tile_full[4], tile_empty[4],
-        info_full[kInfos], info_empty[kInfos], s_full[2], p_ready[2], q_full, o_full, mma_end;
+        info_full[kInfos], info_empty[kInfos], item_full[kItems], item_empty[kItems], s_full[2], p_ready[2], q_full, o_full,
+        mma_end;
     __shared__ __align__(16) Info infos[kInfos];
+    __shared__ Item items[kItems];
     __shared__ float row_m[2][kRows], row_l[2][kRows], row_top[2][kRows], stream_unit[2];
     __shared__ uint32_t present[kMaxStages], tmem_slot;
     uint8_t *smem = raw + (-smem_u32(raw) & 1023u);  // the swizzle's atoms
@@ -241,6 +269,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         for (int i = 0; i < kInfos; ++i) {
             mbar_init(smem_u32(&info_full[i]), 1);
             mbar_init(smem_u32(&info_empty[i]), kRowWarps / 2);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(smem_u32(&item_full[i]), 1);
+            mbar_init(smem_u32(&item_empty[i]), kRowWarps + 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&s_full[i]), 1);
@@ -270,6 +302,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
     const int chunks = (int)(share.to - share.from);
 
     bool ok = true;
+    auto release = [&](uint64_t &bar) {  // what the warp has read may be written again
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bar));
+    };
     auto wait = [&](uint64_t &bar, int use) {  // the use-th phase of a barrier, by a whole warp
         ok = ok && __all_sync(0xffffffffu, mbar_wait_idle(smem_u32(&bar), (uint32_t)use & 1u, c.status));
         return ok;
@@ -278,11 +314,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
     // 128 registers a thread at the launch, and as many after: 80 + 80 + 2 * 176 = 4 * 128
     if (warp < kCodeWarp0) {
     regs_dec<80>();
-    AttnCursor at;
-    if (chunks > 0) at.find(a, sums, share.from, kRows);
     if (chunks <= 0) {
     } else if (warp == 0) {
-        int page = -1, in_page = 0, asked = 0;
+        AttnCursor at;
+        at.find(a, sums, share.from, kRows);
+        int page = -1, in_page = 0, asked = 0, left = 0, item = 0;
+        Ring ring;
         auto look_up = [&]() {
             const int tile = at.chunk * (kTokens / 16) + lane;
             page = -1;
@@ -290,13 +327,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         };
         look_up();
         for (int n = 0; n < chunks && ok; ++n) {
+            if (left == 0) {
+                const int slot = item % kItems;
+                if (item >= kItems && !wait(item_empty[slot], item / kItems - 1)) break;
+                left = min(at.units - at.chunk, chunks - n);
+                if (lane == 0) {
+                    items[slot] = {at.first, at.b, at.rt, at.h, at.chunk, left, at.units, at.T, at.len};
+                    mbar_arrive(smem_u32(&item_full[slot]));
+                }
+                ++item;
+            }
+            --left;
             const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
             const int rows = 16 * c.row_bytes, all = c.page * c.row_bytes;
             const uint8_t *head = c.pages + page * c.page_bytes + (int64_t)at.h * c.head_bytes;
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-                const int stage = asked % ST, use = asked / ST;
-                if (use > 0 && !wait(code_empty[stage], use - 1)) break;
+#pragma unroll 1
+            for (int o = 0; o < 2; ++o, ring.next(ST)) {
+                const int stage = ring.stage;
+                if (ring.use > 0 && !wait(code_empty[stage], ring.use - 1)) break;
                 const uint32_t to = codes + stage * code_bytes, bar = smem_u32(&code_full[stage]);
                 if (lane == 0) {
                     present[stage] = there;
@@ -327,9 +375,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             tc_fence_after();
             if (lane == 0) {
                 const uint64_t qd = sdesc_sw128(q_tile), kd = sdesc_sw128(tiles + slot * TILE);
-                for (int s = 0; s < steps; ++s) {
+#pragma unroll
+                for (int s = 0; s < DP / 16; ++s) {
                     const uint64_t off = (uint64_t)((s >> 2) * (PANEL >> 4) + (s & 3) * 2);
-                    mma_f16_ss(tmem + slot * kTokens, qd + off, kd + off, idesc_s, s > 0);
+                    if (s < steps) mma_f16_ss(tmem + slot * kTokens, qd + off, kd + off, idesc_s, s > 0);
                 }
                 mma_commit(smem_u32(&tile_empty[slot]));
                 mma_commit(smem_u32(&s_full[slot]));
@@ -338,7 +387,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         };
         int n = 0, item = 0;
         while (n < chunks && ok) {
-            const int count = min(at.units - at.chunk, chunks - n);
+            if (!wait(item_full[item % kItems], item / kItems)) break;
+            const int count = items[item % kItems].count;
+            release(item_empty[item % kItems]);
             if (!wait(q_full, item)) break;
             for (int i = 0; i < 2 && i < count; ++i) scores(n + i);
             for (int i = 0; i < count && ok; ++i) {
@@ -360,8 +411,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             __syncwarp();
             n += count;
             ++item;
-            at.chunk = at.units - 1;
-            at.next(a, kRows);
         }
         // nothing of this thread's is in flight when the block ends
         if (lane == 0) {
@@ -371,16 +420,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         __syncwarp();
     } else if (warp == 2) {
         float unit[2] = {0.0f, 0.0f};
+        Ring ring;
+        int left = 0, item = 0, len = 0, pos = 0;
         for (int n = 0; n < chunks && ok; ++n) {
-            if (n == 0 || at.chunk == 0) unit[0] = unit[1] = pow2i(-126);
+            if (left == 0) {
+                if (!wait(item_full[item % kItems], item / kItems)) break;
+                const Item &at = items[item % kItems];
+                left = at.count, len = at.len, pos = at.chunk * kTokens + 4 * lane;
+                release(item_empty[item % kItems]);
+                ++item;
+                unit[0] = unit[1] = pow2i(-126);
+            }
+            --left;
             Info &info = infos[n % kInfos];
             if (n >= kInfos && !wait(info_empty[n % kInfos], n / kInfos - 1)) break;
-            const int pos = at.chunk * kTokens + 4 * lane;
             uint32_t there = 0;
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-                const int q = 2 * n + o, stage = q % ST;
-                if (!wait(code_full[stage], q / ST)) break;
+#pragma unroll 1
+            for (int o = 0; o < 2; ++o, ring.next(ST)) {
+                const int stage = ring.stage;
+                if (!wait(code_full[stage], ring.use)) break;
                 there = *reinterpret_cast<volatile uint32_t *>(&present[stage]);
                 const uint4 w = lds_v4(codes + stage * code_bytes + kTokens * c.row_bytes + 16 * lane);
                 __syncwarp();
@@ -390,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 for (int e = 0; e < 4; ++e) {
                     if (U4) s[e] = __uint_as_float(__float_as_uint(s[e]) & 0xffff0000u);
                     // beyond the sequence the words are anything
-                    if (!(there >> (lane / 4) & 1u) || pos + e >= at.len) s[e] = 0.0f;
+                    if (!(there >> (lane / 4) & 1u) || pos + e >= len) s[e] = 0.0f;
                 }
                 if (o == 0) {
                     *reinterpret_cast<float4 *>(info.k + 4 * lane) = make_float4(s[0], s[1], s[2], s[3]);
@@ -410,43 +468,46 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             }
             __syncwarp();
             if (ok && lane == 0) mbar_arrive(smem_u32(&info_full[n % kInfos]));
-            if (n + 1 < chunks) at.next(a, kRows);
+            pos += kTokens;
         }
     }
     } else if (warp < kRowWarp0) {
         regs_dec<80>();
         const int t = threadIdx.x - kCodeWarp0 * 32;
+        Ring ring;
         for (int n = 0; n < chunks && ok; ++n) {
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-                const int q = 2 * n + o, stage = q % ST, slot = 2 * o + (n & 1);
+#pragma unroll 1
+            for (int o = 0; o < 2; ++o, ring.next(ST)) {
+                const int stage = ring.stage, slot = 2 * o + (n & 1);
                 if (n >= 2 && !wait(tile_empty[slot], (n >> 1) - 1)) break;
-                if (!wait(code_full[stage], q / ST)) break;
+                if (!wait(code_full[stage], ring.use)) break;
                 const uint32_t from = codes + stage * code_bytes, row = from + t * c.row_bytes;
                 const uint32_t to = tiles + slot * TILE + t * 128;
                 auto put = [&](int chunk, const uint32_t (&f)[4]) {  // chunk of 8 f16
                     sts_v4(to + (chunk >> 3) * PANEL + (((chunk & 7) ^ (t & 7)) << 4), f[0], f[1], f[2], f[3]);
                 };
-                if constexpr (U4) {
-                    uint32_t word;
+                // all loads of the row, then all stores: one after the other each waits for the last
+                constexpr int N = U4 ? DP / 32 : DP / 16;
+                uint4 w[N];
+#pragma unroll
+                for (int ch = 0; ch < N; ++ch)
+                    if (ch < c.chunks) w[ch] = lds_v4(row + 16 * kv_chunk(c.chunks, t, ch));
+                uint32_t word = 0;
+                if constexpr (U4)
                     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(word) : "r"(from + kTokens * c.row_bytes + 4 * t) : "memory");
-                    const Zero z = zero_of(word & 15u, word & 15u);
-#pragma unroll 2
-                    for (int ch = 0; ch < c.chunks; ++ch) {
-                        const uint4 w = lds_v4(row + 16 * kv_chunk(c.chunks, t, ch));
-                        uint32_t f[4];
-                        u4_pairs(w.x, z, f), put(4 * ch, f);
-                        u4_pairs(w.y, z, f), put(4 * ch + 1, f);
-                        u4_pairs(w.z, z, f), put(4 * ch + 2, f);
-                        u4_pairs(w.w, z, f), put(4 * ch + 3, f);
-                    }
-                } else {
-#pragma unroll 4
-                    for (int ch = 0; ch < c.chunks; ++ch) {
-                        const uint4 w = lds_v4(row + 16 * kv_chunk(c.chunks, t, ch));
-                        uint32_t f[4];
-                        s8_pairs(w.x, f[0], f[1]), s8_pairs(w.y, f[2], f[3]), put(2 * ch, f);
-                        s8_pairs(w.z, f[0], f[1]), s8_pairs(w.w, f[2], f[3]), put(2 * ch + 1, f);
+                const Zero z = zero_of(word & 15u, word & 15u);
+#pragma unroll
+                for (int ch = 0; ch < N; ++ch) {
+                    if (ch >= c.chunks) break;
+                    uint32_t f[4];
+                    if constexpr (U4) {
+                        u4_pairs(w[ch].x, z, f), put(4 * ch, f);
+                        u4_pairs(w[ch].y, z, f), put(4 * ch + 1, f);
+                        u4_pairs(w[ch].z, z, f), put(4 * ch + 2, f);
+                        u4_pairs(w[ch].w, z, f), put(4 * ch + 3, f);
+                    } else {
+                        s8_pairs(w[ch].x, f[0], f[1]), s8_pairs(w[ch].y, f[2], f[3]), put(2 * ch, f);
+                        s8_pairs(w[ch].z, f[0], f[1]), s8_pairs(w[ch].w, f[2], f[3]), put(2 * ch + 1, f);
                     }
                 }
                 fence_proxy_async_smem();
@@ -459,16 +520,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         }
     } else {
         regs_inc<176>();
-        AttnCursor at;
-        if (chunks > 0) at.find(a, sums, share.from, kRows);
         const int stream = (warp - kRowWarp0) >> 2, r = (threadIdx.x - kRowWarp0 * 32) & 127;
         const int g = lane >> 2, j = lane & 3;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         auto meet = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
         int n = 0, item = 0;
         while (n < chunks) {
-            const int count = min(at.units - at.chunk, chunks - n), row0 = at.rt * kRows;
-            const int width = (int)min((int64_t)kRows, (int64_t)at.T * a.group - row0);
+            if (!wait(item_full[item % kItems], item / kItems)) break;
+            const Item &at = items[item % kItems];
+            const int count = at.count, row0 = at.rt * kRows;
+            const int width = min(kRows, at.T * a.group - row0);
             const int rr = row0 + r, t = min(rr / a.group, at.T - 1);
             const int t_first = row0 / a.group;
             const bool live = r < width, starts_here = n > 0 || at.chunk == 0, ends_here = at.chunk + count == at.units;
@@ -599,46 +660,34 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 float *slot = attn_slot(a, blockIdx.x, starts_here ? 1 : 0, kRows, DP);
                 uint16_t *out = static_cast<uint16_t *>(a.out) + out_row * a.ld_out + (int64_t)hq * c.D;
                 const float weight = top_unit * kAttnWeightUnit;
-                // blocks of 32 channels, in turn for the two streams' threads
-                for (int b = stream; b < c.D / 32; b += 2) {
-                    float o[32];
+                // 8 channels at a time, in turn for the two streams' threads
+                const float by = total == 0.0f ? 0.0f : weight / total;
+#pragma unroll 1
+                for (int d = 8 * stream; d < c.D; d += 16) {
+                    uint32_t v0[8], v1[8];
+                    float v[8];
                     __syncwarp();
-                    {
-                        uint32_t v[32];
+                    tmem_ld8(lanes + kOCol + d, v0);
+                    tmem_ld8(lanes + kOCol + 128 + d, v1);
+                    tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0.0f;
-                        if (has0) {
-                            tmem_ld32(lanes + kOCol + 32 * b, v);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(v[e]) * g0;
-                        }
-                        if (has1) {
-                            tmem_ld32(lanes + kOCol + 128 + 32 * b, v);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __fmaf_rn(__uint_as_float(v[e]), g1, o[e]);
-                        }
+                    for (int e = 0; e < 8; ++e) {
+                        const int at_e = U4 ? 2 * (e & 3) + (e >> 2) : e;  // codes are unpacked 0 4, 1 5, 2 6, 3 7
+                        const float x0 = has0 ? __uint_as_float(v0[at_e]) * g0 : 0.0f;
+                        v[e] = has1 ? __fmaf_rn(__uint_as_float(v1[at_e]), g1, x0) : x0;
+                        if (done) v[e] *= by;
                     }
                     if (!live || !ok) continue;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = o[8 * i + (U4 ? 2 * (e & 3) + (e >> 2) : e)];
-                        const int d = 32 * b + 8 * i;
-                        if (done) {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) v[e] = total == 0.0f ? 0.0f : v[e] / total * weight;
-                            *reinterpret_cast<uint4 *>(out + d) = make_uint4(attn_pack(a, v[0], v[1]), attn_pack(a, v[2], v[3]),
-                                                                            attn_pack(a, v[4], v[5]), attn_pack(a, v[6], v[7]));
-                        } else {
-                            float4 *to = reinterpret_cast<float4 *>(slot + r * DP + d);
-                            to[0] = make_float4(v[0], v[1], v[2], v[3]);
-                            to[1] = make_float4(v[4], v[5], v[6], v[7]);
-                        }
+                    if (done) {
+                        *reinterpret_cast<uint4 *>(out + d) = make_uint4(attn_pack(a, v[0], v[1]), attn_pack(a, v[2], v[3]),
+                                                                        attn_pack(a, v[4], v[5]), attn_pack(a, v[6], v[7]));
+                    } else {
+                        float4 *to = reinterpret_cast<float4 *>(slot + r * DP + d);
+                        to[0] = make_float4(v[0], v[1], v[2], v[3]);
+                        to[1] = make_float4(v[4], v[5], v[6], v[7]);
                     }
                 }
+                __syncwarp();
                 if (live && ok && stream == 0) {
                     if (done) {
                         if (a.lse) a.lse[out_row * a.heads_q + hq] = attn_lse(up, total);
@@ -650,10 +699,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             }
             tc_fence_before();  // O has been read before q_full says so
             meet();
+            release(item_empty[item % kItems]);
             n += count;
             ++item;
-            at.chunk = at.units - 1;
-            at.next(a, kRows);
         }
     }
     tc_fence_before();
