@@ -26,12 +26,13 @@ struct KvArgs {
 };
 
 // Chunk c of token t's row lies at chunk kv_chunk(t, c): so that the attention's reads of
-// shared memory, four tokens' equal chunks or two tokens' four neighbouring ones at a time,
-// meet no bank twice (rows of 128 and 256 bytes) or twice at most (64 bytes).
+// shared memory (four even or odd tokens' pairs of chunks, two tokens' four chunks, eight tokens'
+// equal chunks at a time) meet no bank twice where rows have 128 or 256 bytes, or twice at most
+// where they have 64.
 __host__ __device__ __forceinline__ int kv_chunk(int chunks, int t, int c)
 {
-    if ((chunks & 7) == 0) return c ^ (t & 6) ^ ((t & 1) << 2);
-    if (chunks == 4) return c ^ (t & 2);
+    if ((chunks & 7) == 0) return c ^ (t & 7) ^ ((t & 1) << 2);
+    if (chunks == 4) return c ^ (t >> 1 & 3);
     return c;
 }
 

@@ -10,7 +10,7 @@
 // Roles of a block's warps:
 //   0       copies: codes of K and V of 128 tokens at a time, page by page, to a ring
 //   1       MMA: S of a chunk, then O of the same stream's chunk before ... in order
-//   2       scales: of K for the scores, of V over a unit for the weights
+//   2, 3    scales: of K for the scores; of V over a unit for the weights
 //   4..7    codes: a token's row each, codes -> f16 integers -> the swizzled operand tiles, for K
 //           (K-major) and V (N-major) the same image
 //   8..15   rows: a row of S each, in tensor memory -> weights as f16 over it; the other way for O
@@ -38,6 +38,17 @@ struct Ring {
     __device__ __forceinline__ void next(int stages)
     {
         if (++stage == stages) stage = 0, ++use;
+    }
+};
+
+// Operands go through the block in this order: K of chunk 0, then K of each chunk before V of the
+// chunk before it, so that no V that waits for its place holds up the scores of the next chunk.
+struct Operand {
+    int n, is_v;
+    __device__ __forceinline__ Operand(int i, int chunks)
+    {
+        is_v = i > 0 && (!(i & 1) || i == 2 * chunks - 1);
+        n = is_v ? (i - 1) / 2 : (i + 1) / 2;
     }
 };
 
@@ -267,12 +278,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             mbar_init(smem_u32(&tile_empty[i]), 1);
         }
         for (int i = 0; i < kInfos; ++i) {
-            mbar_init(smem_u32(&info_full[i]), 1);
+            mbar_init(smem_u32(&info_full[i]), 2);
             mbar_init(smem_u32(&info_empty[i]), kRowWarps / 2);
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(smem_u32(&item_full[i]), 1);
-            mbar_init(smem_u32(&item_empty[i]), kRowWarps + 2);
+            mbar_init(smem_u32(&item_empty[i]), kRowWarps + 3);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&s_full[i]), 1);
@@ -318,18 +329,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
     } else if (warp == 0) {
         AttnCursor at;
         at.find(a, sums, share.from, kRows);
-        int page = -1, in_page = 0, asked = 0, left = 0, item = 0;
-        Ring ring;
-        auto look_up = [&]() {
-            const int tile = at.chunk * (kTokens / 16) + lane;
-            page = -1;
-            if (lane < kTokens / 16 && tile * 16 < at.len) page = attn_page(a, at.b, tile, &in_page);
-        };
-        look_up();
-        for (int n = 0; n < chunks && ok; ++n) {
+        // places of the next chunk's codes (looked up ahead of their use), of the last K's and of the one before
+        int page[3], in_page[3], head[3], asked = 0, left = 0, item = 0;
+        auto look_up = [&](int n) {
             if (left == 0) {
                 const int slot = item % kItems;
-                if (item >= kItems && !wait(item_empty[slot], item / kItems - 1)) break;
+                if (item >= kItems && !wait(item_empty[slot], item / kItems - 1)) return;
                 left = min(at.units - at.chunk, chunks - n);
                 if (lane == 0) {
                     items[slot] = {at.first, at.b, at.rt, at.h, at.chunk, left, at.units, at.T, at.len};
@@ -338,29 +343,45 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 ++item;
             }
             --left;
-            const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
-            const int rows = 16 * c.row_bytes, all = c.page * c.row_bytes;
-            const uint8_t *head = c.pages + page * c.page_bytes + (int64_t)at.h * c.head_bytes;
+            const int tile = at.chunk * (kTokens / 16) + lane;
+            page[0] = -1, head[0] = at.h;
+            if (lane < kTokens / 16 && tile * 16 < at.len) page[0] = attn_page(a, at.b, tile, &in_page[0]);
+        };
+        Ring ring;
+        in_page[0] = 0;
+        look_up(0);
+#pragma unroll
+        for (int e = 1; e < 3; ++e) page[e] = -1, in_page[e] = head[e] = 0;
 #pragma unroll 1
-            for (int o = 0; o < 2; ++o, ring.next(ST)) {
-                const int stage = ring.stage;
-                if (ring.use > 0 && !wait(code_empty[stage], ring.use - 1)) break;
-                const uint32_t to = codes + stage * code_bytes, bar = smem_u32(&code_full[stage]);
-                if (lane == 0) {
-                    present[stage] = there;
-                    mbar_arrive_expect_tx(bar, __popc(there) * (rows + 64));
+        for (int i = 0; i < 2 * chunks && ok; ++i, ring.next(ST)) {
+            const Operand op(i, chunks);
+            if (!op.is_v) {
+#pragma unroll
+                for (int e = 2; e > 0; --e) page[e] = page[e - 1], in_page[e] = in_page[e - 1], head[e] = head[e - 1];
+                if (op.n + 1 < chunks) {
+                    at.next(a, kRows);
+                    look_up(op.n + 1);
+                    if (!ok) break;
                 }
-                __syncwarp();
-                if (page >= 0) {
-                    bulk_g2s(to + lane * rows, head + o * all + in_page * rows, rows, bar);
-                    bulk_g2s(to + kTokens * c.row_bytes + lane * 64, head + 2 * all + o * 4 * c.page + in_page * 64, 64, bar);
-                }
-                ++asked;
             }
-            if (n + 1 < chunks) {
-                at.next(a, kRows);
-                look_up();
+            // V is of the chunk before the last K's, but for the last V
+            const int back = op.is_v && i < 2 * chunks - 1;
+            const int pg = back ? page[2] : page[1], tile = back ? in_page[2] : in_page[1];
+            const uint32_t there = __ballot_sync(0xffffffffu, pg >= 0);
+            const int rows = 16 * c.row_bytes, all = c.page * c.row_bytes;
+            const uint8_t *from = c.pages + pg * c.page_bytes + (int64_t)(back ? head[2] : head[1]) * c.head_bytes;
+            if (ring.use > 0 && !wait(code_empty[ring.stage], ring.use - 1)) break;
+            const uint32_t to = codes + ring.stage * code_bytes, bar = smem_u32(&code_full[ring.stage]);
+            if (lane == 0) {
+                present[ring.stage] = there;
+                mbar_arrive_expect_tx(bar, __popc(there) * (rows + 64));
             }
+            __syncwarp();
+            if (pg >= 0) {
+                bulk_g2s(to + lane * rows, from + op.is_v * all + tile * rows, rows, bar);
+                bulk_g2s(to + kTokens * c.row_bytes + lane * 64, from + 2 * all + op.is_v * 4 * c.page + tile * 64, 64, bar);
+            }
+            ++asked;
         }
         // nothing that was asked for is in flight when the block ends
         for (int s = 0; s < min(ST, asked); ++s)
@@ -368,17 +389,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
     } else if (warp == 1) {
         const uint32_t idesc_s = idesc_f32acc(0, 0, kRows, kTokens);
         const uint32_t idesc_o = idesc_f32acc(0, 0, kRows, 0) | (uint32_t)(c.D >> 3) << 17 | 1u << 16;  // B is N-major
-        const int steps = c.D / 16;
         auto scores = [&](int n) {
             const int slot = n & 1;
             if (!wait(tile_full[slot], n >> 1)) return;
             tc_fence_after();
             if (lane == 0) {
                 const uint64_t qd = sdesc_sw128(q_tile), kd = sdesc_sw128(tiles + slot * TILE);
-#pragma unroll
-                for (int s = 0; s < DP / 16; ++s) {
+                auto step = [&](int s) {
                     const uint64_t off = (uint64_t)((s >> 2) * (PANEL >> 4) + (s & 3) * 2);
-                    if (s < steps) mma_f16_ss(tmem + slot * kTokens, qd + off, kd + off, idesc_s, s > 0);
+                    mma_f16_ss(tmem + slot * kTokens, qd + off, kd + off, idesc_s, s > 0);
+                };
+                // not an unrolled loop with a condition inside: what came of it read operands elsewhere
+                if (c.D == DP) {
+#pragma unroll
+                    for (int s = 0; s < DP / 16; ++s) step(s);
+                } else {
+#pragma unroll 1
+                    for (int s = 0; s < c.D / 16; ++s) step(s);
                 }
                 mma_commit(smem_u32(&tile_empty[slot]));
                 mma_commit(smem_u32(&s_full[slot]));
@@ -418,11 +445,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             (void)mbar_wait_idle(smem_u32(&mma_end), 0, c.status);
         }
         __syncwarp();
-    } else if (warp == 2) {
+    } else {
+        // warp 2: scales of K, 3: of V; four tokens a lane
+        const bool is_v = warp == 3;
         float unit[2] = {0.0f, 0.0f};
         Ring ring;
         int left = 0, item = 0, len = 0, pos = 0;
-        for (int n = 0; n < chunks && ok; ++n) {
+#pragma unroll 1
+        for (int i = 0; i < 2 * chunks && ok; ++i, ring.next(ST)) {
+            const Operand op(i, chunks);
+            if (op.is_v != is_v) continue;
+            const int n = op.n, slot = n % kInfos;
             if (left == 0) {
                 if (!wait(item_full[item % kItems], item / kItems)) break;
                 const Item &at = items[item % kItems];
@@ -432,42 +465,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 unit[0] = unit[1] = pow2i(-126);
             }
             --left;
-            Info &info = infos[n % kInfos];
-            if (n >= kInfos && !wait(info_empty[n % kInfos], n / kInfos - 1)) break;
-            uint32_t there = 0;
-#pragma unroll 1
-            for (int o = 0; o < 2; ++o, ring.next(ST)) {
-                const int stage = ring.stage;
-                if (!wait(code_full[stage], ring.use)) break;
-                there = *reinterpret_cast<volatile uint32_t *>(&present[stage]);
-                const uint4 w = lds_v4(codes + stage * code_bytes + kTokens * c.row_bytes + 16 * lane);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&code_empty[stage]));
-                float s[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
+            Info &info = infos[slot];
+            if (n >= kInfos && !wait(info_empty[slot], n / kInfos - 1)) break;
+            if (!wait(code_full[ring.stage], ring.use)) break;
+            const uint32_t there = *reinterpret_cast<volatile uint32_t *>(&present[ring.stage]);
+            const uint4 w = lds_v4(codes + ring.stage * code_bytes + kTokens * c.row_bytes + 16 * lane);
+            release(code_empty[ring.stage]);
+            float s[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
+            const int valid = there >> (lane / 4) & 1u ? len - pos : 0;  // beyond the sequence the words are anything
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (U4) s[e] = __uint_as_float(__float_as_uint(s[e]) & 0xffff0000u);
-                    // beyond the sequence the words are anything
-                    if (!(there >> (lane / 4) & 1u) || pos + e >= len) s[e] = 0.0f;
-                }
-                if (o == 0) {
-                    *reinterpret_cast<float4 *>(info.k + 4 * lane) = make_float4(s[0], s[1], s[2], s[3]);
-                } else {
-                    uint32_t top = __float_as_uint(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])));
-                    top = __reduce_max_sync(0xffffffffu, top);
-                    const float old = n & 1 ? unit[1] : unit[0];
-                    const float now = fmaxf(old, __uint_as_float((top + 0x7fffffu) & 0xff800000u));
-                    const float per = __uint_as_float(0x7f000000u - __float_as_uint(now));
-                    if (n & 1) unit[1] = now;
-                    else unit[0] = now;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[e] = s[e] * per * (float)(1 << kAttnRoom);
-                    *reinterpret_cast<float4 *>(info.v + 4 * lane) = make_float4(s[0], s[1], s[2], s[3]);
-                    if (lane == 0) info.ratio = old * per, info.unit = now, info.present = there;
-                }
+            for (int e = 0; e < 4; ++e) {
+                if (U4) s[e] = __uint_as_float(__float_as_uint(s[e]) & 0xffff0000u);
+                if (e >= valid) s[e] = 0.0f;
             }
-            __syncwarp();
-            if (ok && lane == 0) mbar_arrive(smem_u32(&info_full[n % kInfos]));
+            if (is_v) {
+                uint32_t top = __float_as_uint(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])));
+                top = __reduce_max_sync(0xffffffffu, top);
+                const float old = n & 1 ? unit[1] : unit[0];
+                const float now = fmaxf(old, __uint_as_float((top + 0x7fffffu) & 0xff800000u));
+                const float per = __uint_as_float(0x7f000000u - __float_as_uint(now));
+                if (n & 1) unit[1] = now;
+                else unit[0] = now;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] = s[e] * per * (float)(1 << kAttnRoom);
+                if (lane == 0) info.ratio = old * per, info.unit = now, info.present = there;
+            }
+            *reinterpret_cast<float4 *>((is_v ? info.v : info.k) + 4 * lane) = make_float4(s[0], s[1], s[2], s[3]);
+            release(info_full[slot]);
             pos += kTokens;
         }
     }
@@ -475,10 +499,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         regs_dec<80>();
         const int t = threadIdx.x - kCodeWarp0 * 32;
         Ring ring;
-        for (int n = 0; n < chunks && ok; ++n) {
 #pragma unroll 1
-            for (int o = 0; o < 2; ++o, ring.next(ST)) {
-                const int stage = ring.stage, slot = 2 * o + (n & 1);
+        for (int i = 0; i < 2 * chunks && ok; ++i, ring.next(ST)) {
+            {
+                const Operand op(i, chunks);
+                const int n = op.n, stage = ring.stage, slot = 2 * op.is_v + (n & 1);
                 if (n >= 2 && !wait(tile_empty[slot], (n >> 1) - 1)) break;
                 if (!wait(code_full[stage], ring.use)) break;
                 const uint32_t from = codes + stage * code_bytes, row = from + t * c.row_bytes;
@@ -524,9 +549,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         const int g = lane >> 2, j = lane & 3;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         auto meet = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+        auto all_ok = [&]() {  // of all rows' warps: they wait for each other below, so they leave together
+            uint32_t r;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\t"
+                "setp.ne.u32 p, %1, 0;\n\t"
+                "bar.red.and.pred q, 1, 256, p;\n\t"
+                "selp.u32 %0, 1, 0, q;\n\t}"
+                : "=r"(r)
+                : "r"((uint32_t)ok)
+                : "memory");
+            return r != 0;
+        };
         int n = 0, item = 0;
         while (n < chunks) {
-            if (!wait(item_full[item % kItems], item / kItems)) break;
+            (void)wait(item_full[item % kItems], item / kItems);
+            if (!all_ok()) break;
             const Item &at = items[item % kItems];
             const int count = at.count, row0 = at.rt * kRows;
             const int width = min(kRows, at.T * a.group - row0);
