@@ -259,7 +259,7 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
 
         for (; x < end && ok; ++x, at.next(a, S::kRows)) {
             const int pos0 = (at.chunk * kWarps + warp) * 16;
-            ok = __all_sync(0xffffffffu, mbar_wait_idle(bar + 8 * stage, phase, c.status));
+            ok = __all_sync(0xffffffffu, mbar_wait_short(bar + 8 * stage, phase, c.status));
             if (!ok) break;
             ++waiting;
             const int seen_by_all = a.mask ? at.len - at.T : min(at.len, at.len - at.T + t_first + 1);
@@ -436,7 +436,7 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
         // lets the copies that it has asked for land
         if (!ok) {
             for (; waiting < asked; ++waiting) {
-                (void)mbar_wait_idle(bar + 8 * stage, phase, c.status);
+                (void)mbar_wait_short(bar + 8 * stage, phase, c.status);
                 if (++stage == ST) stage = 0, phase ^= 1u;
             }
             for (; x < end; ++x) at.next(a, S::kRows);

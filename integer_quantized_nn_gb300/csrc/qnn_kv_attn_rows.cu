@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         if (lane == 0) mbar_arrive(smem_u32(&bar));
     };
     auto wait = [&](uint64_t &bar, int use) {  // the use-th phase of a barrier, by a whole warp
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_idle(smem_u32(&bar), (uint32_t)use & 1u, c.status));
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_short(smem_u32(&bar), (uint32_t)use & 1u, c.status));
         return ok;
     };
 
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         }
         // nothing that was asked for is in flight when the block ends
         for (int s = 0; s < min(ST, asked); ++s)
-            (void)mbar_wait_idle(smem_u32(&code_full[s]), (uint32_t)((asked - 1 - s) / ST) & 1u, c.status);
+            (void)mbar_wait_short(smem_u32(&code_full[s]), (uint32_t)((asked - 1 - s) / ST) & 1u, c.status);
     } else if (warp == 1) {
         const uint32_t idesc_s = idesc_f32acc(0, 0, kRows, kTokens);
         const uint32_t idesc_o = idesc_f32acc(0, 0, kRows, 0) | (uint32_t)(c.D >> 3) << 17 | 1u << 16;  // B is N-major
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         // nothing of this thread's is in flight when the block ends
         if (lane == 0) {
             mma_commit(smem_u32(&mma_end));
-            (void)mbar_wait_idle(smem_u32(&mma_end), 0, c.status);
+            (void)mbar_wait_short(smem_u32(&mma_end), 0, c.status);
         }
         __syncwarp();
     } else {
