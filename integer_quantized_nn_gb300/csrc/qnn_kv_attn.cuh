@@ -270,6 +270,35 @@ struct AttnShare {
     __device__ __forceinline__ int block_of(int64_t x) const { return (int)(((x + 1) * active - 1) / all); }
 };
 
+// 16 bytes global -> shared, asynchronously.  Whole warps copy this way: bulk copies of lanes that each
+// have an address of their own are issued one lane after the other, 20 instructions each.
+__device__ __forceinline__ void copy_async16(uint32_t to, const void *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
+__device__ __forceinline__ void copy_async4(uint32_t to, const void *from)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// All but the thread's last n groups of copies have landed.
+__device__ __forceinline__ void copies_wait(int n)
+{
+    switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+    }
+}
+
 // The page of 16-token tile `tile` of sequence b, or -1.
 __device__ __forceinline__ int attn_page(const KvAttnArgs &a, int b, int tile, int *in_page)
 {

@@ -8,8 +8,8 @@
 // one subtraction; the products are exact, scales of K multiply the scores, scales of V the weights.
 //
 // It is bound by the stream of codes.  Each warp has a ring of its own in shared memory, stages
-// of 16 tokens (their K and V rows and words), filled by bulk copies that its first lanes issue;
-// warps meet only where an item ends.  Maxima move only when a score passes the warp's by 2^8 (the
+// of 16 tokens (their K and V rows and words), filled by asynchronous copies; warps meet only
+// where an item ends.  Maxima move only when a score passes the warp's by 2^8 (the
 // weights have that room), which one vote a tile finds.
 #include "qnn_kv_attn.cuh"
 
@@ -66,6 +66,7 @@ __device__ __forceinline__ void lds(uint32_t at, uint32_t *w)
 template <bool U4, int DP, int NT>
 struct Shape {
     static constexpr int kRows = 8 * NT;
+    static constexpr int kChunks = DP / (U4 ? 32 : 16);   // of a row, at most
     static constexpr int kKWords = DP / (U4 ? 32 : 16);   // of a token's K that a lane has
     static constexpr int kVWords = DP / (U4 ? 64 : 32);   // of a token's V
     static constexpr int kSteps = DP / 16;                // of K, and tiles of 16 channels of V
@@ -117,7 +118,6 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
     using S = Shape<U4, DP, NT>;
     const KvArgs &c = a.c;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t bars[kWarps][8];
     __shared__ float stats[kWarps][S::kRows][2], units_of[kWarps];
     __shared__ uint2 q_smem[S::kQRegs ? 1 : NT * S::kSteps * 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, j = lane & 3;
@@ -125,13 +125,8 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
     float *join = reinterpret_cast<float *>(smem);  // [warps][8][kPitch]
     uint8_t *ring = smem + kWarps * 8 * S::kPitch * 4 + warp * ST * stage_b;
     int64_t *sums = reinterpret_cast<int64_t *>(smem + kWarps * (8 * S::kPitch * 4 + ST * stage_b) + 128);
-    const uint32_t ring_at = smem_u32(ring), bar = smem_u32(bars[warp]);
+    const uint32_t ring_at = smem_u32(ring);
 
-    if (lane == 0) {
-        for (int i = 0; i < ST; ++i) mbar_init(bar + 8 * i, 1);
-        fence_mbar_init();
-    }
-    __syncwarp();
     grid_dependency_launch();
     grid_dependency_wait();
     const AttnShare share(attn_sums<kThreads>(a, sums, S::kRows), a.blocks, blockIdx.x);
@@ -153,31 +148,35 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
         if (tile * 16 < ahead.len) page = attn_page(a, ahead.b, tile, &in_page);
     };
     uint32_t absent = 0;  // stages whose tile is not there
-    auto ask = [&](int stage) {
-        const bool there = page >= 0;
-        absent = there ? absent & ~(1u << stage) : absent | 1u << stage;
-        const uint32_t to = ring_at + stage * stage_b, b = bar + 8 * stage;
-        if (lane == 0) mbar_arrive_expect_tx(b, there ? stage_b : 0);
-        __syncwarp();
-        if (there && lane < 4) {
-            const uint8_t *head = c.pages + page * c.page_bytes + (int64_t)ahead.h * c.head_bytes;
-            const int rows = 16 * c.row_bytes, all = c.page * c.row_bytes;
-            if (lane < 2) bulk_g2s(to + lane * rows, head + lane * all + in_page * rows, rows, b);
-            else bulk_g2s(to + 2 * rows + (lane - 2) * 64, head + 2 * all + (lane - 2) * 4 * c.page + in_page * 64, 64, b);
-        }
-        ++asked;
+    auto ask = [&](int stage) {  // a group of copies, if only an empty one
         if (asked < share.to) {
-            ahead.next(a, S::kRows);
-            look_up();
+            const bool there = page >= 0;
+            absent = there ? absent & ~(1u << stage) : absent | 1u << stage;
+            if (there) {
+                const uint32_t to = ring_at + stage * stage_b + 16 * lane;
+                const uint8_t *head = c.pages + page * c.page_bytes + (int64_t)ahead.h * c.head_bytes;
+                const int rows = 16 * c.row_bytes, all = c.page * c.row_bytes;
+                const uint8_t *k = head + in_page * rows + 16 * lane;
+#pragma unroll
+                for (int e = 0; e < 16 * S::kChunks; e += 32)
+                    if (e + lane < 16 * c.chunks) {
+                        copy_async16(to + 16 * e, k + 16 * e);
+                        copy_async16(to + rows + 16 * e, k + all + 16 * e);
+                    }
+                if (lane < 8)
+                    copy_async16(to + 2 * rows, head + 2 * all + (lane < 4 ? 0 : 4 * c.page - 64) + in_page * 64 + 16 * lane);
+            }
+            if (++asked < share.to) {
+                ahead.next(a, S::kRows);
+                look_up();
+            }
         }
+        copies_commit();
     };
     look_up();
-    for (int i = 0; i < ST && asked < share.to; ++i) ask(i);
+    for (int i = 0; i < ST; ++i) ask(i);
 
-    bool ok = true;
-    int64_t waiting = share.from;  // units whose copies have been waited for
     int stage = 0;
-    uint32_t phase = 0;
     int64_t x = share.from;
     while (x < share.to) {
         // one item, or the part of it that is this block's
@@ -257,11 +256,10 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
             ref[nt][0] = ref[nt][1] = l[nt][0] = l[nt][1] = 0.0f;
         }
 
-        for (; x < end && ok; ++x, at.next(a, S::kRows)) {
+        for (; x < end; ++x, at.next(a, S::kRows)) {
             const int pos0 = (at.chunk * kWarps + warp) * 16;
-            ok = __all_sync(0xffffffffu, mbar_wait_short(bar + 8 * stage, phase, c.status));
-            if (!ok) break;
-            ++waiting;
+            copies_wait(ST - 1);
+            __syncwarp();
             const int seen_by_all = a.mask ? at.len - at.T : min(at.len, at.len - at.T + t_first + 1);
             const int seen_by_any = a.mask ? at.len : at.len - at.T + t_last + 1;
             if (!(absent >> stage & 1u) && pos0 < seen_by_any) {
@@ -429,19 +427,9 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
                 }
             }
             __syncwarp();  // the stage has been read
-            if (asked < share.to) ask(stage);
-            if (++stage == ST) stage = 0, phase ^= 1u;
+            ask(stage);
+            if (++stage == ST) stage = 0;
         }
-        // a wait that gave up: this warp goes on in step with the others, without its tiles, and
-        // lets the copies that it has asked for land
-        if (!ok) {
-            for (; waiting < asked; ++waiting) {
-                (void)mbar_wait_short(bar + 8 * stage, phase, c.status);
-                if (++stage == ST) stage = 0, phase ^= 1u;
-            }
-            for (; x < end; ++x) at.next(a, S::kRows);
-        }
-
         // the warps' parts meet
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)

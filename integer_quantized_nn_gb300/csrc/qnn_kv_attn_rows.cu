@@ -8,11 +8,11 @@
 // warps of one stream make P of a chunk, the tensor cores work on the other's.
 //
 // Roles of a block's warps:
-//   0       copies: codes of K and V of 128 tokens at a time, page by page, to a ring
+//   0       places: which pages hold a chunk of 128 tokens, and which item comes next
 //   1       MMA: S of a chunk, then O of the same stream's chunk before ... in order
 //   2, 3    scales: of K for the scores; of V over a unit for the weights
-//   4..7    codes: a token's row each, codes -> f16 integers -> the swizzled operand tiles, for K
-//           (K-major) and V (N-major) the same image
+//   4..7    codes: global -> registers -> f16 integers -> the swizzled operand tiles, for K (K-major)
+//           and V (N-major) the same image
 //   8..15   rows: a row of S each, in tensor memory -> weights as f16 over it; the other way for O
 //           when a maximum has moved by more than 2^8 or the unit has grown
 #include "qnn_kv_attn.cuh"
@@ -20,7 +20,7 @@
 namespace qnn {
 namespace {
 
-constexpr int kRows = 128, kTokens = kAttnChunk, kThreads = 512, kInfos = 4, kMaxStages = 6;
+constexpr int kRows = 128, kTokens = kAttnChunk, kThreads = 512, kInfos = 4;
 constexpr int kCodeWarp0 = 4, kCodeWarps = 4, kRowWarp0 = 8, kRowWarps = 8;
 constexpr uint32_t kTmemCols = 512, kOCol = 256;  // S of both streams, then O
 
@@ -32,25 +32,12 @@ struct Item {
 };
 constexpr int kItems = 4;
 
-// A place in the ring of codes, and how often the ring has come round to it.
-struct Ring {
-    int stage = 0, use = 0;
-    __device__ __forceinline__ void next(int stages)
-    {
-        if (++stage == stages) stage = 0, ++use;
-    }
+// Where 16 tokens of a chunk are: bytes from the first page to their K rows and their K words; -1:
+// they are not there.
+struct Tile16 {
+    int64_t rows, words;
 };
-
-// Operands go through the block in this order: K of chunk 0, then K of each chunk before V of the
-// chunk before it, so that no V that waits for its place holds up the scores of the next chunk.
-struct Operand {
-    int n, is_v;
-    __device__ __forceinline__ Operand(int i, int chunks)
-    {
-        is_v = i > 0 && (!(i & 1) || i == 2 * chunks - 1);
-        n = is_v ? (i - 1) / 2 : (i + 1) / 2;
-    }
-};
+constexpr int kPlaces = 8;
 
 // Of a chunk: scales of K, and of V over the stream's unit, for each token.
 struct Info {
@@ -254,28 +241,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
     constexpr uint32_t PANEL = kTokens * 128, TILE = PANEL * (DP / 64);
     const KvArgs &c = a.c;
     extern __shared__ __align__(16) uint8_t raw[];
-    __shared__ __align__(8) uint64_t code_full[kMaxStages], code_empty[kMaxStages], tile_full[4], tile_empty[4],
+    __shared__ __align__(8) uint64_t place_full[kPlaces], place_empty[kPlaces], tile_full[4], v_empty[2],
         info_full[kInfos], info_empty[kInfos], item_full[kItems], item_empty[kItems], s_full[2], p_ready[2], q_full, o_full,
         mma_end;
     __shared__ __align__(16) Info infos[kInfos];
+    __shared__ __align__(16) Tile16 places[kPlaces][kTokens / 16];
     __shared__ Item items[kItems];
     __shared__ float row_m[2][kRows], row_l[2][kRows], row_top[2][kRows], stream_unit[2];
-    __shared__ uint32_t present[kMaxStages], tmem_slot;
+    __shared__ uint32_t tmem_slot;
     uint8_t *smem = raw + (-smem_u32(raw) & 1023u);  // the swizzle's atoms
-    // tiles: K of even and odd chunks, V of both; q; codes; the sums of the line
-    const uint32_t tiles = smem_u32(smem), q_tile = tiles + 4 * TILE, codes = q_tile + TILE;
-    const int ST = a.stages, code_bytes = kTokens * (c.row_bytes + 4);
-    int64_t *sums = reinterpret_cast<int64_t *>(smem + 5 * TILE + ST * code_bytes);
+    // tiles: K of even and odd chunks, V of both; q; the sums of the line
+    const uint32_t tiles = smem_u32(smem), q_tile = tiles + 4 * TILE;
+    int64_t *sums = reinterpret_cast<int64_t *>(smem + 5 * TILE);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < ST; ++i) {
-            mbar_init(smem_u32(&code_full[i]), 1);
-            mbar_init(smem_u32(&code_empty[i]), kCodeWarps + 1);
+        for (int i = 0; i < kPlaces; ++i) {
+            mbar_init(smem_u32(&place_full[i]), 1);
+            mbar_init(smem_u32(&place_empty[i]), kCodeWarps + 2);
         }
         for (int i = 0; i < 4; ++i) {
-            mbar_init(smem_u32(&tile_full[i]), kCodeWarps);
-            mbar_init(smem_u32(&tile_empty[i]), 1);
+            mbar_init(smem_u32(&tile_full[i]), kCodeWarps / 2);
         }
         for (int i = 0; i < kInfos; ++i) {
             mbar_init(smem_u32(&info_full[i]), 2);
@@ -286,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             mbar_init(smem_u32(&item_empty[i]), kRowWarps + 3);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&v_empty[i]), 1);
             mbar_init(smem_u32(&s_full[i]), 1);
             mbar_init(smem_u32(&p_ready[i]), kRowWarps / 2);
         }
@@ -322,19 +309,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         return ok;
     };
 
-    // 128 registers a thread at the launch, and as many after: 80 + 80 + 2 * 176 = 4 * 128
+    // 128 registers a thread at the launch, and as many after: 72 + 104 + 2 * 168 = 4 * 128
     if (warp < kCodeWarp0) {
-    regs_dec<80>();
+    regs_dec<72>();
     if (chunks <= 0) {
     } else if (warp == 0) {
         AttnCursor at;
         at.find(a, sums, share.from, kRows);
-        // places of the next chunk's codes (looked up ahead of their use), of the last K's and of the one before
-        int page[3], in_page[3], head[3], asked = 0, left = 0, item = 0;
-        auto look_up = [&](int n) {
+        int left = 0, item = 0;
+#pragma unroll 1
+        for (int n = 0; n < chunks && ok; ++n) {
             if (left == 0) {
                 const int slot = item % kItems;
-                if (item >= kItems && !wait(item_empty[slot], item / kItems - 1)) return;
+                if (item >= kItems && !wait(item_empty[slot], item / kItems - 1)) break;
                 left = min(at.units - at.chunk, chunks - n);
                 if (lane == 0) {
                     items[slot] = {at.first, at.b, at.rt, at.h, at.chunk, left, at.units, at.T, at.len};
@@ -343,49 +330,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 ++item;
             }
             --left;
-            const int tile = at.chunk * (kTokens / 16) + lane;
-            page[0] = -1, head[0] = at.h;
-            if (lane < kTokens / 16 && tile * 16 < at.len) page[0] = attn_page(a, at.b, tile, &in_page[0]);
-        };
-        Ring ring;
-        in_page[0] = 0;
-        look_up(0);
-#pragma unroll
-        for (int e = 1; e < 3; ++e) page[e] = -1, in_page[e] = head[e] = 0;
-#pragma unroll 1
-        for (int i = 0; i < 2 * chunks && ok; ++i, ring.next(ST)) {
-            const Operand op(i, chunks);
-            if (!op.is_v) {
-#pragma unroll
-                for (int e = 2; e > 0; --e) page[e] = page[e - 1], in_page[e] = in_page[e - 1], head[e] = head[e - 1];
-                if (op.n + 1 < chunks) {
-                    at.next(a, kRows);
-                    look_up(op.n + 1);
-                    if (!ok) break;
+            const int slot = n % kPlaces, tile = at.chunk * (kTokens / 16) + lane;
+            Tile16 place = {-1, -1};
+            if (lane < kTokens / 16 && tile * 16 < at.len) {
+                int in_page;
+                const int page = attn_page(a, at.b, tile, &in_page);
+                if (page >= 0) {
+                    const int64_t head = page * c.page_bytes + (int64_t)at.h * c.head_bytes;
+                    place = {head + in_page * 16 * c.row_bytes, head + 2 * c.page * c.row_bytes + in_page * 64};
                 }
             }
-            // V is of the chunk before the last K's, but for the last V
-            const int back = op.is_v && i < 2 * chunks - 1;
-            const int pg = back ? page[2] : page[1], tile = back ? in_page[2] : in_page[1];
-            const uint32_t there = __ballot_sync(0xffffffffu, pg >= 0);
-            const int rows = 16 * c.row_bytes, all = c.page * c.row_bytes;
-            const uint8_t *from = c.pages + pg * c.page_bytes + (int64_t)(back ? head[2] : head[1]) * c.head_bytes;
-            if (ring.use > 0 && !wait(code_empty[ring.stage], ring.use - 1)) break;
-            const uint32_t to = codes + ring.stage * code_bytes, bar = smem_u32(&code_full[ring.stage]);
-            if (lane == 0) {
-                present[ring.stage] = there;
-                mbar_arrive_expect_tx(bar, __popc(there) * (rows + 64));
-            }
-            __syncwarp();
-            if (pg >= 0) {
-                bulk_g2s(to + lane * rows, from + op.is_v * all + tile * rows, rows, bar);
-                bulk_g2s(to + kTokens * c.row_bytes + lane * 64, from + 2 * all + op.is_v * 4 * c.page + tile * 64, 64, bar);
-            }
-            ++asked;
+            if (n >= kPlaces && !wait(place_empty[slot], n / kPlaces - 1)) break;
+            if (lane < kTokens / 16) places[slot][lane] = place;
+            release(place_full[slot]);
+            if (n + 1 < chunks) at.next(a, kRows);
         }
-        // nothing that was asked for is in flight when the block ends
-        for (int s = 0; s < min(ST, asked); ++s)
-            (void)mbar_wait_short(smem_u32(&code_full[s]), (uint32_t)((asked - 1 - s) / ST) & 1u, c.status);
     } else if (warp == 1) {
         const uint32_t idesc_s = idesc_f32acc(0, 0, kRows, kTokens);
         const uint32_t idesc_o = idesc_f32acc(0, 0, kRows, 0) | (uint32_t)(c.D >> 3) << 17 | 1u << 16;  // B is N-major
@@ -407,8 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
 #pragma unroll 1
                     for (int s = 0; s < c.D / 16; ++s) step(s);
                 }
-                mma_commit(smem_u32(&tile_empty[slot]));
-                mma_commit(smem_u32(&s_full[slot]));
+                mma_commit(smem_u32(&s_full[slot]));  // the tile's end as well
             }
             __syncwarp();
         };
@@ -429,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
 #pragma unroll
                     for (int s = 0; s < kTokens / 16; ++s)
                         mma_ts(o, p + 8 * s, vd + (uint64_t)s * (2048 >> 4), idesc_o, i >= 2 || s > 0);
-                    mma_commit(smem_u32(&tile_empty[2 + slot]));
+                    mma_commit(smem_u32(&v_empty[slot]));
                 }
                 __syncwarp();
                 if (i + 2 < count) scores(m + 2);
@@ -446,16 +404,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         }
         __syncwarp();
     } else {
-        // warp 2: scales of K, 3: of V; four tokens a lane
+        // warp 2: scales of K, 3: of V; four tokens a lane, their words asked for a chunk ahead
         const bool is_v = warp == 3;
         float unit[2] = {0.0f, 0.0f};
-        Ring ring;
         int left = 0, item = 0, len = 0, pos = 0;
+        uint4 ahead = make_uint4(0, 0, 0, 0);
+        uint32_t ahead_there = 0;
+        auto ask = [&](int n) {
+            if (!wait(place_full[n % kPlaces], n / kPlaces)) return;
+            const int64_t at = places[n % kPlaces][lane / 4].words;
+            release(place_empty[n % kPlaces]);
+            const uint32_t lanes_there = __ballot_sync(0xffffffffu, at >= 0);  // of each four lanes, a 16-token tile
+            ahead_there = 0;
+#pragma unroll
+            for (int t = 0; t < 8; ++t) ahead_there |= (lanes_there >> (4 * t) & 1u) << t;
+            if (at >= 0)
+                asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(ahead.x), "=r"(ahead.y), "=r"(ahead.z), "=r"(ahead.w)
+                             : "l"(c.pages + at + (is_v ? 4 * c.page : 0) + 16 * (lane & 3)));
+        };
+        ask(0);
 #pragma unroll 1
-        for (int i = 0; i < 2 * chunks && ok; ++i, ring.next(ST)) {
-            const Operand op(i, chunks);
-            if (op.is_v != is_v) continue;
-            const int n = op.n, slot = n % kInfos;
+        for (int n = 0; n < chunks && ok; ++n) {
+            const int slot = n % kInfos;
             if (left == 0) {
                 if (!wait(item_full[item % kItems], item / kItems)) break;
                 const Item &at = items[item % kItems];
@@ -466,11 +437,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             }
             --left;
             Info &info = infos[slot];
+            const uint4 w = ahead;
+            const uint32_t there = ahead_there;
+            if (n + 1 < chunks) ask(n + 1);
             if (n >= kInfos && !wait(info_empty[slot], n / kInfos - 1)) break;
-            if (!wait(code_full[ring.stage], ring.use)) break;
-            const uint32_t there = *reinterpret_cast<volatile uint32_t *>(&present[ring.stage]);
-            const uint4 w = lds_v4(codes + ring.stage * code_bytes + kTokens * c.row_bytes + 16 * lane);
-            release(code_empty[ring.stage]);
             float s[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
             const int valid = there >> (lane / 4) & 1u ? len - pos : 0;  // beyond the sequence the words are anything
 #pragma unroll
@@ -496,55 +466,91 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         }
     }
     } else if (warp < kRowWarp0) {
-        regs_dec<80>();
-        const int t = threadIdx.x - kCodeWarp0 * 32;
-        Ring ring;
+        regs_dec<104>();
+        // Warps 4 and 5 have K, 6 and 7 V, each 64 tokens of a chunk, in registers a chunk ahead.  Eight
+        // lanes have four 16-byte pieces of two rows at a time: what they store of a chunk of 8 f16 then
+        // lies in eight different places of the swizzle.
+        const int is_v = (warp - kCodeWarp0) >> 1, side = warp & 1;
+        const int r8 = 2 * (lane >> 3) + (lane >> 2 & 1), quad = lane & 3;
+        constexpr int H = U4 ? 1 : DP / 64;  // pieces of a row that a lane has
+        const uint8_t *from = c.pages + (is_v ? c.page * c.row_bytes : 0) + r8 * c.row_bytes + 16 * quad;
+        const uint8_t *word_from = c.pages + (is_v ? 4 * c.page : 0) + 4 * r8;
+        uint32_t to[H];  // of the lane's pieces, in a tile
+        bool has[H];
+        const uint32_t top = tiles + 2 * is_v * TILE + (64 * side + r8) * 128;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const int piece = 4 * h + quad;
+            has[h] = piece < c.chunks;
+            const int chunk = has[h] ? kv_chunk(c.chunks, r8, piece) : 0;  // which it holds: the order is its own inverse
+            // u4: a piece has four chunks of f16; those of the second panel begin with the third of them
+            if constexpr (U4) to[h] = top + (chunk >> 1) * PANEL + (((4 * (chunk & 1) + (chunk & 2)) ^ r8) << 4);
+            else to[h] = top + (chunk >> 2) * PANEL + (((2 * (chunk & 3)) ^ r8) << 4);
+        }
+        const bool second = U4 && to[0] - top >= PANEL;
+        uint4 w[2][4][H];  // two halves of 32 tokens, 8 of them at a time
+        uint32_t word[2][4];
+        auto ask = [&](int n, int u) {
+            const Tile16 *place = places[n % kPlaces] + 4 * side + 2 * u;
+            const int64_t at[2] = {place[0].rows, place[1].rows};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint8_t *row = from + at[k >> 1] + (k & 1) * 8 * c.row_bytes;
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    w[u][k][h] = make_uint4(0, 0, 0, 0);
+                    if (has[h] && at[k >> 1] >= 0)
+                        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w[u][k][h].x), "=r"(w[u][k][h].y), "=r"(w[u][k][h].z), "=r"(w[u][k][h].w)
+                                     : "l"(row + 64 * h));
+                }
+                word[u][k] = 0;
+                if (U4 && at[k >> 1] >= 0)
+                    asm volatile("ld.global.u32 %0, [%1];"
+                                 : "=r"(word[u][k])
+                                 : "l"(word_from + place[k >> 1].words + (k & 1) * 32));
+            }
+        };
+        if (chunks > 0 && wait(place_full[0], 0)) {
+            ask(0, 0);
+            ask(0, 1);
+            release(place_empty[0]);
+        }
 #pragma unroll 1
-        for (int i = 0; i < 2 * chunks && ok; ++i, ring.next(ST)) {
-            {
-                const Operand op(i, chunks);
-                const int n = op.n, stage = ring.stage, slot = 2 * op.is_v + (n & 1);
-                if (n >= 2 && !wait(tile_empty[slot], (n >> 1) - 1)) break;
-                if (!wait(code_full[stage], ring.use)) break;
-                const uint32_t from = codes + stage * code_bytes, row = from + t * c.row_bytes;
-                const uint32_t to = tiles + slot * TILE + t * 128;
-                auto put = [&](int chunk, const uint32_t (&f)[4]) {  // chunk of 8 f16
-                    sts_v4(to + (chunk >> 3) * PANEL + (((chunk & 7) ^ (t & 7)) << 4), f[0], f[1], f[2], f[3]);
-                };
-                // all loads of the row, then all stores: one after the other each waits for the last
-                constexpr int N = U4 ? DP / 32 : DP / 16;
-                uint4 w[N];
+        for (int n = 0; n < chunks && ok; ++n) {
+            if (n + 1 < chunks && !wait(place_full[(n + 1) % kPlaces], (n + 1) / kPlaces)) break;
+            if (n >= 2 && !wait((is_v ? v_empty : s_full)[n & 1], (n >> 1) - 1)) break;
+            const uint32_t tile = (n & 1) * TILE;
 #pragma unroll
-                for (int ch = 0; ch < N; ++ch)
-                    if (ch < c.chunks) w[ch] = lds_v4(row + 16 * kv_chunk(c.chunks, t, ch));
-                uint32_t word = 0;
-                if constexpr (U4)
-                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(word) : "r"(from + kTokens * c.row_bytes + 4 * t) : "memory");
-                const Zero z = zero_of(word & 15u, word & 15u);
+            for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                for (int ch = 0; ch < N; ++ch) {
-                    if (ch >= c.chunks) break;
-                    uint32_t f[4];
-                    if constexpr (U4) {
-                        u4_pairs(w[ch].x, z, f), put(4 * ch, f);
-                        u4_pairs(w[ch].y, z, f), put(4 * ch + 1, f);
-                        u4_pairs(w[ch].z, z, f), put(4 * ch + 2, f);
-                        u4_pairs(w[ch].w, z, f), put(4 * ch + 3, f);
-                    } else {
-                        s8_pairs(w[ch].x, f[0], f[1]), s8_pairs(w[ch].y, f[2], f[3]), put(2 * ch, f);
-                        s8_pairs(w[ch].z, f[0], f[1]), s8_pairs(w[ch].w, f[2], f[3]), put(2 * ch + 1, f);
+                for (int k = 0; k < 4; ++k) {
+                    const Zero z = zero_of(word[u][k] & 15u, word[u][k] & 15u);
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        if (!has[h]) continue;
+                        const uint32_t at = to[h] + tile + (4 * u + k) * 1024;
+                        const uint4 v = w[u][k][h];
+                        uint32_t f[4];
+                        if constexpr (U4) {
+                            u4_pairs(second ? v.z : v.x, z, f), sts_v4(at, f[0], f[1], f[2], f[3]);
+                            u4_pairs(second ? v.w : v.y, z, f), sts_v4(at ^ 16u, f[0], f[1], f[2], f[3]);
+                            u4_pairs(second ? v.x : v.z, z, f), sts_v4(at ^ 32u, f[0], f[1], f[2], f[3]);
+                            u4_pairs(second ? v.y : v.w, z, f), sts_v4(at ^ 48u, f[0], f[1], f[2], f[3]);
+                        } else {
+                            s8_pairs(v.x, f[0], f[1]), s8_pairs(v.y, f[2], f[3]), sts_v4(at, f[0], f[1], f[2], f[3]);
+                            s8_pairs(v.z, f[0], f[1]), s8_pairs(v.w, f[2], f[3]), sts_v4(at ^ 16u, f[0], f[1], f[2], f[3]);
+                        }
                     }
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&tile_full[slot]));
-                    mbar_arrive(smem_u32(&code_empty[stage]));
-                }
+                if (n + 1 < chunks) ask(n + 1, u);
             }
+            if (n + 1 < chunks) release(place_empty[(n + 1) % kPlaces]);
+            fence_proxy_async_smem();
+            release(tile_full[2 * is_v + (n & 1)]);
         }
     } else {
-        regs_inc<176>();
+        regs_inc<168>();
         const int stream = (warp - kRowWarp0) >> 2, r = (threadIdx.x - kRowWarp0 * 32) & 127;
         const int g = lane >> 2, j = lane & 3;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -753,11 +759,11 @@ qnn_status launch(KvAttnArgs a, cudaStream_t s)
 {
     auto kern = kv_attn_rows_kernel<U4, DP>;
     static std::atomic<uint64_t> opted_in{0};
-    constexpr int kStatic = 9 << 10, kMost = (227 << 10) - kStatic;
-    const int fixed = 1024 + 5 * kTokens * DP * 2 + (a.c.batch + 1) * 8, stage = kTokens * (a.c.row_bytes + 4);
-    a.stages = std::min(kMaxStages, (kMost - fixed) / stage);
+    // one block on an SM, whatever it needs: tensor memory is taken whole
+    constexpr int kMost = 200 << 10;
+    const int need = 1024 + 5 * kTokens * DP * 2 + (a.c.batch + 1) * 8;
     if (!opt_in_smem(kern, kMost, opted_in, 100)) return QNN_ERR_CUDA;
-    return kv_launch(kern, dim3((unsigned)a.blocks), kThreads, fixed + a.stages * stage, s, a);
+    return kv_launch(kern, dim3((unsigned)a.blocks), kThreads, std::max(need, 120 << 10), s, a);
 }
 
 }  // namespace
