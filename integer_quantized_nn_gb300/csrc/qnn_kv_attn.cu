@@ -96,6 +96,7 @@ extern "C" qnn_status q_kv_attn(const void *q, qnn_dtype x_dt, int64_t ld_q, int
     a.ld_q = ld_q ? ld_q : width;
     a.ld_out = ld_out ? ld_out : width;
     if (a.ld_q < width || a.ld_out < width || a.ld_q > most || a.ld_out > most) return QNN_ERR_INVALID_ARG;
+    if ((int64_t)a.c.tokens * (heads_q / g->heads) > INT32_MAX - 256) return QNN_ERR_UNSUPPORTED;
     if (a.c.batch == 0 || a.c.rows == 0) return QNN_OK;
     if (!q || !out || !workspace || workspace_bytes < qnn_kv_attn_workspace_bytes(g, seqs, heads_q))
         return QNN_ERR_INVALID_ARG;

@@ -150,15 +150,15 @@ __device__ __forceinline__ int attn_units(const KvAttnArgs &a, int T, int len, i
 {
     int seen = len;
     if (!a.mask) {
-        const int64_t last = min((int64_t)(rt + 1) * width, (int64_t)T * a.group) - 1;
-        seen = len - T + (int)(last / a.group) + 1;
+        const int last = min((rt + 1) * width, T * a.group) - 1;  // all rows of a call are fewer than 2^31
+        seen = len - T + last / a.group + 1;
     }
-    return max(1, (int)(((int64_t)seen + kAttnChunk - 1) / kAttnChunk));
+    return max(1, (seen + kAttnChunk - 1) / kAttnChunk);
 }
 
 __device__ __forceinline__ int attn_row_tiles(const KvAttnArgs &a, int T, int width)
 {
-    return (int)(((int64_t)T * a.group + width - 1) / width);
+    return (T * a.group + width - 1) / width;
 }
 
 // A sequence's units.
@@ -173,56 +173,69 @@ __device__ __forceinline__ int64_t attn_weight(const KvAttnArgs &a, const KvSeq 
     return n * a.c.heads;
 }
 
-// Where a unit stands; next() goes along the line.
+// Where a unit stands.
 struct AttnCursor {
-    int b, rt, h, chunk, units, tiles, T, len;
     int64_t first;
-
-    __device__ __forceinline__ void sequence(const KvAttnArgs &a, int width)
-    {
-        const KvSeq s = kv_seq(a.c, b);
-        T = max(s.T, 0);
-        len = s.len;
-        first = s.first;
-        tiles = attn_row_tiles(a, T, width);
-    }
-    // unit x of the line, whose sums up to each sequence are `sums`
-    __device__ __forceinline__ void find(const KvAttnArgs &a, const int64_t *sums, int64_t x, int width)
-    {
-        int lo = 0, hi = a.c.batch - 1;  // the last sequence that begins at or before x
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (sums[mid] <= x) lo = mid;
-            else hi = mid - 1;
-        }
-        b = lo;
-        sequence(a, width);
-        x -= sums[b];
-        for (rt = 0;; ++rt) {
-            units = attn_units(a, T, len, rt, width);
-            const int64_t n = (int64_t)units * a.c.heads;
-            if (x < n || rt + 1 >= tiles) break;
-            x -= n;
-        }
-        h = (int)(x / units);
-        chunk = (int)(x - (int64_t)h * units);
-    }
-    __device__ __forceinline__ void next(const KvAttnArgs &a, int width)
-    {
-        if (++chunk < units) return;
-        chunk = 0;
-        if (++h < a.c.heads) return;
-        h = 0;
-        if (++rt >= tiles) {
-            rt = 0;
-            do {
-                if (++b >= a.c.batch) return;
-                sequence(a, width);
-            } while (T <= 0);
-        }
-        units = attn_units(a, T, len, rt, width);
-    }
+    int b, rt, h, chunk, units, tiles, T, len;
 };
+
+__device__ __forceinline__ void attn_sequence(const KvAttnArgs &a, AttnCursor &c, int width)
+{
+    const KvSeq s = kv_seq(a.c, c.b);
+    c.T = max(s.T, 0);
+    c.len = s.len;
+    c.first = s.first;
+    c.tiles = attn_row_tiles(a, c.T, width);
+}
+
+// The cursor at unit x of the line, whose sums up to each sequence are `sums`.
+__device__ __forceinline__ AttnCursor attn_find(const KvAttnArgs &a, const int64_t *sums, int64_t x, int width)
+{
+    AttnCursor c;
+    int lo = 0, hi = a.c.batch - 1;  // the last sequence that begins at or before x
+#pragma unroll 1
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (sums[mid] <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    c.b = lo;
+    attn_sequence(a, c, width);
+    x -= sums[lo];
+#pragma unroll 1
+    for (c.rt = 0;; ++c.rt) {
+        c.units = attn_units(a, c.T, c.len, c.rt, width);
+        const int64_t n = (int64_t)c.units * a.c.heads;
+        if (x < n || c.rt + 1 >= c.tiles) break;
+        x -= n;
+    }
+    c.h = (int)(x / c.units);
+    c.chunk = (int)(x - (int64_t)c.h * c.units);
+    return c;
+}
+
+// The cursor at the first unit of the next row tile.
+__device__ __forceinline__ AttnCursor attn_next_rows(const KvAttnArgs &a, AttnCursor c, int width)
+{
+    c.h = 0;
+    if (++c.rt >= c.tiles) {
+        c.rt = 0;
+#pragma unroll 1
+        do {
+            if (++c.b >= a.c.batch) return c;
+            attn_sequence(a, c, width);
+        } while (c.T <= 0);
+    }
+    c.units = attn_units(a, c.T, c.len, c.rt, width);
+    return c;
+}
+
+__device__ __forceinline__ void attn_next(const KvAttnArgs &a, AttnCursor &c, int width)
+{
+    if (++c.chunk < c.units) return;
+    c.chunk = 0;
+    if (++c.h >= a.c.heads) c = attn_next_rows(a, c, width);
+}
 
 // sums[i]: the units of sequences 0 .. i - 1, by all threads of a block; returns all of them.
 template <int THREADS>

@@ -108,6 +108,22 @@ __device__ __forceinline__ int sum_channel(int g, int i, int half)
     else return DP == 64 ? 8 * g + 2 * i + half : 128 * (i / 8) + 16 * g + 2 * (i % 8) + half;
 }
 
+// Finding an item is kept out of the loop from tile to tile, which has to stay in the instruction cache.
+__device__ __noinline__ AttnCursor find(const KvAttnArgs &a, const int64_t *sums, int64_t x, int width)
+{
+    return attn_find(a, sums, x, width);
+}
+__device__ __noinline__ AttnCursor next_rows(const KvAttnArgs &a, AttnCursor c, int width)
+{
+    return attn_next_rows(a, c, width);
+}
+__device__ __forceinline__ void next(const KvAttnArgs &a, AttnCursor &c, int width)
+{
+    if (++c.chunk < c.units) return;
+    c.chunk = 0;
+    if (++c.h >= a.c.heads) c = next_rows(a, c, width);
+}
+
 // A stage: K rows, V rows, K words, V words of 16 tokens.
 __host__ __device__ inline int stage_bytes(int row_bytes) { return 16 * (2 * row_bytes + 8); }
 
@@ -137,9 +153,7 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
     }
 
     // the copies' side: `ahead` is the unit whose page has been looked up
-    AttnCursor ahead, at;
-    ahead.find(a, sums, share.from, S::kRows);
-    at = ahead;
+    AttnCursor ahead = find(a, sums, share.from, S::kRows), at = ahead;
     int64_t asked = share.from;  // units whose copies have been issued
     int page, in_page;
     auto look_up = [&]() {
@@ -167,7 +181,7 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
                     copy_async16(to + 2 * rows, head + 2 * all + (lane < 4 ? 0 : 4 * c.page - 64) + in_page * 64 + 16 * lane);
             }
             if (++asked < share.to) {
-                ahead.next(a, S::kRows);
+                next(a, ahead, S::kRows);
                 look_up();
             }
         }
@@ -256,7 +270,7 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
             ref[nt][0] = ref[nt][1] = l[nt][0] = l[nt][1] = 0.0f;
         }
 
-        for (; x < end; ++x, at.next(a, S::kRows)) {
+        for (; x < end; ++x, next(a, at, S::kRows)) {
             const int pos0 = (at.chunk * kWarps + warp) * 16;
             copies_wait(ST - 1);
             __syncwarp();

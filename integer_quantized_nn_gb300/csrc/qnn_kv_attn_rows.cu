@@ -32,8 +32,8 @@ struct Item {
 };
 constexpr int kItems = 4;
 
-// Where 16 tokens of a chunk are: bytes from the first page to their K rows and their K words; -1:
-// they are not there.
+// Where 16 tokens of a chunk are: bytes from the first page to their K rows and their K words; words -1:
+// they are not there, and rows are those of some place in the cache.
 struct Tile16 {
     int64_t rows, words;
 };
@@ -314,14 +314,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
     regs_dec<72>();
     if (chunks <= 0) {
     } else if (warp == 0) {
-        AttnCursor at;
-        at.find(a, sums, share.from, kRows);
+        AttnCursor at = attn_find(a, sums, share.from, kRows);
         int left = 0, item = 0;
 #pragma unroll 1
         for (int n = 0; n < chunks && ok; ++n) {
             if (left == 0) {
-                const int slot = item % kItems;
-                if (item >= kItems && !wait(item_empty[slot], item / kItems - 1)) break;
+                const int slot = (unsigned)item % kItems;
+                if (item >= kItems && !wait(item_empty[slot], (unsigned)item / kItems - 1)) break;
                 left = min(at.units - at.chunk, chunks - n);
                 if (lane == 0) {
                     items[slot] = {at.first, at.b, at.rt, at.h, at.chunk, left, at.units, at.T, at.len};
@@ -330,8 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 ++item;
             }
             --left;
-            const int slot = n % kPlaces, tile = at.chunk * (kTokens / 16) + lane;
-            Tile16 place = {-1, -1};
+            const int slot = (unsigned)n % kPlaces, tile = at.chunk * (kTokens / 16) + lane;
+            Tile16 place = {0, -1};
             if (lane < kTokens / 16 && tile * 16 < at.len) {
                 int in_page;
                 const int page = attn_page(a, at.b, tile, &in_page);
@@ -340,10 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                     place = {head + in_page * 16 * c.row_bytes, head + 2 * c.page * c.row_bytes + in_page * 64};
                 }
             }
-            if (n >= kPlaces && !wait(place_empty[slot], n / kPlaces - 1)) break;
+            if (n >= kPlaces && !wait(place_empty[slot], (unsigned)n / kPlaces - 1)) break;
             if (lane < kTokens / 16) places[slot][lane] = place;
             release(place_full[slot]);
-            if (n + 1 < chunks) at.next(a, kRows);
+            if (n + 1 < chunks) attn_next(a, at, kRows);
         }
     } else if (warp == 1) {
         const uint32_t idesc_s = idesc_f32acc(0, 0, kRows, kTokens);
@@ -372,25 +371,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         };
         int n = 0, item = 0;
         while (n < chunks && ok) {
-            if (!wait(item_full[item % kItems], item / kItems)) break;
-            const int count = items[item % kItems].count;
-            release(item_empty[item % kItems]);
+            if (!wait(item_full[(unsigned)item % kItems], (unsigned)item / kItems)) break;
+            const int count = items[(unsigned)item % kItems].count;
+            release(item_empty[(unsigned)item % kItems]);
             if (!wait(q_full, item)) break;
-            for (int i = 0; i < 2 && i < count; ++i) scores(n + i);
-            for (int i = 0; i < count && ok; ++i) {
-                const int m = n + i, slot = m & 1;
-                if (!wait(p_ready[slot], m >> 1) || !wait(tile_full[2 + slot], m >> 1)) break;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint64_t vd = sdesc_n_major(tiles + (2 + slot) * TILE, PANEL);
-                    const uint32_t p = tmem + slot * kTokens, o = tmem + kOCol + slot * 128;
+#pragma unroll 1
+            for (int i = 0; i < count + 2 && ok; ++i) {  // S of chunk i, after O of chunk i - 2
+                if (i >= 2) {
+                    const int m = n + i - 2, slot = m & 1;
+                    if (!wait(p_ready[slot], m >> 1) || !wait(tile_full[2 + slot], m >> 1)) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint64_t vd = sdesc_n_major(tiles + (2 + slot) * TILE, PANEL);
+                        const uint32_t p = tmem + slot * kTokens, o = tmem + kOCol + slot * 128;
 #pragma unroll
-                    for (int s = 0; s < kTokens / 16; ++s)
-                        mma_ts(o, p + 8 * s, vd + (uint64_t)s * (2048 >> 4), idesc_o, i >= 2 || s > 0);
-                    mma_commit(smem_u32(&v_empty[slot]));
+                        for (int s = 0; s < kTokens / 16; ++s)
+                            mma_ts(o, p + 8 * s, vd + (uint64_t)s * (2048 >> 4), idesc_o, i >= 4 || s > 0);
+                        mma_commit(smem_u32(&v_empty[slot]));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-                if (i + 2 < count) scores(m + 2);
+                if (i < count) scores(n + i);
             }
             if (ok && lane == 0) mma_commit(smem_u32(&o_full));
             __syncwarp();
@@ -411,9 +412,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         uint4 ahead = make_uint4(0, 0, 0, 0);
         uint32_t ahead_there = 0;
         auto ask = [&](int n) {
-            if (!wait(place_full[n % kPlaces], n / kPlaces)) return;
-            const int64_t at = places[n % kPlaces][lane / 4].words;
-            release(place_empty[n % kPlaces]);
+            if (!wait(place_full[(unsigned)n % kPlaces], (unsigned)n / kPlaces)) return;
+            const int64_t at = places[(unsigned)n % kPlaces][lane / 4].words;
+            release(place_empty[(unsigned)n % kPlaces]);
             const uint32_t lanes_there = __ballot_sync(0xffffffffu, at >= 0);  // of each four lanes, a 16-token tile
             ahead_there = 0;
 #pragma unroll
@@ -423,24 +424,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                              : "=r"(ahead.x), "=r"(ahead.y), "=r"(ahead.z), "=r"(ahead.w)
                              : "l"(c.pages + at + (is_v ? 4 * c.page : 0) + 16 * (lane & 3)));
         };
-        ask(0);
 #pragma unroll 1
-        for (int n = 0; n < chunks && ok; ++n) {
-            const int slot = n % kInfos;
+        for (int n = -1; n < chunks && ok; ++n) {
+            const int slot = n & (kInfos - 1);
+            const uint4 w = ahead;
+            const uint32_t there = ahead_there;
+            if (n + 1 < chunks) ask(n + 1);
+            if (n < 0) continue;
             if (left == 0) {
-                if (!wait(item_full[item % kItems], item / kItems)) break;
-                const Item &at = items[item % kItems];
+                if (!wait(item_full[(unsigned)item % kItems], (unsigned)item / kItems)) break;
+                const Item &at = items[(unsigned)item % kItems];
                 left = at.count, len = at.len, pos = at.chunk * kTokens + 4 * lane;
-                release(item_empty[item % kItems]);
+                release(item_empty[(unsigned)item % kItems]);
                 ++item;
                 unit[0] = unit[1] = pow2i(-126);
             }
             --left;
             Info &info = infos[slot];
-            const uint4 w = ahead;
-            const uint32_t there = ahead_there;
-            if (n + 1 < chunks) ask(n + 1);
-            if (n >= kInfos && !wait(info_empty[slot], n / kInfos - 1)) break;
+            if (n >= kInfos && !wait(info_empty[slot], (unsigned)n / kInfos - 1)) break;
             float s[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
             const int valid = there >> (lane / 4) & 1u ? len - pos : 0;  // beyond the sequence the words are anything
 #pragma unroll
@@ -473,16 +474,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         const int is_v = (warp - kCodeWarp0) >> 1, side = warp & 1;
         const int r8 = 2 * (lane >> 3) + (lane >> 2 & 1), quad = lane & 3;
         constexpr int H = U4 ? 1 : DP / 64;  // pieces of a row that a lane has
-        const uint8_t *from = c.pages + (is_v ? c.page * c.row_bytes : 0) + r8 * c.row_bytes + 16 * quad;
-        const uint8_t *word_from = c.pages + (is_v ? 4 * c.page : 0) + 4 * r8;
+        const uint8_t *from[H], *word_from = c.pages + (is_v ? 4 * c.page : 0) + 4 * r8;
         uint32_t to[H];  // of the lane's pieces, in a tile
-        bool has[H];
         const uint32_t top = tiles + 2 * is_v * TILE + (64 * side + r8) * 128;
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-            const int piece = 4 * h + quad;
-            has[h] = piece < c.chunks;
-            const int chunk = has[h] ? kv_chunk(c.chunks, r8, piece) : 0;  // which it holds: the order is its own inverse
+            const int piece = min(4 * h + quad, c.chunks - 1);  // beyond the row: its last once more
+            from[h] = c.pages + (is_v ? c.page * c.row_bytes : 0) + r8 * c.row_bytes + 16 * piece;
+            const int chunk = kv_chunk(c.chunks, r8, piece);  // which the piece holds: the order is its own inverse
             // u4: a piece has four chunks of f16; those of the second panel begin with the third of them
             if constexpr (U4) to[h] = top + (chunk >> 1) * PANEL + (((4 * (chunk & 1) + (chunk & 2)) ^ r8) << 4);
             else to[h] = top + (chunk >> 2) * PANEL + (((2 * (chunk & 3)) ^ r8) << 4);
@@ -491,24 +490,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         uint4 w[2][4][H];  // two halves of 32 tokens, 8 of them at a time
         uint32_t word[2][4];
         auto ask = [&](int n, int u) {
-            const Tile16 *place = places[n % kPlaces] + 4 * side + 2 * u;
-            const int64_t at[2] = {place[0].rows, place[1].rows};
+            const Tile16 *place = places[(unsigned)n % kPlaces] + 4 * side + 2 * u;
+            if (c.num_pages == 0) return;  // any codes will do for tiles that are not there, but not from nowhere
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint8_t *row = from + at[k >> 1] + (k & 1) * 8 * c.row_bytes;
+                const int64_t at = place[k >> 1].rows + (k & 1) * 8 * c.row_bytes;
 #pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    w[u][k][h] = make_uint4(0, 0, 0, 0);
-                    if (has[h] && at[k >> 1] >= 0)
-                        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(w[u][k][h].x), "=r"(w[u][k][h].y), "=r"(w[u][k][h].z), "=r"(w[u][k][h].w)
-                                     : "l"(row + 64 * h));
-                }
-                word[u][k] = 0;
-                if (U4 && at[k >> 1] >= 0)
+                for (int h = 0; h < H; ++h)
+                    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[u][k][h].x), "=r"(w[u][k][h].y), "=r"(w[u][k][h].z), "=r"(w[u][k][h].w)
+                                 : "l"(from[h] + at));
+                if (U4)
                     asm volatile("ld.global.u32 %0, [%1];"
                                  : "=r"(word[u][k])
-                                 : "l"(word_from + place[k >> 1].words + (k & 1) * 32));
+                                 : "l"(word_from + max(place[k >> 1].words, (int64_t)0) + (k & 1) * 32));
             }
         };
         if (chunks > 0 && wait(place_full[0], 0)) {
@@ -518,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         }
 #pragma unroll 1
         for (int n = 0; n < chunks && ok; ++n) {
-            if (n + 1 < chunks && !wait(place_full[(n + 1) % kPlaces], (n + 1) / kPlaces)) break;
+            if (n + 1 < chunks && !wait(place_full[(unsigned)(n + 1) % kPlaces], (unsigned)(n + 1) / kPlaces)) break;
             if (n >= 2 && !wait((is_v ? v_empty : s_full)[n & 1], (n >> 1) - 1)) break;
             const uint32_t tile = (n & 1) * TILE;
 #pragma unroll
@@ -528,24 +523,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                     const Zero z = zero_of(word[u][k] & 15u, word[u][k] & 15u);
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
-                        if (!has[h]) continue;
-                        const uint32_t at = to[h] + tile + (4 * u + k) * 1024;
+                        const uint32_t at = tile + (4 * u + k) * 1024;
                         const uint4 v = w[u][k][h];
                         uint32_t f[4];
                         if constexpr (U4) {
-                            u4_pairs(second ? v.z : v.x, z, f), sts_v4(at, f[0], f[1], f[2], f[3]);
-                            u4_pairs(second ? v.w : v.y, z, f), sts_v4(at ^ 16u, f[0], f[1], f[2], f[3]);
-                            u4_pairs(second ? v.x : v.z, z, f), sts_v4(at ^ 32u, f[0], f[1], f[2], f[3]);
-                            u4_pairs(second ? v.y : v.w, z, f), sts_v4(at ^ 48u, f[0], f[1], f[2], f[3]);
+                            u4_pairs(second ? v.z : v.x, z, f), sts_v4(to[0] + at, f[0], f[1], f[2], f[3]);
+                            u4_pairs(second ? v.w : v.y, z, f), sts_v4((to[0] ^ 16u) + at, f[0], f[1], f[2], f[3]);
+                            u4_pairs(second ? v.x : v.z, z, f), sts_v4((to[0] ^ 32u) + at, f[0], f[1], f[2], f[3]);
+                            u4_pairs(second ? v.y : v.w, z, f), sts_v4((to[0] ^ 48u) + at, f[0], f[1], f[2], f[3]);
                         } else {
-                            s8_pairs(v.x, f[0], f[1]), s8_pairs(v.y, f[2], f[3]), sts_v4(at, f[0], f[1], f[2], f[3]);
-                            s8_pairs(v.z, f[0], f[1]), s8_pairs(v.w, f[2], f[3]), sts_v4(at ^ 16u, f[0], f[1], f[2], f[3]);
+                            s8_pairs(v.x, f[0], f[1]), s8_pairs(v.y, f[2], f[3]);
+                            sts_v4(to[h] + at, f[0], f[1], f[2], f[3]);
+                            s8_pairs(v.z, f[0], f[1]), s8_pairs(v.w, f[2], f[3]);
+                            sts_v4((to[h] ^ 16u) + at, f[0], f[1], f[2], f[3]);
                         }
                     }
                 }
                 if (n + 1 < chunks) ask(n + 1, u);
             }
-            if (n + 1 < chunks) release(place_empty[(n + 1) % kPlaces]);
+            if (n + 1 < chunks) release(place_empty[(unsigned)(n + 1) % kPlaces]);
             fence_proxy_async_smem();
             release(tile_full[2 * is_v + (n & 1)]);
         }
@@ -569,9 +565,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         };
         int n = 0, item = 0;
         while (n < chunks) {
-            (void)wait(item_full[item % kItems], item / kItems);
+            (void)wait(item_full[(unsigned)item % kItems], (unsigned)item / kItems);
             if (!all_ok()) break;
-            const Item &at = items[item % kItems];
+            const Item &at = items[(unsigned)item % kItems];
             const int count = at.count, row0 = at.rt * kRows;
             const int width = min(kRows, at.T * a.group - row0);
             const int rr = row0 + r, t = min(rr / a.group, at.T - 1);
@@ -649,8 +645,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             bool first = true;
             const int seen_by_all = a.mask ? at.len - at.T : min(at.len, at.len - at.T + t_first + 1);
             for (int i = (n ^ stream) & 1; i < count; i += 2) {
-                const int x = n + i, slot = x % kInfos;
-                if (!wait(info_full[slot], x / kInfos) || !wait(s_full[stream], x >> 1)) break;
+                const int x = n + i, slot = (unsigned)x % kInfos;
+                if (!wait(info_full[slot], (unsigned)x / kInfos) || !wait(s_full[stream], x >> 1)) break;
                 tc_fence_after();
                 const int pos0 = (at.chunk + i) * kTokens;
                 const uint32_t there = infos[slot].present;
@@ -743,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             }
             tc_fence_before();  // O has been read before q_full says so
             meet();
-            release(item_empty[item % kItems]);
+            release(item_empty[(unsigned)item % kItems]);
             n += count;
             ++item;
         }

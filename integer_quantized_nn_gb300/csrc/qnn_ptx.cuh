@@ -126,21 +126,17 @@ __device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity, ui
     return mbar_wait_idle_slow(bar, parity, status);
 }
 
-// The same bounded wait by the SM's clock: %globaltimer is read outside the SM, which a thread that
-// waits a few hundred cycles notices.  kWaitLimitClocks is about 2 s.
-constexpr long long kWaitLimitClocks = 1ll << 32;
+// The same bounded wait by counting: a tenth of the code and no clock to read, for kernels whose
+// loops fill the instruction cache.  A probe takes 20 cycles at least, so the limit is a second or more.
+constexpr uint32_t kWaitLimitProbes = 1u << 27;
 
 __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, uint32_t *status)
 {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (uint32_t i = 1;; ++i) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < kWaitLimitProbes; ++i)
         if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 15u) == 0 && clock64() - t0 > kWaitLimitClocks) {
-            if (status) atomicOr(status, kStatusTimeout);
-            return false;
-        }
-    }
+    if (status) atomicOr(status, kStatusTimeout);
+    return false;
 }
 
 // ---- proxies / bulk copies ---------------------------------------------------
