@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
     __shared__ __align__(16) Tile16 places[kPlaces][kTokens / 16];
     __shared__ Item items[kItems];
     __shared__ float row_m[2][kRows], row_l[2][kRows], row_top[2][kRows], stream_unit[2];
-    __shared__ uint32_t tmem_slot;
+    __shared__ uint32_t present[kPlaces], tmem_slot;  // 16-token tiles of a chunk that are there
     uint8_t *smem = raw + (-smem_u32(raw) & 1023u);  // the swizzle's atoms
     // tiles: K of even and odd chunks, V of both; q; the sums of the line
     const uint32_t tiles = smem_u32(smem), q_tile = tiles + 4 * TILE;
@@ -305,8 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         if (lane == 0) mbar_arrive(smem_u32(&bar));
     };
     auto wait = [&](uint64_t &bar, int use) {  // the use-th phase of a barrier, by a whole warp
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_short(smem_u32(&bar), (uint32_t)use & 1u, c.status));
-        return ok;
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_short(smem_u32(&bar), (uint32_t)use & 1u, nullptr));
+        return ok;  // a wait that gave up is reported at the end
     };
 
     // 128 registers a thread at the launch, and as many after: 72 + 104 + 2 * 168 = 4 * 128
@@ -340,7 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 }
             }
             if (n >= kPlaces && !wait(place_empty[slot], (unsigned)n / kPlaces - 1)) break;
+            const uint32_t there = __ballot_sync(0xffffffffu, place.words >= 0);
             if (lane < kTokens / 16) places[slot][lane] = place;
+            if (lane == 0) present[slot] = there;
             release(place_full[slot]);
             if (n + 1 < chunks) attn_next(a, at, kRows);
         }
@@ -414,11 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         auto ask = [&](int n) {
             if (!wait(place_full[(unsigned)n % kPlaces], (unsigned)n / kPlaces)) return;
             const int64_t at = places[(unsigned)n % kPlaces][lane / 4].words;
+            ahead_there = present[(unsigned)n % kPlaces];
             release(place_empty[(unsigned)n % kPlaces]);
-            const uint32_t lanes_there = __ballot_sync(0xffffffffu, at >= 0);  // of each four lanes, a 16-token tile
-            ahead_there = 0;
-#pragma unroll
-            for (int t = 0; t < 8; ++t) ahead_there |= (lanes_there >> (4 * t) & 1u) << t;
             if (at >= 0)
                 asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                              : "=r"(ahead.x), "=r"(ahead.y), "=r"(ahead.z), "=r"(ahead.w)
@@ -744,6 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             ++item;
         }
     }
+    if (!ok && lane == 0) atomicOr(c.status, kStatusTimeout);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
