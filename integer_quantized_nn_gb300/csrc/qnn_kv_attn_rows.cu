@@ -165,8 +165,8 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, const floa
         // by selection and not by index: the arrays stay in registers
         const float c0 = half ? cr[2] : cr[0], c1 = half ? cr[3] : cr[1];
         float m0 = half ? m[2] : m[0], m1 = half ? m[3] : m[1], r0 = half ? ref[2] : ref[0], r1 = half ? ref[3] : ref[1];
-        float l0 = half ? l[2] : l[0], l1 = half ? l[3] : l[1], top0 = -INFINITY, top1 = -INFINITY;
-        uint32_t b0[4], b1[4];
+        float l0 = half ? l[2] : l[0], l1 = half ? l[3] : l[1];
+        uint32_t b0[4], b1[4], p[32];
         if constexpr (MASKED) {
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
@@ -183,65 +183,82 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, const floa
                 y0.x = b0[i >> 2] & bit ? y0.x : -INFINITY, y0.y = b0[i >> 2] & (2 * bit) ? y0.y : -INFINITY;
                 y1.x = b1[i >> 2] & bit ? y1.x : -INFINITY, y1.y = b1[i >> 2] & (2 * bit) ? y1.y : -INFINITY;
             }
-            top0 = max3(top0, y0.x, y0.y), top1 = max3(top1, y1.x, y1.y);
             v[4 * i] = __float_as_uint(y0.x), v[4 * i + 1] = __float_as_uint(y0.y);
             v[4 * i + 2] = __float_as_uint(y1.x), v[4 * i + 3] = __float_as_uint(y1.y);
         }
-        top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 1)), top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
-        top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 2)), top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 2));
-        if (top0 != -INFINITY) top0 *= c0;
-        if (top1 != -INFINITY) top1 *= c1;
-        if (__any_sync(0xffffffffu, top0 > m0 + kAttnSlack || top1 > m1 + kAttnSlack || ratio != 1.0f)) {
-            const float u0 = fmaxf(m0, top0), u1 = fmaxf(m1, top1);
-            float f0 = m0 == -INFINITY ? 0.0f : ex2(m0 - u0), f1 = m1 == -INFINITY ? 0.0f : ex2(m1 - u1);
-            m0 = u0, m1 = u1;
-            r0 = u0 == -INFINITY ? 0.0f : u0, r1 = u1 == -INFINITY ? 0.0f : u1;
-            l0 *= f0, l1 *= f1, f0 *= ratio, f1 *= ratio;
-            if (!first) {
+        // The maxima so far are tried first: a thread's 32 weights of a row whose sum stays below 2^8 are
+        // all below it.  New maxima are looked for where they do not, at first and with a new unit.
+        bool fresh = MASKED || first || ratio != 1.0f;
+        float2 s0, s1;
 #pragma unroll 1
-                for (int b = 0; b < DP / 32; ++b) {
-                    uint32_t o[16];
-                    tmem_ld_frag(o_at + down + 32 * b, o);
-                    tmem_ld_wait();
+        for (int tries = 0;; ++tries) {
+            if (fresh) {
+                float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (e & 2 ? f1 : f0));
-                    tmem_st_frag(o_at + down + 32 * b, o);
+                for (int i = 0; i < 16; ++i) {
+                    top0 = max3(top0, __uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]));
+                    top1 = max3(top1, __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+                }
+                top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 1)), top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
+                top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 2)), top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 2));
+                if (top0 != -INFINITY) top0 *= c0;
+                if (top1 != -INFINITY) top1 *= c1;
+                const float u0 = fmaxf(m0, top0), u1 = fmaxf(m1, top1);
+                float f0 = m0 == -INFINITY ? 0.0f : ex2(m0 - u0), f1 = m1 == -INFINITY ? 0.0f : ex2(m1 - u1);
+                m0 = u0, m1 = u1;
+                r0 = u0 == -INFINITY ? 0.0f : u0, r1 = u1 == -INFINITY ? 0.0f : u1;
+                l0 *= f0, l1 *= f1, f0 *= ratio, f1 *= ratio;
+                if (!first && __any_sync(0xffffffffu, f0 != 1.0f || f1 != 1.0f)) {
+#pragma unroll 1
+                    for (int b = 0; b < DP / 32; ++b) {
+                        uint32_t o[16];
+                        tmem_ld_frag(o_at + down + 32 * b, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (e & 2 ? f1 : f0));
+                        tmem_st_frag(o_at + down + 32 * b, o);
+                    }
                 }
             }
-        }
-        uint32_t p[32];
-        float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
-        const float2 cc0 = make_float2(c0, c0), cc1 = make_float2(c1, c1), n0 = make_float2(-r0, -r0), n1 = make_float2(-r1, -r1);
+            const float2 cc0 = make_float2(c0, c0), cc1 = make_float2(c1, c1), n0 = make_float2(-r0, -r0), n1 = make_float2(-r1, -r1);
+            s0 = s1 = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float2 w = *reinterpret_cast<const float2 *>(vs + 8 * i);
-            float2 y0 = fma2(as_f2(v[4 * i], v[4 * i + 1]), cc0, n0), y1 = fma2(as_f2(v[4 * i + 2], v[4 * i + 3]), cc1, n1);
-            y0.x = ex2(y0.x), y0.y = ex2(y0.y), y1.x = ex2(y1.x), y1.y = ex2(y1.y);
-            if constexpr (MASKED) {  // -inf times a scale of zero is not
-                const uint32_t bit = 1u << (8 * (i & 3));
-                y0.x = b0[i >> 2] & bit ? y0.x : 0.0f, y0.y = b0[i >> 2] & (2 * bit) ? y0.y : 0.0f;
-                y1.x = b1[i >> 2] & bit ? y1.x : 0.0f, y1.y = b1[i >> 2] & (2 * bit) ? y1.y : 0.0f;
+            for (int i = 0; i < 16; ++i) {
+                const float2 w = *reinterpret_cast<const float2 *>(vs + 8 * i);
+                float2 y0 = fma2(as_f2(v[4 * i], v[4 * i + 1]), cc0, n0), y1 = fma2(as_f2(v[4 * i + 2], v[4 * i + 3]), cc1, n1);
+                y0.x = ex2(y0.x), y0.y = ex2(y0.y), y1.x = ex2(y1.x), y1.y = ex2(y1.y);
+                if constexpr (MASKED) {  // -inf times a scale of zero is not
+                    const uint32_t bit = 1u << (8 * (i & 3));
+                    y0.x = b0[i >> 2] & bit ? y0.x : 0.0f, y0.y = b0[i >> 2] & (2 * bit) ? y0.y : 0.0f;
+                    y1.x = b1[i >> 2] & bit ? y1.x : 0.0f, y1.y = b1[i >> 2] & (2 * bit) ? y1.y : 0.0f;
+                }
+                s0 = add2(s0, y0), s1 = add2(s1, y1);
+                y0 = mul2(y0, w), y1 = mul2(y1, w);
+                const __half2 h0 = __floats2half2_rn(y0.x, y0.y), h1 = __floats2half2_rn(y1.x, y1.y);
+                p[2 * i] = *reinterpret_cast<const uint32_t *>(&h0);
+                p[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&h1);
             }
-            s0 = add2(s0, y0), s1 = add2(s1, y1);
-            y0 = mul2(y0, w), y1 = mul2(y1, w);
-            const __half2 h0 = __floats2half2_rn(y0.x, y0.y), h1 = __floats2half2_rn(y1.x, y1.y);
-            p[2 * i] = *reinterpret_cast<const uint32_t *>(&h0);
-            p[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&h1);
+            s0.x += s0.y, s1.x += s1.y;
+            if (fresh) break;
+            fresh = __any_sync(0xffffffffu, s0.x > (float)(1 << kAttnSlack) || s1.x > (float)(1 << kAttnSlack));
+            if (!fresh) break;
         }
         tmem_st_pairs(s_at + down, p);
-        l0 += s0.x + s0.y, l1 += s1.x + s1.y;
+        l0 += s0.x, l1 += s1.x;
         if (half) m[2] = m0, m[3] = m1, ref[2] = r0, ref[3] = r1, l[2] = l0, l[3] = l1;
         else m[0] = m0, m[1] = m1, ref[0] = r0, ref[1] = r1, l[0] = l0, l[1] = l1;
     }
 }
 
-template <bool U4, int DP>
+// PAIR: the streams are two tiles of rows over the same chunks, which are converted once for both.
+template <bool U4, int DP, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_constant__ KvAttnArgs a)
 {
     constexpr uint32_t PANEL = kTokens * 128, TILE = PANEL * (DP / 64);
+    constexpr int ROWS = PAIR ? 2 * kRows : kRows;  // of an item
     const KvArgs &c = a.c;
     extern __shared__ __align__(16) uint8_t raw[];
-    __shared__ __align__(8) uint64_t place_full[kPlaces], place_empty[kPlaces], tile_full[4], v_empty[2],
+    __shared__ __align__(8) uint64_t place_full[kPlaces], place_empty[kPlaces], tile_full[4], tile_empty[4],
         info_full[kInfos], info_empty[kInfos], item_full[kItems], item_empty[kItems], s_full[2], p_ready[2], q_full, o_full,
         mma_end;
     __shared__ __align__(16) Info infos[kInfos];
@@ -250,9 +267,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
     __shared__ float row_m[2][kRows], row_l[2][kRows], row_top[2][kRows], stream_unit[2];
     __shared__ uint32_t present[kPlaces], tmem_slot;  // 16-token tiles of a chunk that are there
     uint8_t *smem = raw + (-smem_u32(raw) & 1023u);  // the swizzle's atoms
-    // tiles: K of even and odd chunks, V of both; q; the sums of the line
+    // tiles: K of even and odd chunks, V of both; q (of both streams); the sums of the line
     const uint32_t tiles = smem_u32(smem), q_tile = tiles + 4 * TILE;
-    int64_t *sums = reinterpret_cast<int64_t *>(smem + 5 * TILE);
+    int64_t *sums = reinterpret_cast<int64_t *>(smem + (PAIR ? 6 : 5) * TILE);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
     if (threadIdx.x == 0) {
@@ -262,17 +279,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(smem_u32(&tile_full[i]), kCodeWarps / 2);
+            mbar_init(smem_u32(&tile_empty[i]), 1);
         }
         for (int i = 0; i < kInfos; ++i) {
             mbar_init(smem_u32(&info_full[i]), 2);
-            mbar_init(smem_u32(&info_empty[i]), kRowWarps / 2);
+            mbar_init(smem_u32(&info_empty[i]), PAIR ? kRowWarps : kRowWarps / 2);
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(smem_u32(&item_full[i]), 1);
             mbar_init(smem_u32(&item_empty[i]), kRowWarps + 3);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&v_empty[i]), 1);
             mbar_init(smem_u32(&s_full[i]), 1);
             mbar_init(smem_u32(&p_ready[i]), kRowWarps / 2);
         }
@@ -294,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
     grid_dependency_launch();
     grid_dependency_wait();
 
-    const AttnShare share(attn_sums<kThreads>(a, sums, kRows), a.blocks, blockIdx.x);
+    const AttnShare share(attn_sums<kThreads>(a, sums, ROWS), a.blocks, blockIdx.x);
     int *record = reinterpret_cast<int *>(a.ws) + blockIdx.x * kAttnRecord;
     if (threadIdx.x == 0 && share.from >= share.to) record[0] = 0;
     const int chunks = (int)(share.to - share.from);
@@ -314,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
     regs_dec<72>();
     if (chunks <= 0) {
     } else if (warp == 0) {
-        AttnCursor at = attn_find(a, sums, share.from, kRows);
+        AttnCursor at = attn_find(a, sums, share.from, ROWS);
         int left = 0, item = 0;
 #pragma unroll 1
         for (int n = 0; n < chunks && ok; ++n) {
@@ -344,62 +361,65 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             if (lane < kTokens / 16) places[slot][lane] = place;
             if (lane == 0) present[slot] = there;
             release(place_full[slot]);
-            if (n + 1 < chunks) attn_next(a, at, kRows);
+            if (n + 1 < chunks) attn_next(a, at, ROWS);
         }
     } else if (warp == 1) {
         const uint32_t idesc_s = idesc_f32acc(0, 0, kRows, kTokens);
         const uint32_t idesc_o = idesc_f32acc(0, 0, kRows, 0) | (uint32_t)(c.D >> 3) << 17 | 1u << 16;  // B is N-major
-        auto scores = [&](int n) {
-            const int slot = n & 1;
-            if (!wait(tile_full[slot], n >> 1)) return;
-            tc_fence_after();
-            if (lane == 0) {
-                const uint64_t qd = sdesc_sw128(q_tile), kd = sdesc_sw128(tiles + slot * TILE);
-                auto step = [&](int s) {
-                    const uint64_t off = (uint64_t)((s >> 2) * (PANEL >> 4) + (s & 3) * 2);
-                    mma_f16_ss(tmem + slot * kTokens, qd + off, kd + off, idesc_s, s > 0);
-                };
-                // not an unrolled loop with a condition inside: what came of it read operands elsewhere
-                if (c.D == DP) {
-#pragma unroll
-                    for (int s = 0; s < DP / 16; ++s) step(s);
-                } else {
-#pragma unroll 1
-                    for (int s = 0; s < c.D / 16; ++s) step(s);
-                }
-                mma_commit(smem_u32(&s_full[slot]));  // the tile's end as well
-            }
-            __syncwarp();
-        };
+        // one thread, step by step: S of step t after O of step t - 2, which is of the same stream
+        const uint64_t kd0 = sdesc_sw128(tiles), vd0 = sdesc_n_major(tiles + 2 * TILE, PANEL), qd0 = sdesc_sw128(q_tile);
         int n = 0, item = 0;
-        while (n < chunks && ok) {
-            if (!wait(item_full[(unsigned)item % kItems], (unsigned)item / kItems)) break;
-            const int count = items[(unsigned)item % kItems].count;
-            release(item_empty[(unsigned)item % kItems]);
-            if (!wait(q_full, item)) break;
+        auto wait1 = [&](uint64_t &bar, int use) {
+            ok = ok && mbar_wait_short(smem_u32(&bar), (uint32_t)use & 1u, nullptr);
+            return ok;
+        };
+        while (lane == 0 && n < chunks && ok) {
+            if (!wait1(item_full[(unsigned)item % kItems], (unsigned)item / kItems)) break;
+            const int count = items[(unsigned)item % kItems].count, steps = PAIR ? 2 * count : count;
+            mbar_arrive(smem_u32(&item_empty[(unsigned)item % kItems]));
+            if (!wait1(q_full, item)) break;
 #pragma unroll 1
-            for (int i = 0; i < count + 2 && ok; ++i) {  // S of chunk i, after O of chunk i - 2
-                if (i >= 2) {
-                    const int m = n + i - 2, slot = m & 1;
-                    if (!wait(p_ready[slot], m >> 1) || !wait(tile_full[2 + slot], m >> 1)) break;
+            for (int t = 0; t < steps + 2; ++t) {
+                const int x = n + (PAIR ? t >> 1 : t), stream = PAIR ? t & 1 : x & 1;  // of S
+                const uint32_t s_at = tmem + stream * kTokens;
+                if (t >= 2) {
+                    const int y = PAIR ? x - 1 : x - 2, tile = y & 1;  // the chunk of O
+                    if (!wait1(p_ready[stream], PAIR ? y : y >> 1) || !wait1(tile_full[2 + tile], y >> 1)) break;
                     tc_fence_after();
-                    if (lane == 0) {
-                        const uint64_t vd = sdesc_n_major(tiles + (2 + slot) * TILE, PANEL);
-                        const uint32_t p = tmem + slot * kTokens, o = tmem + kOCol + slot * 128;
+                    const uint64_t vd = vd0 + (uint64_t)(tile * (TILE >> 4));
+                    const uint32_t o = tmem + kOCol + stream * 128;
 #pragma unroll
-                        for (int s = 0; s < kTokens / 16; ++s)
-                            mma_ts(o, p + 8 * s, vd + (uint64_t)s * (2048 >> 4), idesc_o, i >= 4 || s > 0);
-                        mma_commit(smem_u32(&v_empty[slot]));
-                    }
-                    __syncwarp();
+                    for (int s = 0; s < kTokens / 16; ++s)
+                        mma_ts(o, s_at + 8 * s, vd + (uint64_t)s * (2048 >> 4), idesc_o, t >= 4 || s > 0);
+                    if (!PAIR || stream) mma_commit(smem_u32(&tile_empty[2 + tile]));
                 }
-                if (i < count) scores(n + i);
+                if (t < steps) {
+                    const int tile = x & 1;
+                    if (!wait1(tile_full[tile], x >> 1)) break;
+                    tc_fence_after();
+                    const uint64_t kd = kd0 + (uint64_t)(tile * (TILE >> 4)), qd = qd0 + (uint64_t)(PAIR ? stream * (TILE >> 4) : 0);
+                    auto step = [&](int s) {
+                        const uint64_t off = (uint64_t)((s >> 2) * (PANEL >> 4) + (s & 3) * 2);
+                        mma_f16_ss(s_at, qd + off, kd + off, idesc_s, s > 0);
+                    };
+                    // not an unrolled loop with a condition inside: what came of it read operands elsewhere
+                    if (c.D == DP) {
+#pragma unroll
+                        for (int s = 0; s < DP / 16; ++s) step(s);
+                    } else {
+#pragma unroll 1
+                        for (int s = 0; s < c.D / 16; ++s) step(s);
+                    }
+                    mma_commit(smem_u32(&s_full[stream]));
+                    if (!PAIR || stream) mma_commit(smem_u32(&tile_empty[tile]));
+                }
             }
-            if (ok && lane == 0) mma_commit(smem_u32(&o_full));
-            __syncwarp();
+            if (ok) mma_commit(smem_u32(&o_full));
             n += count;
             ++item;
         }
+        __syncwarp();
+        ok = __shfl_sync(0xffffffffu, ok, 0);
         // nothing of this thread's is in flight when the block ends
         if (lane == 0) {
             mma_commit(smem_u32(&mma_end));
@@ -451,10 +471,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             if (is_v) {
                 uint32_t top = __float_as_uint(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])));
                 top = __reduce_max_sync(0xffffffffu, top);
-                const float old = n & 1 ? unit[1] : unit[0];
+                const float old = !PAIR && (n & 1) ? unit[1] : unit[0];
                 const float now = fmaxf(old, __uint_as_float((top + 0x7fffffu) & 0xff800000u));
                 const float per = __uint_as_float(0x7f000000u - __float_as_uint(now));
-                if (n & 1) unit[1] = now;
+                if (!PAIR && (n & 1)) unit[1] = now;
                 else unit[0] = now;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[e] = s[e] * per * (float)(1 << kAttnRoom);
@@ -513,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
 #pragma unroll 1
         for (int n = 0; n < chunks && ok; ++n) {
             if (n + 1 < chunks && !wait(place_full[(unsigned)(n + 1) % kPlaces], (unsigned)(n + 1) / kPlaces)) break;
-            if (n >= 2 && !wait((is_v ? v_empty : s_full)[n & 1], (n >> 1) - 1)) break;
+            if (n >= 2 && !wait(tile_empty[2 * is_v + (n & 1)], (n >> 1) - 1)) break;
             const uint32_t tile = (n & 1) * TILE;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -567,10 +587,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             (void)wait(item_full[(unsigned)item % kItems], (unsigned)item / kItems);
             if (!all_ok()) break;
             const Item &at = items[(unsigned)item % kItems];
-            const int count = at.count, row0 = at.rt * kRows;
+            const int count = at.count, row0 = at.rt * ROWS + (PAIR ? stream * kRows : 0);
             const int width = min(kRows, at.T * a.group - row0);
             const int rr = row0 + r, t = min(rr / a.group, at.T - 1);
-            const int t_first = row0 / a.group;
+            const int t_first = min(row0 / a.group, at.T - 1);
             const bool live = r < width, starts_here = n > 0 || at.chunk == 0, ends_here = at.chunk + count == at.units;
             if (threadIdx.x == kRowWarp0 * 32 && n + count == chunks) {
                 record[0] = starts_here && !ends_here;
@@ -580,17 +600,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             const int64_t out_row = at.first + rr / a.group;
             const int hq = at.h * a.group + rr % a.group;
 
-            // q: half a row for each thread; a row's largest value is brought near f16's by a power of two
+            // q: a row for each thread, or half a row; its largest value is brought near f16's by a power of two
             float cq;
             {
-                const int half = c.D / 2;  // a multiple of 16
-                const uint16_t *qp = static_cast<const uint16_t *>(a.q) + out_row * a.ld_q + (int64_t)hq * c.D + stream * half;
-                uint4 w[DP / 16];
+                constexpr int W = PAIR ? DP / 8 : DP / 16;  // pieces of 8 values
+                const int mine = PAIR ? c.D : c.D / 2;      // a multiple of 16
+                const uint16_t *qp = static_cast<const uint16_t *>(a.q) + out_row * a.ld_q + (int64_t)hq * c.D +
+                                     (PAIR ? 0 : stream * mine);
+                uint4 w[W];
                 float top = 0.0f;
 #pragma unroll
-                for (int i = 0; i < DP / 16; ++i) {
+                for (int i = 0; i < W; ++i) {
                     w[i] = make_uint4(0, 0, 0, 0);
-                    if (live && 8 * i < half)
+                    if (live && 8 * i < mine)
                         asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
                                      : "l"(qp + 8 * i));
@@ -600,21 +622,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                     return a.bf16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((uint16_t)h));
                 };
 #pragma unroll
-                for (int i = 0; i < DP / 16; ++i) {
+                for (int i = 0; i < W; ++i) {
                     const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
                     for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(value(u[e / 2], e & 1)));
                 }
-                row_top[stream][r] = top;
-                meet();
-                top = fmaxf(row_top[0][r], row_top[1][r]);
+                if constexpr (!PAIR) {
+                    row_top[stream][r] = top;
+                    meet();
+                    top = fmaxf(row_top[0][r], row_top[1][r]);
+                }
                 const int e2 = (int)(__float_as_uint(top) >> 23);
                 const int k = top == 0.0f || e2 == 255 ? 0 : max(-126, min(126, 14 + 127 - e2));
                 const float up = a.scale_log2 < 0.0f ? -pow2i(k) : pow2i(k);  // cq >= 0
                 cq = fabsf(a.scale_log2) * pow2i(-k);
 #pragma unroll
-                for (int i = 0; i < DP / 16; ++i) {
-                    if (8 * i >= half) break;
+                for (int i = 0; i < W; ++i) {
+                    if (8 * i >= mine) break;
                     const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
                     uint32_t f[4];
 #pragma unroll
@@ -625,12 +649,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                         const __half2 h = __floats2half2_rn(lo * up, hi * up);
                         f[e] = *reinterpret_cast<const uint32_t *>(&h);
                     }
-                    const int chunk = stream * (half / 8) + i;
-                    sts_v4(q_tile + (chunk >> 3) * PANEL + r * 128 + (((chunk & 7) ^ (r & 7)) << 4), f[0], f[1], f[2], f[3]);
+                    const int chunk = (PAIR ? 0 : stream * (mine / 8)) + i;
+                    sts_v4(q_tile + (PAIR ? stream * TILE : 0) + (chunk >> 3) * PANEL + r * 128 + (((chunk & 7) ^ (r & 7)) << 4),
+                           f[0], f[1], f[2], f[3]);
                 }
                 fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&q_full));
+                release(q_full);
             }
 
             // rows of this thread: of q = 0 .. 3, 16 (q / 2) + 8 (q % 2) + g of the warp's 32
@@ -643,9 +667,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             }
             bool first = true;
             const int seen_by_all = a.mask ? at.len - at.T : min(at.len, at.len - at.T + t_first + 1);
-            for (int i = (n ^ stream) & 1; i < count; i += 2) {
+#pragma unroll 1
+            for (int i = PAIR ? 0 : (n ^ stream) & 1; i < count; i += PAIR ? 1 : 2) {
                 const int x = n + i, slot = (unsigned)x % kInfos;
-                if (!wait(info_full[slot], (unsigned)x / kInfos) || !wait(s_full[stream], x >> 1)) break;
+                if (!wait(info_full[slot], (unsigned)x / kInfos) || !wait(s_full[stream], PAIR ? x : x >> 1)) break;
                 tc_fence_after();
                 const int pos0 = (at.chunk + i) * kTokens;
                 const uint32_t there = infos[slot].present;
@@ -675,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 }
             }
 
-            // the two streams meet
+            // the row's part of the item; without PAIR of both streams, whose warps meet, 8 channels in turn
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 l[q] += __shfl_xor_sync(0xffffffffu, l[q], 1);
@@ -686,34 +711,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             if (r == 0) stream_unit[stream] = unit;
             (void)wait(o_full, item);
             tc_fence_after();
-            meet();
+            if constexpr (PAIR) __syncwarp();
+            else meet();
             {
-                const float m0 = row_m[0][r], m1 = row_m[1][r], up = fmaxf(m0, m1);
-                const float f0 = m0 == up ? 1.0f : ex2(m0 - up), f1 = m1 == up ? 1.0f : ex2(m1 - up);
-                const float total = __fmaf_rn(row_l[0][r], f0, row_l[1][r] * f1);
-                const float top_unit = fmaxf(stream_unit[0], stream_unit[1]);
+                const int s0 = PAIR ? stream : 0, s1 = PAIR ? stream : 1;
+                const float m0 = row_m[s0][r], m1 = row_m[s1][r], up = fmaxf(m0, m1);
+                const float f0 = m0 == up ? 1.0f : ex2(m0 - up), f1 = PAIR ? 0.0f : m1 == up ? 1.0f : ex2(m1 - up);
+                const float total = PAIR ? row_l[s0][r] : __fmaf_rn(row_l[0][r], f0, row_l[1][r] * f1);
+                const float top_unit = PAIR ? unit : fmaxf(stream_unit[0], stream_unit[1]);
                 const float per = __uint_as_float(0x7f000000u - __float_as_uint(top_unit));
-                const bool has0 = count > 1 || !(n & 1), has1 = count > 1 || (n & 1);
-                const float g0 = f0 * (stream_unit[0] * per), g1 = f1 * (stream_unit[1] * per);
+                const bool has0 = PAIR || count > 1 || !(n & 1), has1 = !PAIR && (count > 1 || (n & 1));
+                const float g0 = PAIR ? 1.0f : f0 * (stream_unit[0] * per), g1 = PAIR ? 0.0f : f1 * (stream_unit[1] * per);
                 const bool done = starts_here && ends_here;
-                float *slot = attn_slot(a, blockIdx.x, starts_here ? 1 : 0, kRows, DP);
+                const int part_row = PAIR ? stream * kRows + r : r;
+                float *slot = attn_slot(a, blockIdx.x, starts_here ? 1 : 0, ROWS, DP);
                 uint16_t *out = static_cast<uint16_t *>(a.out) + out_row * a.ld_out + (int64_t)hq * c.D;
-                const float weight = top_unit * kAttnWeightUnit;
-                // 8 channels at a time, in turn for the two streams' threads
-                const float by = total == 0.0f ? 0.0f : weight / total;
+                const float by = total == 0.0f ? 0.0f : top_unit * kAttnWeightUnit / total;
 #pragma unroll 1
-                for (int d = 8 * stream; d < c.D; d += 16) {
+                for (int d = PAIR ? 0 : 8 * stream; d < c.D; d += PAIR ? 8 : 16) {
                     uint32_t v0[8], v1[8];
                     float v[8];
                     __syncwarp();
-                    tmem_ld8(lanes + kOCol + d, v0);
-                    tmem_ld8(lanes + kOCol + 128 + d, v1);
+                    tmem_ld8(lanes + kOCol + s0 * 128 + d, v0);
+                    if constexpr (!PAIR) tmem_ld8(lanes + kOCol + 128 + d, v1);
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int at_e = U4 ? 2 * (e & 3) + (e >> 2) : e;  // codes are unpacked 0 4, 1 5, 2 6, 3 7
-                        const float x0 = has0 ? __uint_as_float(v0[at_e]) * g0 : 0.0f;
-                        v[e] = has1 ? __fmaf_rn(__uint_as_float(v1[at_e]), g1, x0) : x0;
+                        v[e] = has0 ? __uint_as_float(v0[at_e]) * g0 : 0.0f;
+                        if constexpr (!PAIR)
+                            if (has1) v[e] = __fmaf_rn(__uint_as_float(v1[at_e]), g1, v[e]);
                         if (done) v[e] *= by;
                     }
                     if (!live || !ok) continue;
@@ -721,18 +748,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                         *reinterpret_cast<uint4 *>(out + d) = make_uint4(attn_pack(a, v[0], v[1]), attn_pack(a, v[2], v[3]),
                                                                         attn_pack(a, v[4], v[5]), attn_pack(a, v[6], v[7]));
                     } else {
-                        float4 *to = reinterpret_cast<float4 *>(slot + r * DP + d);
+                        float4 *to = reinterpret_cast<float4 *>(slot + part_row * DP + d);
                         to[0] = make_float4(v[0], v[1], v[2], v[3]);
                         to[1] = make_float4(v[4], v[5], v[6], v[7]);
                     }
                 }
                 __syncwarp();
-                if (live && ok && stream == 0) {
+                if (live && ok && (PAIR || stream == 0)) {
                     if (done) {
                         if (a.lse) a.lse[out_row * a.heads_q + hq] = attn_lse(up, total);
                     } else {
-                        slot[kRows * DP + 2 * r] = up, slot[kRows * DP + 2 * r + 1] = total;
-                        if (r == 0) slot[kRows * (DP + 2)] = top_unit;
+                        slot[ROWS * DP + 2 * part_row] = up, slot[ROWS * DP + 2 * part_row + 1] = total;
+                        if (part_row == 0) slot[ROWS * (DP + 2)] = top_unit;
                     }
                 }
             }
@@ -750,29 +777,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <bool U4, int DP>
+template <bool U4, int DP, bool PAIR>
 qnn_status launch(KvAttnArgs a, cudaStream_t s)
 {
-    auto kern = kv_attn_rows_kernel<U4, DP>;
+    auto kern = kv_attn_rows_kernel<U4, DP, PAIR>;
     static std::atomic<uint64_t> opted_in{0};
     // one block on an SM, whatever it needs: tensor memory is taken whole
-    constexpr int kMost = 200 << 10;
-    const int need = 1024 + 5 * kTokens * DP * 2 + (a.c.batch + 1) * 8;
+    constexpr int kMost = 216 << 10;
+    const int need = 1024 + (PAIR ? 6 : 5) * kTokens * DP * 2 + (a.c.batch + 1) * 8;
     if (!opt_in_smem(kern, kMost, opted_in, 100)) return QNN_ERR_CUDA;
     return kv_launch(kern, dim3((unsigned)a.blocks), kThreads, std::max(need, 120 << 10), s, a);
 }
 
 }  // namespace
 
-AttnPlan attn_rows_plan(const KvArgs &c, int)
+// Two tiles of rows to an item where there are rows for both (and room for the sums of the line beside
+// six tiles).
+AttnPlan attn_rows_plan(const KvArgs &c, int group)
 {
-    return {kRows, c.D <= 64 ? 64 : 128, std::min(kAttnMaxBlocks, sm_count())};
+    const bool pair = (int64_t)c.tokens * group > kRows && c.batch <= 2048;
+    return {pair ? 2 * kRows : kRows, c.D <= 64 ? 64 : 128, std::min(kAttnMaxBlocks, sm_count())};
 }
 
 qnn_status launch_attn_rows(const KvAttnArgs &a, const AttnPlan &p, bool u4, cudaStream_t s)
 {
-    if (p.channels == 64) return u4 ? launch<true, 64>(a, s) : launch<false, 64>(a, s);
-    return u4 ? launch<true, 128>(a, s) : launch<false, 128>(a, s);
+    if (p.rows > kRows) {
+        if (p.channels == 64) return u4 ? launch<true, 64, true>(a, s) : launch<false, 64, true>(a, s);
+        return u4 ? launch<true, 128, true>(a, s) : launch<false, 128, true>(a, s);
+    }
+    if (p.channels == 64) return u4 ? launch<true, 64, false>(a, s) : launch<false, 64, false>(a, s);
+    return u4 ? launch<true, 128, false>(a, s) : launch<false, 128, false>(a, s);
 }
 
 }  // namespace qnn
