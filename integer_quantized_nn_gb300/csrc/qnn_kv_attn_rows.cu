@@ -39,9 +39,9 @@ struct Tile16 {
 };
 constexpr int kPlaces = 8;
 
-// Of a chunk: scales of K, and of V over the stream's unit, for each token.
+// Of a chunk: scales of K, and of V over the stream's unit, for two tokens together (k k v v).
 struct Info {
-    float k[kTokens], v[kTokens];
+    float scales[kTokens / 2][4];
     float ratio, unit;  // the unit before over this one; this one
     uint32_t present;   // 16-token tiles that are there
     uint32_t pad;
@@ -132,6 +132,14 @@ __device__ __forceinline__ uint64_t sdesc_n_major(uint32_t addr, uint32_t panel)
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
+// 16 bytes of shared memory that nothing writes meanwhile: the compiler may read them early
+__device__ __forceinline__ uint4 lds_scales(uint32_t at)
+{
+    uint4 v;
+    asm("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+
 // the lowest n bits, n from 0 (or below) to 32 (or above)
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; }
 
@@ -148,20 +156,17 @@ __device__ __forceinline__ uint32_t seen_bits(const KvAttnArgs &a, const Item &c
 
 // A warp's 32 rows of S of a chunk -> P over it.  A thread has 4 rows and the columns 8 i + 2 j and + 1 of each:
 // with a row to a thread each would read all scales of the chunk from shared memory, 1500 cycles
-// of its bandwidth a chunk; so it is a quarter.  ks, vs: scales of the thread's columns; bits: lane
-// t has those of the positions that row t sees.
+// of its bandwidth a chunk; so it is a quarter.  scales: of K and V, of the thread's first two columns; bits:
+// lane t has those of the positions that row t sees.
 template <bool MASKED, int DP>
-__device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, const float *ks, const float *vs,
-                                        const uint32_t (&bits)[4], int j, bool first, float ratio, const float (&cr)[4],
-                                        float (&m)[4], float (&ref)[4], float (&l)[4])
+__device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, uint32_t scales, const uint32_t (&bits)[4], int j,
+                                        bool first, float ratio, const float (&cr)[4], float (&m)[4], float (&ref)[4],
+                                        float (&l)[4])
 {
     const int g = (threadIdx.x & 31) >> 2;
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
         const uint32_t down = (uint32_t)(16 * half) << 16;
-        uint32_t v[64];
-        tmem_ld_frag(s_at + down, v);
-        tmem_ld_wait();
         // by selection and not by index: the arrays stay in registers
         const float c0 = half ? cr[2] : cr[0], c1 = half ? cr[3] : cr[1];
         float m0 = half ? m[2] : m[0], m1 = half ? m[3] : m[1], r0 = half ? ref[2] : ref[0], r1 = half ? ref[3] : ref[1];
@@ -174,30 +179,28 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, const floa
                 b1[b] = __shfl_sync(0xffffffffu, bits[b], 16 * half + 8 + g) >> (2 * j);
             }
         }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float2 k = *reinterpret_cast<const float2 *>(ks + 8 * i);
-            float2 y0 = mul2(as_f2(v[4 * i], v[4 * i + 1]), k), y1 = mul2(as_f2(v[4 * i + 2], v[4 * i + 3]), k);
-            if constexpr (MASKED) {
-                const uint32_t bit = 1u << (8 * (i & 3));
-                y0.x = b0[i >> 2] & bit ? y0.x : -INFINITY, y0.y = b0[i >> 2] & (2 * bit) ? y0.y : -INFINITY;
-                y1.x = b1[i >> 2] & bit ? y1.x : -INFINITY, y1.y = b1[i >> 2] & (2 * bit) ? y1.y : -INFINITY;
-            }
-            v[4 * i] = __float_as_uint(y0.x), v[4 * i + 1] = __float_as_uint(y0.y);
-            v[4 * i + 2] = __float_as_uint(y1.x), v[4 * i + 3] = __float_as_uint(y1.y);
-        }
         // The maxima so far are tried first: a thread's 32 weights of a row whose sum stays below 2^8 are
         // all below it.  New maxima are looked for where they do not, at first and with a new unit.
         bool fresh = MASKED || first || ratio != 1.0f;
         float2 s0, s1;
 #pragma unroll 1
-        for (int tries = 0;; ++tries) {
+        for (;;) {
+            uint32_t v[64];
             if (fresh) {
                 float top0 = -INFINITY, top1 = -INFINITY;
+                tmem_ld_frag(s_at + down, v);
+                tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    top0 = max3(top0, __uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]));
-                    top1 = max3(top1, __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+                    const uint4 kw = lds_v4(scales + 64 * i);
+                    const float2 k = as_f2(kw.x, kw.y);
+                    float2 y0 = mul2(as_f2(v[4 * i], v[4 * i + 1]), k), y1 = mul2(as_f2(v[4 * i + 2], v[4 * i + 3]), k);
+                    if constexpr (MASKED) {
+                        const uint32_t bit = 1u << (8 * (i & 3));
+                        y0.x = b0[i >> 2] & bit ? y0.x : -INFINITY, y0.y = b0[i >> 2] & (2 * bit) ? y0.y : -INFINITY;
+                        y1.x = b1[i >> 2] & bit ? y1.x : -INFINITY, y1.y = b1[i >> 2] & (2 * bit) ? y1.y : -INFINITY;
+                    }
+                    top0 = max3(top0, y0.x, y0.y), top1 = max3(top1, y1.x, y1.y);
                 }
                 top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 1)), top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
                 top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 2)), top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 2));
@@ -222,12 +225,16 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, const floa
             }
             const float2 cc0 = make_float2(c0, c0), cc1 = make_float2(c1, c1), n0 = make_float2(-r0, -r0), n1 = make_float2(-r1, -r1);
             s0 = s1 = make_float2(0.0f, 0.0f);
+            tmem_ld_frag(s_at + down, v);
+            tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float2 w = *reinterpret_cast<const float2 *>(vs + 8 * i);
-                float2 y0 = fma2(as_f2(v[4 * i], v[4 * i + 1]), cc0, n0), y1 = fma2(as_f2(v[4 * i + 2], v[4 * i + 3]), cc1, n1);
+                const uint4 kw = lds_scales(scales + 64 * i);
+                const float2 k = as_f2(kw.x, kw.y), w = as_f2(kw.z, kw.w);
+                float2 y0 = mul2(as_f2(v[4 * i], v[4 * i + 1]), k), y1 = mul2(as_f2(v[4 * i + 2], v[4 * i + 3]), k);
+                y0 = fma2(y0, cc0, n0), y1 = fma2(y1, cc1, n1);
                 y0.x = ex2(y0.x), y0.y = ex2(y0.y), y1.x = ex2(y1.x), y1.y = ex2(y1.y);
-                if constexpr (MASKED) {  // -inf times a scale of zero is not
+                if constexpr (MASKED) {
                     const uint32_t bit = 1u << (8 * (i & 3));
                     y0.x = b0[i >> 2] & bit ? y0.x : 0.0f, y0.y = b0[i >> 2] & (2 * bit) ? y0.y : 0.0f;
                     y1.x = b1[i >> 2] & bit ? y1.x : 0.0f, y1.y = b1[i >> 2] & (2 * bit) ? y1.y : 0.0f;
@@ -384,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 const uint32_t s_at = tmem + stream * kTokens;
                 if (t >= 2) {
                     const int y = PAIR ? x - 1 : x - 2, tile = y & 1;  // the chunk of O
-                    if (!wait1(p_ready[stream], PAIR ? y : y >> 1) || !wait1(tile_full[2 + tile], y >> 1)) break;
+                    if (!wait1(tile_full[2 + tile], y >> 1) || !wait1(p_ready[stream], PAIR ? y : y >> 1)) break;
                     tc_fence_after();
                     const uint64_t vd = vd0 + (uint64_t)(tile * (TILE >> 4));
                     const uint32_t o = tmem + kOCol + stream * 128;
@@ -480,7 +487,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 for (int e = 0; e < 4; ++e) s[e] = s[e] * per * (float)(1 << kAttnRoom);
                 if (lane == 0) info.ratio = old * per, info.unit = now, info.present = there;
             }
-            *reinterpret_cast<float4 *>((is_v ? info.v : info.k) + 4 * lane) = make_float4(s[0], s[1], s[2], s[3]);
+            *reinterpret_cast<float2 *>(info.scales[2 * lane] + 2 * is_v) = make_float2(s[0], s[1]);
+            *reinterpret_cast<float2 *>(info.scales[2 * lane + 1] + 2 * is_v) = make_float2(s[2], s[3]);
             release(info_full[slot]);
             pos += kTokens;
         }
@@ -676,11 +684,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 const uint32_t there = infos[slot].present;
                 const float ratio = infos[slot].ratio;
                 unit = infos[slot].unit;
-                const float *ks = infos[slot].k + 2 * j, *vs = infos[slot].v + 2 * j;
+                uint32_t scales = smem_u32(infos[slot].scales[j]);
+                asm volatile("" : "+r"(scales));  // so that no read of them goes ahead of the waits above
                 const uint32_t s_at = lanes + stream * kTokens, o_at = lanes + kOCol + stream * 128;
                 if (pos0 + kTokens <= seen_by_all && there == 0xffu) {
                     const uint32_t none[4] = {};
-                    weights<false, DP>(s_at, o_at, ks, vs, none, j, first, ratio, cr, m, ref, l);
+                    weights<false, DP>(s_at, o_at, scales, none, j, first, ratio, cr, m, ref, l);
                 } else {
                     uint32_t bits[4];
 #pragma unroll
@@ -688,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                         bits[b] = seen_bits(a, at, t, pos0 + 32 * b) &
                                   ((there >> (2 * b) & 1u ? 0xffffu : 0u) | (there >> (2 * b + 1) & 1u ? 0xffff0000u : 0u));
                     __syncwarp();
-                    weights<true, DP>(s_at, o_at, ks, vs, bits, j, first, ratio, cr, m, ref, l);
+                    weights<true, DP>(s_at, o_at, scales, bits, j, first, ratio, cr, m, ref, l);
                 }
                 first = false;
                 tmem_st_wait();
