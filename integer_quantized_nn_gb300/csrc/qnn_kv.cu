@@ -44,7 +44,7 @@ qnn_status kv_args(const qnn_kv_geom *g, const qnn_kv_seqs *q, KvArgs *a)
 
 namespace {
 
-constexpr int kWarps = 8, kUnroll = 4;
+constexpr int kWarps = 8, kUnroll = 4;  // items of a group at a time
 
 struct KvIoArgs {
     KvArgs c;
@@ -187,12 +187,26 @@ __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const __grid_cons
             } else {
                 s = __fdiv_rn(hi, 127.0f);
             }
+            // By a product with 1 / s first: that is within 2^-21 of the quotient, relatively, and so the same
+            // integer but near a tie (and where s or a value is out of the ordinary): then by division.
             uint32_t q[8];
+            const float per = __fdiv_rn(1.0f, s);
+            bool plain = s > 1e-30f;
+            const float zero = 12582912.0f + (U4 ? z : 128.0f);  // 1.5 * 2^23 + the code of zero: integers in its low bits
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float r = s > 0.0f && x[i][e] == x[i][e] ? rintf(__fdiv_rn(x[i][e], s)) : 0.0f;
-                if constexpr (U4) q[e] = (uint32_t)fminf(fmaxf(__fadd_rn(r, z), 0.0f), 15.0f);
-                else q[e] = (uint32_t)(fminf(fmaxf(r, -127.0f), 127.0f) + 128.0f);
+                const float t = __fmul_rn(x[i][e], per), r = __fadd_rn(t, 12582912.0f);
+                plain = plain && fabsf(__fadd_rn(t, -__fadd_rn(r, -12582912.0f))) < 0.4999f;
+                q[e] = __float_as_uint(__fadd_rn(r, zero - 12582912.0f)) & 0xffu;
+                if constexpr (U4) q[e] = min(max((int)(int8_t)q[e], 0), 15);
+            }
+            if (!plain) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float r = s > 0.0f && x[i][e] == x[i][e] ? rintf(__fdiv_rn(x[i][e], s)) : 0.0f;
+                    if constexpr (U4) q[e] = (uint32_t)fminf(fmaxf(__fadd_rn(r, z), 0.0f), 15.0f);
+                    else q[e] = (uint32_t)(fminf(fmaxf(r, -127.0f), 127.0f) + 128.0f);
+                }
             }
             if (item >= 2 * c.heads || !live) continue;
             const bool is_v = item >= c.heads;

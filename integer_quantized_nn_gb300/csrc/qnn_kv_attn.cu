@@ -6,56 +6,88 @@
 namespace qnn {
 namespace {
 
-constexpr int kJoinThreads = 128, kJoinRows = 8;
+constexpr int kJoinWarps = 8;
 
-// A block joins kJoinRows rows of the item that begins in block blockIdx.x's share and ends in a
-// later one's, if there is one.
-__global__ void __launch_bounds__(kJoinThreads) kv_attn_join_kernel(const __grid_constant__ KvAttnArgs a, int rows,
-                                                                    int channels, float weight_unit)
+// A warp joins a row of the item that begins in block blockIdx.x's share and ends in a later one's, if
+// there is one: lane k has the statistics of part k (and k + 32, ..), all lanes the channels.  Only the
+// record is waited for before everything else is asked for.
+template <int V>  // channels of a lane: 2, 4 or 8
+__global__ void __launch_bounds__(kJoinWarps * 32) kv_attn_join_kernel(const __grid_constant__ KvAttnArgs a, int rows)
 {
-    __shared__ float factor[kJoinRows][kAttnMaxBlocks], tops[kJoinRows], totals[kJoinRows], unit_of[kJoinRows];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = blockIdx.x, r0 = blockIdx.y * kJoinRows;
+    constexpr int channels = 32 * V;
+    const int lane = threadIdx.x & 31, block = blockIdx.x;
     grid_dependency_launch();
     grid_dependency_wait();
-    const volatile int *record = reinterpret_cast<const int *>(a.ws) + block * kAttnRecord;
-    if (!record[0]) return;
-    const int b = record[1], rt = record[2], head = record[3], n = record[4] - block + 1;
-    const KvSeq s = kv_seq(a.c, b);
-    const int width = (int)min((int64_t)rows, (int64_t)s.T * a.group - (int64_t)rt * rows);
-    if (r0 >= width) return;
-    auto slot = [&](int k) { return attn_slot(a, block + k, k == 0 ? 1 : 0, rows, channels); };
-    for (int r = warp; r < kJoinRows && r0 + r < width; r += kJoinThreads / 32) {
-        const int64_t stat = (int64_t)rows * channels + 2 * (r0 + r);
-        float top = -INFINITY, unit = 0.0f, total = 0.0f;
-        for (int k = lane; k < n; k += 32) {
-            top = fmaxf(top, slot(k)[stat]);
-            unit = fmaxf(unit, slot(k)[(int64_t)rows * (channels + 2)]);
+    int4 rec;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(rec.x), "=r"(rec.y), "=r"(rec.z), "=r"(rec.w)
+                 : "l"(reinterpret_cast<const int4 *>(a.ws) + 2 * block));
+    const int n = rec.x - block + 1, row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+    if (rec.x < 0 || row >= rec.w) return;
+    const int64_t first = *reinterpret_cast<const volatile int64_t *>(reinterpret_cast<const int4 *>(a.ws) + 2 * block + 1);
+    const float *part0 = attn_slot(a, block, 1, rows, channels), *part1 = attn_slot(a, block + 1, 0, rows, channels);
+    const int64_t pitch = 2 * attn_slot_floats(rows, channels);  // between the parts after the first
+    auto part = [&](int k) { return k == 0 ? part0 : part1 + (k - 1) * pitch; };
+    const int d = lane * V;
+    float top = -INFINITY, unit = 0.0f, total = 0.0f, sum[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) sum[e] = 0.0f;
+    // 32 parts at a time; what came before is scaled to the new maximum and unit
+    for (int k0 = 0; k0 < n; k0 += 32) {
+        const int here = min(32, n - k0);
+        float m = -INFINITY, l = 0.0f, u = 0.0f;
+        if (lane < here) {
+            const float *p = part(k0 + lane) + (int64_t)rows * channels;
+            const float2 ml = *reinterpret_cast<const float2 *>(p + 2 * row);
+            m = ml.x, l = ml.y, u = p[2 * rows];
         }
-        for (int d = 16; d > 0; d /= 2) {
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            unit = fmaxf(unit, __shfl_xor_sync(0xffffffffu, unit, d));
+        float was = top, was_unit = unit;
+        top = fmaxf(top, m), unit = fmaxf(unit, u);
+#pragma unroll
+        for (int b = 16; b > 0; b /= 2) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, b));
+            unit = fmaxf(unit, __shfl_xor_sync(0xffffffffu, unit, b));
         }
-        for (int k = lane; k < n; k += 32) {
-            const float m = slot(k)[stat], f = m == top ? 1.0f : ex2(m - top);
-            total = __fmaf_rn(slot(k)[stat + 1], f, total);
-            // units are powers of two: the quotient by a reciprocal is exact
-            factor[r][k] = f * (slot(k)[(int64_t)rows * (channels + 2)] * __uint_as_float(0x7f000000u - __float_as_uint(unit)));
+        // units are powers of two: the quotient by a reciprocal is exact
+        const float per = __uint_as_float(0x7f000000u - __float_as_uint(unit));
+        const float f = m == top ? 1.0f : ex2(m - top), g = lane < here ? f * (u * per) : 0.0f;
+        float t = lane < here ? l * f : 0.0f;
+#pragma unroll
+        for (int b = 16; b > 0; b /= 2) t += __shfl_xor_sync(0xffffffffu, t, b);
+        const float back = was == top ? 1.0f : ex2(was - top);
+        total = k0 ? __fmaf_rn(total, back, t) : t;
+        if (k0) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum[e] *= back * (was_unit * per);
         }
-        for (int d = 16; d > 0; d /= 2) total += __shfl_xor_sync(0xffffffffu, total, d);
-        if (lane == 0) tops[r] = top, totals[r] = total, unit_of[r] = unit;
+#pragma unroll 8
+        for (int k = 0; k < here; ++k) {
+            const float *p = part(k0 + k) + (int64_t)row * channels + d;
+            const float w = __shfl_sync(0xffffffffu, g, k);
+            if constexpr (V == 8) {
+                const float4 x = *reinterpret_cast<const float4 *>(p), y = *reinterpret_cast<const float4 *>(p + 4);
+                sum[0] = __fmaf_rn(x.x, w, sum[0]), sum[1] = __fmaf_rn(x.y, w, sum[1]), sum[2] = __fmaf_rn(x.z, w, sum[2]);
+                sum[3] = __fmaf_rn(x.w, w, sum[3]), sum[4] = __fmaf_rn(y.x, w, sum[4]), sum[5] = __fmaf_rn(y.y, w, sum[5]);
+                sum[6] = __fmaf_rn(y.z, w, sum[6]), sum[7] = __fmaf_rn(y.w, w, sum[7]);
+            } else if constexpr (V == 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(p);
+                sum[0] = __fmaf_rn(x.x, w, sum[0]), sum[1] = __fmaf_rn(x.y, w, sum[1]);
+                sum[2] = __fmaf_rn(x.z, w, sum[2]), sum[3] = __fmaf_rn(x.w, w, sum[3]);
+            } else {
+                const float2 x = *reinterpret_cast<const float2 *>(p);
+                sum[0] = __fmaf_rn(x.x, w, sum[0]), sum[1] = __fmaf_rn(x.y, w, sum[1]);
+            }
+        }
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < kJoinRows * a.c.D / 2; i += kJoinThreads) {
-        const int r = i / (a.c.D / 2), d = 2 * (i - r * (a.c.D / 2));
-        if (r0 + r >= width) break;
-        float v0 = 0.0f, v1 = 0.0f;
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-            const float2 v = *reinterpret_cast<const float2 *>(slot(k) + (int64_t)(r0 + r) * channels + d);
-            v0 = __fmaf_rn(v.x, factor[r][k], v0), v1 = __fmaf_rn(v.y, factor[r][k], v1);
-        }
-        attn_store(a, s.first, head, rt * rows + r0 + r, d, v0, v1, tops[r], totals[r], unit_of[r] * weight_unit);
+    const float by = total == 0.0f ? 0.0f : kAttnWeightUnit * unit / total;
+    const int r = rec.z + row, tok = r / a.group, hq = rec.y * a.group + (r - tok * a.group);
+    if (d < a.c.D) {
+        uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + (first + tok) * a.ld_out +
+                                                     (int64_t)hq * a.c.D + d);
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) out[e] = attn_pack(a, sum[2 * e] * by, sum[2 * e + 1] * by);
     }
+    if (a.lse && lane == 0) a.lse[(first + tok) * a.heads_q + hq] = attn_lse(top, total);
 }
 
 bool many_rows(const KvArgs &c, int group) { return c.D <= 128 && (int64_t)c.tokens * group > 32; }
@@ -121,6 +153,7 @@ extern "C" qnn_status q_kv_attn(const void *q, qnn_dtype x_dt, int64_t ld_q, int
     const qnn_status sent = (many_rows(a.c, a.group) ? launch_attn_rows : launch_attn_few)(a, p, g->kv_dt == QNN_U4,
                                                                                           (cudaStream_t)stream);
     if (sent != QNN_OK) return sent;
-    return kv_launch(kv_attn_join_kernel, dim3((unsigned)p.blocks, (unsigned)(p.rows / kJoinRows)), kJoinThreads, 0,
-                     (cudaStream_t)stream, a, p.rows, p.channels, kAttnWeightUnit);
+    const dim3 grid((unsigned)p.blocks, (unsigned)(p.rows / kJoinWarps));
+    auto join = p.channels == 64 ? kv_attn_join_kernel<2> : p.channels == 128 ? kv_attn_join_kernel<4> : kv_attn_join_kernel<8>;
+    return kv_launch(join, grid, kJoinWarps * 32, 0, (cudaStream_t)stream, a, p.rows);
 }

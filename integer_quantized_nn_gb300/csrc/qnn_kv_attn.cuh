@@ -27,8 +27,8 @@ struct KvAttnArgs {
 // lies in one block is finished there; one that goes on behind a block's end is finished by the
 // joining kernel, from one part of each block.
 //
-// Workspace: for each block a record of 8 ints (of the item that its part of the line ends
-// inside: whether there is one, sequence, row tile, head, the block that it ends in), then two
+// Workspace: for each block a record of 8 ints (of the item that begins in its part of the line and
+// goes on behind it: attn_record), then two
 // slots of parts: slot 0 for an item that began in an earlier block, slot 1 for one that begins
 // here and goes on.  A slot: [rows][channels] sums, then for each row the maximum and the sum of
 // weights, then the unit of V's scales.
@@ -45,6 +45,15 @@ __host__ __device__ inline int64_t attn_slot_floats(int rows, int channels) { re
 __device__ __forceinline__ float *attn_slot(const KvAttnArgs &a, int block, int slot, int rows, int channels)
 {
     return a.ws + (int64_t)a.blocks * kAttnRecord + (2 * (int64_t)block + slot) * attn_slot_floats(rows, channels);
+}
+
+// The block's record: `last` is the block in which the item ends, < 0 where no item begins here and
+// goes on.  The item's rows are rows row0 .. row0 + width - 1 of those of its sequence.
+__device__ __forceinline__ void attn_record(const KvAttnArgs &a, int last, int64_t first, int row0, int width, int head)
+{
+    int4 *record = reinterpret_cast<int4 *>(a.ws) + 2 * blockIdx.x;
+    record[0] = make_int4(last, head, row0, width);
+    *reinterpret_cast<int64_t *>(record + 1) = first;
 }
 
 __device__ __forceinline__ float ex2(float x)

@@ -146,9 +146,8 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
     grid_dependency_launch();
     grid_dependency_wait();
     const AttnShare share(attn_sums<kThreads>(a, sums, S::kRows), a.blocks, blockIdx.x);
-    int *record = reinterpret_cast<int *>(a.ws) + blockIdx.x * kAttnRecord;
     if (share.from >= share.to) {
-        if (threadIdx.x == 0) record[0] = 0;
+        if (threadIdx.x == 0) attn_record(a, -1, 0, 0, 0, 0);
         return;
     }
 
@@ -200,11 +199,8 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
         const int width = (int)min((int64_t)S::kRows, (int64_t)at.T * a.group - row0);
         const int t_first = row0 / a.group, t_last = (row0 + width - 1) / a.group;
         const bool starts_here = item_first >= share.from, ends_here = item_end <= share.to;
-        if (threadIdx.x == 0 && end == share.to) {
-            record[0] = starts_here && !ends_here;
-            record[1] = at.b, record[2] = at.rt, record[3] = at.h;
-            if (!ends_here) record[4] = share.block_of(item_end - 1);
-        }
+        if (threadIdx.x == 0 && end == share.to)
+            attn_record(a, starts_here && !ends_here ? share.block_of(item_end - 1) : -1, first, row0, width, head);
 
         // q's fragments: B of m16n8k16, column g, each row scaled to f16's range
         uint32_t qf[S::kQRegs ? NT : 1][S::kQRegs ? S::kSteps : 1][2];

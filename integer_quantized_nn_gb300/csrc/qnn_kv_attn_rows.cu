@@ -319,8 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
     grid_dependency_wait();
 
     const AttnShare share(attn_sums<kThreads>(a, sums, ROWS), a.blocks, blockIdx.x);
-    int *record = reinterpret_cast<int *>(a.ws) + blockIdx.x * kAttnRecord;
-    if (threadIdx.x == 0 && share.from >= share.to) record[0] = 0;
+    if (threadIdx.x == 0 && share.from >= share.to) attn_record(a, -1, 0, 0, 0, 0);
     const int chunks = (int)(share.to - share.from);
 
     bool ok = true;
@@ -601,9 +600,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             const int t_first = min(row0 / a.group, at.T - 1);
             const bool live = r < width, starts_here = n > 0 || at.chunk == 0, ends_here = at.chunk + count == at.units;
             if (threadIdx.x == kRowWarp0 * 32 && n + count == chunks) {
-                record[0] = starts_here && !ends_here;
-                record[1] = at.b, record[2] = at.rt, record[3] = at.h;
-                if (!ends_here) record[4] = share.block_of(share.from + n - at.chunk + at.units - 1);
+                const int tile0 = at.rt * ROWS;
+                attn_record(a, starts_here && !ends_here ? share.block_of(share.from + n - at.chunk + at.units - 1) : -1,
+                            at.first, tile0, min(ROWS, at.T * a.group - tile0), at.h);
             }
             const int64_t out_row = at.first + rr / a.group;
             const int hq = at.h * a.group + rr % a.group;
