@@ -38,19 +38,21 @@ qnn_status kv_args(const qnn_kv_geom *g, const qnn_kv_seqs *q, KvArgs *a)
     a->chunks = a->row_bytes / 16;
     a->head_bytes = g->page * (2 * a->row_bytes + 8);
     a->page_bytes = (int64_t)a->head_bytes * g->heads;
+    a->per16 = (uint32_t)g->page / 16;
+    a->magic16 = (uint32_t)(((1ull << 32) + a->per16 - 1) / a->per16);
     a->status = nullptr;
     return QNN_OK;
 }
 
 namespace {
 
-constexpr int kWarps = 8, kUnroll = 4;  // items of a group at a time
+constexpr int kWarps = 8, kWriteItems = 2, kReadItems = 4;  // of a row, to a group of lanes at a time
 
 struct KvIoArgs {
     KvArgs c;
     const void *k, *v;
     int64_t ld_k, ld_v;
-    int parts;  // of a row: each 2 * heads / parts items, kUnroll to a group
+    int run;    // rows of a warp, one after the other; their places are looked up together, one by a lane
     int vec;    // rows of k and v start on 16-byte boundaries
 };
 
@@ -60,35 +62,38 @@ struct Place {
     int seq;         // 0: no sequence has the row
 };
 
-// The sequence whose rows hold `row`: the number of starts[1 .. batch] that are <= row, by a warp.
+// The sequence whose rows hold `row`: the number of starts[1 .. batch] that are <= row.
 // (Where they descend the answer is some sequence, and what follows is checked.)
-__device__ __forceinline__ int seq_of_row(const KvArgs &a, int64_t row, int lane)
+__device__ __forceinline__ int seq_of_row(const KvArgs &a, int row)
 {
-    if (!a.starts) return (int)(row / a.tokens);
+    if (!a.starts) return (unsigned)row / (unsigned)a.tokens;
     int lo = 0, n = a.batch;  // the answer is in lo .. lo + n
     const volatile int32_t *st = a.starts + 1;
+#pragma unroll 1
     while (n > 0) {
-        const int step = (n + 31) / 32, at = (lane + 1) * step - 1;
-        const int below = __popc(__ballot_sync(0xffffffffu, at < n && st[lo + at] <= row)) * step;
-        lo += below;
-        n = min(n - below, step - 1);
+        const int half = n >> 1;
+        if (st[lo + half] <= row) lo += half + 1, n -= half + 1;
+        else n = half;
     }
     return lo;
 }
 
-__device__ __forceinline__ Place place_of(const KvArgs &a, int64_t row, int lane)
+__device__ __forceinline__ Place place_of(const KvArgs &a, int row)
 {
     Place p = {-1, 0, 0};
-    const int b = seq_of_row(a, row, lane);
+    if (row >= a.rows) return p;
+    const int b = seq_of_row(a, row);
     if (b >= a.batch) return p;
     const KvSeq s = kv_seq(a, b);
-    const int64_t t = row - s.first;
+    const int t = row - (int)s.first;
     if (s.T < 0 || t < 0 || t >= s.T) return p;
     p.seq = 1;
-    const int64_t pos = s.len - s.T + t;
+    const int pos = s.len - s.T + t;
     if (pos < 0) return p;
-    p.page = kv_page(a, b, (int)(pos / a.page));
-    p.slot = (int)(pos % a.page);
+    int tile;
+    const int index = kv_page_index(a, pos >> 4, &tile);
+    p.page = kv_page(a, b, index);
+    p.slot = tile * 16 + (pos & 15);
     return p;
 }
 
@@ -139,8 +144,19 @@ __device__ __forceinline__ float group_max(float v)
     return v;
 }
 
+// a / b, rounded to nearest as by a division, where b has 8 significant bits at most, `per` is 1 / b rounded, and
+// nothing underflows: a product, what it leaves, and the product corrected by that (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990).  The corrected value before its rounding is
+// within 2^-45 of a / b, relatively.  a / b is no middle of two fp32 numbers (b times one, which has 25 bits and is
+// odd, has more than 24), and so lies 2^-33 or more from each: both round to the same.
+__device__ __forceinline__ float2 quotients(float2 a, float2 b, float2 per)
+{
+    const float2 q = mul2(a, per);
+    return fma2(fma2(make_float2(-q.x, -q.y), b, a), per, q);
+}
+
 template <typename T, bool U4, int W>
-__global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const __grid_constant__ KvIoArgs a)
+__global__ void __launch_bounds__(kWarps * 32, 3) kv_write_kernel(const __grid_constant__ KvIoArgs a)
 {
     const KvArgs &c = a.c;
     constexpr int G = 32 / W;  // items of a warp at a time
@@ -148,80 +164,126 @@ __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const __grid_cons
     const bool live = d0 < c.D;
     grid_dependency_launch();
     grid_dependency_wait();
-    const int64_t units = c.rows * a.parts;
-    for (int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += (int64_t)gridDim.x * kWarps) {
-        const int64_t row = u / a.parts;
-        const int first = (int)(u - row * a.parts) * kUnroll * G + group;
-        float x[kUnroll][8];
+    const int first = blockIdx.y * kWriteItems * G + group;
+    const int64_t r0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * a.run;
+    const int rows = (int)min((int64_t)a.run, c.rows - r0);
+    if (rows <= 0) return;
+    float ahead[kWriteItems][8];
+    auto ask = [&](int64_t row) {
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
+        for (int i = 0; i < kWriteItems; ++i) {
             const int item = first + i * G;  // K's heads, then V's
             if (item < 2 * c.heads && live) {
                 const bool is_v = item >= c.heads;
                 const int64_t at = row * (is_v ? a.ld_v : a.ld_k) + (item - (is_v ? c.heads : 0)) * c.D + d0;
-                load8(static_cast<const T *>(is_v ? a.v : a.k) + at, a.vec, x[i]);
+                load8(static_cast<const T *>(is_v ? a.v : a.k) + at, a.vec, ahead[i]);
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
+                for (int e = 0; e < 8; ++e) ahead[i][e] = 0.0f;
             }
         }
-        const Place p = place_of(c, row, lane);
+    };
+    ask(r0);
+    const Place places = place_of(c, lane < rows ? (int)r0 + lane : INT32_MAX);
+#pragma unroll 1
+    for (int t = 0; t < rows; ++t) {
+        float x[kWriteItems][8];
+#pragma unroll
+        for (int i = 0; i < kWriteItems; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[i][e] = ahead[i][e];
+        if (t + 1 < rows) ask(r0 + t + 1);
+        Place p;
+        p.page = __shfl_sync(0xffffffffu, places.page, t);
+        p.slot = __shfl_sync(0xffffffffu, places.slot, t);
         if (p.page < 0) continue;
         uint8_t *base = c.pages + p.page * c.page_bytes;
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
+        for (int i = 0; i < kWriteItems; ++i) {
             const int item = first + i * G;
-            float hi = 0.0f, lo = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (!finite(x[i][e])) continue;
-                hi = fmaxf(hi, U4 ? x[i][e] : fabsf(x[i][e]));
-                if (U4) lo = fmaxf(lo, -x[i][e]);
+            float hi, lo = 0.0f;  // the largest value and -min, both 0 at least (NaN aside)
+            if constexpr (U4) {
+                hi = max3(max3(x[i][0], x[i][1], x[i][2]), max3(x[i][3], x[i][4], x[i][5]), max3(x[i][6], x[i][7], 0.0f));
+                lo = max3(max3(-x[i][0], -x[i][1], -x[i][2]), max3(-x[i][3], -x[i][4], -x[i][5]), max3(-x[i][6], -x[i][7], 0.0f));
+                lo = group_max<W>(lo);
+            } else {
+                hi = max3(max3(fabsf(x[i][0]), fabsf(x[i][1]), fabsf(x[i][2])),
+                          max3(fabsf(x[i][3]), fabsf(x[i][4]), fabsf(x[i][5])), max3(fabsf(x[i][6]), fabsf(x[i][7]), 0.0f));
             }
             hi = group_max<W>(hi);
-            if (U4) lo = group_max<W>(lo);  // -min
-            float s, z = 0.0f;
-            if constexpr (U4) {
-                s = __bfloat162float(__float2bfloat16_rn(__fadd_rn(__fdiv_rn(hi, 15.0f), __fdiv_rn(lo, 15.0f))));
-                if (s > 0.0f) z = fminf(rintf(__fdiv_rn(lo, s)), 15.0f);
-            } else {
-                s = __fdiv_rn(hi, 127.0f);
-            }
-            // By a product with 1 / s first: that is within 2^-21 of the quotient, relatively, and so the same
-            // integer but near a tie (and where s or a value is out of the ordinary): then by division.
-            uint32_t q[8];
-            const float per = __fdiv_rn(1.0f, s);
-            bool plain = s > 1e-30f;
-            const float zero = 12582912.0f + (U4 ? z : 128.0f);  // 1.5 * 2^23 + the code of zero: integers in its low bits
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float t = __fmul_rn(x[i][e], per), r = __fadd_rn(t, 12582912.0f);
-                plain = plain && fabsf(__fadd_rn(t, -__fadd_rn(r, -12582912.0f))) < 0.4999f;
-                q[e] = __float_as_uint(__fadd_rn(r, zero - 12582912.0f)) & 0xffu;
-                if constexpr (U4) q[e] = min(max((int)(int8_t)q[e], 0), 15);
-            }
-            if (!plain) {
+            if (__any_sync(0xffffffffu, fmaxf(hi, lo) == INFINITY)) {  // once more, of what is finite
+                hi = lo = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float r = s > 0.0f && x[i][e] == x[i][e] ? rintf(__fdiv_rn(x[i][e], s)) : 0.0f;
-                    if constexpr (U4) q[e] = (uint32_t)fminf(fmaxf(__fadd_rn(r, z), 0.0f), 15.0f);
-                    else q[e] = (uint32_t)(fminf(fmaxf(r, -127.0f), 127.0f) + 128.0f);
+                    if (!finite(x[i][e])) continue;
+                    hi = fmaxf(hi, U4 ? x[i][e] : fabsf(x[i][e]));
+                    if (U4) lo = fmaxf(lo, -x[i][e]);
+                }
+                hi = group_max<W>(hi);
+                if (U4) lo = group_max<W>(lo);
+            }
+            float s, z = 0.0f;
+            uint32_t q[8];
+            constexpr float kInteger = 12582912.0f;  // 1.5 * 2^23: a sum with it is an integer in the low bits
+            bool plain = fmaxf(hi, lo) > 0x1p-60f;
+            if constexpr (U4) {
+                const float2 of = quotients(make_float2(hi, lo), both(15.0f), both(1.0f / 15.0f));
+                s = __bfloat162float(__float2bfloat16_rn(__fadd_rn(of.x, of.y)));
+                const float2 by = both(s), per = both(__fdiv_rn(1.0f, s));
+                z = fminf(rintf(quotients(both(lo), by, per).x), 15.0f);
+                float2 sum = both(0.0f);  // not a number where a value is none, or infinite
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float2 t = quotients(make_float2(x[i][e], x[i][e + 1]), by, per);
+                    sum = add2(sum, t);
+                    const float2 r = add2(add2(t, both(kInteger)), both(z));
+                    q[e] = __float_as_uint(fminf(fmaxf(r.x, kInteger), kInteger + 15.0f));
+                    q[e + 1] = __float_as_uint(fminf(fmaxf(r.y, kInteger), kInteger + 15.0f));
+                }
+                plain = plain && sum.x + sum.y == sum.x + sum.y;
+            } else {
+                s = quotients(both(hi), both(127.0f), both(1.0f / 127.0f)).x;
+                // By a product with 1 / s: that is within 2^-21 of the quotient, relatively, and so the same integer
+                // but near a tie.
+                const float2 per = both(__fdiv_rn(1.0f, s));
+                float far = 0.0f;  // from the nearest integer
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float2 t = mul2(make_float2(x[i][e], x[i][e + 1]), per), r = add2(t, both(kInteger));
+                    const float2 d = add2(add2(r, both(-kInteger)), make_float2(-t.x, -t.y));
+                    // NaN does not pass the comparison: max would drop it
+                    far = max3(far, fabsf(d.x) < 0.4999f ? 0.0f : 1.0f, fabsf(d.y) < 0.4999f ? 0.0f : 1.0f);
+                    q[e] = __float_as_uint(r.x), q[e + 1] = __float_as_uint(r.y);
+                }
+                plain = plain && far == 0.0f;
+            }
+            if (!plain) {  // by division
+                if constexpr (U4) {
+                    s = __bfloat162float(__float2bfloat16_rn(__fadd_rn(__fdiv_rn(hi, 15.0f), __fdiv_rn(lo, 15.0f))));
+                    z = s > 0.0f ? fminf(rintf(__fdiv_rn(lo, s)), 15.0f) : 0.0f;
+                } else {
+                    s = __fdiv_rn(hi, 127.0f);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float v = x[i][e], r = s > 0.0f && v == v ? rintf(__fdiv_rn(v, s)) : 0.0f;
+                    q[e] = U4 ? (uint32_t)fminf(fmaxf(__fadd_rn(r, z), 0.0f), 15.0f)
+                              : (uint32_t)(int)fminf(fmaxf(r, -127.0f), 127.0f);
                 }
             }
+            // the low bytes of all
+            uint32_t w0 = prmt(prmt(q[0], q[1], 0x0040), prmt(q[2], q[3], 0x0040), 0x5410);
+            uint32_t w1 = prmt(prmt(q[4], q[5], 0x0040), prmt(q[6], q[7], 0x0040), 0x5410);
             if (item >= 2 * c.heads || !live) continue;
             const bool is_v = item >= c.heads;
             uint8_t *head = base + (int64_t)(item - (is_v ? c.heads : 0)) * c.head_bytes;
             uint8_t *to = head + (is_v ? c.page * c.row_bytes : 0) + p.slot * c.row_bytes;
             if constexpr (U4) {
-                uint32_t w = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w |= q[e] << (4 * e);
-                *reinterpret_cast<uint32_t *>(to + 16 * kv_chunk(c.chunks, p.slot, j / 4) + 4 * (j % 4)) = w;
+                w0 |= w0 >> 4, w1 |= w1 >> 4;  // bytes 0 and 2: two codes each
+                *reinterpret_cast<uint32_t *>(to + 16 * kv_chunk(c.chunks, p.slot, j / 4) + 4 * (j % 4)) = prmt(w0, w1, 0x6420);
             } else {
-                const uint32_t w0 = q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24;
-                const uint32_t w1 = q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24;
                 *reinterpret_cast<uint2 *>(to + 16 * kv_chunk(c.chunks, p.slot, j / 2) + 8 * (j % 2)) =
-                    make_uint2(w0, w1);
+                    make_uint2(w0 ^ 0x80808080u, w1 ^ 0x80808080u);
             }
             if (j == 0) {
                 const uint32_t word = U4 ? __float_as_uint(s) | (uint32_t)z : __float_as_uint(s);
@@ -240,34 +302,46 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const __grid_const
     const bool live = d0 < c.D;
     grid_dependency_launch();
     grid_dependency_wait();
-    const int64_t units = c.rows * a.parts;
-    for (int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += (int64_t)gridDim.x * kWarps) {
-        const int64_t row = u / a.parts;
-        const int first = (int)(u - row * a.parts) * kUnroll * G + group;
-        const Place p = place_of(c, row, lane);
-        if (!p.seq || !live) continue;
-        uint32_t w[kUnroll][2], word[kUnroll];
+    const int first = blockIdx.y * kReadItems * G + group;
+    const int64_t r0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * a.run;
+    const int rows = (int)min((int64_t)a.run, c.rows - r0);
+    if (rows <= 0) return;
+    const Place places = place_of(c, lane < rows ? (int)r0 + lane : INT32_MAX);
+    uint32_t ahead[kReadItems][2], ahead_word[kReadItems];
+    auto ask = [&](int t) {
+        const int page = __shfl_sync(0xffffffffu, places.page, t), slot = __shfl_sync(0xffffffffu, places.slot, t);
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
+        for (int i = 0; i < kReadItems; ++i) {
             const int item = first + i * G;
             const bool is_v = item >= c.heads;
-            w[i][0] = w[i][1] = U4 ? 0 : 0x80808080u;
-            word[i] = 0;
-            if (item >= 2 * c.heads || p.page < 0) continue;
-            const uint8_t *head = c.pages + p.page * c.page_bytes + (int64_t)(item - (is_v ? c.heads : 0)) * c.head_bytes;
-            const uint8_t *from = head + (is_v ? c.page * c.row_bytes : 0) + p.slot * c.row_bytes;
+            ahead[i][0] = ahead[i][1] = U4 ? 0 : 0x80808080u;
+            ahead_word[i] = 0;
+            if (item >= 2 * c.heads || page < 0 || !live) continue;
+            const uint8_t *head = c.pages + page * c.page_bytes + (int64_t)(item - (is_v ? c.heads : 0)) * c.head_bytes;
+            const uint8_t *from = head + (is_v ? c.page * c.row_bytes : 0) + slot * c.row_bytes;
             if constexpr (U4) {
-                w[i][0] = *reinterpret_cast<const volatile uint32_t *>(from + 16 * kv_chunk(c.chunks, p.slot, j / 4) +
-                                                                       4 * (j % 4));
+                ahead[i][0] = *reinterpret_cast<const volatile uint32_t *>(from + 16 * kv_chunk(c.chunks, slot, j / 4) +
+                                                                           4 * (j % 4));
             } else {
-                const uint8_t *at = from + 16 * kv_chunk(c.chunks, p.slot, j / 2) + 8 * (j % 2);
-                asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(w[i][0]), "=r"(w[i][1]) : "l"(at));
+                const uint8_t *at = from + 16 * kv_chunk(c.chunks, slot, j / 2) + 8 * (j % 2);
+                asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(ahead[i][0]), "=r"(ahead[i][1]) : "l"(at));
             }
-            word[i] = reinterpret_cast<const volatile uint32_t *>(head + 2 * c.page * c.row_bytes)[(is_v ? c.page : 0) +
-                                                                                                   p.slot];
+            ahead_word[i] =
+                reinterpret_cast<const volatile uint32_t *>(head + 2 * c.page * c.row_bytes)[(is_v ? c.page : 0) + slot];
         }
+    };
+    ask(0);
+#pragma unroll 1
+    for (int t = 0; t < rows; ++t) {
+        const int64_t r = r0 + t;
+        const int seq = __shfl_sync(0xffffffffu, places.seq, t);
+        uint32_t w[kReadItems][2], word[kReadItems];
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
+        for (int i = 0; i < kReadItems; ++i) w[i][0] = ahead[i][0], w[i][1] = ahead[i][1], word[i] = ahead_word[i];
+        if (t + 1 < rows) ask(t + 1);
+        if (!seq || !live) continue;
+#pragma unroll
+        for (int i = 0; i < kReadItems; ++i) {
             const int item = first + i * G;
             const bool is_v = item >= c.heads;
             if (item >= 2 * c.heads) continue;
@@ -281,7 +355,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const __grid_const
                 const int q = U4 ? (int)(w[i][0] >> (4 * e) & 15u) : (int)(w[i][e / 4] >> (8 * (e % 4)) & 255u);
                 x[e] = __fmul_rn((float)(q - z), s);
             }
-            store8(to + row * (is_v ? a.ld_v : a.ld_k) + (int64_t)(item - (is_v ? c.heads : 0)) * c.D + d0, a.vec, x);
+            store8(to + r * (is_v ? a.ld_v : a.ld_k) + (int64_t)(item - (is_v ? c.heads : 0)) * c.D + d0, a.vec, x);
         }
     }
 }
@@ -320,15 +394,17 @@ __global__ void __launch_bounds__(kKeepThreads) kv_keep_kernel(const __grid_cons
         return;
     }
     for (int i = threadIdx.x; i < n; i += kKeepThreads) {
-        const int64_t pf = (int64_t)s.len - s.T + keep[i], pt = (int64_t)s.len - s.T + i;
+        const int pf = s.len - s.T + keep[i], pt = s.len - s.T + i;
         from_page[i] = to_page[i] = -1;
         slots[i] = 0;
         if (pf == pt || pt < 0) continue;
-        const int f = kv_page(c, b, (int)(pf / c.page)), t = kv_page(c, b, (int)(pt / c.page));
+        int tile_f, tile_t;
+        const int index_f = kv_page_index(c, pf >> 4, &tile_f), index_t = kv_page_index(c, pt >> 4, &tile_t);
+        const int f = kv_page(c, b, index_f), t = kv_page(c, b, index_t);
         if (f < 0 || t < 0) continue;
         from_page[i] = f * c.page_bytes;
         to_page[i] = t * c.page_bytes;
-        slots[i] = (int)(pf % c.page) | (int)(pt % c.page) << 16;
+        slots[i] = (tile_f * 16 + (pf & 15)) | (tile_t * 16 + (pt & 15)) << 16;
     }
     __syncthreads();
     const int columns = 2 * (c.chunks + 1), col = blockIdx.x * kKeepThreads + threadIdx.x;
@@ -363,10 +439,11 @@ __global__ void __launch_bounds__(kKeepThreads) kv_keep_kernel(const __grid_cons
 template <typename T, bool U4, int W>
 qnn_status launch_io(KvIoArgs a, bool read, cudaStream_t s)
 {
-    const int per = kUnroll * (32 / W);
-    a.parts = (2 * a.c.heads + per - 1) / per;
-    const int64_t units = a.c.rows * a.parts, blocks = (units + kWarps - 1) / kWarps;
-    const dim3 grid((unsigned)std::min<int64_t>(blocks, (int64_t)sm_count() * 8));
+    // a row of blocks for each few items of a warp's groups; rows of a warp so that all warps run at once
+    const int per = (read ? kReadItems : kWriteItems) * (32 / W), parts = (2 * a.c.heads + per - 1) / per;
+    a.run = (int)std::min<int64_t>(32, std::max<int64_t>(1, (a.c.rows * parts + sm_count() * 24 - 1) / (sm_count() * 24)));
+    const int64_t block_rows = (int64_t)kWarps * a.run;
+    const dim3 grid((unsigned)((a.c.rows + block_rows - 1) / block_rows), (unsigned)parts);
     return read ? kv_launch(kv_read_kernel<T, U4, W>, grid, kWarps * 32, 0, s, a)
                 : kv_launch(kv_write_kernel<T, U4, W>, grid, kWarps * 32, 0, s, a);
 }

@@ -22,6 +22,7 @@ struct KvArgs {
     int64_t ld_table, rows, page_bytes;
     int num_pages, batch, tokens;
     int heads, D, page, head_bytes, row_bytes, chunks;  // chunks: of a row
+    uint32_t per16, magic16;  // 16-token tiles of a page, and 2^32 / per16 rounded up
     uint32_t *status;
 };
 
@@ -34,6 +35,48 @@ __host__ __device__ __forceinline__ int kv_chunk(int chunks, int t, int c)
     if ((chunks & 7) == 0) return c ^ (t & 7) ^ ((t & 1) << 2);
     if (chunks == 4) return c ^ (t >> 1 & 3);
     return c;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 as_f2(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ uint64_t as_u64(float2 v)
+{
+    uint64_t u;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(u) : "f"(v.x), "f"(v.y));
+    return u;
+}
+__device__ __forceinline__ float2 as_f2(uint64_t u)
+{
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(u));
+    return v;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
+    return as_f2(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
+    return as_f2(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
+    return as_f2(d);
+}
+
+// the largest, NaN aside
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 struct KvSeq {
@@ -67,7 +110,16 @@ __device__ __forceinline__ KvSeq kv_seq(const KvArgs &a, int b)
     return s;
 }
 
-// The page of position p of sequence b, or -1.
+// Tile / per16 for tiles of positions below 2^31 (per16 <= 16: the rounding of magic16 does not reach a
+// quotient), and the rest.
+__device__ __forceinline__ int kv_page_index(const KvArgs &a, int tile, int *rest)
+{
+    const int index = a.per16 == 1 ? tile : (int)__umulhi((uint32_t)tile, a.magic16);
+    *rest = tile - index * (int)a.per16;
+    return index;
+}
+
+// The index-th page of sequence b, or -1.
 __device__ __forceinline__ int kv_page(const KvArgs &a, int b, int index)
 {
     const int pg = *reinterpret_cast<const volatile int32_t *>(a.table + b * a.ld_table + index);

@@ -148,8 +148,6 @@ extern "C" qnn_status q_kv_attn(const void *q, qnn_dtype x_dt, int64_t ld_q, int
     a.blocks = p.blocks;
     a.bf16 = x_dt == QNN_BF16;
     a.ws = static_cast<float *>(workspace);
-    a.per16 = g->page / 16;
-    a.magic16 = (int)(((1ull << 32) + a.per16 - 1) / a.per16);
     const qnn_status sent = (many_rows(a.c, a.group) ? launch_attn_rows : launch_attn_few)(a, p, g->kv_dt == QNN_U4,
                                                                                           (cudaStream_t)stream);
     if (sent != QNN_OK) return sent;

@@ -17,7 +17,6 @@ struct KvAttnArgs {
     int heads_q, group, mask_words, bf16;
     int blocks;        // of the attention's grid
     int stages;        // of a ring
-    int per16, magic16;  // 16-token tiles of a page, and 2^32 / per16 rounded up
 };
 
 // The work: an item is a sequence's tile of rows (rows t * group + g, t a newest token, g one of
@@ -107,47 +106,6 @@ __device__ __forceinline__ void u4_pairs(uint32_t w, const Zero &z, uint32_t (&r
     r[1] = fma2(and_or(w, 0x00f000f0u, kMagic), kSixteenth, z.hi);
     r[2] = fma2(and_or(v, 0x000f000fu, kMagic), kOne, z.lo);
     r[3] = fma2(and_or(v, 0x00f000f0u, kMagic), kSixteenth, z.hi);
-}
-
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 as_f2(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
-__device__ __forceinline__ uint64_t as_u64(float2 v)
-{
-    uint64_t u;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(u) : "f"(v.x), "f"(v.y));
-    return u;
-}
-__device__ __forceinline__ float2 as_f2(uint64_t u)
-{
-    float2 v;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(u));
-    return v;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
-    return as_f2(d);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
-    return as_f2(d);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
-    return as_f2(d);
-}
-
-// the largest, NaN aside
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
 }
 
 // 2^k as fp32, -126 <= k <= 127
@@ -324,9 +282,7 @@ __device__ __forceinline__ void copies_wait(int n)
 // The page of 16-token tile `tile` of sequence b, or -1.
 __device__ __forceinline__ int attn_page(const KvAttnArgs &a, int b, int tile, int *in_page)
 {
-    const int index = a.per16 == 1 ? tile : (int)__umulhi((uint32_t)tile, (uint32_t)a.magic16);
-    *in_page = tile - index * a.per16;
-    return kv_page(a.c, b, index);
+    return kv_page(a.c, b, kv_page_index(a.c, tile, in_page));
 }
 
 // Whether newest token t's row sees position p.
