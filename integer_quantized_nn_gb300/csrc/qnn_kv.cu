@@ -411,18 +411,19 @@ __global__ void __launch_bounds__(kKeepThreads) kv_keep_kernel(const __grid_cons
     if (col >= columns * c.heads) return;
     const int head = col / columns, x = col % columns, is_v = x / (c.chunks + 1), chunk = x % (c.chunks + 1);
     uint8_t *base = c.pages + (int64_t)head * c.head_bytes;
-    auto move = [&](auto kind, auto at) {  // four at a time: loads, then stores
+    constexpr int kAtOnce = 8;
+    auto move = [&](auto kind, auto at) {  // some at a time: loads, then stores
         using V = decltype(kind);
-        for (int i0 = 0; i0 < n; i0 += 4) {
-            V v[4];
+        for (int i0 = 0; i0 < n; i0 += kAtOnce) {
+            V v[kAtOnce];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < kAtOnce; ++e) {
                 const int i = i0 + e;
                 if (i < n && from_page[i] >= 0)
                     v[e] = *reinterpret_cast<const V *>(base + from_page[i] + at(slots[i] & 0xffff));
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < kAtOnce; ++e) {
                 const int i = i0 + e;
                 if (i < n && from_page[i] >= 0) *reinterpret_cast<V *>(base + to_page[i] + at(slots[i] >> 16)) = v[e];
             }
@@ -439,9 +440,12 @@ __global__ void __launch_bounds__(kKeepThreads) kv_keep_kernel(const __grid_cons
 template <typename T, bool U4, int W>
 qnn_status launch_io(KvIoArgs a, bool read, cudaStream_t s)
 {
-    // a row of blocks for each few items of a warp's groups; rows of a warp so that all warps run at once
+    // A row of blocks for each few items of a warp's groups.  Rows of a warp: as many as let all warps run at once,
+    // 8 at most for a read, whose later blocks even out the rest (8 x 4096 tokens of 8 heads of 128 in 8 bits to bf16:
+    // 40.5 us with 4 or 8, 49.4 with 32, 48.7 with 1; 4 x 4000 tokens written and read in 4 bits: 47.7 us with 8 or
+    // 32 for the read, 60.9 to 73 with 4 for the write).
     const int per = (read ? kReadItems : kWriteItems) * (32 / W), parts = (2 * a.c.heads + per - 1) / per;
-    a.run = (int)std::min<int64_t>(32, std::max<int64_t>(1, (a.c.rows * parts + sm_count() * 24 - 1) / (sm_count() * 24)));
+    a.run = (int)std::min<int64_t>(read ? 8 : 32, std::max<int64_t>(1, (a.c.rows * parts + sm_count() * 24 - 1) / (sm_count() * 24)));
     const int64_t block_rows = (int64_t)kWarps * a.run;
     const dim3 grid((unsigned)((a.c.rows + block_rows - 1) / block_rows), (unsigned)parts);
     return read ? kv_launch(kv_read_kernel<T, U4, W>, grid, kWarps * 32, 0, s, a)
