@@ -6,79 +6,135 @@
 namespace qnn {
 namespace {
 
+// What joins parts of the online softmax: the maximum, the power of two that the values are in, sums.
+template <int V>
+struct Joined {
+    float top = -INFINITY, unit = 0.0f, total = 0.0f, sum[V] = {};
+
+    // what there is, in a larger maximum and unit
+    __device__ __forceinline__ void move(float new_top, float new_unit)
+    {
+        const float f = top == new_top ? 1.0f : ex2(top - new_top), g = f * (unit * per(new_unit));
+        total *= f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum[e] *= g;
+        top = new_top, unit = new_unit;
+    }
+    // 1 / unit: of powers of two, so that a product with it is exact
+    static __device__ __forceinline__ float per(float unit) { return __uint_as_float(0x7f000000u - __float_as_uint(unit)); }
+};
+
+template <int V>
+__device__ __forceinline__ void load_channels(const float *p, float (&x)[V])
+{
+    if constexpr (V == 2) {
+        const float2 w = *reinterpret_cast<const float2 *>(p);
+        x[0] = w.x, x[1] = w.y;
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; e += 4) {
+            const float4 w = *reinterpret_cast<const float4 *>(p + e);
+            x[e] = w.x, x[e + 1] = w.y, x[e + 2] = w.z, x[e + 3] = w.w;
+        }
+    }
+}
+
 constexpr int kJoinWarps = 8;
 
-// A warp joins a row of the item that begins in block blockIdx.x's share and ends in a later one's, if
-// there is one: lane k has the statistics of part k (and k + 32, ..), all lanes the channels.  Only the
-// record is waited for before everything else is asked for.
+// Block (x, y) joins up to 8 rows of the item that begins in block x's share and ends in a later
+// one's, if there is one.  Where fewer rows are left than warps, several warps have a row: each joins
+// every so manieth part, the first of them what all have (a row with 38 parts: 12 us, 21 with one warp).  Lane k has the statistics of a warp's part k
+// (and k + 32, ..), all lanes the channels.  A chain of reads that wait for one another is all that takes
+// time here, so only the record is waited for before the first parts are asked for.
 template <int V>  // channels of a lane: 2, 4 or 8
 __global__ void __launch_bounds__(kJoinWarps * 32) kv_attn_join_kernel(const __grid_constant__ KvAttnArgs a, int rows)
 {
-    constexpr int channels = 32 * V;
-    const int lane = threadIdx.x & 31, block = blockIdx.x;
+    constexpr int channels = 32 * V, kWarps = kJoinWarps, kAtOnce = 4;
+    __shared__ float values[kWarps][channels];
+    __shared__ float stats[kWarps][3];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, block = blockIdx.x;
     grid_dependency_launch();
     grid_dependency_wait();
     int4 rec;
     asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(rec.x), "=r"(rec.y), "=r"(rec.z), "=r"(rec.w)
                  : "l"(reinterpret_cast<const int4 *>(a.ws) + 2 * block));
-    const int n = rec.x - block + 1, row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
-    if (rec.x < 0 || row >= rec.w) return;
+    const int left = rec.w - (int)blockIdx.y * kWarps;
+    if (rec.x < 0 || left <= 0) return;
     const int64_t first = *reinterpret_cast<const volatile int64_t *>(reinterpret_cast<const int4 *>(a.ws) + 2 * block + 1);
+    // a power of two of warps to a row
+    const int shift = left >= kWarps ? 0 : __clz(left > 1 ? left - 1 : 0) - __clz(kWarps - 1);
+    const int each = 1 << shift, sub = warp & (each - 1), row = blockIdx.y * kWarps + (warp >> shift);
+    const bool live = row < rec.w;
+    const int n = live ? (rec.x - block + 1 - sub + each - 1) >> shift : 0;  // parts of this warp
     const float *part0 = attn_slot(a, block, 1, rows, channels), *part1 = attn_slot(a, block + 1, 0, rows, channels);
     const int64_t pitch = 2 * attn_slot_floats(rows, channels);  // between the parts after the first
-    auto part = [&](int k) { return k == 0 ? part0 : part1 + (k - 1) * pitch; };
+    auto part = [&](int i) {
+        const int k = (i << shift) + sub;
+        return k == 0 ? part0 : part1 + (k - 1) * pitch;
+    };
     const int d = lane * V;
-    float top = -INFINITY, unit = 0.0f, total = 0.0f, sum[V];
+    Joined<V> j;
+    for (int i0 = 0; i0 < n; i0 += 32) {  // 32 parts at a time
+        const int here = min(32, n - i0);
+        float x[kAtOnce][V], m = -INFINITY, l = 0.0f, u = 0.0f;
+        auto ask = [&](int i) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) sum[e] = 0.0f;
-    // 32 parts at a time; what came before is scaled to the new maximum and unit
-    for (int k0 = 0; k0 < n; k0 += 32) {
-        const int here = min(32, n - k0);
-        float m = -INFINITY, l = 0.0f, u = 0.0f;
+            for (int k = 0; k < kAtOnce; ++k)
+                if (i + k < here) load_channels(part(i0 + i + k) + (int64_t)row * channels + d, x[k]);
+        };
         if (lane < here) {
-            const float *p = part(k0 + lane) + (int64_t)rows * channels;
+            const float *p = part(i0 + lane) + (int64_t)rows * channels;
             const float2 ml = *reinterpret_cast<const float2 *>(p + 2 * row);
             m = ml.x, l = ml.y, u = p[2 * rows];
         }
-        float was = top, was_unit = unit;
-        top = fmaxf(top, m), unit = fmaxf(unit, u);
+        ask(0);
+        float top = fmaxf(j.top, m), unit = fmaxf(j.unit, u);
 #pragma unroll
         for (int b = 16; b > 0; b /= 2) {
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, b));
             unit = fmaxf(unit, __shfl_xor_sync(0xffffffffu, unit, b));
         }
-        // units are powers of two: the quotient by a reciprocal is exact
-        const float per = __uint_as_float(0x7f000000u - __float_as_uint(unit));
-        const float f = m == top ? 1.0f : ex2(m - top), g = lane < here ? f * (u * per) : 0.0f;
+        j.move(top, unit);
+        const float f = m == top ? 1.0f : ex2(m - top), g = lane < here ? f * (u * j.per(unit)) : 0.0f;
         float t = lane < here ? l * f : 0.0f;
 #pragma unroll
         for (int b = 16; b > 0; b /= 2) t += __shfl_xor_sync(0xffffffffu, t, b);
-        const float back = was == top ? 1.0f : ex2(was - top);
-        total = k0 ? __fmaf_rn(total, back, t) : t;
-        if (k0) {
+        j.total += t;
+        for (int i = 0; i < here; i += kAtOnce) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) sum[e] *= back * (was_unit * per);
-        }
-#pragma unroll 8
-        for (int k = 0; k < here; ++k) {
-            const float *p = part(k0 + k) + (int64_t)row * channels + d;
-            const float w = __shfl_sync(0xffffffffu, g, k);
-            if constexpr (V == 8) {
-                const float4 x = *reinterpret_cast<const float4 *>(p), y = *reinterpret_cast<const float4 *>(p + 4);
-                sum[0] = __fmaf_rn(x.x, w, sum[0]), sum[1] = __fmaf_rn(x.y, w, sum[1]), sum[2] = __fmaf_rn(x.z, w, sum[2]);
-                sum[3] = __fmaf_rn(x.w, w, sum[3]), sum[4] = __fmaf_rn(y.x, w, sum[4]), sum[5] = __fmaf_rn(y.y, w, sum[5]);
-                sum[6] = __fmaf_rn(y.z, w, sum[6]), sum[7] = __fmaf_rn(y.w, w, sum[7]);
-            } else if constexpr (V == 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(p);
-                sum[0] = __fmaf_rn(x.x, w, sum[0]), sum[1] = __fmaf_rn(x.y, w, sum[1]);
-                sum[2] = __fmaf_rn(x.z, w, sum[2]), sum[3] = __fmaf_rn(x.w, w, sum[3]);
-            } else {
-                const float2 x = *reinterpret_cast<const float2 *>(p);
-                sum[0] = __fmaf_rn(x.x, w, sum[0]), sum[1] = __fmaf_rn(x.y, w, sum[1]);
+            for (int k = 0; k < kAtOnce; ++k) {
+                const float w = __shfl_sync(0xffffffffu, g, i + k);
+                if (i + k >= here) continue;
+#pragma unroll
+                for (int e = 0; e < V; ++e) j.sum[e] = __fmaf_rn(x[k][e], w, j.sum[e]);
             }
+            ask(i + kAtOnce);
         }
     }
+    if (each > 1) {
+        if (sub) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) values[warp][e * 32 + lane] = j.sum[e];
+            if (lane == 0) stats[warp][0] = j.top, stats[warp][1] = j.unit, stats[warp][2] = j.total;
+        }
+        __syncthreads();
+        if (sub) return;
+        for (int w = warp + 1; w < warp + min(each, rec.x - block + 1); ++w) {
+            Joined<V> o;
+            o.top = stats[w][0], o.unit = stats[w][1], o.total = stats[w][2];
+#pragma unroll
+            for (int e = 0; e < V; ++e) o.sum[e] = values[w][e * 32 + lane];
+            const float top = fmaxf(j.top, o.top), unit = fmaxf(j.unit, o.unit);
+            j.move(top, unit), o.move(top, unit);
+            j.total += o.total;
+#pragma unroll
+            for (int e = 0; e < V; ++e) j.sum[e] += o.sum[e];
+        }
+    }
+    if (!live) return;
+    const float total = j.total, unit = j.unit, top = j.top;
+    const float (&sum)[V] = j.sum;
     const float by = total == 0.0f ? 0.0f : kAttnWeightUnit * unit / total;
     const int r = rec.z + row, tok = r / a.group, hq = rec.y * a.group + (r - tok * a.group);
     if (d < a.c.D) {
