@@ -119,16 +119,18 @@ __device__ __forceinline__ int kv_page_index(const KvArgs &a, int tile, int *res
     return index;
 }
 
-// The index-th page of sequence b, or -1.
-__device__ __forceinline__ int kv_page(const KvArgs &a, int b, int index)
+// The index-th page of sequence b as it stands in the table, and that page if it is one, or -1.
+__device__ __forceinline__ int kv_entry(const KvArgs &a, int b, int index)
 {
-    const int pg = *reinterpret_cast<const volatile int32_t *>(a.table + b * a.ld_table + index);
-    if (pg < 0 || pg >= a.num_pages) {
-        kv_bad(a);
-        return -1;
-    }
-    return pg;
+    return *reinterpret_cast<const volatile int32_t *>(a.table + b * a.ld_table + index);
 }
+__device__ __forceinline__ int kv_checked(const KvArgs &a, int pg)
+{
+    if (pg >= 0 && pg < a.num_pages) return pg;
+    kv_bad(a);
+    return -1;
+}
+__device__ __forceinline__ int kv_page(const KvArgs &a, int b, int index) { return kv_checked(a, kv_entry(a, b, index)); }
 
 inline int kv_row_bytes(const qnn_kv_geom &g) { return g.kv_dt == QNN_S8 ? g.D : g.D / 2; }
 
