@@ -171,7 +171,7 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
 
     // the copies' side: `ahead` is the unit whose page has been looked up
     AttnCursor ahead = find(a, sums, share.from, S::kRows), at = ahead;
-    int64_t asked = share.from;  // units whose copies have been issued
+    int64_t unasked = share.to - share.from;  // units whose copies are still to be issued
     int entry = 0, in_page = 0;
     bool some = false;
     auto look_up = [&]() {  // what it asks for is looked at a tile later
@@ -181,7 +181,7 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
     };
     uint32_t absent = 0;  // stages whose tile is not there
     auto ask = [&](int stage) {  // a group of copies, if only an empty one
-        if (asked < share.to) {
+        if (unasked > 0) {
             const int page = some ? kv_checked(c, entry) : -1;
             const bool there = page >= 0;
             absent = there ? absent & ~(1u << stage) : absent | 1u << stage;
@@ -199,7 +199,7 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
                 if (lane < 8)
                     copy_async16(to + 2 * rows, head + 2 * all + (lane < 4 ? 0 : 4 * c.page - 64) + in_page * 64 + 16 * lane);
             }
-            if (++asked < share.to) {
+            if (--unasked > 0) {
                 next(a, ahead, S::kRows);
                 look_up();
             }
@@ -208,6 +208,22 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
     };
     look_up();
     for (int i = 0; i < ST; ++i) ask(i);
+
+    // where a lane's words are in a stage: of K's token g, of V's tokens 2j and 2j + 1 (8 tokens on: the same
+    // order of chunks, 8 rows on)
+    constexpr int kKLoads = (S::kKWords + 3) / 4, kVLoads = (S::kVWords + 3) / 4;
+    int k_off[kKLoads], v_off[2][kVLoads];
+#pragma unroll
+    for (int w = 0; w < kKLoads; ++w)
+        k_off[w] = g * c.row_bytes + 16 * kv_chunk(c.chunks, g, k_chunk<U4, DP>(j, 4 * w)) + k_byte<U4, DP>(j);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int w = 0; w < kVLoads; ++w) {
+            const int byte = v_byte<U4, DP>(g) + w * 128;
+            v_off[e][w] = (16 + 2 * j + e) * c.row_bytes + 16 * kv_chunk(c.chunks, 2 * j + e, byte / 16) + byte % 16;
+        }
+    const int eight = 8 * c.row_bytes;
 
     int stage = 0;
     int64_t x = share.from;
@@ -298,15 +314,14 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
             ref[nt][0] = ref[nt][1] = l[nt][0] = l[nt][1] = 0.0f;
         }
 
-        for (; x < end; ++x, next(a, at, S::kRows)) {
-            const int pos0 = (at.chunk * kWarps + warp) * 16;
+        const int seen_by_all = a.mask ? at.len - at.T : min(at.len, at.len - at.T + t_first + 1);
+        const int seen_by_any = a.mask ? at.len : at.len - at.T + t_last + 1;
+        int pos0 = (at.chunk * kWarps + warp) * 16;
+        for (int left = (int)(end - x); left > 0; --left, pos0 += kAttnChunk) {
             copies_wait(ST - 1);
             __syncwarp();
-            const int seen_by_all = a.mask ? at.len - at.T : min(at.len, at.len - at.T + t_first + 1);
-            const int seen_by_any = a.mask ? at.len : at.len - at.T + t_last + 1;
             if (!(absent >> stage & 1u) && pos0 < seen_by_any) {
-                const uint32_t k_at = ring_at + stage * stage_b, v_at = k_at + 16 * c.row_bytes,
-                               w_at = v_at + 16 * c.row_bytes;
+                const uint32_t k_at = ring_at + stage * stage_b, w_at = k_at + 4 * eight;
                 // scales of K and V of tokens g and g + 8
                 const uint32_t wk0 = lds32(w_at + 4 * g), wk1 = lds32(w_at + 4 * g + 32);
                 const uint32_t wv0 = lds32(w_at + 64 + 4 * g), wv1 = lds32(w_at + 64 + 4 * g + 32);
@@ -322,10 +337,8 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
                     constexpr int step_w = S::kKWords < 4 ? S::kKWords : 4;
 #pragma unroll
                     for (int w = 0; w < S::kKWords; w += step_w) {
-                        const int ch = k_chunk<U4, DP>(j, w);
-                        lds<step_w>(k_at + g * c.row_bytes + 16 * kv_chunk(c.chunks, g, ch) + k_byte<U4, DP>(j), k0 + w);
-                        lds<step_w>(k_at + (g + 8) * c.row_bytes + 16 * kv_chunk(c.chunks, g + 8, ch) + k_byte<U4, DP>(j),
-                                    k1 + w);
+                        lds<step_w>(k_at + k_off[w / 4], k0 + w);
+                        lds<step_w>(k_at + k_off[w / 4] + eight, k1 + w);
                     }
 #pragma unroll
                     for (int w = 0; w < S::kKWords; ++w) {
@@ -384,7 +397,7 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
                         }
                     }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) over = over || s[nt][e] > m[nt][e & 1] + kAttnSlack;
+                    for (int e = 0; e < 2; ++e) over = over || fmaxf(s[nt][e], s[nt][e + 2]) > m[nt][e] + kAttnSlack;
                 }
                 over = over || sv0 > unit || sv1 > unit;
                 if (__any_sync(0xffffffffu, over)) {
@@ -433,14 +446,10 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
                 uint32_t vw[4][S::kVWords];
                 constexpr int step_v = S::kVWords < 4 ? S::kVWords : 4;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = 2 * j + (e & 1) + 8 * (e >> 1);
+                for (int e = 0; e < 4; ++e)
 #pragma unroll
-                    for (int w = 0; w < S::kVWords; w += step_v) {
-                        const int byte = v_byte<U4, DP>(g) + (w / 4) * 128;
-                        lds<step_v>(v_at + t * c.row_bytes + 16 * kv_chunk(c.chunks, t, byte / 16) + byte % 16, vw[e] + w);
-                    }
-                }
+                    for (int w = 0; w < S::kVWords; w += step_v)
+                        lds<step_v>(k_at + v_off[e & 1][w / 4] + (e >> 1) * eight, vw[e] + w);
                 uint32_t za = 0x00800080u, zb = za;  // zero points of tokens 2j and 2j + 1, 2j + 8 and 2j + 9
                 if constexpr (U4) {
                     const uint2 ta = lds64(w_at + 64 + 8 * j), tb = lds64(w_at + 64 + 8 * j + 32);
@@ -481,6 +490,9 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
             ask(stage);
             if (++stage == ST) stage = 0;
         }
+        x = end;
+        at.chunk = at.units - 1;  // (where this is not so, nothing follows)
+        if (x < share.to) next(a, at, S::kRows);
         // the warps' parts meet
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
