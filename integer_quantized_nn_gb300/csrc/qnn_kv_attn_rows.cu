@@ -154,107 +154,101 @@ __device__ __forceinline__ uint32_t seen_bits(const KvAttnArgs &a, const Item &c
     return (low_bits(-j0) | __funnelshift_r(lo, hi, j0 & 31)) & low_bits(c.len - p0);
 }
 
-// A warp's 32 rows of S of a chunk -> P over it.  A thread has 4 rows and the columns 8 i + 2 j and + 1 of each:
-// with a row to a thread each would read all scales of the chunk from shared memory, 1500 cycles
-// of its bandwidth a chunk; so it is a quarter.  scales: of K and V, of the thread's first two columns; bits:
-// lane t has those of the positions that row t sees.
+// A warp's 16 rows of S of a chunk -> P over it.  A thread has 2 rows (8 q + g) and the columns 8 i + 2 j and + 1 of
+// each: with a row to a thread each would read all scales of the chunk from shared memory, 1500 cycles
+// of its bandwidth a chunk.  scales: of K and V, of the thread's first two columns; bits: lanes t and t + 16 have
+// those of the positions that row t sees.
 template <bool MASKED, int DP>
 __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, uint32_t scales, const uint32_t (&bits)[4], int j,
-                                        bool first, float ratio, const float (&cr)[4], float (&m)[4], float (&ref)[4],
-                                        float (&l)[4])
+                                        bool first, float ratio, const float (&cr)[2], float (&m)[2], float (&ref)[2],
+                                        float (&l)[2])
 {
     const int g = (threadIdx.x & 31) >> 2;
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-        const uint32_t down = (uint32_t)(16 * half) << 16;
-        // by selection and not by index: the arrays stay in registers
-        const float c0 = half ? cr[2] : cr[0], c1 = half ? cr[3] : cr[1];
-        float m0 = half ? m[2] : m[0], m1 = half ? m[3] : m[1], r0 = half ? ref[2] : ref[0], r1 = half ? ref[3] : ref[1];
-        float l0 = half ? l[2] : l[0], l1 = half ? l[3] : l[1];
-        uint32_t b0[4], b1[4], p[32];
-        if constexpr (MASKED) {
+    uint32_t b[2][4], p[32];
+    if constexpr (MASKED) {
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                b0[b] = __shfl_sync(0xffffffffu, bits[b], 16 * half + g) >> (2 * j);
-                b1[b] = __shfl_sync(0xffffffffu, bits[b], 16 * half + 8 + g) >> (2 * j);
-            }
-        }
-        // The maxima so far are tried first: a thread's 32 weights of a row whose sum stays below 2^8 are
-        // all below it.  New maxima are looked for where they do not, at first and with a new unit.
-        bool fresh = MASKED || first || ratio != 1.0f;
-        float2 s0, s1;
-#pragma unroll 1
-        for (;;) {
-            uint32_t v[64];
-            if (fresh) {
-                float top0 = -INFINITY, top1 = -INFINITY;
-                tmem_ld_frag(s_at + down, v);
-                tmem_ld_wait();
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const uint4 kw = lds_v4(scales + 64 * i);
-                    const float2 k = as_f2(kw.x, kw.y);
-                    float2 y0 = mul2(as_f2(v[4 * i], v[4 * i + 1]), k), y1 = mul2(as_f2(v[4 * i + 2], v[4 * i + 3]), k);
-                    if constexpr (MASKED) {
-                        const uint32_t bit = 1u << (8 * (i & 3));
-                        y0.x = b0[i >> 2] & bit ? y0.x : -INFINITY, y0.y = b0[i >> 2] & (2 * bit) ? y0.y : -INFINITY;
-                        y1.x = b1[i >> 2] & bit ? y1.x : -INFINITY, y1.y = b1[i >> 2] & (2 * bit) ? y1.y : -INFINITY;
-                    }
-                    top0 = max3(top0, y0.x, y0.y), top1 = max3(top1, y1.x, y1.y);
-                }
-                top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 1)), top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
-                top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 2)), top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 2));
-                if (top0 != -INFINITY) top0 *= c0;
-                if (top1 != -INFINITY) top1 *= c1;
-                const float u0 = fmaxf(m0, top0), u1 = fmaxf(m1, top1);
-                float f0 = m0 == -INFINITY ? 0.0f : ex2(m0 - u0), f1 = m1 == -INFINITY ? 0.0f : ex2(m1 - u1);
-                m0 = u0, m1 = u1;
-                r0 = u0 == -INFINITY ? 0.0f : u0, r1 = u1 == -INFINITY ? 0.0f : u1;
-                l0 *= f0, l1 *= f1, f0 *= ratio, f1 *= ratio;
-                if (!first && __any_sync(0xffffffffu, f0 != 1.0f || f1 != 1.0f)) {
+            for (int w = 0; w < 4; ++w) b[q][w] = __shfl_sync(0xffffffffu, bits[w], 8 * q + g) >> (2 * j);
+    }
+    // The maxima so far are tried first: a thread's 32 weights of a row whose sum stays below 2^8 are
+    // all below it.  New maxima are looked for where they do not, at first and with a new unit.
+    bool fresh = MASKED || first || ratio != 1.0f;
+    float2 s[2];
 #pragma unroll 1
-                    for (int b = 0; b < DP / 32; ++b) {
-                        uint32_t o[16];
-                        tmem_ld_frag(o_at + down + 32 * b, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (e & 2 ? f1 : f0));
-                        tmem_st_frag(o_at + down + 32 * b, o);
-                    }
-                }
-            }
-            const float2 cc0 = make_float2(c0, c0), cc1 = make_float2(c1, c1), n0 = make_float2(-r0, -r0), n1 = make_float2(-r1, -r1);
-            s0 = s1 = make_float2(0.0f, 0.0f);
-            tmem_ld_frag(s_at + down, v);
+    for (;;) {
+        uint32_t v[64];
+        if (fresh) {
+            float top[2] = {-INFINITY, -INFINITY}, f[2];
+            tmem_ld_frag(s_at, v);
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const uint4 kw = lds_scales(scales + 64 * i);
-                const float2 k = as_f2(kw.x, kw.y), w = as_f2(kw.z, kw.w);
-                float2 y0 = mul2(as_f2(v[4 * i], v[4 * i + 1]), k), y1 = mul2(as_f2(v[4 * i + 2], v[4 * i + 3]), k);
-                y0 = fma2(y0, cc0, n0), y1 = fma2(y1, cc1, n1);
-                y0.x = ex2(y0.x), y0.y = ex2(y0.y), y1.x = ex2(y1.x), y1.y = ex2(y1.y);
-                if constexpr (MASKED) {
-                    const uint32_t bit = 1u << (8 * (i & 3));
-                    y0.x = b0[i >> 2] & bit ? y0.x : 0.0f, y0.y = b0[i >> 2] & (2 * bit) ? y0.y : 0.0f;
-                    y1.x = b1[i >> 2] & bit ? y1.x : 0.0f, y1.y = b1[i >> 2] & (2 * bit) ? y1.y : 0.0f;
+                const uint4 kw = lds_v4(scales + 64 * i);
+                const float2 k = as_f2(kw.x, kw.y);
+                const uint32_t bit = 1u << (8 * (i & 3));
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float2 y = mul2(as_f2(v[4 * i + 2 * q], v[4 * i + 2 * q + 1]), k);
+                    if constexpr (MASKED) {
+                        y.x = b[q][i >> 2] & bit ? y.x : -INFINITY;
+                        y.y = b[q][i >> 2] & (2 * bit) ? y.y : -INFINITY;
+                    }
+                    top[q] = max3(top[q], y.x, y.y);
                 }
-                s0 = add2(s0, y0), s1 = add2(s1, y1);
-                y0 = mul2(y0, w), y1 = mul2(y1, w);
-                const __half2 h0 = __floats2half2_rn(y0.x, y0.y), h1 = __floats2half2_rn(y1.x, y1.y);
-                p[2 * i] = *reinterpret_cast<const uint32_t *>(&h0);
-                p[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&h1);
             }
-            s0.x += s0.y, s1.x += s1.y;
-            if (fresh) break;
-            fresh = __any_sync(0xffffffffu, s0.x > (float)(1 << kAttnSlack) || s1.x > (float)(1 << kAttnSlack));
-            if (!fresh) break;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                top[q] = fmaxf(top[q], __shfl_xor_sync(0xffffffffu, top[q], 1));
+                top[q] = fmaxf(top[q], __shfl_xor_sync(0xffffffffu, top[q], 2));
+                if (top[q] != -INFINITY) top[q] *= cr[q];
+                const float u = fmaxf(m[q], top[q]);
+                f[q] = m[q] == -INFINITY ? 0.0f : ex2(m[q] - u);
+                m[q] = u;
+                ref[q] = u == -INFINITY ? 0.0f : u;
+                l[q] *= f[q], f[q] *= ratio;
+            }
+            if (!first && __any_sync(0xffffffffu, f[0] != 1.0f || f[1] != 1.0f)) {
+#pragma unroll 1
+                for (int at = 0; at < DP; at += 32) {
+                    uint32_t o[16];
+                    tmem_ld_frag(o_at + at, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (e & 2 ? f[1] : f[0]));
+                    tmem_st_frag(o_at + at, o);
+                }
+            }
         }
-        tmem_st_pairs(s_at + down, p);
-        l0 += s0.x, l1 += s1.x;
-        if (half) m[2] = m0, m[3] = m1, ref[2] = r0, ref[3] = r1, l[2] = l0, l[3] = l1;
-        else m[0] = m0, m[1] = m1, ref[0] = r0, ref[1] = r1, l[0] = l0, l[1] = l1;
+        tmem_ld_frag(s_at, v);
+        tmem_ld_wait();
+        s[0] = s[1] = both(0.0f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint4 kw = lds_scales(scales + 64 * i);
+            const float2 k = as_f2(kw.x, kw.y), w = as_f2(kw.z, kw.w);
+            const uint32_t bit = 1u << (8 * (i & 3));
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float2 y = fma2(mul2(as_f2(v[4 * i + 2 * q], v[4 * i + 2 * q + 1]), k), both(cr[q]), both(-ref[q]));
+                y.x = ex2(y.x), y.y = ex2(y.y);
+                if constexpr (MASKED) {
+                    y.x = b[q][i >> 2] & bit ? y.x : 0.0f;
+                    y.y = b[q][i >> 2] & (2 * bit) ? y.y : 0.0f;
+                }
+                s[q] = add2(s[q], y);
+                y = mul2(y, w);
+                const __half2 h = __floats2half2_rn(y.x, y.y);
+                p[2 * i + q] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+        }
+        s[0].x += s[0].y, s[1].x += s[1].y;
+        if (fresh) break;
+        fresh = __any_sync(0xffffffffu, s[0].x > (float)(1 << kAttnSlack) || s[1].x > (float)(1 << kAttnSlack));
+        if (!fresh) break;
     }
+    tmem_st_pairs(s_at, p);
+    l[0] += s[0].x, l[1] += s[1].x;
 }
 
 // PAIR: the streams are two tiles of rows over the same chunks, which are converted once for both.
@@ -271,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
     __shared__ __align__(16) Info infos[kInfos];
     __shared__ __align__(16) Tile16 places[kPlaces][kTokens / 16];
     __shared__ Item items[kItems];
-    __shared__ float row_m[2][kRows], row_l[2][kRows], row_top[2][kRows], stream_unit[2];
+    __shared__ float row_m[2][kRows], row_l[2][kRows], row_top[2][kRows], row_c[2][kRows], stream_unit[2];
     __shared__ uint32_t present[kPlaces], tmem_slot;  // 16-token tiles of a chunk that are there
     uint8_t *smem = raw + (-smem_u32(raw) & 1023u);  // the swizzle's atoms
     // tiles: K of even and odd chunks, V of both; q (of both streams); the sums of the line
@@ -290,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         }
         for (int i = 0; i < kInfos; ++i) {
             mbar_init(smem_u32(&info_full[i]), 2);
-            mbar_init(smem_u32(&info_empty[i]), PAIR ? kRowWarps : kRowWarps / 2);
+            mbar_init(smem_u32(&info_empty[i]), kRowWarps);
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(smem_u32(&item_full[i]), 1);
@@ -298,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&s_full[i]), 1);
-            mbar_init(smem_u32(&p_ready[i]), kRowWarps / 2);
+            mbar_init(smem_u32(&p_ready[i]), kRowWarps);
         }
         mbar_init(smem_u32(&q_full), kRowWarps);
         mbar_init(smem_u32(&o_full), 1);
@@ -332,9 +326,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         return ok;  // a wait that gave up is reported at the end
     };
 
-    // 128 registers a thread at the launch, and as many after: 72 + 104 + 2 * 168 = 4 * 128
+    // 128 registers a thread at the launch, and as many after: 88 + 120 + 2 * 152 = 4 * 128
     if (warp < kCodeWarp0) {
-    regs_dec<72>();
+    regs_dec<88>();
     if (chunks <= 0) {
     } else if (warp == 0) {
         AttnCursor at = attn_find(a, sums, share.from, ROWS);
@@ -493,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         }
     }
     } else if (warp < kRowWarp0) {
-        regs_dec<104>();
+        regs_dec<120>();
         // Warps 4 and 5 have K, 6 and 7 V, each 64 tokens of a chunk, in registers a chunk ahead.  Eight
         // lanes have four 16-byte pieces of two rows at a time: what they store of a chunk of 8 f16 then
         // lies in eight different places of the swizzle.
@@ -572,8 +566,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             release(tile_full[2 * is_v + (n & 1)]);
         }
     } else {
-        regs_inc<168>();
-        const int stream = (warp - kRowWarp0) >> 2, r = (threadIdx.x - kRowWarp0 * 32) & 127;
+        regs_inc<152>();
+        // All eight warps have the streams' steps in turn, while the other stream's products are under way: warps
+        // w and w + 4 have 16 rows each of a quarter of them.
+        const int part = (warp - kRowWarp0) >> 2, r = (threadIdx.x - kRowWarp0 * 32) & 127;
         const int g = lane >> 2, j = lane & 3;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         auto meet = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
@@ -594,10 +590,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             (void)wait(item_full[(unsigned)item % kItems], (unsigned)item / kItems);
             if (!all_ok()) break;
             const Item &at = items[(unsigned)item % kItems];
-            const int count = at.count, row0 = at.rt * ROWS + (PAIR ? stream * kRows : 0);
+            // row0, r: of q and the sums; PAIR: the rows of stream `part`, else all, half of the channels each
+            const int count = at.count, row0 = at.rt * ROWS + (PAIR ? part * kRows : 0);
             const int width = min(kRows, at.T * a.group - row0);
-            const int rr = row0 + r, t = min(rr / a.group, at.T - 1);
-            const int t_first = min(row0 / a.group, at.T - 1);
+            const int rr = row0 + r;
             const bool live = r < width, starts_here = n > 0 || at.chunk == 0, ends_here = at.chunk + count == at.units;
             if (threadIdx.x == kRowWarp0 * 32 && n + count == chunks) {
                 const int tile0 = at.rt * ROWS;
@@ -608,12 +604,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             const int hq = at.h * a.group + rr % a.group;
 
             // q: a row for each thread, or half a row; its largest value is brought near f16's by a power of two
-            float cq;
             {
                 constexpr int W = PAIR ? DP / 8 : DP / 16;  // pieces of 8 values
                 const int mine = PAIR ? c.D : c.D / 2;      // a multiple of 16
                 const uint16_t *qp = static_cast<const uint16_t *>(a.q) + out_row * a.ld_q + (int64_t)hq * c.D +
-                                     (PAIR ? 0 : stream * mine);
+                                     (PAIR ? 0 : part * mine);
                 uint4 w[W];
                 float top = 0.0f;
 #pragma unroll
@@ -635,14 +630,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                     for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(value(u[e / 2], e & 1)));
                 }
                 if constexpr (!PAIR) {
-                    row_top[stream][r] = top;
+                    row_top[part][r] = top;
                     meet();
                     top = fmaxf(row_top[0][r], row_top[1][r]);
                 }
                 const int e2 = (int)(__float_as_uint(top) >> 23);
                 const int k = top == 0.0f || e2 == 255 ? 0 : max(-126, min(126, 14 + 127 - e2));
-                const float up = a.scale_log2 < 0.0f ? -pow2i(k) : pow2i(k);  // cq >= 0
-                cq = fabsf(a.scale_log2) * pow2i(-k);
+                const float up = a.scale_log2 < 0.0f ? -pow2i(k) : pow2i(k);  // row_c >= 0
+                if (PAIR || part == 0) row_c[part][r] = fabsf(a.scale_log2) * pow2i(-k);
 #pragma unroll
                 for (int i = 0; i < W; ++i) {
                     if (8 * i >= mine) break;
@@ -656,87 +651,111 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                         const __half2 h = __floats2half2_rn(lo * up, hi * up);
                         f[e] = *reinterpret_cast<const uint32_t *>(&h);
                     }
-                    const int chunk = (PAIR ? 0 : stream * (mine / 8)) + i;
-                    sts_v4(q_tile + (PAIR ? stream * TILE : 0) + (chunk >> 3) * PANEL + r * 128 + (((chunk & 7) ^ (r & 7)) << 4),
+                    const int chunk = (PAIR ? 0 : part * (mine / 8)) + i;
+                    sts_v4(q_tile + (PAIR ? part * TILE : 0) + (chunk >> 3) * PANEL + r * 128 + (((chunk & 7) ^ (r & 7)) << 4),
                            f[0], f[1], f[2], f[3]);
                 }
                 fence_proxy_async_smem();
                 release(q_full);
             }
 
-            // rows of this thread: of q = 0 .. 3, 16 (q / 2) + 8 (q % 2) + g of the warp's 32
-            float cr[4], m[4], ref[4], l[4], unit = pow2i(-126);
+            meet();
+            // of rows q = 0, 1 of this thread, in both streams
+            const int own = 32 * (warp & 3) + 16 * part + g, steps = PAIR ? 2 * count : count;
+            float cr[2][2], m[2][2], ref[2][2], l[2][2], unit[2] = {pow2i(-126), pow2i(-126)};
+            int first_row[2], seen_by_all[2];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                cr[q] = __shfl_sync(0xffffffffu, cq, 16 * (q >> 1) + 8 * (q & 1) + g);
-                m[q] = -INFINITY;
-                ref[q] = l[q] = 0.0f;
+            for (int st = 0; st < 2; ++st) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    cr[st][q] = row_c[PAIR ? st : 0][own + 8 * q];
+                    m[st][q] = -INFINITY;
+                    ref[st][q] = l[st][q] = 0.0f;
+                }
+                first_row[st] = at.rt * ROWS + (PAIR ? st * kRows : 0);
+                const int t_first = min(first_row[st] / a.group, at.T - 1);
+                seen_by_all[st] = (a.mask ? at.len - at.T : min(at.len, at.len - at.T + t_first + 1)) - kTokens;
             }
-            bool first = true;
-            const int seen_by_all = a.mask ? at.len - at.T : min(at.len, at.len - at.T + t_first + 1);
+            const uint32_t down = (uint32_t)(16 * part) << 16;
+            // a warp whose wait gave up goes on to the end of the item: the others wait for it there
 #pragma unroll 1
-            for (int i = PAIR ? 0 : (n ^ stream) & 1; i < count; i += PAIR ? 1 : 2) {
-                const int x = n + i, slot = (unsigned)x % kInfos;
-                if (!wait(info_full[slot], (unsigned)x / kInfos) || !wait(s_full[stream], PAIR ? x : x >> 1)) break;
+            for (int step = 0; step < steps; ++step) {
+                const int i = PAIR ? step >> 1 : step, x = n + i, stream = (PAIR ? step : x) & 1, slot = (unsigned)x % kInfos;
+                if (!PAIR || !stream) (void)wait(info_full[slot], (unsigned)x / kInfos);
+                (void)wait(s_full[stream], PAIR ? x : x >> 1);
                 tc_fence_after();
                 const int pos0 = (at.chunk + i) * kTokens;
                 const uint32_t there = infos[slot].present;
                 const float ratio = infos[slot].ratio;
-                unit = infos[slot].unit;
                 uint32_t scales = smem_u32(infos[slot].scales[j]);
                 asm volatile("" : "+r"(scales));  // so that no read of them goes ahead of the waits above
-                const uint32_t s_at = lanes + stream * kTokens, o_at = lanes + kOCol + stream * 128;
-                if (pos0 + kTokens <= seen_by_all && there == 0xffu) {
+                const uint32_t s_at = lanes + down + stream * kTokens, o_at = lanes + down + kOCol + stream * 128;
+                // by selection and not by index: the arrays stay in registers
+                float sc[2], sm[2], sr[2], sl[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    sc[q] = stream ? cr[1][q] : cr[0][q], sm[q] = stream ? m[1][q] : m[0][q];
+                    sr[q] = stream ? ref[1][q] : ref[0][q], sl[q] = stream ? l[1][q] : l[0][q];
+                }
+                if (pos0 <= (stream ? seen_by_all[1] : seen_by_all[0]) && there == 0xffu) {
                     const uint32_t none[4] = {};
-                    weights<false, DP>(s_at, o_at, scales, none, j, first, ratio, cr, m, ref, l);
+                    weights<false, DP>(s_at, o_at, scales, none, j, step < 2, ratio, sc, sm, sr, sl);
                 } else {
                     uint32_t bits[4];
+                    const int row = (stream ? first_row[1] : first_row[0]) + 32 * (warp & 3) + 16 * part + (lane & 15);
+                    const int t = min(row / a.group, at.T - 1);
 #pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                        bits[b] = seen_bits(a, at, t, pos0 + 32 * b) &
-                                  ((there >> (2 * b) & 1u ? 0xffffu : 0u) | (there >> (2 * b + 1) & 1u ? 0xffff0000u : 0u));
+                    for (int w = 0; w < 4; ++w)
+                        bits[w] = seen_bits(a, at, t, pos0 + 32 * w) &
+                                  ((there >> (2 * w) & 1u ? 0xffffu : 0u) | (there >> (2 * w + 1) & 1u ? 0xffff0000u : 0u));
                     __syncwarp();
-                    weights<true, DP>(s_at, o_at, scales, bits, j, first, ratio, cr, m, ref, l);
+                    weights<true, DP>(s_at, o_at, scales, bits, j, step < 2, ratio, sc, sm, sr, sl);
                 }
-                first = false;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    if (stream) m[1][q] = sm[q], ref[1][q] = sr[q], l[1][q] = sl[q];
+                    else m[0][q] = sm[q], ref[0][q] = sr[q], l[0][q] = sl[q];
+                }
+                if (stream) unit[1] = infos[slot].unit;
+                else unit[0] = infos[slot].unit;
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(smem_u32(&p_ready[stream]));
-                    mbar_arrive(smem_u32(&info_empty[slot]));
+                    if (!PAIR || stream) mbar_arrive(smem_u32(&info_empty[slot]));
                 }
             }
 
-            // the row's part of the item; without PAIR of both streams, whose warps meet, 8 channels in turn
+            // the row's part of the item: of stream `part`, without PAIR of both streams, 8 channels in turn
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                l[q] += __shfl_xor_sync(0xffffffffu, l[q], 1);
-                l[q] += __shfl_xor_sync(0xffffffffu, l[q], 2);
-                const int own = 32 * (warp & 3) + 16 * (q >> 1) + 8 * (q & 1) + g;
-                if (j == 0) row_m[stream][own] = m[q], row_l[stream][own] = l[q];
-            }
-            if (r == 0) stream_unit[stream] = unit;
+            for (int st = 0; st < 2; ++st)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    l[st][q] += __shfl_xor_sync(0xffffffffu, l[st][q], 1);
+                    l[st][q] += __shfl_xor_sync(0xffffffffu, l[st][q], 2);
+                    if (j == 0) row_m[st][own + 8 * q] = m[st][q], row_l[st][own + 8 * q] = l[st][q];
+                }
+            if (threadIdx.x == kRowWarp0 * 32) stream_unit[0] = unit[0], stream_unit[1] = unit[1];
             (void)wait(o_full, item);
             tc_fence_after();
-            if constexpr (PAIR) __syncwarp();
-            else meet();
+            meet();
             {
-                const int s0 = PAIR ? stream : 0, s1 = PAIR ? stream : 1;
+                const int s0 = PAIR ? part : 0, s1 = PAIR ? part : 1;
                 const float m0 = row_m[s0][r], m1 = row_m[s1][r], up = fmaxf(m0, m1);
                 const float f0 = m0 == up ? 1.0f : ex2(m0 - up), f1 = PAIR ? 0.0f : m1 == up ? 1.0f : ex2(m1 - up);
                 const float total = PAIR ? row_l[s0][r] : __fmaf_rn(row_l[0][r], f0, row_l[1][r] * f1);
-                const float top_unit = PAIR ? unit : fmaxf(stream_unit[0], stream_unit[1]);
+                const float top_unit = PAIR ? stream_unit[part] : fmaxf(stream_unit[0], stream_unit[1]);
                 const float per = __uint_as_float(0x7f000000u - __float_as_uint(top_unit));
                 const bool has0 = PAIR || count > 1 || !(n & 1), has1 = !PAIR && (count > 1 || (n & 1));
                 const float g0 = PAIR ? 1.0f : f0 * (stream_unit[0] * per), g1 = PAIR ? 0.0f : f1 * (stream_unit[1] * per);
                 const bool done = starts_here && ends_here;
-                const int part_row = PAIR ? stream * kRows + r : r;
+                const int part_row = PAIR ? part * kRows + r : r;
                 float *slot = attn_slot(a, blockIdx.x, starts_here ? 1 : 0, ROWS, DP);
                 uint16_t *out = static_cast<uint16_t *>(a.out) + out_row * a.ld_out + (int64_t)hq * c.D;
                 const float by = total == 0.0f ? 0.0f : top_unit * kAttnWeightUnit / total;
 #pragma unroll 1
-                for (int d = PAIR ? 0 : 8 * stream; d < c.D; d += PAIR ? 8 : 16) {
+                for (int d = PAIR ? 0 : 8 * part; d < c.D; d += PAIR ? 8 : 16) {
                     uint32_t v0[8], v1[8];
                     float v[8];
                     __syncwarp();
@@ -762,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                     }
                 }
                 __syncwarp();
-                if (live && ok && (PAIR || stream == 0)) {
+                if (live && ok && (PAIR || part == 0)) {
                     if (done) {
                         if (a.lse) a.lse[out_row * a.heads_q + hq] = attn_lse(up, total);
                     } else {
@@ -790,8 +809,8 @@ qnn_status launch(KvAttnArgs a, cudaStream_t s)
 {
     auto kern = kv_attn_rows_kernel<U4, DP, PAIR>;
     static std::atomic<uint64_t> opted_in{0};
-    // one block on an SM, whatever it needs: tensor memory is taken whole
-    constexpr int kMost = 216 << 10;
+    // one block on an SM, whatever it needs: tensor memory is taken whole (of 227 KB, the static part aside)
+    constexpr int kMost = 214 << 10;
     const int need = 1024 + (PAIR ? 6 : 5) * kTokens * DP * 2 + (a.c.batch + 1) * 8;
     if (!opt_in_smem(kern, kMost, opted_in, 100)) return QNN_ERR_CUDA;
     return kv_launch(kern, dim3((unsigned)a.blocks), kThreads, std::max(need, 120 << 10), s, a);
