@@ -326,9 +326,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         return ok;  // a wait that gave up is reported at the end
     };
 
-    // 128 registers a thread at the launch, and as many after: 88 + 120 + 2 * 152 = 4 * 128
+    // 128 registers a thread at the launch, and as many after: 80 + 128 + 2 * 152 = 4 * 128
     if (warp < kCodeWarp0) {
-    regs_dec<88>();
+    regs_dec<80>();
     if (chunks <= 0) {
     } else if (warp == 0) {
         AttnCursor at = attn_find(a, sums, share.from, ROWS);
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         }
     }
     } else if (warp < kRowWarp0) {
-        regs_dec<120>();
+        regs_dec<128>();
         // Warps 4 and 5 have K, 6 and 7 V, each 64 tokens of a chunk, in registers a chunk ahead.  Eight
         // lanes have four 16-byte pieces of two rows at a time: what they store of a chunk of 8 f16 then
         // lies in eight different places of the swizzle.
@@ -603,67 +603,86 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             const int64_t out_row = at.first + rr / a.group;
             const int hq = at.h * a.group + rr % a.group;
 
-            // q: a row for each thread, or half a row; its largest value is brought near f16's by a power of two
+            // q: four lanes have a row of the warp's 32, or its half, eight rows at a time; a row's largest value is
+            // brought near f16's by a power of two
             {
-                constexpr int W = PAIR ? DP / 8 : DP / 16;  // pieces of 8 values
-                const int mine = PAIR ? c.D : c.D / 2;      // a multiple of 16
-                const uint16_t *qp = static_cast<const uint16_t *>(a.q) + out_row * a.ld_q + (int64_t)hq * c.D +
-                                     (PAIR ? 0 : part * mine);
-                uint4 w[W];
-                float top = 0.0f;
+                constexpr int W = PAIR ? DP / 32 : DP / 64;  // pieces of 8 values of a lane
+                const int mine = PAIR ? c.D : c.D / 2;       // a multiple of 16
+                const int quad = lane & 3, r0 = 32 * (warp & 3) + (lane >> 2);
+                constexpr int E = 2;  // of a lane's four rows at a time
+#pragma unroll 1
+                for (int e0 = 0; e0 < 4; e0 += E) {
+                    uint4 w[E][W];
+                    float top[E];
 #pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    w[i] = make_uint4(0, 0, 0, 0);
-                    if (live && 8 * i < mine)
-                        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
-                                     : "l"(qp + 8 * i));
-                }
-                auto value = [&](uint32_t v, int hi) {
-                    const uint32_t h = hi ? v >> 16 : v & 0xffffu;
-                    return a.bf16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((uint16_t)h));
-                };
+                    for (int e = 0; e < E; ++e) {
+                        const int row = row0 + r0 + 8 * (e0 + e);
+                        const uint16_t *qp = static_cast<const uint16_t *>(a.q) + (at.first + row / a.group) * a.ld_q +
+                                             (int64_t)(at.h * a.group + row % a.group) * c.D + (PAIR ? 0 : part * mine);
 #pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(value(u[e / 2], e & 1)));
-                }
-                if constexpr (!PAIR) {
-                    row_top[part][r] = top;
-                    meet();
-                    top = fmaxf(row_top[0][r], row_top[1][r]);
-                }
-                const int e2 = (int)(__float_as_uint(top) >> 23);
-                const int k = top == 0.0f || e2 == 255 ? 0 : max(-126, min(126, 14 + 127 - e2));
-                const float up = a.scale_log2 < 0.0f ? -pow2i(k) : pow2i(k);  // row_c >= 0
-                if (PAIR || part == 0) row_c[part][r] = fabsf(a.scale_log2) * pow2i(-k);
-#pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    if (8 * i >= mine) break;
-                    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                    uint32_t f[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        // the order in which codes are unpacked: u4 0 4, 1 5, 2 6, 3 7
-                        const float lo = U4 ? value(u[e / 2], e & 1) : value(u[e], 0);
-                        const float hi = U4 ? value(u[2 + e / 2], e & 1) : value(u[e], 1);
-                        const __half2 h = __floats2half2_rn(lo * up, hi * up);
-                        f[e] = *reinterpret_cast<const uint32_t *>(&h);
+                        for (int i = 0; i < W; ++i) {
+                            const int piece = quad + 4 * i;
+                            w[e][i] = make_uint4(0, 0, 0, 0);
+                            if (r0 + 8 * (e0 + e) < width && 8 * piece < mine)
+                                asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                             : "=r"(w[e][i].x), "=r"(w[e][i].y), "=r"(w[e][i].z), "=r"(w[e][i].w)
+                                             : "l"(qp + 8 * piece));
+                        }
                     }
-                    const int chunk = (PAIR ? 0 : part * (mine / 8)) + i;
-                    sts_v4(q_tile + (PAIR ? part * TILE : 0) + (chunk >> 3) * PANEL + r * 128 + (((chunk & 7) ^ (r & 7)) << 4),
-                           f[0], f[1], f[2], f[3]);
+                    auto value = [&](uint32_t v, int hi) {
+                        const uint32_t h = hi ? v >> 16 : v & 0xffffu;
+                        return a.bf16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((uint16_t)h));
+                    };
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        top[e] = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < W; ++i) {
+                            const uint32_t u[4] = {w[e][i].x, w[e][i].y, w[e][i].z, w[e][i].w};
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) top[e] = fmaxf(top[e], fabsf(value(u[k / 2], k & 1)));
+                        }
+                        top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+                        top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+                        if (!PAIR && quad == 0) row_top[part][r0 + 8 * (e0 + e)] = top[e];
+                    }
+                    if constexpr (!PAIR) meet();
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const int own = r0 + 8 * (e0 + e);
+                        const float most = PAIR ? top[e] : fmaxf(row_top[0][own], row_top[1][own]);
+                        const int e2 = (int)(__float_as_uint(most) >> 23);
+                        const int k = most == 0.0f || e2 == 255 ? 0 : max(-126, min(126, 14 + 127 - e2));
+                        const float up = a.scale_log2 < 0.0f ? -pow2i(k) : pow2i(k);  // row_c >= 0
+                        if (quad == 0 && (PAIR || part == 0)) row_c[part][own] = fabsf(a.scale_log2) * pow2i(-k);
+#pragma unroll
+                        for (int i = 0; i < W; ++i) {
+                            const int piece = quad + 4 * i, chunk = (PAIR ? 0 : part * (mine / 8)) + piece;
+                            const uint32_t u[4] = {w[e][i].x, w[e][i].y, w[e][i].z, w[e][i].w};
+                            uint32_t f[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                // the order in which codes are unpacked: u4 0 4, 1 5, 2 6, 3 7
+                                const float lo = U4 ? value(u[x / 2], x & 1) : value(u[x], 0);
+                                const float hi = U4 ? value(u[2 + x / 2], x & 1) : value(u[x], 1);
+                                const __half2 h = __floats2half2_rn(lo * up, hi * up);
+                                f[x] = *reinterpret_cast<const uint32_t *>(&h);
+                            }
+                            if (8 * piece < mine)
+                                sts_v4(q_tile + (PAIR ? part * TILE : 0) + (chunk >> 3) * PANEL + own * 128 +
+                                           (((chunk & 7) ^ (own & 7)) << 4),
+                                       f[0], f[1], f[2], f[3]);
+                        }
+                    }
                 }
                 fence_proxy_async_smem();
                 release(q_full);
             }
-
             meet();
             // of rows q = 0, 1 of this thread, in both streams
             const int own = 32 * (warp & 3) + 16 * part + g, steps = PAIR ? 2 * count : count;
-            float cr[2][2], m[2][2], ref[2][2], l[2][2], unit[2] = {pow2i(-126), pow2i(-126)};
-            int first_row[2], seen_by_all[2];
+            float cr[2][2], m[2][2], ref[2][2], l[2][2], unit[PAIR ? 1 : 2];  // PAIR: the same of both
+            int seen_by_all[2];
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
 #pragma unroll
@@ -672,8 +691,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                     m[st][q] = -INFINITY;
                     ref[st][q] = l[st][q] = 0.0f;
                 }
-                first_row[st] = at.rt * ROWS + (PAIR ? st * kRows : 0);
-                const int t_first = min(first_row[st] / a.group, at.T - 1);
+                if (st == 0 || !PAIR) unit[st] = pow2i(-126);
+                const int t_first = min((at.rt * ROWS + (PAIR ? st * kRows : 0)) / a.group, at.T - 1);
                 seen_by_all[st] = (a.mask ? at.len - at.T : min(at.len, at.len - at.T + t_first + 1)) - kTokens;
             }
             const uint32_t down = (uint32_t)(16 * part) << 16;
@@ -702,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                     weights<false, DP>(s_at, o_at, scales, none, j, step < 2, ratio, sc, sm, sr, sl);
                 } else {
                     uint32_t bits[4];
-                    const int row = (stream ? first_row[1] : first_row[0]) + 32 * (warp & 3) + 16 * part + (lane & 15);
+                    const int row = at.rt * ROWS + (PAIR ? stream * kRows : 0) + 32 * (warp & 3) + 16 * part + (lane & 15);
                     const int t = min(row / a.group, at.T - 1);
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
@@ -716,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                     if (stream) m[1][q] = sm[q], ref[1][q] = sr[q], l[1][q] = sl[q];
                     else m[0][q] = sm[q], ref[0][q] = sr[q], l[0][q] = sl[q];
                 }
-                if (stream) unit[1] = infos[slot].unit;
+                if (!PAIR && stream) unit[PAIR ? 0 : 1] = infos[slot].unit;
                 else unit[0] = infos[slot].unit;
                 tmem_st_wait();
                 tc_fence_before();
@@ -736,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                     l[st][q] += __shfl_xor_sync(0xffffffffu, l[st][q], 2);
                     if (j == 0) row_m[st][own + 8 * q] = m[st][q], row_l[st][own + 8 * q] = l[st][q];
                 }
-            if (threadIdx.x == kRowWarp0 * 32) stream_unit[0] = unit[0], stream_unit[1] = unit[1];
+            if (threadIdx.x == kRowWarp0 * 32) stream_unit[0] = unit[0], stream_unit[1] = unit[PAIR ? 0 : 1];
             (void)wait(o_full, item);
             tc_fence_after();
             meet();
