@@ -146,7 +146,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_attn_join_kernel(const __g
     if (a.lse && lane == 0) a.lse[(first + tok) * a.heads_q + hq] = attn_lse(top, total);
 }
 
-bool many_rows(const KvArgs &c, int group) { return c.D <= 128 && (int64_t)c.tokens * group > 32; }
+// Where the tensor memory's kernel takes over.  Few against many rows, in 8 bits, 32 heads of q on 8, us:
+//   16 sequences of 4096, D = 128:  8 rows 43 / 56, 16 rows 60 / 57, 32 rows 77 / 58
+//   1 of 512, D = 128:             16 rows 12.9 / 12.9, 32 rows 15.5 / 12.9
+//   16 of 4096, D = 64:            16 rows 47 / 46, 32 rows 57 / 47; 32 heads on 32 over 1024, 16 rows 53 / 74
+bool many_rows(const KvArgs &c, int group)
+{
+    return c.D <= 128 && (int64_t)c.tokens * group > (c.D <= 64 ? 16 : 8);
+}
 
 AttnPlan attn_plan(const KvArgs &c, int group)
 {

@@ -1,5 +1,5 @@
-// qnn_kv_attn_few.cu -- q_kv_attn for few rows of a head of the cache (up to 32 at a time: the
-// heads of q that share it, times the newest tokens): decoding.
+// qnn_kv_attn_few.cu -- q_kv_attn for few rows of a head of the cache (up to 16 at a time: the
+// heads of q that share it, times the newest tokens): decoding; and all rows of more than 128 channels.
 //
 //   S^T = K Q^T,  P^T = e^(S^T - m),  O^T = V^T P^T
 // on mma.sync m16n8k16 with the codes as the A operand (16 tokens, or 16 channels) and 8 rows as
@@ -8,10 +8,13 @@
 // an f16 is the number u 2^-24, so a mask, or a byte permutation, is all that the stream of codes goes
 // through; the products are exact.  Zero points come off the sums: sum (u - z) q = sum u q - z sum q, whose second
 // part S begins with, and one more product for each tile has sum p z.  Scales of K multiply the scores, scales
-// of V the weights.  (64 sequences of 8192 tokens in 8 bits, against codes made f16 integers before the
-// products: @@ us, 147; one of 131072 in 4 bits: @@ us, 62.)
+// of V the weights.  (One sequence of 131072 tokens in 4 bits: 58 us, 62 with codes made f16 integers
+// before the products.)
 //
-// It is bound by the stream of codes.  Each warp has a ring of its own in shared memory, stages
+// The stream of codes is what it cannot do without: 64 sequences of 8192 tokens, 8 of 64 heads, in 8 bits take
+// 144 us, 4.3 TB/s; the copies alone take 109, the rest alone 113, and a warp of each scheduler's four waits
+// for memory, another for its chain of products.  One sequence of 131072 tokens in 4 bits: 55 us, 2.6 TB/s, by
+// instructions (430 for a tile of 16 tokens).  Each warp has a ring of its own in shared memory, stages
 // of 16 tokens (their K and V rows and words), filled by asynchronous copies; warps meet only
 // where an item ends.  Maxima move only when a score passes the warp's by 2^8 (the
 // weights have that room), which one vote a tile finds.
@@ -577,10 +580,8 @@ qnn_status launch(KvAttnArgs a, cudaStream_t s)
 template <bool U4>
 qnn_status launch_channels(const KvAttnArgs &a, const AttnPlan &p, cudaStream_t s)
 {
-    if (p.channels == 64)
-        return p.rows == 8 ? launch<U4, 64, 1>(a, s) : p.rows == 16 ? launch<U4, 64, 2>(a, s) : launch<U4, 64, 4>(a, s);
-    if (p.channels == 128)
-        return p.rows == 8 ? launch<U4, 128, 1>(a, s) : p.rows == 16 ? launch<U4, 128, 2>(a, s) : launch<U4, 128, 4>(a, s);
+    if (p.channels == 64) return p.rows == 8 ? launch<U4, 64, 1>(a, s) : launch<U4, 64, 2>(a, s);
+    if (p.channels == 128) return launch<U4, 128, 1>(a, s);
     return p.rows == 8 ? launch<U4, 256, 1>(a, s) : launch<U4, 256, 2>(a, s);
 }
 
@@ -591,7 +592,7 @@ AttnPlan attn_few_plan(const KvArgs &c, int group)
     AttnPlan p;
     p.channels = c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256;
     const int64_t rows = (int64_t)c.tokens * group;
-    p.rows = rows <= 8 ? 8 : rows <= 16 || p.channels == 256 ? 16 : 32;
+    p.rows = rows <= 8 ? 8 : 16;  // with 128 channels: 8 at most come here
     p.blocks = std::min(kAttnMaxBlocks, sm_count() * (p.rows * p.channels <= 1024 ? 2 : 1));
     return p;
 }
