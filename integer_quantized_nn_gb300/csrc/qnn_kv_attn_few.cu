@@ -4,17 +4,15 @@
 //   S^T = K Q^T,  P^T = e^(S^T - m),  O^T = V^T P^T
 // on mma.sync m16n8k16 with the codes as the A operand (16 tokens, or 16 channels) and 8 rows as
 // N: codes go from shared memory to A fragments in registers, no value twice, and P^T's fragment
-// is S^T's transposed 8 x 8 by 8 x 8 (movmatrix).  A stored code u (0 .. 255, 0 .. 15) in the low bits of
-// an f16 is the number u 2^-24, so a mask, or a byte permutation, is all that the stream of codes goes
-// through; the products are exact.  Zero points come off the sums: sum (u - z) q = sum u q - z sum q, whose second
-// part S begins with, and one more product for each tile has sum p z.  Scales of K multiply the scores, scales
-// of V the weights.  (One sequence of 131072 tokens in 4 bits: 58 us, 62 with codes made f16 integers
-// before the products.)
+// is S^T's transposed 8 x 8 by 8 x 8 (movmatrix).  A code becomes an f16 integer, its zero point taken off, by a
+// magic number and one subtraction; the products are exact, scales of K multiply the scores, scales of V the
+// weights.  (Codes as they are stored, as f16 numbers u 2^-24, and zero points off the sums, are 5% faster in 4
+// bits; but a product's unit then is its number's exponent, 2^-14, and sums lose ten bits.)
 //
 // The stream of codes is what it cannot do without: 64 sequences of 8192 tokens, 8 of 64 heads, in 8 bits take
-// 144 us, 4.3 TB/s; the copies alone take 109, the rest alone 113, and a warp of each scheduler's four waits
-// for memory, another for its chain of products.  One sequence of 131072 tokens in 4 bits: 55 us, 2.6 TB/s, by
-// instructions (430 for a tile of 16 tokens).  Each warp has a ring of its own in shared memory, stages
+// 140 us, 4.5 TB/s; the copies alone take 109, the rest alone 113, and a warp of each scheduler's four waits
+// for memory, another for its chain of products.  One sequence of 131072 tokens in 4 bits: 57 us, 2.5 TB/s, by
+// instructions (450 for a tile of 16 tokens).  Each warp has a ring of its own in shared memory, stages
 // of 16 tokens (their K and V rows and words), filled by asynchronous copies; warps meet only
 // where an item ends.  Maxima move only when a score passes the warp's by 2^8 (the
 // weights have that room), which one vote a tile finds.
@@ -24,7 +22,6 @@ namespace qnn {
 namespace {
 
 constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr float kCode = 0x1p-24f;  // what 1 is as an f16's bits
 static_assert(kAttnChunk == 16 * kWarps, "a unit is a tile for each warp");
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -40,19 +37,6 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v)
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
-}
-
-// Codes as f16 numbers: of a word of four bytes to bytes 0 and 2, and 1 and 3; of a word of eight 4-bit ones to
-// 0 and 4, 16 times 1 and 5, 2 and 6, 16 times 3 and 7.
-__device__ __forceinline__ void bytes_f16(uint32_t w, uint32_t &even, uint32_t &odd)
-{
-    even = w & 0x00ff00ffu;
-    odd = prmt(w, 0, 0x4341);
-}
-__device__ __forceinline__ void nibbles_f16(uint32_t w, uint32_t (&r)[4])
-{
-    const uint32_t v = w >> 8;
-    r[0] = w & 0x000f000fu, r[1] = w & 0x00f000f0u, r[2] = v & 0x000f000fu, r[3] = v & 0x00f000f0u;
 }
 
 __device__ __forceinline__ uint32_t lds32(uint32_t at)
@@ -119,7 +103,7 @@ __device__ __forceinline__ int k_channel(int j, int step, int e)  // e: k = 2j, 
         if (DP == 64) return 16 * j + 8 * w + n;
         return 128 * (w / 4) + 32 * j + 8 * (w % 4) + n;
     } else {
-        return 64 * (step / 4) + 16 * j + 4 * (step % 4) + (e / 2) + 2 * (e % 2);
+        return 64 * (step / 4) + 16 * j + 4 * (step % 4) + e;
     }
 }
 template <bool U4, int DP>
@@ -243,7 +227,7 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
 
         // q's fragments: B of m16n8k16, column g, each row scaled to f16's range
         uint32_t qf[S::kQRegs ? NT : 1][S::kQRegs ? S::kSteps : 1][2];
-        float cq[NT][2], qs[NT][2];  // of rows 2j, 2j + 1: the scores' factor, the sum of what is in f16, in codes' units
+        float cq[NT][2];  // of rows 2j, 2j + 1
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = row0 + 8 * nt + g;
@@ -268,43 +252,32 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
                 const int e2 = (int)(__float_as_uint(top) >> 23);
                 const int k = top == 0.0f || e2 == 255 ? 0 : max(-126, min(126, 14 + 127 - e2));
                 const float up = pow2i(k);
-                float sum = 0.0f;
 #pragma unroll
                 for (int s = 0; s < S::kSteps; ++s) {
                     const __half2 lo = __floats2half2_rn(v[s][0] * up, v[s][1] * up);
-                    __half2 hi = __floats2half2_rn(v[s][2] * up, v[s][3] * up);
-                    if constexpr (U4) hi = __floats2half2_rn(v[s][2] * up * 0.0625f, v[s][3] * up * 0.0625f);
-                    const float2 fl = __half22float2(lo), fh = __half22float2(hi);
-                    sum += (fl.x + fl.y) + (U4 ? 16.0f : 1.0f) * (fh.x + fh.y);
+                    const __half2 hi = __floats2half2_rn(v[s][2] * up, v[s][3] * up);
                     const uint32_t b0 = *reinterpret_cast<const uint32_t *>(&lo);
                     const uint32_t b1 = *reinterpret_cast<const uint32_t *>(&hi);
                     if constexpr (S::kQRegs) qf[nt][s][0] = b0, qf[nt][s][1] = b1;
                     else q_smem[(nt * S::kSteps + s) * 32 + lane] = make_uint2(b0, b1);
                 }
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                sum *= U4 ? kCode : 128.0f * kCode;
                 const float cr = a.scale_log2 * pow2i(-k);
                 if constexpr (S::kQRegs) {
                     cq[nt][0] = __shfl_sync(0xffffffffu, cr, 8 * j);
                     cq[nt][1] = __shfl_sync(0xffffffffu, cr, 8 * j + 4);
-                    qs[nt][0] = __shfl_sync(0xffffffffu, sum, 8 * j);
-                    qs[nt][1] = __shfl_sync(0xffffffffu, sum, 8 * j + 4);
                 } else if (j == 0) {
-                    stats[0][8 * nt + g][0] = cr, stats[0][8 * nt + g][1] = sum;
+                    stats[0][8 * nt + g][0] = cr;
                 }
             }
         }
         if constexpr (!S::kQRegs) {
             __syncthreads();
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) cq[nt][e] = stats[0][8 * nt + 2 * j + e][0], qs[nt][e] = stats[0][8 * nt + 2 * j + e][1];
+            for (int nt = 0; nt < NT; ++nt) cq[nt][0] = stats[0][8 * nt + 2 * j][0], cq[nt][1] = stats[0][8 * nt + 2 * j + 1][0];
             __syncthreads();
         }
 
-        float acc[NT][S::kSteps][4], zero[NT][4], m[NT][2], ref[NT][2], l[NT][2];
+        float acc[NT][S::kSteps][4], m[NT][2], ref[NT][2], l[NT][2];
         float unit = pow2i(-126), per_unit = pow2i(126);  // V's scales are taken in units of 2^k
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -312,7 +285,6 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
             for (int s = 0; s < S::kSteps; ++s)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[nt][s][e] = 0.0f;
-            zero[nt][0] = zero[nt][1] = zero[nt][2] = zero[nt][3] = 0.0f;
             m[nt][0] = m[nt][1] = -INFINITY;
             ref[nt][0] = ref[nt][1] = l[nt][0] = l[nt][1] = 0.0f;
         }
@@ -330,11 +302,7 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
                 const uint32_t wv0 = lds32(w_at + 64 + 4 * g), wv1 = lds32(w_at + 64 + 4 * g + 32);
                 float s[NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float z0 = U4 ? -(float)(wk0 & 15u) : -1.0f, z1 = U4 ? -(float)(wk1 & 15u) : -1.0f;
-                    s[nt][0] = z0 * qs[nt][0], s[nt][1] = z0 * qs[nt][1];
-                    s[nt][2] = z1 * qs[nt][0], s[nt][3] = z1 * qs[nt][1];
-                }
+                for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
                 {
                     uint32_t k0[S::kKWords], k1[S::kKWords];
                     constexpr int step_w = S::kKWords < 4 ? S::kKWords : 4;
@@ -343,20 +311,21 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
                         lds<step_w>(k_at + k_off[w / 4], k0 + w);
                         lds<step_w>(k_at + k_off[w / 4] + eight, k1 + w);
                     }
+                    const Zero z0 = zero_of(wk0 & 15u, wk0 & 15u), z1 = zero_of(wk1 & 15u, wk1 & 15u);
 #pragma unroll
                     for (int w = 0; w < S::kKWords; ++w) {
                         uint32_t f[U4 ? 2 : 1][4];
                         if constexpr (U4) {
                             uint32_t r0[4], r1[4];
-                            nibbles_f16(k0[w], r0);
-                            nibbles_f16(k1[w], r1);
+                            u4_pairs(k0[w], z0, r0);
+                            u4_pairs(k1[w], z1, r1);
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 f[e][0] = r0[2 * e], f[e][1] = r1[2 * e], f[e][2] = r0[2 * e + 1], f[e][3] = r1[2 * e + 1];
                             }
                         } else {
-                            bytes_f16(k0[w], f[0][0], f[0][2]);
-                            bytes_f16(k1[w], f[0][1], f[0][3]);
+                            s8_pairs(k0[w], f[0][0], f[0][2]);
+                            s8_pairs(k1[w], f[0][1], f[0][3]);
                         }
 #pragma unroll
                         for (int e = 0; e < (U4 ? 2 : 1); ++e) {
@@ -385,13 +354,8 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    // by 2^24 first, which is exact and keeps within the range that the whole product has
-#pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                        const float2 by = mul2(make_float2(cq[nt][0], cq[nt][1]), both(e ? sk1 : sk0));
-                        const float2 v = mul2(mul2(make_float2(s[nt][e], s[nt][e + 1]), both(1.0f / kCode)), by);
-                        s[nt][e] = v.x, s[nt][e + 1] = v.y;
-                    }
+                    s[nt][0] = s[nt][0] * (cq[nt][0] * sk0), s[nt][1] = s[nt][1] * (cq[nt][1] * sk0);
+                    s[nt][2] = s[nt][2] * (cq[nt][0] * sk1), s[nt][3] = s[nt][3] * (cq[nt][1] * sk1);
                     if (!whole) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -431,7 +395,6 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
                         for (int st = 0; st < S::kSteps; ++st)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) acc[nt][st][e] *= f[e & 1];
-                        zero[nt][0] *= f[0], zero[nt][1] *= f[1];
                     }
                 }
                 const float w0 = sv0 * per_unit * (float)(1 << kAttnRoom), w1 = sv1 * per_unit * (float)(1 << kAttnRoom);
@@ -453,23 +416,20 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
 #pragma unroll
                     for (int w = 0; w < S::kVWords; w += step_v)
                         lds<step_v>(k_at + v_off[e & 1][w / 4] + (e >> 1) * eight, vw[e] + w);
-                uint32_t za = 0x00800080u, zb = za;  // zero points of tokens 2j and 2j + 1, 2j + 8 and 2j + 9
+                Zero za, zb;
                 if constexpr (U4) {
                     const uint2 ta = lds64(w_at + 64 + 8 * j), tb = lds64(w_at + 64 + 8 * j + 32);
-                    za = prmt(ta.x, ta.y, 0x5410) & 0x000f000fu;
-                    zb = prmt(tb.x, tb.y, 0x5410) & 0x000f000fu;
+                    za = zero_of(ta.x & 15u, ta.y & 15u);
+                    zb = zero_of(tb.x & 15u, tb.y & 15u);
                 }
-                const uint32_t zf[4] = {za, za, zb, zb};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma16816(zero[nt], zf, p[nt][0], p[nt][1]);
 #pragma unroll
                 for (int w = 0; w < S::kVWords; ++w) {
                     if constexpr (U4) {
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             uint32_t ra[4], rb[4];
-                            nibbles_f16(prmt(vw[0][w], vw[1][w], half ? 0x7632 : 0x5410), ra);
-                            nibbles_f16(prmt(vw[2][w], vw[3][w], half ? 0x7632 : 0x5410), rb);
+                            u4_pairs(prmt(vw[0][w], vw[1][w], half ? 0x7632 : 0x5410), za, ra);
+                            u4_pairs(prmt(vw[2][w], vw[3][w], half ? 0x7632 : 0x5410), zb, rb);
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const uint32_t f[4] = {ra[2 * e], ra[2 * e + 1], rb[2 * e], rb[2 * e + 1]};
@@ -480,9 +440,12 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
                     } else {
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
+                            // the tokens' codes of a channel side by side: a0 b0 a1 b1
+                            const uint32_t ta = prmt(vw[0][w], vw[1][w], half ? 0x7362 : 0x5140);
+                            const uint32_t tb = prmt(vw[2][w], vw[3][w], half ? 0x7362 : 0x5140);
                             uint32_t f[4];
-                            bytes_f16(prmt(vw[0][w], vw[1][w], half ? 0x7632 : 0x5410), f[0], f[1]);
-                            bytes_f16(prmt(vw[2][w], vw[3][w], half ? 0x7632 : 0x5410), f[2], f[3]);
+                            s8_pairs(ta, f[0], f[1]);
+                            s8_pairs(tb, f[2], f[3]);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt][2 * w + half], f, p[nt][0], p[nt][1]);
                         }
@@ -521,15 +484,12 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
                 float top = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[w][r][0]);
-                const float f = (m[nt][e] == top ? 1.0f : ex2(m[nt][e] - top)) * shrink * (1.0f / kCode);
+                const float f = (m[nt][e] == top ? 1.0f : ex2(m[nt][e] - top)) * shrink;
                 float *to = join + (warp * 8 + 2 * j + e) * S::kPitch + g;
 #pragma unroll
                 for (int s = 0; s < S::kSteps; ++s)
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const float v = acc[nt][s][2 * half + e];
-                        to[(2 * s + half) * 8] = ((U4 && half ? v * 0.0625f : v) - zero[nt][e]) * f;
-                    }
+                    for (int half = 0; half < 2; ++half) to[(2 * s + half) * 8] = acc[nt][s][2 * half + e] * f;
             }
             __syncthreads();
             // pairs of channels of a row, in the order of (step, half, g)

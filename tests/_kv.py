@@ -38,12 +38,6 @@ def values(x, kv):
     return (q - z).astype(np.float32) * s
 
 
-def added(x, kv):
-    """(u + z) s of the stored codes u and zero points z of x."""
-    q, z, s = codes(x, kv)
-    return (q + z if kv == "u4" else q + 256).astype(np.float64) * s
-
-
 class Cache:
     """Sequences with their tokens' keys and values in numpy (fp32 numbers of the type x_dt) and
     their pages in any order: entries that no token needs are -1."""
@@ -109,11 +103,7 @@ def attention(cache, q, scale, sees=None):
     after its row's scaling 2^-37 of the row's largest; 2^-21 for the exponential and what is
     near it.  A weight, with V's scale in it, is rounded to f16: 2^-11, or 2^-31 of the largest
     where it is small, codes up to 127.  Sums over n tokens pass n / 16 + 64 roundings at most
-    (one in 16 tokens' products, the parts' joining), the denominator's as many.
-
-    Both kinds of sums may be taken over stored codes u, q = u - z, with z's part taken off at the end:
-    sum (u - z) x = sum u x - z sum x.  Their roundings are then 2^-23 of the magnitudes that are
-    added, (u + z) |x|, not of |u - z| |x|."""
+    (one in 16 tokens' products, the parts' joining), the denominator's as many."""
     rows, HQ, D = q.shape
     G = HQ // cache.heads
     out, lse = np.zeros(q.shape), np.full((rows, HQ), -np.inf)
@@ -121,7 +111,6 @@ def attention(cache, q, scale, sees=None):
     kq = [values(k, cache.kv).astype(np.float64) for k in cache.k]
     vq = [values(v, cache.kv).astype(np.float64) for v in cache.v]
     sv = [codes(v, cache.kv)[2].astype(np.float64) for v in cache.v]
-    ku, vu = [added(k, cache.kv) for k in cache.k], [added(v, cache.kv) for v in cache.v]
     for r, (b, pos) in enumerate(cache.row_places()):
         n, T = cache.lens[b], cache.tokens[b]
         t = pos - (n - T)
@@ -138,7 +127,7 @@ def attention(cache, q, scale, sees=None):
         for h in range(HQ):
             qh, k, v = q[r, h].astype(np.float64), kq[b][at, h // G], vq[b][at, h // G]
             x = scale * (k @ qh)
-            mag = abs(scale) * (ku[b][at, h // G] @ np.abs(qh))
+            mag = abs(scale) * (np.abs(k) @ np.abs(qh))
             m = x.max()
             p = np.exp(x - m)
             total = p.sum()
@@ -148,7 +137,7 @@ def attention(cache, q, scale, sees=None):
             wide = (p * delta).sum() / total  # of the denominator, relative
             out[r, h] = p @ v / total
             terms = np.abs(v)
-            tol_out[r, h] = (p * (delta + 2.0 ** -11)) @ terms / total + sums * (p @ vu[b][at, h // G]) / total \
+            tol_out[r, h] = (p * (delta + 2.0 ** -11 + sums)) @ terms / total \
                 + (wide + sums) * (p @ terms) / total \
                 + len(at) * 2.0 ** -31 * 127 * sv[b][at, h // G].max() / total
             lse[r, h] = m + np.log(total)

@@ -113,7 +113,8 @@ def test_attention_refusals(lib):
                                       dict(mask_words=-1), dict(ld_q=255), dict(ld_out=8), dict(ld_q=1 << 61),
                                       dict(ws_bytes=0)]:
         assert call(**bad) == INVALID, bad
-    for bad in [dict(x_dt="f32"), dict(x_dt="s8"), dict(batch=4097, rows=8194)]:
+    for bad in [dict(x_dt="f32"), dict(x_dt="s8"), dict(batch=4097, rows=8194), dict(starts=4, tokens=(1 << 31) - 1),
+                dict(starts=4, tokens=1 << 30)]:
         assert call(**bad) == UNSUPPORTED, bad
     for bad in BAD_ALIGNMENT + [dict(q=8), dict(out=18), dict(ws=8), dict(mask=2, mask_words=1), dict(lse=2),
                                 dict(ld_q=257), dict(ld_out=260)]:
