@@ -55,7 +55,7 @@ class Layer:
             return torch.empty(shape, device="cuda").normal_(0.0, std, generator=gen).bfloat16()
         self.heads, self.heads_q, self.D = heads, heads_q, D
         self.qkv = normal(C, (heads_q + 2 * heads) * D, std=C ** -0.5)
-        self.out = normal(heads_q * D, C, std=4.0 * (heads_q * D) ** -0.5)
+        self.out = normal(heads_q * D, C, std=1.5 * (heads_q * D) ** -0.5)
         self.mlp = normal(C, C, std=C ** -0.5)
         self.norm = qnn.block_norm(pre="rms")
         self.geom = qnn.kv_geom(heads, D, 16, kv_dt=kv)
@@ -87,13 +87,13 @@ class Layer:
 
 class Model:
     def __init__(self, vocabulary, C, layers, heads, heads_q, D, kv, batch, most, gen):
-        self.embed = torch.empty(vocabulary, C, device="cuda").normal_(generator=gen)
+        self.embed, self.head = (torch.empty(vocabulary, C, device="cuda").normal_(generator=gen) for _ in range(2))
         self.layers = [Layer(C, heads, heads_q, D, kv, batch, most, gen) for _ in range(layers)]
         self.lens = torch.zeros(batch, dtype=torch.int32, device="cuda")
         self.batch = batch
 
     def logits(self, r):
-        return self.layers[0].normed(r).float() @ self.embed.T
+        return self.layers[0].normed(r).float() @ self.head.T
 
     def __call__(self, tokens, starts=None, most=0, mask=None):
         """Logits of the newest tokens, which are in the cache afterwards; lens counts them already."""
