@@ -9,8 +9,8 @@
 // way while it works on one.
 //
 // Bytes bound the read: 8 x 4096 tokens of 8 heads of 128, 8 bits to bf16, take 41 us, 5.0 TB/s.  A write is
-// bound by instructions as well: 4 x 4000 tokens at most (10 000 in all) to 4 bits take 32 us, 20 million values,
-// 60 with divisions for all values near ties.  One token takes 5 us, latency.
+// bound by latency and instructions: 4 sequences, 10 000 tokens in all, to 4 bits take 27 us, 20 million values (60
+// with divisions for all values near ties); 16 x 4096 tokens of 8 heads of 128 written and read, 220 us in 8 bits.  One token takes 5 us, latency.
 #include "qnn_kv.cuh"
 
 namespace qnn {
@@ -103,23 +103,26 @@ __device__ __forceinline__ Place place_of(const KvArgs &a, int row)
     return p;
 }
 
+// Eight values as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, int vec, float (&x)[8])
+struct Raw8 {
+    uint4 w[sizeof(T) / 2];
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, int vec, Raw8<T> &x)
 {
     if (vec) {
-        uint4 w[sizeof(T) / 2];
 #pragma unroll
         for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
             asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                         : "=r"(x.w[i].x), "=r"(x.w[i].y), "=r"(x.w[i].z), "=r"(x.w[i].w)
                          : "l"(reinterpret_cast<const uint4 *>(p) + i));
         }
-        const T *e = reinterpret_cast<const T *>(w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = to_f32(e[i]);
     } else {
+        T *e = reinterpret_cast<T *>(x.w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = to_f32(p[i]);
+        for (int i = 0; i < 8; ++i) e[i] = p[i];
     }
 }
 
@@ -174,31 +177,38 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv_write_kernel(const __grid_c
     const int64_t r0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * a.run;
     const int rows = (int)min((int64_t)a.run, c.rows - r0);
     if (rows <= 0) return;
-    float ahead[kWriteItems][8];
-    auto ask = [&](int64_t row) {
+    // Rows on their way, as they lie in memory, and converted when their turn comes: two, or one of fp32, whose
+    // second would not fit the registers (prompts written and read in 4 bits: 42 us, 48 with one).
+    constexpr int kAhead = sizeof(T) == 2 ? 2 : 1;
+    Raw8<T> ahead[kAhead][kWriteItems];
+    auto ask = [&](int64_t row, Raw8<T> (&to)[kWriteItems]) {
 #pragma unroll
         for (int i = 0; i < kWriteItems; ++i) {
             const int item = first + i * G;  // K's heads, then V's
             if (item < 2 * c.heads && live) {
                 const bool is_v = item >= c.heads;
                 const int64_t at = row * (is_v ? a.ld_v : a.ld_k) + (item - (is_v ? c.heads : 0)) * c.D + d0;
-                load8(static_cast<const T *>(is_v ? a.v : a.k) + at, a.vec, ahead[i]);
+                load8(static_cast<const T *>(is_v ? a.v : a.k) + at, a.vec, to[i]);
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ahead[i][e] = 0.0f;
+                for (int e = 0; e < (int)sizeof(T) / 2; ++e) to[i].w[e] = make_uint4(0, 0, 0, 0);
             }
         }
     };
-    ask(r0);
+    ask(r0, ahead[0]);
+    if (kAhead > 1 && rows > 1) ask(r0 + 1, ahead[kAhead - 1]);
     const Place places = place_of(c, lane < rows ? (int)r0 + lane : INT32_MAX);
 #pragma unroll 1
     for (int t = 0; t < rows; ++t) {
         float x[kWriteItems][8];
 #pragma unroll
-        for (int i = 0; i < kWriteItems; ++i)
+        for (int i = 0; i < kWriteItems; ++i) {
+            const T *raw = reinterpret_cast<const T *>(ahead[0][i].w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[i][e] = ahead[i][e];
-        if (t + 1 < rows) ask(r0 + t + 1);
+            for (int e = 0; e < 8; ++e) x[i][e] = to_f32(raw[e]);
+            if constexpr (kAhead > 1) ahead[0][i] = ahead[1][i];
+        }
+        if (t + kAhead < rows) ask(r0 + t + kAhead, ahead[kAhead - 1]);
         Place p;
         p.page = __shfl_sync(0xffffffffu, places.page, t);
         p.slot = __shfl_sync(0xffffffffu, places.slot, t);
