@@ -150,9 +150,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_attn_join_kernel(const __g
 //   16 sequences of 4096, D = 128:  8 rows 43 / 56, 16 rows 60 / 57, 32 rows 77 / 58
 //   1 of 512, D = 128:             16 rows 12.9 / 12.9, 32 rows 15.5 / 12.9
 //   16 of 4096, D = 64:            16 rows 47 / 46, 32 rows 57 / 47; 32 heads on 32 over 1024, 16 rows 53 / 74
+//   16 of 4096, D = 256:           32 rows 117 / 129; 8 of 8192: 256 rows 744 / 244
 bool many_rows(const KvArgs &c, int group)
 {
-    return c.D <= 128 && (int64_t)c.tokens * group > (c.D <= 64 ? 16 : 8);
+    const int64_t rows = (int64_t)c.tokens * group;
+    return c.D <= 128 ? rows > (c.D <= 64 ? 16 : 8) : rows > 32 && c.batch <= 2048;  // the sums of a longer batch: no room
 }
 
 AttnPlan attn_plan(const KvArgs &c, int group)

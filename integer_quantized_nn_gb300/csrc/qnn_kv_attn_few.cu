@@ -1,5 +1,6 @@
 // qnn_kv_attn_few.cu -- q_kv_attn for few rows of a head of the cache (up to 16 at a time: the
-// heads of q that share it, times the newest tokens): decoding; and all rows of more than 128 channels.
+// heads of q that share it, times the newest tokens): decoding; of more than 128 channels up to 32, in large
+// batches all.
 //
 //   S^T = K Q^T,  P^T = e^(S^T - m),  O^T = V^T P^T
 // on mma.sync m16n8k16 with the codes as the A operand (16 tokens, or 16 channels) and 8 rows as

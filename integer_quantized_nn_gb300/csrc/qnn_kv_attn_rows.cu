@@ -9,7 +9,8 @@
 // tensor cores work on the other's.
 //
 // A chunk of 2048 tokens over 8192, 32 heads on 8, D = 128, in 8 bits takes 280 us, 860 TFLOP/s (45% of the
-// library's bf16 products); 8 trees of 64 tokens over 8192 take 104 us.  Of the 2800 cycles of a step the
+// library's bf16 products); 8 trees of 64 tokens over 8192 take 104 us; with D = 256, 16
+// heads on 8, the chunk takes 359 us, 669 TFLOP/s (a tile of K or V is then made while nothing multiplies by it).  Of the 2800 cycles of a step the
 // rows' warps work in 1850, the tensor cores in 1200; an item's start and end (q to f16, the sums out) take
 // 6 us in which the tensor cores wait.
 //
@@ -163,11 +164,11 @@ __device__ __forceinline__ uint32_t seen_bits(const KvAttnArgs &a, const Item &c
 // A warp's 16 rows of S of a chunk -> P over it.  A thread has 2 rows (8 q + g) and the columns 8 i + 2 j and + 1 of
 // each: with a row to a thread each would read all scales of the chunk from shared memory, 1500 cycles
 // of its bandwidth a chunk.  scales: of K and V, of the thread's first two columns; bits: lanes t and t + 16 have
-// those of the positions that row t sees.
-template <bool MASKED, int DP>
+// those of the positions that row t sees; sums_still: waits until no product adds to the sums.
+template <bool MASKED, int DP, typename F>
 __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, uint32_t scales, const uint32_t (&bits)[4], int j,
                                         bool first, float ratio, const float (&cr)[2], float (&m)[2], float (&ref)[2],
-                                        float (&l)[2])
+                                        float (&l)[2], const F &sums_still)
 {
     const int g = (threadIdx.x & 31) >> 2;
     uint32_t b[2][4], p[32];
@@ -215,6 +216,7 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, uint32_t s
                 l[q] *= f[q], f[q] *= ratio;
             }
             if (!first && __any_sync(0xffffffffu, f[0] != 1.0f || f[1] != 1.0f)) {
+                sums_still();
 #pragma unroll 1
                 for (int at = 0; at < DP; at += 32) {
                     uint32_t o[16];
@@ -258,25 +260,29 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, uint32_t s
 }
 
 // PAIR: the streams are two tiles of rows over the same chunks, which are converted once for both.
+// Of more than 128 channels (never PAIR) tensor memory has room for one O and shared memory for one tile of K and
+// one of V: even and odd chunks have an S each, and one maximum, sum and O.
 template <bool U4, int DP, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_constant__ KvAttnArgs a)
 {
     constexpr uint32_t PANEL = kTokens * 128, TILE = PANEL * (DP / 64);
     constexpr int ROWS = PAIR ? 2 * kRows : kRows;  // of an item
+    constexpr bool ONE = DP > 128, SPLIT = !PAIR && !ONE;  // SPLIT: the streams' parts of a row meet at the end
+    constexpr int TILES = ONE ? 1 : 2;                      // of K, and of V
     const KvArgs &c = a.c;
     extern __shared__ __align__(16) uint8_t raw[];
     __shared__ __align__(8) uint64_t place_full[kPlaces], place_empty[kPlaces], tile_full[4], tile_empty[4],
         info_full[kInfos], info_empty[kInfos], item_full[kItems], item_empty[kItems], s_full[2], p_ready[2], q_full, o_full,
-        mma_end;
+        o_added, mma_end;
     __shared__ __align__(16) Info infos[kInfos];
     __shared__ __align__(16) Tile16 places[kPlaces][kTokens / 16];
     __shared__ Item items[kItems];
     __shared__ float row_m[2][kRows], row_l[2][kRows], row_top[2][kRows], row_c[2][kRows], stream_unit[2];
     __shared__ uint32_t present[kPlaces], tmem_slot;  // 16-token tiles of a chunk that are there
     uint8_t *smem = raw + (-smem_u32(raw) & 1023u);  // the swizzle's atoms
-    // tiles: K of even and odd chunks, V of both; q (of both streams); the sums of the line
-    const uint32_t tiles = smem_u32(smem), q_tile = tiles + 4 * TILE;
-    int64_t *sums = reinterpret_cast<int64_t *>(smem + (PAIR ? 6 : 5) * TILE);
+    // tiles: K of even and odd chunks, V of both (ONE: of any); q (of both streams); the sums of the line
+    const uint32_t tiles = smem_u32(smem), q_tile = tiles + 2 * TILES * TILE;
+    int64_t *sums = reinterpret_cast<int64_t *>(smem + (2 * TILES + (PAIR ? 2 : 1)) * TILE);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
     if (threadIdx.x == 0) {
@@ -302,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         }
         mbar_init(smem_u32(&q_full), kRowWarps);
         mbar_init(smem_u32(&o_full), 1);
+        mbar_init(smem_u32(&o_added), 1);
         mbar_init(smem_u32(&mma_end), 1);
         fence_mbar_init();
     }
@@ -375,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         const uint32_t idesc_s = idesc_f32acc(0, 0, kRows, kTokens);
         const uint32_t idesc_o = idesc_f32acc(0, 0, kRows, 0) | (uint32_t)(c.D >> 3) << 17 | 1u << 16;  // B is N-major
         // one thread, step by step: S of step t after O of step t - 2, which is of the same stream
-        const uint64_t kd0 = sdesc_sw128(tiles), vd0 = sdesc_n_major(tiles + 2 * TILE, PANEL), qd0 = sdesc_sw128(q_tile);
+        const uint64_t kd0 = sdesc_sw128(tiles), vd0 = sdesc_n_major(tiles + TILES * TILE, PANEL), qd0 = sdesc_sw128(q_tile);
         int n = 0, item = 0;
         auto wait1 = [&](uint64_t &bar, int use) {
             ok = ok && mbar_wait_short(smem_u32(&bar), (uint32_t)use & 1u, nullptr);
@@ -391,19 +398,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 const int x = n + (PAIR ? t >> 1 : t), stream = PAIR ? t & 1 : x & 1;  // of S
                 const uint32_t s_at = tmem + stream * kTokens;
                 if (t >= 2) {
-                    const int y = PAIR ? x - 1 : x - 2, tile = y & 1;  // the chunk of O
-                    if (!wait1(tile_full[2 + tile], y >> 1) || !wait1(p_ready[stream], PAIR ? y : y >> 1)) break;
+                    const int y = PAIR ? x - 1 : x - 2, tile = y & (TILES - 1);  // the chunk of O
+                    if (!wait1(tile_full[2 + tile], y / TILES) || !wait1(p_ready[stream], PAIR ? y : y >> 1)) break;
                     tc_fence_after();
                     const uint64_t vd = vd0 + (uint64_t)(tile * (TILE >> 4));
-                    const uint32_t o = tmem + kOCol + stream * 128;
+                    const uint32_t o = tmem + kOCol + (ONE ? 0 : stream * 128);
 #pragma unroll
                     for (int s = 0; s < kTokens / 16; ++s)
-                        mma_ts(o, s_at + 8 * s, vd + (uint64_t)s * (2048 >> 4), idesc_o, t >= 4 || s > 0);
+                        mma_ts(o, s_at + 8 * s, vd + (uint64_t)s * (2048 >> 4), idesc_o, t >= (ONE ? 3 : 4) || s > 0);
                     if (!PAIR || stream) mma_commit(smem_u32(&tile_empty[2 + tile]));
+                    if constexpr (ONE) mma_commit(smem_u32(&o_added));
                 }
                 if (t < steps) {
-                    const int tile = x & 1;
-                    if (!wait1(tile_full[tile], x >> 1)) break;
+                    const int tile = x & (TILES - 1);
+                    if (!wait1(tile_full[tile], x / TILES)) break;
                     tc_fence_after();
                     const uint64_t kd = kd0 + (uint64_t)(tile * (TILE >> 4)), qd = qd0 + (uint64_t)(PAIR ? stream * (TILE >> 4) : 0);
                     auto step = [&](int s) {
@@ -479,10 +487,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             if (is_v) {
                 uint32_t top = __float_as_uint(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])));
                 top = __reduce_max_sync(0xffffffffu, top);
-                const float old = !PAIR && (n & 1) ? unit[1] : unit[0];
+                const float old = SPLIT && (n & 1) ? unit[1] : unit[0];
                 const float now = fmaxf(old, __uint_as_float((top + 0x7fffffu) & 0xff800000u));
                 const float per = __uint_as_float(0x7f000000u - __float_as_uint(now));
-                if (!PAIR && (n & 1)) unit[1] = now;
+                if (SPLIT && (n & 1)) unit[1] = now;
                 else unit[0] = now;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[e] = s[e] * per * (float)(1 << kAttnRoom);
@@ -501,77 +509,87 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         // lies in eight different places of the swizzle.
         const int is_v = (warp - kCodeWarp0) >> 1, side = warp & 1;
         const int r8 = 2 * (lane >> 3) + (lane >> 2 & 1), quad = lane & 3;
-        constexpr int H = U4 ? 1 : DP / 64;  // pieces of a row that a lane has
+        constexpr int H = U4 ? (DP + 127) / 128 : DP / 64;  // pieces of a row that a lane has
+        constexpr int HB = H < 2 ? H : 2, NB = 2 * H / HB;  // pieces, of a chunk's batches, two of which are in registers
         const uint8_t *from[H], *word_from = c.pages + (is_v ? 4 * c.page : 0) + 4 * r8;
         uint32_t to[H];  // of the lane's pieces, in a tile
-        const uint32_t top = tiles + 2 * is_v * TILE + (64 * side + r8) * 128;
+        bool second[H];
+        const uint32_t top = tiles + TILES * is_v * TILE + (64 * side + r8) * 128;
 #pragma unroll
         for (int h = 0; h < H; ++h) {
             const int piece = min(4 * h + quad, c.chunks - 1);  // beyond the row: its last once more
             from[h] = c.pages + (is_v ? c.page * c.row_bytes : 0) + r8 * c.row_bytes + 16 * piece;
             const int chunk = kv_chunk(c.chunks, r8, piece);  // which the piece holds: the order is its own inverse
-            // u4: a piece has four chunks of f16; those of the second panel begin with the third of them
+            // u4: a piece has four chunks of f16; those of every second panel begin with the third of them
             if constexpr (U4) to[h] = top + (chunk >> 1) * PANEL + (((4 * (chunk & 1) + (chunk & 2)) ^ r8) << 4);
             else to[h] = top + (chunk >> 2) * PANEL + (((2 * (chunk & 3)) ^ r8) << 4);
+            second[h] = U4 && (chunk & 2);
         }
-        const bool second = U4 && to[0] - top >= PANEL;
-        uint4 w[2][4][H];  // two halves of 32 tokens, 8 of them at a time
+        uint4 w[2][4][HB];  // two batches: of 32 tokens, 8 of them at a time, HB of a lane's pieces
         uint32_t word[2][4];
-        auto ask = [&](int n, int u) {
+        auto ask = [&](int n, int batch) {
+            const int u = batch / (H / HB), h0 = batch % (H / HB) * HB;
             const Tile16 *place = places[(unsigned)n % kPlaces] + 4 * side + 2 * u;
             if (c.num_pages == 0) return;  // any codes will do for tiles that are not there, but not from nowhere
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int64_t at = place[k >> 1].rows + (k & 1) * 8 * c.row_bytes;
 #pragma unroll
-                for (int h = 0; h < H; ++h)
+                for (int h = 0; h < HB; ++h) {
+                    uint4 &v = w[batch & 1][k][h];
                     asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w[u][k][h].x), "=r"(w[u][k][h].y), "=r"(w[u][k][h].z), "=r"(w[u][k][h].w)
-                                 : "l"(from[h] + at));
+                                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                 : "l"(from[h0 + h] + at));
+                }
                 if (U4)
                     asm volatile("ld.global.u32 %0, [%1];"
-                                 : "=r"(word[u][k])
+                                 : "=r"(word[batch & 1][k])
                                  : "l"(word_from + max(place[k >> 1].words, (int64_t)0) + (k & 1) * 32));
             }
         };
         if (chunks > 0 && wait(place_full[0], 0)) {
             ask(0, 0);
             ask(0, 1);
-            release(place_empty[0]);
+            if constexpr (NB == 2) release(place_empty[0]);
         }
 #pragma unroll 1
         for (int n = 0; n < chunks && ok; ++n) {
             if (n + 1 < chunks && !wait(place_full[(unsigned)(n + 1) % kPlaces], (unsigned)(n + 1) / kPlaces)) break;
-            if (n >= 2 && !wait(tile_empty[2 * is_v + (n & 1)], (n >> 1) - 1)) break;
-            const uint32_t tile = (n & 1) * TILE;
+            if (n >= TILES && !wait(tile_empty[2 * is_v + (n & (TILES - 1))], n / TILES - 1)) break;
+            const uint32_t tile = (n & (TILES - 1)) * TILE;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int batch = 0; batch < NB; ++batch) {
+                const int u = batch / (H / HB), h0 = batch % (H / HB) * HB;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const Zero z = zero_of(word[u][k] & 15u, word[u][k] & 15u);
+                    const Zero z = zero_of(word[batch & 1][k] & 15u, word[batch & 1][k] & 15u);
+                    const uint32_t at = tile + (4 * u + k) * 1024;
 #pragma unroll
-                    for (int h = 0; h < H; ++h) {
-                        const uint32_t at = tile + (4 * u + k) * 1024;
-                        const uint4 v = w[u][k][h];
+                    for (int h = 0; h < HB; ++h) {
+                        const uint4 v = w[batch & 1][k][h];
+                        const uint32_t t = to[h0 + h];
+                        const bool swap = second[h0 + h];
                         uint32_t f[4];
                         if constexpr (U4) {
-                            u4_pairs(second ? v.z : v.x, z, f), sts_v4(to[0] + at, f[0], f[1], f[2], f[3]);
-                            u4_pairs(second ? v.w : v.y, z, f), sts_v4((to[0] ^ 16u) + at, f[0], f[1], f[2], f[3]);
-                            u4_pairs(second ? v.x : v.z, z, f), sts_v4((to[0] ^ 32u) + at, f[0], f[1], f[2], f[3]);
-                            u4_pairs(second ? v.y : v.w, z, f), sts_v4((to[0] ^ 48u) + at, f[0], f[1], f[2], f[3]);
+                            u4_pairs(swap ? v.z : v.x, z, f), sts_v4(t + at, f[0], f[1], f[2], f[3]);
+                            u4_pairs(swap ? v.w : v.y, z, f), sts_v4((t ^ 16u) + at, f[0], f[1], f[2], f[3]);
+                            u4_pairs(swap ? v.x : v.z, z, f), sts_v4((t ^ 32u) + at, f[0], f[1], f[2], f[3]);
+                            u4_pairs(swap ? v.y : v.w, z, f), sts_v4((t ^ 48u) + at, f[0], f[1], f[2], f[3]);
                         } else {
                             s8_pairs(v.x, f[0], f[1]), s8_pairs(v.y, f[2], f[3]);
-                            sts_v4(to[h] + at, f[0], f[1], f[2], f[3]);
+                            sts_v4(t + at, f[0], f[1], f[2], f[3]);
                             s8_pairs(v.z, f[0], f[1]), s8_pairs(v.w, f[2], f[3]);
-                            sts_v4((to[h] ^ 16u) + at, f[0], f[1], f[2], f[3]);
+                            sts_v4((t ^ 16u) + at, f[0], f[1], f[2], f[3]);
                         }
                     }
                 }
-                if (n + 1 < chunks) ask(n + 1, u);
+                if (batch + 2 < NB) ask(n, batch + 2);
+                else if (n + 1 < chunks) ask(n + 1, batch + 2 - NB);
+                if (NB > 2 && batch + 3 == NB) release(place_empty[(unsigned)n % kPlaces]);
             }
-            if (n + 1 < chunks) release(place_empty[(unsigned)(n + 1) % kPlaces]);
+            if (NB == 2 && n + 1 < chunks) release(place_empty[(unsigned)(n + 1) % kPlaces]);
             fence_proxy_async_smem();
-            release(tile_full[2 * is_v + (n & 1)]);
+            release(tile_full[2 * is_v + (n & (TILES - 1))]);
         }
     } else {
         regs_inc<152>();
@@ -689,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             meet();
             // of rows q = 0, 1 of this thread, in both streams
             const int own = 32 * (warp & 3) + 16 * part + g, steps = PAIR ? 2 * count : count;
-            float cr[2][2], m[2][2], ref[2][2], l[2][2], unit[PAIR ? 1 : 2];  // PAIR: the same of both
+            float cr[2][2], m[2][2], ref[2][2], l[2][2], unit[SPLIT ? 2 : 1];  // PAIR: the same of both
             int seen_by_all[2];
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
@@ -699,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                     m[st][q] = -INFINITY;
                     ref[st][q] = l[st][q] = 0.0f;
                 }
-                if (st == 0 || !PAIR) unit[st] = pow2i(-126);
+                if (st == 0 || SPLIT) unit[st] = pow2i(-126);
                 const int t_first = min((at.rt * ROWS + (PAIR ? st * kRows : 0)) / a.group, at.T - 1);
                 seen_by_all[st] = (a.mask ? at.len - at.T : min(at.len, at.len - at.T + t_first + 1)) - kTokens;
             }
@@ -716,17 +734,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 const float ratio = infos[slot].ratio;
                 uint32_t scales = smem_u32(infos[slot].scales[j]);
                 asm volatile("" : "+r"(scales));  // so that no read of them goes ahead of the waits above
-                const uint32_t s_at = lanes + down + stream * kTokens, o_at = lanes + down + kOCol + stream * 128;
+                const uint32_t s_at = lanes + down + stream * kTokens, o_at = lanes + down + kOCol + (ONE ? 0 : stream * 128);
+                const int own_state = ONE ? 0 : stream;
+                auto sums_still = [&]() {  // the others' products are done where S is
+                    if constexpr (ONE) {
+                        (void)wait(o_added, x - 1);
+                        tc_fence_after();
+                    }
+                };
                 // by selection and not by index: the arrays stay in registers
                 float sc[2], sm[2], sr[2], sl[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    sc[q] = stream ? cr[1][q] : cr[0][q], sm[q] = stream ? m[1][q] : m[0][q];
-                    sr[q] = stream ? ref[1][q] : ref[0][q], sl[q] = stream ? l[1][q] : l[0][q];
+                    sc[q] = own_state ? cr[1][q] : cr[0][q], sm[q] = own_state ? m[1][q] : m[0][q];
+                    sr[q] = own_state ? ref[1][q] : ref[0][q], sl[q] = own_state ? l[1][q] : l[0][q];
                 }
                 if (pos0 <= (stream ? seen_by_all[1] : seen_by_all[0]) && there == 0xffu) {
                     const uint32_t none[4] = {};
-                    weights<false, DP>(s_at, o_at, scales, none, j, step < 2, ratio, sc, sm, sr, sl);
+                    weights<false, DP>(s_at, o_at, scales, none, j, step < (ONE ? 1 : 2), ratio, sc, sm, sr, sl, sums_still);
                 } else {
                     uint32_t bits[4];
                     const int row = at.rt * ROWS + (PAIR ? stream * kRows : 0) + 32 * (warp & 3) + 16 * part + (lane & 15);
@@ -736,14 +761,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                         bits[w] = seen_bits(a, at, t, pos0 + 32 * w) &
                                   ((there >> (2 * w) & 1u ? 0xffffu : 0u) | (there >> (2 * w + 1) & 1u ? 0xffff0000u : 0u));
                     __syncwarp();
-                    weights<true, DP>(s_at, o_at, scales, bits, j, step < 2, ratio, sc, sm, sr, sl);
+                    weights<true, DP>(s_at, o_at, scales, bits, j, step < (ONE ? 1 : 2), ratio, sc, sm, sr, sl, sums_still);
                 }
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    if (stream) m[1][q] = sm[q], ref[1][q] = sr[q], l[1][q] = sl[q];
+                    if (own_state) m[1][q] = sm[q], ref[1][q] = sr[q], l[1][q] = sl[q];
                     else m[0][q] = sm[q], ref[0][q] = sr[q], l[0][q] = sl[q];
                 }
-                if (!PAIR && stream) unit[PAIR ? 0 : 1] = infos[slot].unit;
+                if (SPLIT && stream) unit[SPLIT ? 1 : 0] = infos[slot].unit;
                 else unit[0] = infos[slot].unit;
                 tmem_st_wait();
                 tc_fence_before();
@@ -763,19 +788,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                     l[st][q] += __shfl_xor_sync(0xffffffffu, l[st][q], 2);
                     if (j == 0) row_m[st][own + 8 * q] = m[st][q], row_l[st][own + 8 * q] = l[st][q];
                 }
-            if (threadIdx.x == kRowWarp0 * 32) stream_unit[0] = unit[0], stream_unit[1] = unit[PAIR ? 0 : 1];
+            if (threadIdx.x == kRowWarp0 * 32) stream_unit[0] = unit[0], stream_unit[1] = unit[SPLIT ? 1 : 0];
             (void)wait(o_full, item);
             tc_fence_after();
             meet();
             {
-                const int s0 = PAIR ? part : 0, s1 = PAIR ? part : 1;
+                const int s0 = PAIR ? part : 0, s1 = PAIR ? part : SPLIT;
                 const float m0 = row_m[s0][r], m1 = row_m[s1][r], up = fmaxf(m0, m1);
-                const float f0 = m0 == up ? 1.0f : ex2(m0 - up), f1 = PAIR ? 0.0f : m1 == up ? 1.0f : ex2(m1 - up);
-                const float total = PAIR ? row_l[s0][r] : __fmaf_rn(row_l[0][r], f0, row_l[1][r] * f1);
-                const float top_unit = PAIR ? stream_unit[part] : fmaxf(stream_unit[0], stream_unit[1]);
+                const float f0 = m0 == up ? 1.0f : ex2(m0 - up), f1 = !SPLIT ? 0.0f : m1 == up ? 1.0f : ex2(m1 - up);
+                const float total = !SPLIT ? row_l[s0][r] : __fmaf_rn(row_l[0][r], f0, row_l[1][r] * f1);
+                const float top_unit = !SPLIT ? stream_unit[s0] : fmaxf(stream_unit[0], stream_unit[1]);
                 const float per = __uint_as_float(0x7f000000u - __float_as_uint(top_unit));
-                const bool has0 = PAIR || count > 1 || !(n & 1), has1 = !PAIR && (count > 1 || (n & 1));
-                const float g0 = PAIR ? 1.0f : f0 * (stream_unit[0] * per), g1 = PAIR ? 0.0f : f1 * (stream_unit[1] * per);
+                const bool has0 = !SPLIT || count > 1 || !(n & 1), has1 = SPLIT && (count > 1 || (n & 1));
+                const float g0 = !SPLIT ? 1.0f : f0 * (stream_unit[0] * per), g1 = !SPLIT ? 0.0f : f1 * (stream_unit[1] * per);
                 const bool done = starts_here && ends_here;
                 const int part_row = PAIR ? part * kRows + r : r;
                 float *slot = attn_slot(a, blockIdx.x, starts_here ? 1 : 0, ROWS, DP);
@@ -787,13 +812,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                     float v[8];
                     __syncwarp();
                     tmem_ld8(lanes + kOCol + s0 * 128 + d, v0);
-                    if constexpr (!PAIR) tmem_ld8(lanes + kOCol + 128 + d, v1);
+                    if constexpr (SPLIT) tmem_ld8(lanes + kOCol + 128 + d, v1);
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int at_e = U4 ? 2 * (e & 3) + (e >> 2) : e;  // codes are unpacked 0 4, 1 5, 2 6, 3 7
                         v[e] = has0 ? __uint_as_float(v0[at_e]) * g0 : 0.0f;
-                        if constexpr (!PAIR)
+                        if constexpr (SPLIT)
                             if (has1) v[e] = __fmaf_rn(__uint_as_float(v1[at_e]), g1, v[e]);
                         if (done) v[e] *= by;
                     }
@@ -838,7 +863,7 @@ qnn_status launch(KvAttnArgs a, cudaStream_t s)
     static std::atomic<uint64_t> opted_in{0};
     // one block on an SM, whatever it needs: tensor memory is taken whole (of 227 KB, the static part aside)
     constexpr int kMost = 214 << 10;
-    const int need = 1024 + (PAIR ? 6 : 5) * kTokens * DP * 2 + (a.c.batch + 1) * 8;
+    const int need = 1024 + (PAIR ? 6 : DP > 128 ? 3 : 5) * kTokens * DP * 2 + (a.c.batch + 1) * 8;
     if (!opt_in_smem(kern, kMost, opted_in, 100)) return QNN_ERR_CUDA;
     return kv_launch(kern, dim3((unsigned)a.blocks), kThreads, std::max(need, 120 << 10), s, a);
 }
@@ -851,8 +876,8 @@ qnn_status launch(KvAttnArgs a, cudaStream_t s)
 // 127 / 105; a single one of 8192, 40 tokens 34 / 33, 64 tokens 34 / 38.
 AttnPlan attn_rows_plan(const KvArgs &c, int group)
 {
-    const bool pair = (int64_t)c.tokens * group > kRows && c.batch <= 2048;
-    return {pair ? 2 * kRows : kRows, c.D <= 64 ? 64 : 128, std::min(kAttnMaxBlocks, sm_count())};
+    const bool pair = (int64_t)c.tokens * group > kRows && c.batch <= 2048 && c.D <= 128;
+    return {pair ? 2 * kRows : kRows, c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256, std::min(kAttnMaxBlocks, sm_count())};
 }
 
 qnn_status launch_attn_rows(const KvAttnArgs &a, const AttnPlan &p, bool u4, cudaStream_t s)
@@ -862,6 +887,7 @@ qnn_status launch_attn_rows(const KvAttnArgs &a, const AttnPlan &p, bool u4, cud
         return u4 ? launch<true, 128, true>(a, s) : launch<false, 128, true>(a, s);
     }
     if (p.channels == 64) return u4 ? launch<true, 64, false>(a, s) : launch<false, 64, false>(a, s);
+    if (p.channels == 256) return u4 ? launch<true, 256, false>(a, s) : launch<false, 256, false>(a, s);
     return u4 ? launch<true, 128, false>(a, s) : launch<false, 128, false>(a, s);
 }
 

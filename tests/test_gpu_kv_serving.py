@@ -145,7 +145,8 @@ def test_prompts_then_drafted_trees(kv, x_dt, heads, group, D, page, T, replayed
 
 
 @pytest.mark.parametrize("rows", [8, 9, 16, 17, 127, 128, 129, 255, 256, 257, 300])
-@pytest.mark.parametrize("D, kv", [(64, "u4"), (96, "s8"), (128, "u4"), (128, "s8")])
+@pytest.mark.parametrize("D, kv", [(64, "u4"), (96, "s8"), (128, "u4"), (128, "s8"), (160, "u4"), (192, "s8"), (256, "s8"),
+                                   (256, "u4")])
 def test_row_counts_around_a_tile(rows, D, kv):
     """As many rows of a head as a tile has, one less and one more, causal, the last tokens of longer ones."""
     c = _kv.Cache(np.random.default_rng(rows + D), [rows + 150, rows], [rows, rows // 2], 1, D, 16, kv, "bf16")
