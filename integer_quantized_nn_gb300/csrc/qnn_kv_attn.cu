@@ -151,16 +151,45 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_attn_join_kernel(const __g
 //   1 of 512, D = 128:             16 rows 12.9 / 12.9, 32 rows 15.5 / 12.9
 //   16 of 4096, D = 64:            16 rows 47 / 46, 32 rows 57 / 47; 32 heads on 32 over 1024, 16 rows 53 / 74
 //   16 of 4096, D = 256:           32 rows 117 / 129; 8 of 8192: 256 rows 744 / 244
+int most_few_rows(const KvArgs &c) { return c.D <= 64 ? 16 : c.D <= 128 ? 8 : 32; }
+
 bool many_rows(const KvArgs &c, int group)
 {
-    const int64_t rows = (int64_t)c.tokens * group;
-    return c.D <= 128 ? rows > (c.D <= 64 ? 16 : 8) : rows > 32 && c.batch <= 2048;  // the sums of a longer batch: no room
+    // with D > 128 the sums of a longer batch have no room
+    return (int64_t)c.tokens * group > most_few_rows(c) && (c.D <= 128 || c.batch <= 2048);
 }
 
-AttnPlan attn_plan(const KvArgs &c, int group)
+// A batch in which most sequences have far fewer newest tokens than the longest (prompts beside sequences that
+// decode) goes through both kernels, each with the sequences that suit it.  The host knows the tokens' number and
+// the most of one; where the mean is below a quarter of the most, two more launches (about 4 us) are worth it: 63
+// sequences of 4096 with one token beside one with 512, 32 heads on 8, D = 128, 8 bits: 192 us, 344 by one kernel.
+struct AttnPlans {
+    AttnPlan plan[2];
+    int t_min[2], t_max[2], count;
+    bool many[2];
+};
+
+AttnPlans attn_plans(const KvArgs &c, int group)
 {
-    return many_rows(c, group) ? attn_rows_plan(c, group) : attn_few_plan(c, group);
+    AttnPlans p;
+    const int few = most_few_rows(c) / group;  // tokens of a sequence with few rows
+    p.count = 1;
+    p.many[0] = many_rows(c, group);
+    p.plan[0] = p.many[0] ? attn_rows_plan(c, group) : attn_few_plan(c, group);
+    p.t_min[0] = 0, p.t_max[0] = c.tokens;
+    if (p.many[0] && c.starts && few > 0 && 4 * c.rows <= (int64_t)c.batch * c.tokens) {
+        KvArgs rest = c;
+        rest.tokens = few;
+        p.count = 2;
+        p.many[1] = false;
+        p.plan[1] = attn_few_plan(rest, group);
+        p.t_min[0] = few + 1;
+        p.t_min[1] = 0, p.t_max[1] = few;
+    }
+    return p;
 }
+
+int64_t workspace_floats(const AttnPlan &p) { return p.blocks * (kAttnRecord + 2 * attn_slot_floats(p.rows, p.channels)); }
 
 bool heads_ok(const qnn_kv_geom *g, int heads_q)
 {
@@ -174,8 +203,10 @@ extern "C" size_t qnn_kv_attn_workspace_bytes(const qnn_kv_geom *g, const qnn_kv
 {
     qnn::KvArgs c;
     if (qnn::kv_args(g, seqs, &c) != QNN_OK || !qnn::heads_ok(g, heads_q)) return 0;
-    const qnn::AttnPlan p = qnn::attn_plan(c, heads_q / g->heads);
-    return 4 * (size_t)(p.blocks * (qnn::kAttnRecord + 2 * qnn::attn_slot_floats(p.rows, p.channels)));
+    const qnn::AttnPlans p = qnn::attn_plans(c, heads_q / g->heads);
+    size_t n = 0;
+    for (int i = 0; i < p.count; ++i) n += 4 * (size_t)qnn::workspace_floats(p.plan[i]);
+    return n;
 }
 
 extern "C" qnn_status q_kv_attn(const void *q, qnn_dtype x_dt, int64_t ld_q, int heads_q, const qnn_kv_geom *g,
@@ -209,14 +240,22 @@ extern "C" qnn_status q_kv_attn(const void *q, qnn_dtype x_dt, int64_t ld_q, int
     a.heads_q = heads_q;
     a.group = heads_q / g->heads;
     if (!(a.c.status = status_word())) return QNN_ERR_CUDA;
-    const AttnPlan p = attn_plan(a.c, a.group);
-    a.blocks = p.blocks;
     a.bf16 = x_dt == QNN_BF16;
     a.ws = static_cast<float *>(workspace);
-    const qnn_status sent = (many_rows(a.c, a.group) ? launch_attn_rows : launch_attn_few)(a, p, g->kv_dt == QNN_U4,
-                                                                                          (cudaStream_t)stream);
-    if (sent != QNN_OK) return sent;
-    const dim3 grid((unsigned)p.blocks, (unsigned)(p.rows / kJoinWarps));
-    auto join = p.channels == 64 ? kv_attn_join_kernel<2> : p.channels == 128 ? kv_attn_join_kernel<4> : kv_attn_join_kernel<8>;
-    return kv_launch(join, grid, kJoinWarps * 32, 0, (cudaStream_t)stream, a, p.rows);
+    const AttnPlans plans = attn_plans(a.c, a.group);
+    for (int i = 0; i < plans.count; ++i) {
+        const AttnPlan &p = plans.plan[i];
+        a.blocks = p.blocks;
+        a.t_min = plans.t_min[i], a.t_max = plans.t_max[i];
+        qnn_status sent = (plans.many[i] ? launch_attn_rows : launch_attn_few)(a, p, g->kv_dt == QNN_U4, (cudaStream_t)stream);
+        if (sent != QNN_OK) return sent;
+        const dim3 grid((unsigned)p.blocks, (unsigned)(p.rows / kJoinWarps));
+        auto join = p.channels == 64    ? kv_attn_join_kernel<2>
+                    : p.channels == 128 ? kv_attn_join_kernel<4>
+                                        : kv_attn_join_kernel<8>;
+        sent = kv_launch(join, grid, kJoinWarps * 32, 0, (cudaStream_t)stream, a, p.rows);
+        if (sent != QNN_OK) return sent;
+        a.ws += workspace_floats(p);
+    }
+    return QNN_OK;
 }

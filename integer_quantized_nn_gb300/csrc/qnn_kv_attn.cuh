@@ -15,6 +15,7 @@ struct KvAttnArgs {
     int64_t ld_q, ld_out;
     float scale_log2;  // scale * log2(e)
     int heads_q, group, mask_words, bf16;
+    int t_min, t_max;  // sequences with fewer or more newest tokens are not this launch's
     int blocks;        // of the attention's grid
     int stages;        // of a ring
 };
@@ -128,6 +129,14 @@ __device__ __forceinline__ int attn_row_tiles(const KvAttnArgs &a, int T, int wi
     return (T * a.group + width - 1) / width;
 }
 
+// Sequence b, without newest tokens where they are not this launch's.
+__device__ __forceinline__ KvSeq attn_seq(const KvAttnArgs &a, int b)
+{
+    KvSeq s = kv_seq(a.c, b);
+    if (s.T < a.t_min || s.T > a.t_max) s.T = 0;
+    return s;
+}
+
 // A sequence's units.
 __device__ __forceinline__ int64_t attn_weight(const KvAttnArgs &a, const KvSeq &s, int width)
 {
@@ -148,8 +157,8 @@ struct AttnCursor {
 
 __device__ __forceinline__ void attn_sequence(const KvAttnArgs &a, AttnCursor &c, int width)
 {
-    const KvSeq s = kv_seq(a.c, c.b);
-    c.T = max(s.T, 0);
+    const KvSeq s = attn_seq(a, c.b);
+    c.T = s.T;
     c.len = s.len;
     c.first = s.first;
     c.tiles = attn_row_tiles(a, c.T, width);
@@ -213,7 +222,7 @@ __device__ __forceinline__ int64_t attn_sums(const KvAttnArgs &a, int64_t *sums,
     const int b0 = min((int)threadIdx.x * per, a.c.batch), b1 = min(b0 + per, a.c.batch);
     int64_t own = 0;
     for (int b = b0; b < b1; ++b) {
-        const int64_t w = attn_weight(a, kv_seq(a.c, b), width);
+        const int64_t w = attn_weight(a, attn_seq(a, b), width);
         sums[b] = own;
         own += w;
     }

@@ -159,6 +159,18 @@ def test_tiles_that_end_inside_a_token(tokens, group):
     check(c, Dev(c), 2 * group)
 
 
+@pytest.mark.parametrize("D, group, kv, masked", [(128, 4, "s8", False), (64, 2, "u4", True), (160, 8, "s8", False),
+                                                  (96, 8, "u4", True), (64, 32, "s8", False)])
+def test_prompts_beside_sequences_that_decode(D, group, kv, masked):
+    """Few and many newest tokens in a batch, none too, in any order."""
+    rng = np.random.default_rng(D + group)
+    tokens = [1, 0, 2, 1, 1, 90, 1, 4, 1, 1, 3, 0, 1, 40, 1, 1, 1, 5, 8, 9, 1, 1, 0]
+    lens = [n + int(x) for n, x in zip(tokens, rng.integers(0, 300, len(tokens)))]
+    lens[4] = 1
+    c = _kv.Cache(rng, lens, tokens, 2, D, 16, kv, "bf16")
+    check(c, Dev(c), 2 * group, sees=[_kv.random_tree(rng, n) for n in tokens] if masked else None)
+
+
 @pytest.mark.parametrize("most", [1, 12, 140])
 def test_attention_of_a_large_batch(most):
     """More sequences than fit beside two tiles of rows; most have one token, one has `most`."""
@@ -167,6 +179,17 @@ def test_attention_of_a_large_batch(most):
     tokens = [min(1, n) for n in lens]
     lens[1700], tokens[1700] = 200, most
     c = _kv.Cache(rng, lens, tokens, 1, 32, 16, "u4", "bf16")
+    check(c, Dev(c), 1)
+
+
+@pytest.mark.parametrize("most, D, kv", [(1, 128, "s8"), (9, 128, "s8"), (40, 256, "u4")])
+def test_attention_of_the_largest_batch(most, D, kv):
+    """4096 sequences: their sums take shared memory from everything else."""
+    rng = np.random.default_rng(D + most)
+    lens = [int(x) for x in rng.integers(0, 6, 4096)]
+    tokens = [min(1, n) for n in lens]
+    lens[3], tokens[3] = 300, most
+    c = _kv.Cache(rng, lens, tokens, 1, D, 16, kv, "f16")
     check(c, Dev(c), 1)
 
 
