@@ -1,7 +1,7 @@
 // qnn_kv.cu -- the cache of keys and values: quantised as it is written (q_kv_write), read
 // back (q_kv_read), and its accepted tokens kept (q_kv_keep).
 //
-// All three move bytes.  A group of lanes, one for each 8 channels, has a token's head of K or
+// All three move bytes.  A group of lanes, one for each 16 channels (8 for a read), has a token's head of K or
 // V at a time: maxima by shuffles inside the group, one division for 1 / scale, and the rest by products that give
 // what divisions give (so that codes are those of the definition, ties included).  A warp has
 // some of the heads of a run of rows: it looks up the places of all of them at once, a lane a row (the
@@ -52,7 +52,7 @@ qnn_status kv_args(const qnn_kv_geom *g, const qnn_kv_seqs *q, KvArgs *a)
 
 namespace {
 
-constexpr int kWarps = 8, kWriteItems = 2, kReadItems = 4;  // of a row, to a group of lanes at a time
+constexpr int kWarps = 8, kReadItems = 4;  // of a row, to a group of lanes at a time
 
 struct KvIoArgs {
     KvArgs c;
@@ -144,7 +144,7 @@ __device__ __forceinline__ void store8(T *p, int vec, const float (&x)[8])
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.4028235e38f; }  // false for NaN
 
-// W lanes have an item's channels, 8 each; `live`: this lane has some.
+// W lanes have an item's channels; `live`: this lane has some.
 template <int W>
 __device__ __forceinline__ float group_max(float v)
 {
@@ -168,31 +168,29 @@ template <typename T, bool U4, int W>
 __global__ void __launch_bounds__(kWarps * 32, 3) kv_write_kernel(const __grid_constant__ KvIoArgs a)
 {
     const KvArgs &c = a.c;
-    constexpr int G = 32 / W;  // items of a warp at a time
-    const int lane = threadIdx.x & 31, group = lane / W, j = lane % W, d0 = 8 * j;
+    constexpr int G = 32 / W;  // items of a warp
+    const int lane = threadIdx.x & 31, group = lane / W, j = lane % W, d0 = 16 * j;
     const bool live = d0 < c.D;
     grid_dependency_launch();
     grid_dependency_wait();
-    const int first = blockIdx.y * kWriteItems * G + group;
     const int64_t r0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * a.run;
     const int rows = (int)min((int64_t)a.run, c.rows - r0);
     if (rows <= 0) return;
+    const int item = blockIdx.y * G + group;  // K's heads, then V's
+    const bool is_v = item >= c.heads, some = item < 2 * c.heads && live;
+    const T *from = static_cast<const T *>(is_v ? a.v : a.k) + (int64_t)(item - (is_v ? c.heads : 0)) * c.D + d0;
+    const int64_t pitch = is_v ? a.ld_v : a.ld_k;
     // Rows on their way, as they lie in memory, and converted when their turn comes: two, or one of fp32, whose
     // second would not fit the registers (prompts written and read in 4 bits: 42 us, 48 with one).
     constexpr int kAhead = sizeof(T) == 2 ? 2 : 1;
-    Raw8<T> ahead[kAhead][kWriteItems];
-    auto ask = [&](int64_t row, Raw8<T> (&to)[kWriteItems]) {
+    Raw8<T> ahead[kAhead][2];
+    auto ask = [&](int64_t row, Raw8<T> (&to)[2]) {
+        if (some) {
+            load8(from + row * pitch, a.vec, to[0]);
+            load8(from + row * pitch + 8, a.vec, to[1]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kWriteItems; ++i) {
-            const int item = first + i * G;  // K's heads, then V's
-            if (item < 2 * c.heads && live) {
-                const bool is_v = item >= c.heads;
-                const int64_t at = row * (is_v ? a.ld_v : a.ld_k) + (item - (is_v ? c.heads : 0)) * c.D + d0;
-                load8(static_cast<const T *>(is_v ? a.v : a.k) + at, a.vec, to[i]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < (int)sizeof(T) / 2; ++e) to[i].w[e] = make_uint4(0, 0, 0, 0);
-            }
+            for (int e = 0; e < (int)sizeof(T) / 2; ++e) to[0].w[e] = to[1].w[e] = make_uint4(0, 0, 0, 0);
         }
     };
     ask(r0, ahead[0]);
@@ -200,12 +198,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv_write_kernel(const __grid_c
     const Place places = place_of(c, lane < rows ? (int)r0 + lane : INT32_MAX);
 #pragma unroll 1
     for (int t = 0; t < rows; ++t) {
-        float x[kWriteItems][8];
+        float x[16];
 #pragma unroll
-        for (int i = 0; i < kWriteItems; ++i) {
+        for (int i = 0; i < 2; ++i) {
             const T *raw = reinterpret_cast<const T *>(ahead[0][i].w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[i][e] = to_f32(raw[e]);
+            for (int e = 0; e < 8; ++e) x[8 * i + e] = to_f32(raw[e]);
             if constexpr (kAhead > 1) ahead[0][i] = ahead[1][i];
         }
         if (t + kAhead < rows) ask(r0 + t + kAhead, ahead[kAhead - 1]);
@@ -214,97 +212,94 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv_write_kernel(const __grid_c
         p.slot = __shfl_sync(0xffffffffu, places.slot, t);
         if (p.page < 0) continue;
         uint8_t *base = c.pages + p.page * c.page_bytes;
+        float hi = 0.0f, lo = 0.0f;  // the largest value and -min, both 0 at least (NaN aside)
 #pragma unroll
-        for (int i = 0; i < kWriteItems; ++i) {
-            const int item = first + i * G;
-            float hi, lo = 0.0f;  // the largest value and -min, both 0 at least (NaN aside)
-            if constexpr (U4) {
-                hi = max3(max3(x[i][0], x[i][1], x[i][2]), max3(x[i][3], x[i][4], x[i][5]), max3(x[i][6], x[i][7], 0.0f));
-                lo = max3(max3(-x[i][0], -x[i][1], -x[i][2]), max3(-x[i][3], -x[i][4], -x[i][5]), max3(-x[i][6], -x[i][7], 0.0f));
-                lo = group_max<W>(lo);
-            } else {
-                hi = max3(max3(fabsf(x[i][0]), fabsf(x[i][1]), fabsf(x[i][2])),
-                          max3(fabsf(x[i][3]), fabsf(x[i][4]), fabsf(x[i][5])), max3(fabsf(x[i][6]), fabsf(x[i][7]), 0.0f));
+        for (int e = 0; e < 16; e += 2) {
+            hi = U4 ? max3(hi, x[e], x[e + 1]) : max3(hi, fabsf(x[e]), fabsf(x[e + 1]));
+            if (U4) lo = max3(lo, -x[e], -x[e + 1]);
+        }
+        if (U4) lo = group_max<W>(lo);
+        hi = group_max<W>(hi);
+        if (__any_sync(0xffffffffu, fmaxf(hi, lo) == INFINITY)) {  // once more, of what is finite
+            hi = lo = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                if (!finite(x[e])) continue;
+                hi = fmaxf(hi, U4 ? x[e] : fabsf(x[e]));
+                if (U4) lo = fmaxf(lo, -x[e]);
             }
             hi = group_max<W>(hi);
-            if (__any_sync(0xffffffffu, fmaxf(hi, lo) == INFINITY)) {  // once more, of what is finite
-                hi = lo = 0.0f;
+            if (U4) lo = group_max<W>(lo);
+        }
+        float s, z = 0.0f;
+        uint32_t q[16];
+        constexpr float kInteger = 12582912.0f;  // 1.5 * 2^23: a sum with it is an integer in the low bits
+        bool plain = fmaxf(hi, lo) > 0x1p-60f;
+        if constexpr (U4) {
+            const float2 of = quotients(make_float2(hi, lo), both(15.0f), both(1.0f / 15.0f));
+            s = __bfloat162float(__float2bfloat16_rn(__fadd_rn(of.x, of.y)));
+            const float2 by = both(s), per = both(__fdiv_rn(1.0f, s));
+            z = fminf(rintf(quotients(both(lo), by, per).x), 15.0f);
+            float2 sum = both(0.0f);  // not a number where a value is none, or infinite
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (!finite(x[i][e])) continue;
-                    hi = fmaxf(hi, U4 ? x[i][e] : fabsf(x[i][e]));
-                    if (U4) lo = fmaxf(lo, -x[i][e]);
-                }
-                hi = group_max<W>(hi);
-                if (U4) lo = group_max<W>(lo);
+            for (int e = 0; e < 16; e += 2) {
+                const float2 t = quotients(make_float2(x[e], x[e + 1]), by, per);
+                sum = add2(sum, t);
+                const float2 r = add2(add2(t, both(kInteger)), both(z));
+                q[e] = __float_as_uint(fminf(fmaxf(r.x, kInteger), kInteger + 15.0f));
+                q[e + 1] = __float_as_uint(fminf(fmaxf(r.y, kInteger), kInteger + 15.0f));
             }
-            float s, z = 0.0f;
-            uint32_t q[8];
-            constexpr float kInteger = 12582912.0f;  // 1.5 * 2^23: a sum with it is an integer in the low bits
-            bool plain = fmaxf(hi, lo) > 0x1p-60f;
+            plain = plain && sum.x + sum.y == sum.x + sum.y;
+        } else {
+            s = quotients(both(hi), both(127.0f), both(1.0f / 127.0f)).x;
+            // By a product with 1 / s: that is within 2^-21 of the quotient, relatively, and so the same integer
+            // but near a tie.
+            const float2 per = both(__fdiv_rn(1.0f, s));
+            float far = 0.0f;  // from the nearest integer
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+                const float2 t = mul2(make_float2(x[e], x[e + 1]), per), r = add2(t, both(kInteger));
+                const float2 d = add2(add2(r, both(-kInteger)), make_float2(-t.x, -t.y));
+                // NaN does not pass the comparison: max would drop it
+                far = max3(far, fabsf(d.x) < 0.4999f ? 0.0f : 1.0f, fabsf(d.y) < 0.4999f ? 0.0f : 1.0f);
+                q[e] = __float_as_uint(r.x), q[e + 1] = __float_as_uint(r.y);
+            }
+            plain = plain && far == 0.0f;
+        }
+        if (!plain) {  // by division
             if constexpr (U4) {
-                const float2 of = quotients(make_float2(hi, lo), both(15.0f), both(1.0f / 15.0f));
-                s = __bfloat162float(__float2bfloat16_rn(__fadd_rn(of.x, of.y)));
-                const float2 by = both(s), per = both(__fdiv_rn(1.0f, s));
-                z = fminf(rintf(quotients(both(lo), by, per).x), 15.0f);
-                float2 sum = both(0.0f);  // not a number where a value is none, or infinite
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float2 t = quotients(make_float2(x[i][e], x[i][e + 1]), by, per);
-                    sum = add2(sum, t);
-                    const float2 r = add2(add2(t, both(kInteger)), both(z));
-                    q[e] = __float_as_uint(fminf(fmaxf(r.x, kInteger), kInteger + 15.0f));
-                    q[e + 1] = __float_as_uint(fminf(fmaxf(r.y, kInteger), kInteger + 15.0f));
-                }
-                plain = plain && sum.x + sum.y == sum.x + sum.y;
+                s = __bfloat162float(__float2bfloat16_rn(__fadd_rn(__fdiv_rn(hi, 15.0f), __fdiv_rn(lo, 15.0f))));
+                z = s > 0.0f ? fminf(rintf(__fdiv_rn(lo, s)), 15.0f) : 0.0f;
             } else {
-                s = quotients(both(hi), both(127.0f), both(1.0f / 127.0f)).x;
-                // By a product with 1 / s: that is within 2^-21 of the quotient, relatively, and so the same integer
-                // but near a tie.
-                const float2 per = both(__fdiv_rn(1.0f, s));
-                float far = 0.0f;  // from the nearest integer
+                s = __fdiv_rn(hi, 127.0f);
+            }
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float2 t = mul2(make_float2(x[i][e], x[i][e + 1]), per), r = add2(t, both(kInteger));
-                    const float2 d = add2(add2(r, both(-kInteger)), make_float2(-t.x, -t.y));
-                    // NaN does not pass the comparison: max would drop it
-                    far = max3(far, fabsf(d.x) < 0.4999f ? 0.0f : 1.0f, fabsf(d.y) < 0.4999f ? 0.0f : 1.0f);
-                    q[e] = __float_as_uint(r.x), q[e + 1] = __float_as_uint(r.y);
-                }
-                plain = plain && far == 0.0f;
+            for (int e = 0; e < 16; ++e) {
+                const float v = x[e], r = s > 0.0f && v == v ? rintf(__fdiv_rn(v, s)) : 0.0f;
+                q[e] = U4 ? (uint32_t)fminf(fmaxf(__fadd_rn(r, z), 0.0f), 15.0f)
+                          : (uint32_t)(int)fminf(fmaxf(r, -127.0f), 127.0f);
             }
-            if (!plain) {  // by division
-                if constexpr (U4) {
-                    s = __bfloat162float(__float2bfloat16_rn(__fadd_rn(__fdiv_rn(hi, 15.0f), __fdiv_rn(lo, 15.0f))));
-                    z = s > 0.0f ? fminf(rintf(__fdiv_rn(lo, s)), 15.0f) : 0.0f;
-                } else {
-                    s = __fdiv_rn(hi, 127.0f);
-                }
+        }
+        // the low bytes of all
+        uint32_t w[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float v = x[i][e], r = s > 0.0f && v == v ? rintf(__fdiv_rn(v, s)) : 0.0f;
-                    q[e] = U4 ? (uint32_t)fminf(fmaxf(__fadd_rn(r, z), 0.0f), 15.0f)
-                              : (uint32_t)(int)fminf(fmaxf(r, -127.0f), 127.0f);
-                }
-            }
-            // the low bytes of all
-            uint32_t w0 = prmt(prmt(q[0], q[1], 0x0040), prmt(q[2], q[3], 0x0040), 0x5410);
-            uint32_t w1 = prmt(prmt(q[4], q[5], 0x0040), prmt(q[6], q[7], 0x0040), 0x5410);
-            if (item >= 2 * c.heads || !live) continue;
-            const bool is_v = item >= c.heads;
-            uint8_t *head = base + (int64_t)(item - (is_v ? c.heads : 0)) * c.head_bytes;
-            uint8_t *to = head + (is_v ? c.page * c.row_bytes : 0) + p.slot * c.row_bytes;
-            if constexpr (U4) {
-                w0 |= w0 >> 4, w1 |= w1 >> 4;  // bytes 0 and 2: two codes each
-                *reinterpret_cast<uint32_t *>(to + 16 * kv_chunk(c.chunks, p.slot, j / 4) + 4 * (j % 4)) = prmt(w0, w1, 0x6420);
-            } else {
-                *reinterpret_cast<uint2 *>(to + 16 * kv_chunk(c.chunks, p.slot, j / 2) + 8 * (j % 2)) =
-                    make_uint2(w0 ^ 0x80808080u, w1 ^ 0x80808080u);
-            }
-            if (j == 0) {
-                const uint32_t word = U4 ? __float_as_uint(s) | (uint32_t)z : __float_as_uint(s);
-                reinterpret_cast<uint32_t *>(head + 2 * c.page * c.row_bytes)[(is_v ? c.page : 0) + p.slot] = word;
-            }
+        for (int e = 0; e < 4; ++e)
+            w[e] = prmt(prmt(q[4 * e], q[4 * e + 1], 0x0040), prmt(q[4 * e + 2], q[4 * e + 3], 0x0040), 0x5410);
+        if (!some) continue;
+        uint8_t *head = base + (int64_t)(item - (is_v ? c.heads : 0)) * c.head_bytes;
+        uint8_t *to = head + (is_v ? c.page * c.row_bytes : 0) + p.slot * c.row_bytes;
+        if constexpr (U4) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] |= w[e] >> 4;  // bytes 0 and 2: two codes each
+            *reinterpret_cast<uint2 *>(to + 16 * kv_chunk(c.chunks, p.slot, j / 2) + 8 * (j % 2)) =
+                make_uint2(prmt(w[0], w[1], 0x6420), prmt(w[2], w[3], 0x6420));
+        } else {
+            *reinterpret_cast<uint4 *>(to + 16 * kv_chunk(c.chunks, p.slot, j)) =
+                make_uint4(w[0] ^ 0x80808080u, w[1] ^ 0x80808080u, w[2] ^ 0x80808080u, w[3] ^ 0x80808080u);
+        }
+        if (j == 0) {
+            const uint32_t word = U4 ? __float_as_uint(s) | (uint32_t)z : __float_as_uint(s);
+            reinterpret_cast<uint32_t *>(head + 2 * c.page * c.row_bytes)[(is_v ? c.page : 0) + p.slot] = word;
         }
     }
 }
@@ -461,12 +456,12 @@ qnn_status launch_io(KvIoArgs a, bool read, cudaStream_t s)
     // 8 at most for a read, whose later blocks even out the rest (8 x 4096 tokens of 8 heads of 128 in 8 bits to bf16:
     // 40.5 us with 4 or 8, 49.4 with 32, 48.7 with 1; 4 x 4000 tokens written and read in 4 bits: 47.7 us with 8 or
     // 32 for the read, 60.9 to 73 with 4 for the write).
-    const int per = (read ? kReadItems : kWriteItems) * (32 / W), parts = (2 * a.c.heads + per - 1) / per;
+    const int per = read ? kReadItems * (32 / W) : 2 * (32 / W), parts = (2 * a.c.heads + per - 1) / per;
     a.run = (int)std::min<int64_t>(read ? 8 : 32, std::max<int64_t>(1, (a.c.rows * parts + sm_count() * 24 - 1) / (sm_count() * 24)));
     const int64_t block_rows = (int64_t)kWarps * a.run;
     const dim3 grid((unsigned)((a.c.rows + block_rows - 1) / block_rows), (unsigned)parts);
     return read ? kv_launch(kv_read_kernel<T, U4, W>, grid, kWarps * 32, 0, s, a)
-                : kv_launch(kv_write_kernel<T, U4, W>, grid, kWarps * 32, 0, s, a);
+                : kv_launch(kv_write_kernel<T, U4, W / 2>, grid, kWarps * 32, 0, s, a);
 }
 
 template <typename T, bool U4>
