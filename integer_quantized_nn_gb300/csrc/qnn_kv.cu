@@ -359,12 +359,21 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const __grid_const
             T *to = static_cast<T *>(const_cast<void *>(is_v ? a.v : a.k));
             if (!to) continue;
             const float s = __uint_as_float(U4 ? word[i] & 0xffff0000u : word[i]);
-            const int z = U4 ? (int)(word[i] & 15u) : 128;
+            // 2^23 + a code, by its bits, less 2^23 and the zero point
+            const float2 less = both(-8388608.0f - (U4 ? (float)(word[i] & 15u) : 128.0f));
             float x[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int q = U4 ? (int)(w[i][0] >> (4 * e) & 15u) : (int)(w[i][e / 4] >> (8 * (e % 4)) & 255u);
-                x[e] = __fmul_rn((float)(q - z), s);
+            for (int e = 0; e < 8; e += 2) {
+                float2 v;
+                if constexpr (U4) {
+                    v = make_float2(__uint_as_float((w[i][0] >> (4 * e) & 15u) | 0x4b000000u),
+                                    __uint_as_float((w[i][0] >> (4 * e + 4) & 15u) | 0x4b000000u));
+                } else {
+                    v = make_float2(__uint_as_float(prmt(w[i][e / 4], 0x4b000000u, 0x7440 + e % 4)),
+                                    __uint_as_float(prmt(w[i][e / 4], 0x4b000000u, 0x7441 + e % 4)));
+                }
+                v = mul2(add2(v, less), both(s));
+                x[e] = v.x, x[e + 1] = v.y;
             }
             store8(to + r * (is_v ? a.ld_v : a.ld_k) + (int64_t)(item - (is_v ? c.heads : 0)) * c.D + d0, a.vec, x);
         }
