@@ -248,3 +248,60 @@ def test_one_large_channel(tokens, kv):
     check(c, Dev(c), 4, q=q)
     # a row of q over many octaves
     check(c, Dev(c), 4, q=rng.normal(0, 1, size=(tokens, 4, 128)) * 2.0 ** -rng.integers(0, 30, size=(tokens, 4, 128)))
+
+
+@pytest.mark.parametrize("D, kv", [(128, "s8"), (256, "u4")])
+def test_many_rows_and_kept_tokens_beyond_32_bits(D, kv):
+    """The last pages of a cache of more than 4 GiB, for 60 rows of a head, and tokens that move there."""
+    t = torch()
+    rng = np.random.default_rng(D)
+    c = _kv.Cache(rng, [200, 133], [30, 25], 2, D, 256, kv, "bf16", spare=0)
+    d = Dev(c, fill=False)
+    pages = (5 << 30) // d.pages.shape[1]
+    d.pages = t.empty((pages, d.pages.shape[1]), dtype=t.uint8, device="cuda")
+    c.table[:, 0] = [pages - 1, pages - 2]
+    c.num_pages = pages
+    d.table.copy_(t.from_numpy(c.table))
+    d.seqs = qnn.kv_seqs(d.pages, d.table, d.lens, c.rows, 30, starts=d.starts)
+    whole_starts = d.ints([0, 200, 333])
+    whole = qnn.kv_seqs(d.pages, d.table, d.lens, 333, 200, starts=whole_starts)
+    qnn.q_kv_write(d.floats(np.concatenate(c.k)), d.floats(np.concatenate(c.v)), "bf16", d.geom, whole)
+    check(c, d, 4)
+    keep = t.tensor([[3, 4, 29], [0, 7, 24]], dtype=t.int32, device="cuda")
+    n_keep = t.tensor([3, 3], dtype=t.int32, device="cuda")
+    qnn.q_kv_keep(d.geom, d.seqs, keep, n_keep)
+    for b, path in enumerate(keep.tolist()):
+        n = c.lens[b] - c.tokens[b]
+        for i, j in enumerate(path):
+            c.k[b][n + i], c.v[b][n + i] = c.k[b][n + j].copy(), c.v[b][n + j].copy()
+    check(c, d, 4)
+
+
+def test_a_captured_mixed_batch():
+    """A graph of prompts beside decoding sequences, replayed when others of them have the prompt."""
+    t = torch()
+    rng = np.random.default_rng(77)
+    one, other = [1, 1, 120, 1, 1, 2, 1, 1], [1, 120, 1, 2, 1, 1, 1, 1]
+    lens = [300, 250, 200, 31, 1, 64, 129, 400]
+    c = _kv.Cache(rng, lens, one, 2, 64, 16, "s8", "bf16")
+    d = Dev(c)
+    q = t.empty((c.rows, 8 * 64), dtype=t.bfloat16, device="cuda")
+    out, lse = t.empty_like(q), t.empty((c.rows, 8), device="cuda")
+    ws = t.empty(qnn.qnn_kv_attn_workspace_bytes(d.geom, d.seqs, 8), dtype=t.uint8, device="cuda")
+    qnn.q_kv_attn(q.zero_(), "bf16", 8, d.geom, d.seqs, 0.125, out, ws, lse=lse)
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        qnn.q_kv_attn(q, "bf16", 8, d.geom, d.seqs, 0.125, out, ws, lse=lse)
+    for tokens in (one, other, one):
+        c.tokens = tokens
+        c.starts = np.concatenate([[0], np.cumsum(tokens)]).astype(np.int32)
+        d.starts.copy_(t.from_numpy(c.starts))
+        x = d.floats(rng.normal(0, 1, size=(c.rows, 8, 64)))
+        q.copy_(x.view(c.rows, -1))
+        t.cuda.synchronize()
+        graph.replay()
+        t.cuda.synchronize()
+        w_out, w_lse, t_out, t_lse = _kv.attention(c, x.double().cpu().numpy(), 0.125)
+        near(out.double().cpu().numpy().reshape(w_out.shape), w_out, t_out, "out")
+        near(lse.double().cpu().numpy(), w_lse, t_lse, "lse")
+    assert qnn.qnn_check_device_error() == OK
