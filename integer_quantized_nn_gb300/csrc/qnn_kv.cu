@@ -8,9 +8,11 @@
 // chain of reads starts -> lens -> table is what a row costs), and has the next row's values on their
 // way while it works on one.
 //
-// Bytes bound the read: 8 x 4096 tokens of 8 heads of 128, 8 bits to bf16, take 41 us, 5.0 TB/s.  A write is
-// bound by latency and instructions: 4 sequences, 10 000 tokens in all, to 4 bits take 27 us, 20 million values (60
-// with divisions for all values near ties); 16 x 4096 tokens of 8 heads of 128 written and read, 220 us in 8 bits.  One token takes 5 us, latency.
+// Bytes bound the read: 8 x 4096 tokens of 8 heads of 128, 8 bits to bf16, take 39 us, 5.2 TB/s.  A write is
+// bound by latency and instructions: 4 sequences, 10 000 tokens in all, to 4 bits take 22 us, 20 million values (60
+// with divisions for all values near ties); 16 x 4096 tokens of 8 heads of 128 written and read, 210 us in 8
+// bits.  A warp has several rows at a time where a row has few heads (2 x 127238 tokens of one head of 64, fp32,
+// written and read: 204 us with one, 79).  One token takes 5 us, latency.
 #include "qnn_kv.cuh"
 
 namespace qnn {
@@ -52,13 +54,14 @@ qnn_status kv_args(const qnn_kv_geom *g, const qnn_kv_seqs *q, KvArgs *a)
 
 namespace {
 
-constexpr int kWarps = 8, kReadItems = 4;  // of a row, to a group of lanes at a time
+constexpr int kWarps = 8, kReadItems = 4;  // of a row, that a group of lanes reads at a time
 
 struct KvIoArgs {
     KvArgs c;
     const void *k, *v;
     int64_t ld_k, ld_v;
-    int run;    // rows of a warp, one after the other; their places are looked up together, one by a lane
+    int run;    // rows of a warp; their places are looked up together, one by a lane
+    int log_r;  // 2^log_r groups of lanes have a row, each a head of K or V; the warp's others the next rows
     int vec;    // rows of k and v start on 16-byte boundaries
 };
 
@@ -168,36 +171,38 @@ template <typename T, bool U4, int W>
 __global__ void __launch_bounds__(kWarps * 32, 3) kv_write_kernel(const __grid_constant__ KvIoArgs a)
 {
     const KvArgs &c = a.c;
-    constexpr int G = 32 / W;  // items of a warp
+    constexpr int G = 32 / W;  // groups of a warp
     const int lane = threadIdx.x & 31, group = lane / W, j = lane % W, d0 = 16 * j;
+    const int per = G >> a.log_r, sub = group >> a.log_r;  // rows at a time
     const bool live = d0 < c.D;
     grid_dependency_launch();
     grid_dependency_wait();
     const int64_t r0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * a.run;
     const int rows = (int)min((int64_t)a.run, c.rows - r0);
     if (rows <= 0) return;
-    const int item = blockIdx.y * G + group;  // K's heads, then V's
+    const int item = (blockIdx.y << a.log_r) + (group & ((1 << a.log_r) - 1));  // K's heads, then V's
     const bool is_v = item >= c.heads, some = item < 2 * c.heads && live;
-    const T *from = static_cast<const T *>(is_v ? a.v : a.k) + (int64_t)(item - (is_v ? c.heads : 0)) * c.D + d0;
     const int64_t pitch = is_v ? a.ld_v : a.ld_k;
+    const T *from = static_cast<const T *>(is_v ? a.v : a.k) + (r0 + sub) * pitch +
+                    (int64_t)(item - (is_v ? c.heads : 0)) * c.D + d0;
     // Rows on their way, as they lie in memory, and converted when their turn comes: two, or one of fp32, whose
     // second would not fit the registers (prompts written and read in 4 bits: 42 us, 48 with one).
     constexpr int kAhead = sizeof(T) == 2 ? 2 : 1;
     Raw8<T> ahead[kAhead][2];
-    auto ask = [&](int64_t row, Raw8<T> (&to)[2]) {
-        if (some) {
-            load8(from + row * pitch, a.vec, to[0]);
-            load8(from + row * pitch + 8, a.vec, to[1]);
+    auto ask = [&](int t, Raw8<T> (&to)[2]) {
+        if (some && t + sub < rows) {
+            load8(from + t * pitch, a.vec, to[0]);
+            load8(from + t * pitch + 8, a.vec, to[1]);
         } else {
 #pragma unroll
             for (int e = 0; e < (int)sizeof(T) / 2; ++e) to[0].w[e] = to[1].w[e] = make_uint4(0, 0, 0, 0);
         }
     };
-    ask(r0, ahead[0]);
-    if (kAhead > 1 && rows > 1) ask(r0 + 1, ahead[kAhead - 1]);
+    ask(0, ahead[0]);
+    if (kAhead > 1) ask(per, ahead[kAhead - 1]);
     const Place places = place_of(c, lane < rows ? (int)r0 + lane : INT32_MAX);
 #pragma unroll 1
-    for (int t = 0; t < rows; ++t) {
+    for (int t = 0; t < rows; t += per) {
         float x[16];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -206,11 +211,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv_write_kernel(const __grid_c
             for (int e = 0; e < 8; ++e) x[8 * i + e] = to_f32(raw[e]);
             if constexpr (kAhead > 1) ahead[0][i] = ahead[1][i];
         }
-        if (t + kAhead < rows) ask(r0 + t + kAhead, ahead[kAhead - 1]);
-        Place p;
-        p.page = __shfl_sync(0xffffffffu, places.page, t);
-        p.slot = __shfl_sync(0xffffffffu, places.slot, t);
-        if (p.page < 0) continue;
+        ask(t + kAhead * per, ahead[kAhead - 1]);
+        Place p;  // of no row: that of a lane without one, -1
+        p.page = __shfl_sync(0xffffffffu, places.page, t + sub);
+        p.slot = __shfl_sync(0xffffffffu, places.slot, t + sub);
+        if (__all_sync(0xffffffffu, p.page < 0)) continue;
         uint8_t *base = c.pages + p.page * c.page_bytes;
         float hi = 0.0f, lo = 0.0f;  // the largest value and -min, both 0 at least (NaN aside)
 #pragma unroll
@@ -285,7 +290,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv_write_kernel(const __grid_c
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             w[e] = prmt(prmt(q[4 * e], q[4 * e + 1], 0x0040), prmt(q[4 * e + 2], q[4 * e + 3], 0x0040), 0x5410);
-        if (!some) continue;
+        if (!some || p.page < 0) continue;
         uint8_t *head = base + (int64_t)(item - (is_v ? c.heads : 0)) * c.head_bytes;
         uint8_t *to = head + (is_v ? c.page * c.row_bytes : 0) + p.slot * c.row_bytes;
         if constexpr (U4) {
@@ -304,26 +309,29 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv_write_kernel(const __grid_c
     }
 }
 
+// Blocks of an SM: four want 64 registers, which 8 bits to 16-bit values nearly do with (8 x 4096 tokens: 39 us, 43
+// with three), fp32 does not (10575 tokens: 36 us, 27 with three).
 template <typename T, bool U4, int W>
-__global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const __grid_constant__ KvIoArgs a)
+__global__ void __launch_bounds__(kWarps * 32, U4 || sizeof(T) == 4 ? 3 : 4) kv_read_kernel(const __grid_constant__ KvIoArgs a)
 {
     const KvArgs &c = a.c;
     constexpr int G = 32 / W;
     const int lane = threadIdx.x & 31, group = lane / W, j = lane % W, d0 = 8 * j;
+    const int per = G >> a.log_r, sub = group >> a.log_r, next = 1 << a.log_r;  // rows at a time; from head to head
     const bool live = d0 < c.D;
     grid_dependency_launch();
     grid_dependency_wait();
-    const int first = blockIdx.y * kReadItems * G + group;
+    const int first = blockIdx.y * kReadItems * next + (group & (next - 1));
     const int64_t r0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * a.run;
     const int rows = (int)min((int64_t)a.run, c.rows - r0);
     if (rows <= 0) return;
     const Place places = place_of(c, lane < rows ? (int)r0 + lane : INT32_MAX);
     uint32_t ahead[kReadItems][2], ahead_word[kReadItems];
     auto ask = [&](int t) {
-        const int page = __shfl_sync(0xffffffffu, places.page, t), slot = __shfl_sync(0xffffffffu, places.slot, t);
+        const int page = __shfl_sync(0xffffffffu, places.page, t + sub), slot = __shfl_sync(0xffffffffu, places.slot, t + sub);
 #pragma unroll
         for (int i = 0; i < kReadItems; ++i) {
-            const int item = first + i * G;
+            const int item = first + i * next;
             const bool is_v = item >= c.heads;
             ahead[i][0] = ahead[i][1] = U4 ? 0 : 0x80808080u;
             ahead_word[i] = 0;
@@ -343,17 +351,17 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const __grid_const
     };
     ask(0);
 #pragma unroll 1
-    for (int t = 0; t < rows; ++t) {
-        const int64_t r = r0 + t;
-        const int seq = __shfl_sync(0xffffffffu, places.seq, t);
+    for (int t = 0; t < rows; t += per) {
+        const int64_t r = r0 + t + sub;
+        const int seq = __shfl_sync(0xffffffffu, places.seq, t + sub);
         uint32_t w[kReadItems][2], word[kReadItems];
 #pragma unroll
         for (int i = 0; i < kReadItems; ++i) w[i][0] = ahead[i][0], w[i][1] = ahead[i][1], word[i] = ahead_word[i];
-        if (t + 1 < rows) ask(t + 1);
+        if (t + per < rows) ask(t + per);
         if (!seq || !live) continue;
 #pragma unroll
         for (int i = 0; i < kReadItems; ++i) {
-            const int item = first + i * G;
+            const int item = first + i * next;
             const bool is_v = item >= c.heads;
             if (item >= 2 * c.heads) continue;
             T *to = static_cast<T *>(const_cast<void *>(is_v ? a.v : a.k));
@@ -461,12 +469,17 @@ __global__ void __launch_bounds__(kKeepThreads) kv_keep_kernel(const __grid_cons
 template <typename T, bool U4, int W>
 qnn_status launch_io(KvIoArgs a, bool read, cudaStream_t s)
 {
-    // A row of blocks for each few items of a warp's groups.  Rows of a warp: as many as let all warps run at once,
-    // 8 at most for a read, whose later blocks even out the rest (8 x 4096 tokens of 8 heads of 128 in 8 bits to bf16:
-    // 40.5 us with 4 or 8, 49.4 with 32, 48.7 with 1; 4 x 4000 tokens written and read in 4 bits: 47.7 us with 8 or
-    // 32 for the read, 60.9 to 73 with 4 for the write).
-    const int per = read ? kReadItems * (32 / W) : 2 * (32 / W), parts = (2 * a.c.heads + per - 1) / per;
-    a.run = (int)std::min<int64_t>(read ? 8 : 32, std::max<int64_t>(1, (a.c.rows * parts + sm_count() * 24 - 1) / (sm_count() * 24)));
+    // A warp's groups have the heads of one row or, where those are fewer, of several.  Where they are more there
+    // is a row of blocks for each part of them.
+    const int groups = 32 / (read ? W : W / 2);
+    a.log_r = 0;
+    while (1 << a.log_r < std::min(groups, 2 * a.c.heads)) ++a.log_r;
+    const int per = groups >> a.log_r, items = (read ? kReadItems : 1) << a.log_r;
+    const int parts = (2 * a.c.heads + items - 1) / items;
+    // Rows of a warp: as many as let all warps run at once, 32 at most, and for a read 8 turns, whose later blocks
+    // even out the rest (8 x 4096 tokens of 8 heads of 128 in 8 bits to bf16: 38 us, 49 with 32).
+    const int64_t turns = (a.c.rows * parts / per + sm_count() * 24 - 1) / (sm_count() * 24);
+    a.run = (int)std::min<int64_t>(32, std::min<int64_t>(read ? 8 : 32, std::max<int64_t>(1, turns)) * per);
     const int64_t block_rows = (int64_t)kWarps * a.run;
     const dim3 grid((unsigned)((a.c.rows + block_rows - 1) / block_rows), (unsigned)parts);
     return read ? kv_launch(kv_read_kernel<T, U4, W>, grid, kWarps * 32, 0, s, a)
