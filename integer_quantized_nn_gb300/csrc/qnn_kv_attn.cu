@@ -43,9 +43,10 @@ constexpr int kJoinWarps = 8;
 
 // Block (x, y) joins up to 8 rows of the item that begins in block x's share and ends in a later
 // one's, if there is one.  Where fewer rows are left than warps, several warps have a row: each joins
-// every so manieth part, the first of them what all have (a row with 38 parts: 12 us, 21 with one warp).  Lane k has the statistics of a warp's part k
-// (and k + 32, ..), all lanes the channels.  A chain of reads that wait for one another is all that takes
-// time here, so only the record is waited for before the first parts are asked for.
+// every so manieth part, the first of them what all have (38 parts a row, cold: 9.5 us, 21 with one
+// warp).  Lane k has the statistics of a warp's part k (and k + 32, ..), all lanes the channels.  A chain of
+// reads that wait for one another is all that takes time here, so only the record is waited for
+// before the first parts are asked for.
 template <int V>  // channels of a lane: 2, 4 or 8
 __global__ void __launch_bounds__(kJoinWarps * 32) kv_attn_join_kernel(const __grid_constant__ KvAttnArgs a, int rows)
 {
