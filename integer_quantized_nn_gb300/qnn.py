@@ -176,6 +176,17 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+def _packed(t, size: int, what: str) -> Optional[int]:
+    """The address of a tensor that the library reads as packed elements of `size` bytes (an int32
+    tensor's, where that is 4): a slice of wider rows, or integers of another size, would be read as
+    other numbers, which may well be valid ones."""
+    if t is None:
+        return None
+    if t.element_size() != size or t.is_floating_point() or not t.is_contiguous():
+        raise QnnError(QNN_ERR_INVALID_ARG, f"{what} must be contiguous, of {8 * size}-bit integers")
+    return t.data_ptr()
+
+
 def _nbytes(t) -> int:
     return int(t.numel()) * int(t.element_size())
 
@@ -527,8 +538,12 @@ def qnn_kv_page_bytes(g: KvGeom) -> int:
 def kv_seqs(pages, table, lens, rows: int, tokens: int, starts=None) -> KvSeqs:
     """The sequences of a call: pages uint8 [num_pages, qnn_kv_page_bytes(g)], table int32
     [batch, most pages], lens int32 [batch], starts int32 [batch + 1] or None (`tokens` rows
-    each).  Holds the tensors' addresses only: keep the tensors alive as long as it is used."""
-    return KvSeqs(_ptr(pages), int(pages.shape[0]), _ptr(table), int(table.shape[1]), _ptr(lens), _ptr(starts),
+    each); all contiguous.  Holds the tensors' addresses only: keep the tensors alive as long as it is used."""
+    for t, n, what in ((lens, table.shape[0], "lens"), (starts, table.shape[0] + 1, "starts")):
+        if t is not None and t.numel() < n:
+            raise QnnError(QNN_ERR_INVALID_ARG, f"kv_seqs: {what} of a batch of {table.shape[0]} has {n} entries")
+    return KvSeqs(_packed(pages, 1, "kv_seqs: pages"), int(pages.shape[0]), _packed(table, 4, "kv_seqs: table"),
+                  int(table.shape[1]), _packed(lens, 4, "kv_seqs: lens"), _packed(starts, 4, "kv_seqs: starts"),
                   int(rows), int(table.shape[0]), int(tokens))
 
 
@@ -547,10 +562,13 @@ def q_kv_read(k, v, x_dt: str, g: KvGeom, seqs: KvSeqs, ld_k: int = 0, ld_v: int
 
 
 def q_kv_keep(g: KvGeom, seqs: KvSeqs, keep, n_keep, stream=None):
-    """keep: int32 [batch, most], ascending newest tokens of each sequence; n_keep: int32 [batch]."""
+    """keep: int32 [batch, most], ascending newest tokens of each sequence; n_keep: int32 [batch]; contiguous."""
     load()
-    _check(_SYMBOLS["q_kv_keep"](ctypes.byref(g), ctypes.byref(seqs), _ptr(keep), int(keep.shape[1]), _ptr(n_keep),
-                                 _stream(stream)), "q_kv_keep")
+    if keep.shape[0] < seqs.batch or n_keep.numel() < seqs.batch:
+        raise QnnError(QNN_ERR_INVALID_ARG, f"q_kv_keep: keep and n_keep of a batch of {seqs.batch}")
+    _check(_SYMBOLS["q_kv_keep"](ctypes.byref(g), ctypes.byref(seqs), _packed(keep, 4, "q_kv_keep: keep"),
+                                 int(keep.shape[1]), _packed(n_keep, 4, "q_kv_keep: n_keep"), _stream(stream)),
+           "q_kv_keep")
 
 
 def qnn_kv_attn_workspace_bytes(g: KvGeom, seqs: KvSeqs, heads_q: int) -> int:
@@ -560,12 +578,13 @@ def qnn_kv_attn_workspace_bytes(g: KvGeom, seqs: KvSeqs, heads_q: int) -> int:
 
 def q_kv_attn(q, x_dt: str, heads_q: int, g: KvGeom, seqs: KvSeqs, scale: float, out, workspace, mask=None, lse=None,
               ld_q: int = 0, ld_out: int = 0, stream=None):
-    """Attention of q [rows, heads_q, D] over the cache into out; mask: int32 [rows, words], bits of
-    the newest tokens that a row sees (None: up to itself); workspace: uint8 device tensor of
+    """Attention of q [rows, heads_q, D] over the cache into out; mask: int32 [rows, words], contiguous, bits
+    of the newest tokens that a row sees (None: up to itself); workspace: uint8 device tensor of
     qnn_kv_attn_workspace_bytes(g, seqs, heads_q) bytes; lse: fp32 [rows, heads_q] or None."""
     load()
     _check(_SYMBOLS["q_kv_attn"](_ptr(q), DTYPES[x_dt], int(ld_q), int(heads_q), ctypes.byref(g), ctypes.byref(seqs),
-                                 float(scale), _ptr(mask), 0 if mask is None else int(mask.shape[-1]), _ptr(out),
+                                 float(scale), _packed(mask, 4, "q_kv_attn: mask"),
+                                 0 if mask is None else int(mask.shape[-1]), _ptr(out),
                                  int(ld_out), _ptr(lse), _ptr(workspace), _nbytes(workspace), _stream(stream)),
            "q_kv_attn")
 

@@ -131,6 +131,38 @@ def test_workspace_sizes(lib):
     assert size(heads_q=3) == size(heads_q=0) == size(heads_q=-2) == 0
 
 
+def test_binding_refuses_tensors_that_would_be_read_as_others(lib):
+    """Columns of a wider table, 64-bit integers (torch's default): their entries are not where, or what, the
+    library would read, and some may be pages of other sequences."""
+    t = pytest.importorskip("torch")
+    pages = t.zeros((6, 64), dtype=t.uint8)
+    table, lens, starts = (t.zeros(n, dtype=t.int32) for n in ((3, 4), (3,), (4,)))
+    s = qnn.kv_seqs(pages, table, lens, 3, 1, starts=starts)
+    assert (s.table, s.ld_table, s.batch, s.num_pages) == (table.data_ptr(), 4, 3, 6)
+    assert qnn.kv_seqs(pages[2:], table[1:], lens[1:], 2, 1).table == table.data_ptr() + 16
+    assert qnn.kv_seqs(pages, table[:1, :2], lens[:1], 1, 1).ld_table == 2  # one row of it is packed
+
+    def refused(what, call, *args, **kwargs):
+        with pytest.raises(qnn.QnnError, match=what) as e:
+            call(*args, **kwargs)
+        assert e.value.status == INVALID
+    for name, bad in (("table", table[:, :2]), ("table", table.long()), ("table", t.zeros((4, 3), dtype=t.int32).T),
+                      ("table", table.float()), ("table", table.to(t.int16)), ("lens", lens.long()),
+                      ("lens", t.zeros(6, dtype=t.int32)[::2]), ("lens", lens[:2]), ("starts", starts.long()),
+                      ("starts", t.zeros(8, dtype=t.int32)[::2]), ("starts", starts[:3]), ("pages", pages[:, :32]),
+                      ("pages", pages[::2]), ("pages", pages.to(t.int32))):
+        a = {**dict(pages=pages, table=table, lens=lens, starts=starts), name: bad}
+        refused(name, qnn.kv_seqs, a["pages"], a["table"], a["lens"], 3, 1, starts=a["starts"])
+    keep, n_keep = t.zeros((3, 4), dtype=t.int32), t.zeros(3, dtype=t.int32)
+    for name, k, n in (("keep", keep[:, :2], n_keep), ("keep", keep.long(), n_keep), ("n_keep", keep, n_keep.long()),
+                       ("n_keep", keep, t.zeros(6, dtype=t.int32)[::2]), ("batch", keep[:2], n_keep),
+                       ("batch", keep, n_keep[:2])):
+        refused(name, qnn.q_kv_keep, geom(), s, k, n, stream=0)
+    x = t.zeros(4, dtype=t.bfloat16)
+    for bad in (t.zeros((3, 4), dtype=t.int32)[:, :2], t.zeros((3, 4), dtype=t.int64), t.zeros((3, 4))):
+        refused("mask", qnn.q_kv_attn, x, "bf16", 4, geom(), s, 0.1, x, x, mask=bad, stream=0)
+
+
 @pytest.mark.parametrize("name, struct", [("qnn_kv_geom", qnn.KvGeom), ("qnn_kv_seqs", qnn.KvSeqs)])
 def test_structs_match_header(tmp_path, name, struct):
     cc = shutil.which("gcc") or shutil.which("cc")
