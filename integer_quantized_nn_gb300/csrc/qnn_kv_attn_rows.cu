@@ -325,8 +325,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
     grid_dependency_launch();
     grid_dependency_wait();
 
+    // Nothing for the join until an item's parts are stored: it trusts the record, and a block whose waits gave up
+    // must not leave it what an earlier call, or nobody, wrote there.  (attn_sums has a barrier behind this.)
+    if (threadIdx.x == 0) attn_record(a, -1, 0, 0, 0, 0);
     const AttnShare share(attn_sums<kThreads>(a, sums, ROWS), a.blocks, blockIdx.x);
-    if (threadIdx.x == 0 && share.from >= share.to) attn_record(a, -1, 0, 0, 0, 0);
     const int chunks = (int)(share.to - share.from);
 
     bool ok = true;
@@ -621,11 +623,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             const int width = min(kRows, at.T * a.group - row0);
             const int rr = row0 + r;
             const bool live = r < width, starts_here = n > 0 || at.chunk == 0, ends_here = at.chunk + count == at.units;
-            if (threadIdx.x == kRowWarp0 * 32 && n + count == chunks) {
-                const int tile0 = at.rt * ROWS;
-                attn_record(a, starts_here && !ends_here ? share.block_of(share.from + n - at.chunk + at.units - 1) : -1,
-                            at.first, tile0, min(ROWS, at.T * a.group - tile0), at.h);
-            }
             const int64_t out_row = at.first + rr / a.group;
             const int hq = at.h * a.group + rr % a.group;
 
@@ -843,7 +840,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 }
             }
             tc_fence_before();  // O has been read before q_full says so
-            meet();
+            const bool stored = all_ok();
+            if (stored && threadIdx.x == kRowWarp0 * 32 && starts_here && !ends_here) {
+                const int tile0 = at.rt * ROWS;
+                attn_record(a, share.block_of(share.from + n - at.chunk + at.units - 1), at.first, tile0,
+                            min(ROWS, at.T * a.group - tile0), at.h);
+            }
             release(item_empty[(unsigned)item % kItems]);
             n += count;
             ++item;
