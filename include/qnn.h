@@ -710,8 +710,9 @@ const char *qnn_status_string(qnn_status s);
 qnn_status qnn_check_device_error(qnn_stream_t stream);
 
 /* Launches one block that waits on a barrier nothing arrives at, giving up
- * after `limit_ns` nanoseconds (<= 1e9) the way every kernel wait gives up:
- * sets the device status word and returns.  For testing the timeout path. */
+ * after `limit_ns` nanoseconds (<= 1e9), and once more, the two ways in which
+ * kernel waits give up (by the clock, by a count of probes): sets the device
+ * status word and returns.  For testing the timeout path. */
 qnn_status qnn_selftest_wait_timeout(uint64_t limit_ns, qnn_stream_t stream);
 
 #ifdef __cplusplus

@@ -56,7 +56,7 @@ int sm_count()
 }
 
 namespace {
-// One block: thread 0 waits on a barrier that nothing ever arrives at.
+// One block: thread 0 waits on a barrier that nothing ever arrives at, by the clock and then by counting.
 __global__ void wait_timeout_kernel(uint32_t *status, uint64_t limit_ns)
 {
     __shared__ __align__(8) uint64_t bar;
@@ -64,7 +64,8 @@ __global__ void wait_timeout_kernel(uint32_t *status, uint64_t limit_ns)
     if (threadIdx.x == 0) {
         mbar_init(b, 1);
         fence_mbar_init();
-        (void)mbar_wait_slow(b, 0, status, limit_ns);
+        if (!mbar_wait_slow(b, 0, nullptr, limit_ns))
+            (void)mbar_wait_short(b, 0, status, (uint32_t)(limit_ns / kProbeNs) + 1);
     }
 }
 }  // namespace

@@ -127,13 +127,16 @@ __device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity, ui
 }
 
 // The same bounded wait by counting: a tenth of the code and no clock to read, for kernels whose
-// loops fill the instruction cache.  A probe takes 20 cycles at least, so the limit is a second or more.
-constexpr uint32_t kWaitLimitProbes = 1u << 27;
+// loops fill the instruction cache.  A probe of a phase that does not complete suspends the thread for
+// 3.94 us (4 to 65536 of them, of 1, 2 or 16 warps at once: 3.942 to 3.960 us each), so the limit is two
+// seconds.
+constexpr uint32_t kProbeNs = 3942, kWaitLimitProbes = 1u << 19;
 
-__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, uint32_t *status)
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, uint32_t *status,
+                                                uint32_t limit = kWaitLimitProbes)
 {
 #pragma unroll 1
-    for (uint32_t i = 0; i < kWaitLimitProbes; ++i)
+    for (uint32_t i = 0; i < limit; ++i)
         if (mbar_try_wait(bar, parity)) return true;
     if (status) atomicOr(status, kStatusTimeout);
     return false;

@@ -305,3 +305,17 @@ def test_a_captured_mixed_batch():
         near(out.double().cpu().numpy().reshape(w_out.shape), w_out, t_out, "out")
         near(lse.double().cpu().numpy(), w_lse, t_lse, "lse")
     assert qnn.qnn_check_device_error() == OK
+
+
+def test_both_kinds_of_wait_give_up_when_they_should():
+    """One by the clock, one by counting probes, 40 ms each: neither much before nor long after."""
+    t = torch()
+    qnn.qnn_selftest_wait_timeout(1000)
+    assert qnn.qnn_check_device_error() == qnn.QNN_ERR_TIMEOUT
+    start, end = (t.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    qnn.qnn_selftest_wait_timeout(40_000_000)
+    end.record()
+    assert qnn.qnn_check_device_error() == qnn.QNN_ERR_TIMEOUT
+    assert 60 < start.elapsed_time(end) < 160
+    assert qnn.qnn_check_device_error() == OK

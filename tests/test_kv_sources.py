@@ -37,3 +37,11 @@ def test_the_other_kernel_has_no_wait_that_gives_up():
     """It always comes to where it writes its record: one for a block without a share, one for every other."""
     s = source("qnn_kv_attn_few.cu")
     assert "mbar" not in s and s.count("attn_record(") == 2
+
+
+def test_waits_by_counting_end_within_seconds():
+    """2^19 probes of 3.94 us each; the self-test of a wait that runs out times that many nanoseconds."""
+    s = source("qnn_ptx.cuh")
+    probe, shift = re.search(r"kProbeNs = (\d+), kWaitLimitProbes = 1u << (\d+);", s).groups()
+    assert 1e9 <= int(probe) * 2 ** int(shift) <= 4e9
+    assert "uint32_t limit = kWaitLimitProbes" in s and "mbar_wait_short(b, 0, status, " in source("qnn_api.cu")
