@@ -167,8 +167,8 @@ __device__ __forceinline__ uint32_t seen_bits(const KvAttnArgs &a, const Item &c
 // those of the positions that row t sees; sums_still: waits until no product adds to the sums.
 template <bool MASKED, int DP, typename F>
 __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, uint32_t scales, const uint32_t (&bits)[4], int j,
-                                        bool first, float ratio, const float (&cr)[2], float (&m)[2], float (&ref)[2],
-                                        float (&l)[2], const F &sums_still)
+                                        bool first, float ratio, const float (&cr)[2], float (&m)[2], float (&l)[2],
+                                        const F &sums_still)
 {
     const int g = (threadIdx.x & 31) >> 2;
     uint32_t b[2][4], p[32];
@@ -179,7 +179,8 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, uint32_t s
             for (int w = 0; w < 4; ++w) b[q][w] = __shfl_sync(0xffffffffu, bits[w], 8 * q + g) >> (2 * j);
     }
     // The maxima so far are tried first: a thread's 32 weights of a row whose sum stays below 2^8 are
-    // all below it.  New maxima are looked for where they do not, at first and with a new unit.
+    // all below it.  New maxima are looked for where they do not, at first and with a new unit.  A row that has
+    // seen nothing yet has the maximum -inf: its weights are infinite, so that they do not, or hidden.
     bool fresh = MASKED || first || ratio != 1.0f;
     float2 s[2];
 #pragma unroll 1
@@ -212,7 +213,6 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, uint32_t s
                 const float u = fmaxf(m[q], top[q]);
                 f[q] = m[q] == -INFINITY ? 0.0f : ex2(m[q] - u);
                 m[q] = u;
-                ref[q] = u == -INFINITY ? 0.0f : u;
                 l[q] *= f[q], f[q] *= ratio;
             }
             if (!first && __any_sync(0xffffffffu, f[0] != 1.0f || f[1] != 1.0f)) {
@@ -238,7 +238,7 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, uint32_t s
             const uint32_t bit = 1u << (8 * (i & 3));
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                float2 y = fma2(mul2(as_f2(v[4 * i + 2 * q], v[4 * i + 2 * q + 1]), k), both(cr[q]), both(-ref[q]));
+                float2 y = fma2(mul2(as_f2(v[4 * i + 2 * q], v[4 * i + 2 * q + 1]), k), both(cr[q]), both(-m[q]));
                 y.x = ex2(y.x), y.y = ex2(y.y);
                 if constexpr (MASKED) {
                     y.x = b[q][i >> 2] & bit ? y.x : 0.0f;
@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             meet();
             // of rows q = 0, 1 of this thread, in both streams
             const int own = 32 * (warp & 3) + 16 * part + g, steps = PAIR ? 2 * count : count;
-            float cr[2][2], m[2][2], ref[2][2], l[2][2], unit[SPLIT ? 2 : 1];  // PAIR: the same of both
+            float cr[2][2], m[2][2], l[2][2], unit[SPLIT ? 2 : 1];  // PAIR: the same of both
             int seen_by_all[2];
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 for (int q = 0; q < 2; ++q) {
                     cr[st][q] = row_c[PAIR ? st : 0][own + 8 * q];
                     m[st][q] = -INFINITY;
-                    ref[st][q] = l[st][q] = 0.0f;
+                    l[st][q] = 0.0f;
                 }
                 if (st == 0 || SPLIT) unit[st] = pow2i(-126);
                 const int t_first = min((at.rt * ROWS + (PAIR ? st * kRows : 0)) / a.group, at.T - 1);
@@ -740,15 +740,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                     }
                 };
                 // by selection and not by index: the arrays stay in registers
-                float sc[2], sm[2], sr[2], sl[2];
+                float sc[2], sm[2], sl[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     sc[q] = own_state ? cr[1][q] : cr[0][q], sm[q] = own_state ? m[1][q] : m[0][q];
-                    sr[q] = own_state ? ref[1][q] : ref[0][q], sl[q] = own_state ? l[1][q] : l[0][q];
+                    sl[q] = own_state ? l[1][q] : l[0][q];
                 }
                 if (pos0 <= (stream ? seen_by_all[1] : seen_by_all[0]) && there == 0xffu) {
                     const uint32_t none[4] = {};
-                    weights<false, DP>(s_at, o_at, scales, none, j, step < (ONE ? 1 : 2), ratio, sc, sm, sr, sl, sums_still);
+                    weights<false, DP>(s_at, o_at, scales, none, j, step < (ONE ? 1 : 2), ratio, sc, sm, sl, sums_still);
                 } else {
                     uint32_t bits[4];
                     const int row = at.rt * ROWS + (PAIR ? stream * kRows : 0) + 32 * (warp & 3) + 16 * part + (lane & 15);
@@ -758,12 +758,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                         bits[w] = seen_bits(a, at, t, pos0 + 32 * w) &
                                   ((there >> (2 * w) & 1u ? 0xffffu : 0u) | (there >> (2 * w + 1) & 1u ? 0xffff0000u : 0u));
                     __syncwarp();
-                    weights<true, DP>(s_at, o_at, scales, bits, j, step < (ONE ? 1 : 2), ratio, sc, sm, sr, sl, sums_still);
+                    weights<true, DP>(s_at, o_at, scales, bits, j, step < (ONE ? 1 : 2), ratio, sc, sm, sl, sums_still);
                 }
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    if (own_state) m[1][q] = sm[q], ref[1][q] = sr[q], l[1][q] = sl[q];
-                    else m[0][q] = sm[q], ref[0][q] = sr[q], l[0][q] = sl[q];
+                    if (own_state) m[1][q] = sm[q], l[1][q] = sl[q];
+                    else m[0][q] = sm[q], l[0][q] = sl[q];
                 }
                 if (SPLIT && stream) unit[SPLIT ? 1 : 0] = infos[slot].unit;
                 else unit[0] = infos[slot].unit;

@@ -319,3 +319,25 @@ def test_both_kinds_of_wait_give_up_when_they_should():
     assert qnn.qnn_check_device_error() == qnn.QNN_ERR_TIMEOUT
     assert 60 < start.elapsed_time(end) < 160
     assert qnn.qnn_check_device_error() == OK
+
+
+@pytest.mark.parametrize("tokens, D, kv", [(1, 32, "s8"), (20, 32, "s8"), (130, 64, "u4"), (40, 160, "s8")])
+def test_first_pages_that_are_not_there(tokens, D, kv):
+    """The first 128 tokens have no pages, and V is zero for a while behind them: that is reported, and the rest
+    is attended to, tokens of zero V too.  Of so many heads that a block has several chunks of most of them."""
+    t = torch()
+    rng = np.random.default_rng(D + tokens)
+    c = _kv.Cache(rng, [900], [tokens], 160, D, 16, kv, "bf16")
+    there = _kv.Cache(rng, [772], [tokens], 160, D, 16, kv, "bf16")
+    q = rng.normal(0, 1.5, size=(tokens, 160, D))
+    for zero in (640, 900):
+        c.v[0][128:zero] = 0
+        d = Dev(c)
+        q = d.floats(q).double().cpu().numpy()
+        d.table[0, :8] = t.tensor([-1, c.num_pages, -5, 2 ** 31 - 1] * 2, dtype=t.int32)
+        out, lse = d.attend(q, D ** -0.5)
+        assert qnn.qnn_check_device_error() == qnn.QNN_ERR_INVALID_ARG
+        there.k, there.v = [c.k[0][128:]], [c.v[0][128:]]
+        w_out, w_lse, t_out, t_lse = _kv.attention(there, q, D ** -0.5)
+        near(out, w_out, t_out, "out")
+        near(lse, w_lse, t_lse, "lse")
