@@ -112,6 +112,20 @@ __device__ __forceinline__ void u4_pairs(uint32_t w, const Zero &z, uint32_t (&r
 // 2^k as fp32, -126 <= k <= 127
 __device__ __forceinline__ float pow2i(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
 
+// A row of q is brought near f16's largest by a power of two, 2^-113 .. 2^141 for 16-bit types, in two exact
+// steps; its inverse multiplies K's scales (which have the call's scale in them), a subnormal at the least, and
+// their product the sums: so nothing on the way is far from the scores or from what K's scales are.
+struct RowUnit {
+    float up0, up1, down;
+    __device__ __forceinline__ explicit RowUnit(float top)  // the row's largest
+    {
+        const int e2 = (int)(__float_as_uint(top) >> 23), k = top == 0.0f || e2 == 255 ? 0 : 14 + 127 - e2;
+        up0 = pow2i(k >> 1), up1 = pow2i(k - (k >> 1));
+        down = pow2i(-(k >> 1)) * pow2i((k >> 1) - k);
+    }
+    __device__ __forceinline__ float up(float v) const { return v * up0 * up1; }
+};
+
 // The units that a tile of `width` rows, number rt, sees of a sequence; one at least, so that
 // rows that see nothing are written too.
 __device__ __forceinline__ int attn_units(const KvAttnArgs &a, int T, int len, int rt, int width)

@@ -250,24 +250,21 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
                     }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int e2 = (int)(__float_as_uint(top) >> 23);
-                const int k = top == 0.0f || e2 == 255 ? 0 : max(-126, min(126, 14 + 127 - e2));
-                const float up = pow2i(k);
+                const RowUnit by(top);
 #pragma unroll
                 for (int s = 0; s < S::kSteps; ++s) {
-                    const __half2 lo = __floats2half2_rn(v[s][0] * up, v[s][1] * up);
-                    const __half2 hi = __floats2half2_rn(v[s][2] * up, v[s][3] * up);
+                    const __half2 lo = __floats2half2_rn(by.up(v[s][0]), by.up(v[s][1]));
+                    const __half2 hi = __floats2half2_rn(by.up(v[s][2]), by.up(v[s][3]));
                     const uint32_t b0 = *reinterpret_cast<const uint32_t *>(&lo);
                     const uint32_t b1 = *reinterpret_cast<const uint32_t *>(&hi);
                     if constexpr (S::kQRegs) qf[nt][s][0] = b0, qf[nt][s][1] = b1;
                     else q_smem[(nt * S::kSteps + s) * 32 + lane] = make_uint2(b0, b1);
                 }
-                const float cr = a.scale_log2 * pow2i(-k);
                 if constexpr (S::kQRegs) {
-                    cq[nt][0] = __shfl_sync(0xffffffffu, cr, 8 * j);
-                    cq[nt][1] = __shfl_sync(0xffffffffu, cr, 8 * j + 4);
+                    cq[nt][0] = __shfl_sync(0xffffffffu, by.down, 8 * j);
+                    cq[nt][1] = __shfl_sync(0xffffffffu, by.down, 8 * j + 4);
                 } else if (j == 0) {
-                    stats[0][8 * nt + g][0] = cr;
+                    stats[0][8 * nt + g][0] = by.down;
                 }
             }
         }
@@ -343,8 +340,8 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
                     }
                 }
                 // scores in units of log2; s[.][0, 1]: token g, rows 2j, 2j + 1; [2, 3]: token g + 8
-                const float sk0 = __uint_as_float(U4 ? wk0 & 0xffff0000u : wk0);
-                const float sk1 = __uint_as_float(U4 ? wk1 & 0xffff0000u : wk1);
+                const float sk0 = __uint_as_float(U4 ? wk0 & 0xffff0000u : wk0) * a.scale_log2;
+                const float sk1 = __uint_as_float(U4 ? wk1 & 0xffff0000u : wk1) * a.scale_log2;
                 float sv0 = __uint_as_float(U4 ? wv0 & 0xffff0000u : wv0);
                 float sv1 = __uint_as_float(U4 ? wv1 & 0xffff0000u : wv1);
                 bool over = false;

@@ -46,7 +46,7 @@ struct Tile16 {
 };
 constexpr int kPlaces = 8;
 
-// Of a chunk: scales of K, and of V over the stream's unit, for two tokens together (k k v v).
+// Of a chunk: scales of K times the call's, and of V over the stream's unit, for two tokens together (k k v v).
 struct Info {
     float scales[kTokens / 2][4];
     float ratio, unit;  // the unit before over this one; this one
@@ -197,7 +197,7 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, uint32_t s
                 const uint32_t bit = 1u << (8 * (i & 3));
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    float2 y = mul2(as_f2(v[4 * i + 2 * q], v[4 * i + 2 * q + 1]), k);
+                    float2 y = mul2(as_f2(v[4 * i + 2 * q], v[4 * i + 2 * q + 1]), mul2(k, both(cr[q])));
                     if constexpr (MASKED) {
                         y.x = b[q][i >> 2] & bit ? y.x : -INFINITY;
                         y.y = b[q][i >> 2] & (2 * bit) ? y.y : -INFINITY;
@@ -209,7 +209,6 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, uint32_t s
             for (int q = 0; q < 2; ++q) {
                 top[q] = fmaxf(top[q], __shfl_xor_sync(0xffffffffu, top[q], 1));
                 top[q] = fmaxf(top[q], __shfl_xor_sync(0xffffffffu, top[q], 2));
-                if (top[q] != -INFINITY) top[q] *= cr[q];
                 const float u = fmaxf(m[q], top[q]);
                 f[q] = m[q] == -INFINITY ? 0.0f : ex2(m[q] - u);
                 m[q] = u;
@@ -238,7 +237,7 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, uint32_t s
             const uint32_t bit = 1u << (8 * (i & 3));
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                float2 y = fma2(mul2(as_f2(v[4 * i + 2 * q], v[4 * i + 2 * q + 1]), k), both(cr[q]), both(-m[q]));
+                float2 y = fma2(as_f2(v[4 * i + 2 * q], v[4 * i + 2 * q + 1]), mul2(k, both(cr[q])), both(-m[q]));
                 y.x = ex2(y.x), y.y = ex2(y.y);
                 if constexpr (MASKED) {
                     y.x = b[q][i >> 2] & bit ? y.x : 0.0f;
@@ -497,6 +496,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[e] = s[e] * per * (float)(1 << kAttnRoom);
                 if (lane == 0) info.ratio = old * per, info.unit = now, info.present = there;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] *= a.scale_log2;
             }
             *reinterpret_cast<float2 *>(info.scales[2 * lane] + 2 * is_v) = make_float2(s[0], s[1]);
             *reinterpret_cast<float2 *>(info.scales[2 * lane + 1] + 2 * is_v) = make_float2(s[2], s[3]);
@@ -674,10 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                     for (int e = 0; e < E; ++e) {
                         const int own = r0 + 8 * (e0 + e);
                         const float most = PAIR ? top[e] : fmaxf(row_top[0][own], row_top[1][own]);
-                        const int e2 = (int)(__float_as_uint(most) >> 23);
-                        const int k = most == 0.0f || e2 == 255 ? 0 : max(-126, min(126, 14 + 127 - e2));
-                        const float up = a.scale_log2 < 0.0f ? -pow2i(k) : pow2i(k);  // row_c >= 0
-                        if (quad == 0 && (PAIR || part == 0)) row_c[part][own] = fabsf(a.scale_log2) * pow2i(-k);
+                        const RowUnit by(most);
+                        if (quad == 0 && (PAIR || part == 0)) row_c[part][own] = by.down;
 #pragma unroll
                         for (int i = 0; i < W; ++i) {
                             const int piece = quad + 4 * i, chunk = (PAIR ? 0 : part * (mine / 8)) + piece;
@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                                 // the order in which codes are unpacked: u4 0 4, 1 5, 2 6, 3 7
                                 const float lo = U4 ? value(u[x / 2], x & 1) : value(u[x], 0);
                                 const float hi = U4 ? value(u[2 + x / 2], x & 1) : value(u[x], 1);
-                                const __half2 h = __floats2half2_rn(lo * up, hi * up);
+                                const __half2 h = __floats2half2_rn(by.up(lo), by.up(hi));
                                 f[x] = *reinterpret_cast<const uint32_t *>(&h);
                             }
                             if (8 * piece < mine)

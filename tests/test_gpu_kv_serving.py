@@ -341,3 +341,15 @@ def test_first_pages_that_are_not_there(tokens, D, kv):
         w_out, w_lse, t_out, t_lse = _kv.attention(there, q, D ** -0.5)
         near(out, w_out, t_out, "out")
         near(lse, w_lse, t_lse, "lse")
+
+
+@pytest.mark.parametrize("size_q, size_k", [(1e-36, 1e36), (1e36, 1e-36), (1e-38, 1e37), (1e-30, 1e30)])
+@pytest.mark.parametrize("tokens, D", [(3, 64), (3, 128), (20, 64), (40, 128), (20, 256)])
+def test_keys_and_queries_at_the_ends_of_the_range(tokens, D, size_q, size_k):
+    """Scores of ordinary size from keys and queries whose products with anything else would not fit fp32."""
+    rng = np.random.default_rng(D + tokens)
+    c = _kv.Cache(rng, [300, 45], [tokens, 2], 1, D, 16, "s8", "bf16")
+    c.k = [_kv.bf16(k * size_k) for k in c.k]
+    q = rng.normal(0, 1, size=(c.rows, 4, D)) * size_q
+    for scale in (D ** -0.5, -0.02, 3.0):
+        check(c, Dev(c), 4, q=q, scale=scale)
