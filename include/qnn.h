@@ -687,8 +687,9 @@ size_t qnn_kv_attn_workspace_bytes(const qnn_kv_geom *g, const qnn_kv_seqs *seqs
  * q enters the products as f16, each row scaled by a power of two that brings its largest value
  * near f16's, so that bf16 keeps its 8 bits (values below 2^-30 of the row's largest lose
  * some); |scale| max|k| and D |scale| max|q| max|k|, of a row and a token that it sees, must fit
- * fp32; weights e^x, with V's scales in them, are f16 too; all sums are fp32, their order set by the
- * sizes and lengths: equal calls give equal bits.  heads_q / heads is at most 1024 (QNN_ERR_INVALID_ARG), and tokens times that at
+ * fp32; weights e^x times V's scales are f16 too (2^-11 of each, or 2^-31 of the largest scale that
+ * the row sees); all sums are fp32, their order set by the sizes and lengths: equal calls give equal
+ * bits.  heads_q / heads is at most 1024 (QNN_ERR_INVALID_ARG), and tokens times that at
  * most 2^31 - 257 (QNN_ERR_UNSUPPORTED).
  * q's rows must start on multiples of 16 bytes (ld_q a multiple of 8), out's too.
  * workspace: device scratch of qnn_kv_attn_workspace_bytes bytes, 16-byte aligned,

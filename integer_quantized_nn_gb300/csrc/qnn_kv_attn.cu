@@ -14,14 +14,12 @@ struct Joined {
     // what there is, in a larger maximum and unit
     __device__ __forceinline__ void move(float new_top, float new_unit)
     {
-        const float f = top == new_top ? 1.0f : ex2(top - new_top), g = f * (unit * per(new_unit));
+        const float f = top == new_top ? 1.0f : ex2(top - new_top), g = f * (unit * pow2_inverse(new_unit));
         total *= f;
 #pragma unroll
         for (int e = 0; e < V; ++e) sum[e] *= g;
         top = new_top, unit = new_unit;
     }
-    // 1 / unit: of powers of two, so that a product with it is exact
-    static __device__ __forceinline__ float per(float unit) { return __uint_as_float(0x7f000000u - __float_as_uint(unit)); }
 };
 
 template <int V>
@@ -87,7 +85,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_attn_join_kernel(const __g
         if (lane < here) {
             const float *p = part(i0 + lane) + (int64_t)rows * channels;
             const float2 ml = *reinterpret_cast<const float2 *>(p + 2 * row);
-            m = ml.x, l = ml.y, u = p[2 * rows];
+            m = ml.x, l = ml.y, u = p[2 * rows + row];
         }
         ask(0);
         float top = fmaxf(j.top, m), unit = fmaxf(j.unit, u);
@@ -97,7 +95,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_attn_join_kernel(const __g
             unit = fmaxf(unit, __shfl_xor_sync(0xffffffffu, unit, b));
         }
         j.move(top, unit);
-        const float f = m == top ? 1.0f : ex2(m - top), g = lane < here ? f * (u * j.per(unit)) : 0.0f;
+        const float f = m == top ? 1.0f : ex2(m - top), g = lane < here ? f * (u * pow2_inverse(unit)) : 0.0f;
         float t = lane < here ? l * f : 0.0f;
 #pragma unroll
         for (int b = 16; b > 0; b /= 2) t += __shfl_xor_sync(0xffffffffu, t, b);

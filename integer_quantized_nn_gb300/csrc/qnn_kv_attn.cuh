@@ -31,16 +31,18 @@ struct KvAttnArgs {
 // goes on behind it: attn_record), then two
 // slots of parts: slot 0 for an item that began in an earlier block, slot 1 for one that begins
 // here and goes on.  A slot: [rows][channels] sums, then for each row the maximum and the sum of
-// weights, then the unit of V's scales.
+// weights, then for each row the unit of V's scales.
 constexpr int kAttnRecord = 8, kAttnChunk = 128;
 
 // Weights are p * (scale of V / unit) * 2^kAttnRoom in f16: p <= 2^kAttnSlack, as maxima move only when a
-// score passes them by more, and scale <= unit, so that they stay below 2^16; the unit is a power
-// of two no smaller than any scale so far.
+// score passes them by more, and scale <= unit, so that they stay below 2^16; a row's unit is a power
+// of two no smaller than any scale that the row has seen so far: the tokens that are hidden from it have no
+// part in it.  Rows differ in what they see only at the end of an item, and their units are one until a token there
+// that some rows do not see has a scale above it; then each has its own.
 constexpr int kAttnSlack = 8, kAttnRoom = 7;
 constexpr float kAttnWeightUnit = 1.0f / (1 << kAttnRoom);
 
-__host__ __device__ inline int64_t attn_slot_floats(int rows, int channels) { return (int64_t)rows * (channels + 2) + 16; }
+__host__ __device__ inline int64_t attn_slot_floats(int rows, int channels) { return (int64_t)rows * (channels + 3); }
 
 __device__ __forceinline__ float *attn_slot(const KvAttnArgs &a, int block, int slot, int rows, int channels)
 {
@@ -111,6 +113,10 @@ __device__ __forceinline__ void u4_pairs(uint32_t w, const Zero &z, uint32_t (&r
 
 // 2^k as fp32, -126 <= k <= 127
 __device__ __forceinline__ float pow2i(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
+
+// Of a power of two from 2^-126 to 2^126, its inverse; the power of two that is no smaller than v, and 2^126 at most.
+__device__ __forceinline__ float pow2_inverse(float v) { return __uint_as_float(0x7f000000u - __float_as_uint(v)); }
+__device__ __forceinline__ float pow2_above(float v) { return __uint_as_float((__float_as_uint(v) + 0x7fffffu) & 0xff800000u); }
 
 // A row of q is brought near f16's largest by a power of two, 2^-113 .. 2^141 for 16-bit types, in two exact
 // steps; its inverse multiplies K's scales (which have the call's scale in them), a subnormal at the least, and

@@ -17,6 +17,7 @@
 // of 16 tokens (their K and V rows and words), filled by asynchronous copies; warps meet only
 // where an item ends.  Maxima move only when a score passes the warp's by 2^8 (the
 // weights have that room), which one vote a tile finds.
+#include <type_traits>
 #include "qnn_kv_attn.cuh"
 
 namespace qnn {
@@ -140,7 +141,8 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
     using S = Shape<U4, DP, NT>;
     const KvArgs &c = a.c;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float stats[kWarps][S::kRows][2], units_of[kWarps];
+    __shared__ float4 stats[kWarps][S::kRows];    // maximum, unit of V's scales, sum of weights
+    __shared__ float row_unit[kWarps][S::kRows];  // where they are apart
     __shared__ uint2 q_smem[S::kQRegs ? 1 : NT * S::kSteps * 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, j = lane & 3;
     const int stage_b = stage_bytes(c.row_bytes), ST = a.stages;
@@ -167,7 +169,8 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
         some = tile * 16 < ahead.len;
         if (some) entry = kv_entry(c, ahead.b, kv_page_index(c, tile, &in_page));
     };
-    uint32_t absent = 0;  // stages whose tile is not there
+    uint32_t absent = 0;  // stages whose tile is not there; kApart: the rows' units are in row_unit
+    constexpr uint32_t kApart = 1u << 31;
     auto ask = [&](int stage) {  // a group of copies, if only an empty one
         if (unasked > 0) {
             const int page = some ? kv_checked(c, entry) : -1;
@@ -264,19 +267,20 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
                     cq[nt][0] = __shfl_sync(0xffffffffu, by.down, 8 * j);
                     cq[nt][1] = __shfl_sync(0xffffffffu, by.down, 8 * j + 4);
                 } else if (j == 0) {
-                    stats[0][8 * nt + g][0] = by.down;
+                    stats[0][8 * nt + g].x = by.down;
                 }
             }
         }
         if constexpr (!S::kQRegs) {
             __syncthreads();
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) cq[nt][0] = stats[0][8 * nt + 2 * j][0], cq[nt][1] = stats[0][8 * nt + 2 * j + 1][0];
+            for (int nt = 0; nt < NT; ++nt) cq[nt][0] = stats[0][8 * nt + 2 * j].x, cq[nt][1] = stats[0][8 * nt + 2 * j + 1].x;
             __syncthreads();
         }
 
         float acc[NT][S::kSteps][4], m[NT][2], ref[NT][2], l[NT][2];
-        float unit = pow2i(-126), per_unit = pow2i(126);  // V's scales are taken in units of 2^k
+        float per_unit = pow2i(126);  // V's scales are taken in units of 2^k
+        absent &= ~kApart;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -290,170 +294,210 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
         const int seen_by_all = a.mask ? at.len - at.T : min(at.len, at.len - at.T + t_first + 1);
         const int seen_by_any = a.mask ? at.len : at.len - at.T + t_last + 1;
         int pos0 = (at.chunk * kWarps + warp) * 16;
-        for (int left = (int)(end - x); left > 0; --left, pos0 += kAttnChunk) {
-            copies_wait(ST - 1);
-            __syncwarp();
-            if (!(absent >> stage & 1u) && pos0 < seen_by_any) {
-                const uint32_t k_at = ring_at + stage * stage_b, w_at = k_at + 4 * eight;
-                // scales of K and V of tokens g and g + 8
-                const uint32_t wk0 = lds32(w_at + 4 * g), wk1 = lds32(w_at + 4 * g + 32);
-                const uint32_t wv0 = lds32(w_at + 64 + 4 * g), wv1 = lds32(w_at + 64 + 4 * g + 32);
-                float s[NT][4];
+        // The tiles of which every row sees all, then the others: a loop each, so that the first, where nearly all
+        // tiles are, is no longer than it must be.
+        auto tiles = [&](auto kind, int left) {
+            constexpr bool whole = decltype(kind)::value;
+#pragma unroll 1
+            for (; left > 0; --left) {
+                copies_wait(ST - 1);
+                __syncwarp();
+                if (!(absent >> stage & 1u) && (whole || pos0 < seen_by_any)) {
+                    const uint32_t k_at = ring_at + stage * stage_b, w_at = k_at + 4 * eight;
+                    // scales of K and V of tokens g and g + 8
+                    const uint32_t wk0 = lds32(w_at + 4 * g), wk1 = lds32(w_at + 4 * g + 32);
+                    const uint32_t wv0 = lds32(w_at + 64 + 4 * g), wv1 = lds32(w_at + 64 + 4 * g + 32);
+                    float s[NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
-                {
-                    uint32_t k0[S::kKWords], k1[S::kKWords];
-                    constexpr int step_w = S::kKWords < 4 ? S::kKWords : 4;
+                    for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+                    {
+                        uint32_t k0[S::kKWords], k1[S::kKWords];
+                        constexpr int step_w = S::kKWords < 4 ? S::kKWords : 4;
 #pragma unroll
-                    for (int w = 0; w < S::kKWords; w += step_w) {
-                        lds<step_w>(k_at + k_off[w / 4], k0 + w);
-                        lds<step_w>(k_at + k_off[w / 4] + eight, k1 + w);
-                    }
-                    const Zero z0 = zero_of(wk0 & 15u, wk0 & 15u), z1 = zero_of(wk1 & 15u, wk1 & 15u);
-#pragma unroll
-                    for (int w = 0; w < S::kKWords; ++w) {
-                        uint32_t f[U4 ? 2 : 1][4];
-                        if constexpr (U4) {
-                            uint32_t r0[4], r1[4];
-                            u4_pairs(k0[w], z0, r0);
-                            u4_pairs(k1[w], z1, r1);
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                f[e][0] = r0[2 * e], f[e][1] = r1[2 * e], f[e][2] = r0[2 * e + 1], f[e][3] = r1[2 * e + 1];
-                            }
-                        } else {
-                            s8_pairs(k0[w], f[0][0], f[0][2]);
-                            s8_pairs(k1[w], f[0][1], f[0][3]);
+                        for (int w = 0; w < S::kKWords; w += step_w) {
+                            lds<step_w>(k_at + k_off[w / 4], k0 + w);
+                            lds<step_w>(k_at + k_off[w / 4] + eight, k1 + w);
                         }
+                        const Zero z0 = zero_of(wk0 & 15u, wk0 & 15u), z1 = zero_of(wk1 & 15u, wk1 & 15u);
 #pragma unroll
-                        for (int e = 0; e < (U4 ? 2 : 1); ++e) {
-                            const int st = w * (U4 ? 2 : 1) + e;
+                        for (int w = 0; w < S::kKWords; ++w) {
+                            uint32_t f[U4 ? 2 : 1][4];
+                            if constexpr (U4) {
+                                uint32_t r0[4], r1[4];
+                                u4_pairs(k0[w], z0, r0);
+                                u4_pairs(k1[w], z1, r1);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                if constexpr (S::kQRegs) mma16816(s[nt], f[e], qf[nt][st][0], qf[nt][st][1]);
-                                else {
-                                    const uint2 b = q_smem[(nt * S::kSteps + st) * 32 + lane];
-                                    mma16816(s[nt], f[e], b.x, b.y);
+                                for (int e = 0; e < 2; ++e) {
+                                    f[e][0] = r0[2 * e], f[e][1] = r1[2 * e], f[e][2] = r0[2 * e + 1], f[e][3] = r1[2 * e + 1];
+                                }
+                            } else {
+                                s8_pairs(k0[w], f[0][0], f[0][2]);
+                                s8_pairs(k1[w], f[0][1], f[0][3]);
+                            }
+#pragma unroll
+                            for (int e = 0; e < (U4 ? 2 : 1); ++e) {
+                                const int st = w * (U4 ? 2 : 1) + e;
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    if constexpr (S::kQRegs) mma16816(s[nt], f[e], qf[nt][st][0], qf[nt][st][1]);
+                                    else {
+                                        const uint2 b = q_smem[(nt * S::kSteps + st) * 32 + lane];
+                                        mma16816(s[nt], f[e], b.x, b.y);
+                                    }
                                 }
                             }
                         }
                     }
-                }
-                // scores in units of log2; s[.][0, 1]: token g, rows 2j, 2j + 1; [2, 3]: token g + 8
-                const float sk0 = __uint_as_float(U4 ? wk0 & 0xffff0000u : wk0) * a.scale_log2;
-                const float sk1 = __uint_as_float(U4 ? wk1 & 0xffff0000u : wk1) * a.scale_log2;
-                float sv0 = __uint_as_float(U4 ? wv0 & 0xffff0000u : wv0);
-                float sv1 = __uint_as_float(U4 ? wv1 & 0xffff0000u : wv1);
-                bool over = false;
-                const bool whole = pos0 + 16 <= seen_by_all;
-                if (!whole) {  // words beyond the sequence hold anything
-                    if (pos0 + g >= at.len) sv0 = 0.0f;
-                    if (pos0 + g + 8 >= at.len) sv1 = 0.0f;
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    s[nt][0] = s[nt][0] * (cq[nt][0] * sk0), s[nt][1] = s[nt][1] * (cq[nt][1] * sk0);
-                    s[nt][2] = s[nt][2] * (cq[nt][0] * sk1), s[nt][3] = s[nt][3] * (cq[nt][1] * sk1);
-                    if (!whole) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int t = min((row0 + 8 * nt + 2 * j + (e & 1)) / a.group, at.T - 1);
-                            if (!attn_sees(a, at, t, pos0 + g + 8 * (e >> 1))) s[nt][e] = -INFINITY;
-                        }
+                    // scores in units of log2; s[.][0, 1]: token g, rows 2j, 2j + 1; [2, 3]: token g + 8
+                    const float sk0 = __uint_as_float(U4 ? wk0 & 0xffff0000u : wk0) * a.scale_log2;
+                    const float sk1 = __uint_as_float(U4 ? wk1 & 0xffff0000u : wk1) * a.scale_log2;
+                    float sv0 = __uint_as_float(U4 ? wv0 & 0xffff0000u : wv0);
+                    float sv1 = __uint_as_float(U4 ? wv1 & 0xffff0000u : wv1);
+                    bool over = false;
+                    if constexpr (!whole) {  // words beyond the sequence hold anything
+                        if (pos0 + g >= at.len) sv0 = 0.0f;
+                        if (pos0 + g + 8 >= at.len) sv1 = 0.0f;
                     }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) over = over || fmaxf(s[nt][e], s[nt][e + 2]) > m[nt][e] + kAttnSlack;
-                }
-                over = over || sv0 > unit || sv1 > unit;
-                if (__any_sync(0xffffffffu, over)) {
-                    // new maxima of rows 2j, 2j + 1 (over the lanes of all tokens), a new unit
-                    uint32_t su = max(__float_as_uint(sv0), __float_as_uint(sv1));
-                    su = __reduce_max_sync(0xffffffffu, su);
-                    su = (su + 0x7fffffu) & 0xff800000u;  // a power of two, 2^126 at most: scales stay below
-                    const float grown = fmaxf(unit, __uint_as_float(su));
-                    const float ratio = unit * __uint_as_float(0x7f000000u - __float_as_uint(grown));  // unit / grown
-                    unit = grown;
-                    per_unit = __uint_as_float(0x7f000000u - __float_as_uint(grown));
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float f[2];
+                        s[nt][0] = s[nt][0] * (cq[nt][0] * sk0), s[nt][1] = s[nt][1] * (cq[nt][1] * sk0);
+                        s[nt][2] = s[nt][2] * (cq[nt][0] * sk1), s[nt][3] = s[nt][3] * (cq[nt][1] * sk1);
+                        if constexpr (!whole) {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float v = fmaxf(s[nt][e], s[nt][e + 2]);
-#pragma unroll
-                            for (int d = 4; d < 32; d *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-                            const float top = fmaxf(m[nt][e], v);
-                            f[e] = m[nt][e] == -INFINITY ? 0.0f : ex2(m[nt][e] - top);
-                            m[nt][e] = top;
-                            ref[nt][e] = top == -INFINITY ? 0.0f : top;
-                            l[nt][e] *= f[e];
-                            f[e] *= ratio;
-                        }
-#pragma unroll
-                        for (int st = 0; st < S::kSteps; ++st)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[nt][st][e] *= f[e & 1];
-                    }
-                }
-                const float w0 = sv0 * per_unit * (float)(1 << kAttnRoom), w1 = sv1 * per_unit * (float)(1 << kAttnRoom);
-                uint32_t p[NT][2];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float p0 = ex2(s[nt][0] - ref[nt][0]), p1 = ex2(s[nt][1] - ref[nt][1]);
-                    const float p2 = ex2(s[nt][2] - ref[nt][0]), p3 = ex2(s[nt][3] - ref[nt][1]);
-                    l[nt][0] += p0 + p2, l[nt][1] += p1 + p3;
-                    const __half2 lo = __floats2half2_rn(p0 * w0, p1 * w0), hi = __floats2half2_rn(p2 * w1, p3 * w1);
-                    p[nt][0] = transposed(*reinterpret_cast<const uint32_t *>(&lo));
-                    p[nt][1] = transposed(*reinterpret_cast<const uint32_t *>(&hi));
-                }
-                // V of tokens 2j, 2j + 1, 2j + 8, 2j + 9, the lane's channels
-                uint32_t vw[4][S::kVWords];
-                constexpr int step_v = S::kVWords < 4 ? S::kVWords : 4;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int w = 0; w < S::kVWords; w += step_v)
-                        lds<step_v>(k_at + v_off[e & 1][w / 4] + (e >> 1) * eight, vw[e] + w);
-                Zero za, zb;
-                if constexpr (U4) {
-                    const uint2 ta = lds64(w_at + 64 + 8 * j), tb = lds64(w_at + 64 + 8 * j + 32);
-                    za = zero_of(ta.x & 15u, ta.y & 15u);
-                    zb = zero_of(tb.x & 15u, tb.y & 15u);
-                }
-#pragma unroll
-                for (int w = 0; w < S::kVWords; ++w) {
-                    if constexpr (U4) {
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            uint32_t ra[4], rb[4];
-                            u4_pairs(prmt(vw[0][w], vw[1][w], half ? 0x7632 : 0x5410), za, ra);
-                            u4_pairs(prmt(vw[2][w], vw[3][w], half ? 0x7632 : 0x5410), zb, rb);
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint32_t f[4] = {ra[2 * e], ra[2 * e + 1], rb[2 * e], rb[2 * e + 1]};
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt][4 * w + 2 * half + e], f, p[nt][0], p[nt][1]);
+                            for (int e = 0; e < 4; ++e) {
+                                const int t = min((row0 + 8 * nt + 2 * j + (e & 1)) / a.group, at.T - 1);
+                                if (!attn_sees(a, at, t, pos0 + g + 8 * (e >> 1))) s[nt][e] = -INFINITY;
                             }
                         }
-                    } else {
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            // the tokens' codes of a channel side by side: a0 b0 a1 b1
-                            const uint32_t ta = prmt(vw[0][w], vw[1][w], half ? 0x7362 : 0x5140);
-                            const uint32_t tb = prmt(vw[2][w], vw[3][w], half ? 0x7362 : 0x5140);
-                            uint32_t f[4];
-                            s8_pairs(ta, f[0], f[1]);
-                            s8_pairs(tb, f[2], f[3]);
+                        for (int e = 0; e < 2; ++e) over = over || fmaxf(s[nt][e], s[nt][e + 2]) > m[nt][e] + kAttnSlack;
+                    }
+                    float w0 = sv0 * per_unit, w1 = sv1 * per_unit;
+                    over = over || w0 > 1.0f || w1 > 1.0f;
+                    if (__any_sync(0xffffffffu, over)) {
+                        // new maxima of rows 2j, 2j + 1 (over the lanes of all tokens); a new unit, of the tokens that
+                        // all rows see, or one for each row
+                        const uint32_t su = max(whole || pos0 + g < seen_by_all ? __float_as_uint(sv0) : 0u,
+                                                whole || pos0 + g + 8 < seen_by_all ? __float_as_uint(sv1) : 0u);
+                        const float before = pow2_inverse(per_unit);
+                        per_unit = pow2_inverse(fmaxf(before, pow2_above(__uint_as_float(__reduce_max_sync(0xffffffffu, su)))));
+                        const float ratio = before * per_unit;
+                        w0 = sv0 * per_unit, w1 = sv1 * per_unit;
+                        bool apart = false, each = false;
+                        if constexpr (!whole) {
+                            apart = absent & kApart;
+                            each = apart || __any_sync(0xffffffffu, w0 > 1.0f || w1 > 1.0f);
+                        }
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt][2 * w + half], f, p[nt][0], p[nt][1]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float f[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float v = fmaxf(s[nt][e], s[nt][e + 2]);
+#pragma unroll
+                                for (int d = 4; d < 32; d *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+                                const float top = fmaxf(m[nt][e], v);
+                                f[e] = m[nt][e] == -INFINITY ? 0.0f : ex2(m[nt][e] - top);
+                                m[nt][e] = top;
+                                ref[nt][e] = top == -INFINITY ? 0.0f : top;
+                                l[nt][e] *= f[e];
+                                if (!each) {
+                                    f[e] *= ratio;
+                                    continue;
+                                }
+                                float big = fmaxf(s[nt][e] == -INFINITY ? 0.0f : sv0, s[nt][e + 2] == -INFINITY ? 0.0f : sv1);
+#pragma unroll
+                                for (int d = 4; d < 32; d *= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+                                float *own = &row_unit[warp][8 * nt + 2 * j + e];
+                                const float old = apart ? *own : before, now = fmaxf(old, pow2_above(big));
+                                f[e] *= old * pow2_inverse(now);
+                                __syncwarp();
+                                if (g == 0) *own = now;
+                            }
+#pragma unroll
+                            for (int st = 0; st < S::kSteps; ++st)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) acc[nt][st][e] *= f[e & 1];
+                        }
+                        if (each) absent |= kApart;
+                        __syncwarp();
+                    }
+                    w0 *= (float)(1 << kAttnRoom), w1 *= (float)(1 << kAttnRoom);
+                    uint32_t p[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float p0 = ex2(s[nt][0] - ref[nt][0]), p1 = ex2(s[nt][1] - ref[nt][1]);
+                        const float p2 = ex2(s[nt][2] - ref[nt][0]), p3 = ex2(s[nt][3] - ref[nt][1]);
+                        l[nt][0] += p0 + p2, l[nt][1] += p1 + p3;
+                        float y[4] = {p0 * w0, p1 * w0, p2 * w1, p3 * w1};
+                        if (!whole && (absent & kApart)) {  // hidden: the scale over the row's unit may be more than fp32 holds
+                            const float z[4] = {p0, p1, p2, p3};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float per = pow2_inverse(row_unit[warp][8 * nt + 2 * j + (e & 1)]);
+                                const float w = (e < 2 ? sv0 : sv1) * per * (float)(1 << kAttnRoom);
+                                y[e] = s[nt][e] == -INFINITY ? 0.0f : z[e] * w;
+                            }
+                        }
+                        const __half2 lo = __floats2half2_rn(y[0], y[1]), hi = __floats2half2_rn(y[2], y[3]);
+                        p[nt][0] = transposed(*reinterpret_cast<const uint32_t *>(&lo));
+                        p[nt][1] = transposed(*reinterpret_cast<const uint32_t *>(&hi));
+                    }
+                    // V of tokens 2j, 2j + 1, 2j + 8, 2j + 9, the lane's channels
+                    uint32_t vw[4][S::kVWords];
+                    constexpr int step_v = S::kVWords < 4 ? S::kVWords : 4;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int w = 0; w < S::kVWords; w += step_v)
+                            lds<step_v>(k_at + v_off[e & 1][w / 4] + (e >> 1) * eight, vw[e] + w);
+                    [[maybe_unused]] Zero za, zb;
+                    if constexpr (U4) {
+                        const uint2 ta = lds64(w_at + 64 + 8 * j), tb = lds64(w_at + 64 + 8 * j + 32);
+                        za = zero_of(ta.x & 15u, ta.y & 15u);
+                        zb = zero_of(tb.x & 15u, tb.y & 15u);
+                    }
+#pragma unroll
+                    for (int w = 0; w < S::kVWords; ++w) {
+                        if constexpr (U4) {
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                uint32_t ra[4], rb[4];
+                                u4_pairs(prmt(vw[0][w], vw[1][w], half ? 0x7632 : 0x5410), za, ra);
+                                u4_pairs(prmt(vw[2][w], vw[3][w], half ? 0x7632 : 0x5410), zb, rb);
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const uint32_t f[4] = {ra[2 * e], ra[2 * e + 1], rb[2 * e], rb[2 * e + 1]};
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt][4 * w + 2 * half + e], f, p[nt][0], p[nt][1]);
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                // the tokens' codes of a channel side by side: a0 b0 a1 b1
+                                const uint32_t ta = prmt(vw[0][w], vw[1][w], half ? 0x7362 : 0x5140);
+                                const uint32_t tb = prmt(vw[2][w], vw[3][w], half ? 0x7362 : 0x5140);
+                                uint32_t f[4];
+                                s8_pairs(ta, f[0], f[1]);
+                                s8_pairs(tb, f[2], f[3]);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt][2 * w + half], f, p[nt][0], p[nt][1]);
+                            }
                         }
                     }
                 }
+                __syncwarp();  // the stage has been read
+                ask(stage);
+                if (++stage == ST) stage = 0;
+                if constexpr (!whole) pos0 += kAttnChunk;
             }
-            __syncwarp();  // the stage has been read
-            ask(stage);
-            if (++stage == ST) stage = 0;
-        }
+        };
+        const int units = (int)(end - x), room = seen_by_all - 16 - pos0;
+        const int all = room < 0 ? 0 : min(units, room / kAttnChunk + 1);
+        tiles(std::true_type{}, all);
+        pos0 += all * kAttnChunk;
+        if (units > all) tiles(std::false_type{}, units - all);
         x = end;
         at.chunk = at.units - 1;  // (where this is not so, nothing follows)
         if (x < share.to) next(a, at, S::kRows);
@@ -464,24 +508,25 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int d = 4; d < 32; d *= 2) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
-                if (g == 0) stats[warp][8 * nt + 2 * j + e][0] = m[nt][e], stats[warp][8 * nt + 2 * j + e][1] = l[nt][e];
+                const int r = 8 * nt + 2 * j + e;
+                const float unit = absent & kApart ? row_unit[warp][r] : pow2_inverse(per_unit);
+                if (g == 0) stats[warp][r] = make_float4(m[nt][e], unit, l[nt][e], 0.0f);
             }
-        if (lane == 0) units_of[warp] = unit;
         __syncthreads();
-        float top_unit = units_of[0];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) top_unit = fmaxf(top_unit, units_of[w]);
         const bool done = starts_here && ends_here;
         float *slot = attn_slot(a, blockIdx.x, starts_here ? 1 : 0, S::kRows, DP);
-        const float shrink = unit * __uint_as_float(0x7f000000u - __float_as_uint(top_unit));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = 8 * nt + 2 * j + e;
-                float top = -INFINITY;
+                float top = -INFINITY, top_unit = 0.0f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[w][r][0]);
+                for (int w = 0; w < kWarps; ++w) {
+                    const float2 o = *reinterpret_cast<const float2 *>(&stats[w][r]);
+                    top = fmaxf(top, o.x), top_unit = fmaxf(top_unit, o.y);
+                }
+                const float shrink = stats[warp][r].y * pow2_inverse(top_unit);
                 const float f = (m[nt][e] == top ? 1.0f : ex2(m[nt][e] - top)) * shrink;
                 float *to = join + (warp * 8 + 2 * j + e) * S::kPitch + g;
 #pragma unroll
@@ -495,22 +540,25 @@ kv_attn_few_kernel(const __grid_constant__ KvAttnArgs a)
                 const int r = i / (DP / 2), p = i % (DP / 2), row = 8 * nt + r;
                 if (row >= width) break;
                 const int step = p / 8, pg = p % 8;
-                float v0 = 0.0f, v1 = 0.0f, top = -INFINITY, total = 0.0f;
+                float v0 = 0.0f, v1 = 0.0f, top = -INFINITY, total = 0.0f, top_unit = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
                     const float *from = join + (w * 8 + r) * S::kPitch + 16 * step + pg;
                     v0 += from[0], v1 += from[8];
-                    top = fmaxf(top, stats[w][row][0]);
+                    const float2 o = *reinterpret_cast<const float2 *>(&stats[w][row]);
+                    top = fmaxf(top, o.x), top_unit = fmaxf(top_unit, o.y);
                 }
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w)
-                    total += stats[w][row][1] * (stats[w][row][0] == top ? 1.0f : ex2(stats[w][row][0] - top));
+                for (int w = 0; w < kWarps; ++w) {
+                    const float4 o = stats[w][row];
+                    total += o.z * (o.x == top ? 1.0f : ex2(o.x - top));
+                }
                 const int d = sum_channel<U4, DP>(pg, step, 0);
                 if (!done) {
                     *reinterpret_cast<float2 *>(slot + row * DP + d) = make_float2(v0, v1);
                     if (p == 0) {
                         slot[S::kRows * DP + 2 * row] = top, slot[S::kRows * DP + 2 * row + 1] = total;
-                        if (row == 0) slot[S::kRows * (DP + 2)] = top_unit;
+                        slot[S::kRows * (DP + 2) + row] = top_unit;
                     }
                 } else if (d < c.D) {
                     attn_store(a, first, head, row0 + row, d, v0, v1, top, total, top_unit * kAttnWeightUnit);

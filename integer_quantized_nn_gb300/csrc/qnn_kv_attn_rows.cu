@@ -47,12 +47,14 @@ struct Tile16 {
 constexpr int kPlaces = 8;
 
 // Of a chunk: scales of K times the call's, and of V over the stream's unit, for two tokens together (k k v v).
+// kWhole: all rows see all of it.  kApart: some rows do not see a token whose scale is above the unit; V's scales
+// are as in the cache, and each row has a unit of its own from there to the item's end.
 struct Info {
     float scales[kTokens / 2][4];
-    float ratio, unit;  // the unit before over this one; this one
-    uint32_t present;   // 16-token tiles that are there
-    uint32_t pad;
+    float ratio, unit, before;  // the unit before over this one; this one; the one before
+    uint32_t present;           // 16-token tiles that are there, in bits 0..7
 };
+constexpr uint32_t kWhole = 0x1ffu, kApart = 0x200u;
 
 // f16 operands, A from tensor memory.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
@@ -164,11 +166,11 @@ __device__ __forceinline__ uint32_t seen_bits(const KvAttnArgs &a, const Item &c
 // A warp's 16 rows of S of a chunk -> P over it.  A thread has 2 rows (8 q + g) and the columns 8 i + 2 j and + 1 of
 // each: with a row to a thread each would read all scales of the chunk from shared memory, 1500 cycles
 // of its bandwidth a chunk.  scales: of K and V, of the thread's first two columns; bits: lanes t and t + 16 have
-// those of the positions that row t sees; sums_still: waits until no product adds to the sums.
-template <bool MASKED, int DP, typename F>
+// those of the positions that row t sees; unit: of each row, APART; sums_still: waits until no product adds to the sums.
+template <bool MASKED, bool APART, int DP, typename F>
 __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, uint32_t scales, const uint32_t (&bits)[4], int j,
                                         bool first, float ratio, const float (&cr)[2], float (&m)[2], float (&l)[2],
-                                        const F &sums_still)
+                                        float *unit, const F &sums_still)
 {
     const int g = (threadIdx.x & 31) >> 2;
     uint32_t b[2][4], p[32];
@@ -187,7 +189,7 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, uint32_t s
     for (;;) {
         uint32_t v[64];
         if (fresh) {
-            float top[2] = {-INFINITY, -INFINITY}, f[2];
+            float top[2] = {-INFINITY, -INFINITY}, f[2], big[2] = {0.0f, 0.0f};
             tmem_ld_frag(s_at, v);
             tmem_ld_wait();
 #pragma unroll
@@ -202,6 +204,9 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, uint32_t s
                         y.x = b[q][i >> 2] & bit ? y.x : -INFINITY;
                         y.y = b[q][i >> 2] & (2 * bit) ? y.y : -INFINITY;
                     }
+                    if constexpr (APART)
+                        big[q] = max3(big[q], b[q][i >> 2] & bit ? __uint_as_float(kw.z) : 0.0f,
+                                      b[q][i >> 2] & (2 * bit) ? __uint_as_float(kw.w) : 0.0f);
                     top[q] = max3(top[q], y.x, y.y);
                 }
             }
@@ -212,7 +217,16 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, uint32_t s
                 const float u = fmaxf(m[q], top[q]);
                 f[q] = m[q] == -INFINITY ? 0.0f : ex2(m[q] - u);
                 m[q] = u;
-                l[q] *= f[q], f[q] *= ratio;
+                l[q] *= f[q];
+                if constexpr (APART) {
+                    big[q] = fmaxf(big[q], __shfl_xor_sync(0xffffffffu, big[q], 1));
+                    big[q] = fmaxf(big[q], __shfl_xor_sync(0xffffffffu, big[q], 2));
+                    const float now = fmaxf(unit[q], pow2_above(big[q]));
+                    f[q] *= unit[q] * pow2_inverse(now);
+                    unit[q] = now;
+                } else {
+                    f[q] *= ratio;
+                }
             }
             if (!first && __any_sync(0xffffffffu, f[0] != 1.0f || f[1] != 1.0f)) {
                 sums_still();
@@ -244,7 +258,14 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, uint32_t s
                     y.y = b[q][i >> 2] & (2 * bit) ? y.y : 0.0f;
                 }
                 s[q] = add2(s[q], y);
-                y = mul2(y, w);
+                if constexpr (APART) {  // hidden: the scale over the row's unit may be more than fp32 holds
+                    float2 v = mul2(w, both(pow2_inverse(unit[q])));
+                    v.x = b[q][i >> 2] & bit ? v.x : 0.0f;
+                    v.y = b[q][i >> 2] & (2 * bit) ? v.y : 0.0f;
+                    y = mul2(mul2(y, both((float)(1 << kAttnRoom))), v);
+                } else {
+                    y = mul2(y, w);
+                }
                 const __half2 h = __floats2half2_rn(y.x, y.y);
                 p[2 * i + q] = *reinterpret_cast<const uint32_t *>(&h);
             }
@@ -276,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
     __shared__ __align__(16) Info infos[kInfos];
     __shared__ __align__(16) Tile16 places[kPlaces][kTokens / 16];
     __shared__ Item items[kItems];
-    __shared__ float row_m[2][kRows], row_l[2][kRows], row_top[2][kRows], row_c[2][kRows], stream_unit[2];
+    __shared__ float row_m[2][kRows], row_l[2][kRows], row_top[2][kRows], row_c[2][kRows], row_unit[2][kRows];
     __shared__ uint32_t present[kPlaces], tmem_slot;  // 16-token tiles of a chunk that are there
     uint8_t *smem = raw + (-smem_u32(raw) & 1023u);  // the swizzle's atoms
     // tiles: K of even and odd chunks, V of both (ONE: of any); q (of both streams); the sums of the line
@@ -447,7 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
         // warp 2: scales of K, 3: of V; four tokens a lane, their words asked for a chunk ahead
         const bool is_v = warp == 3;
         float unit[2] = {0.0f, 0.0f};
-        int left = 0, item = 0, len = 0, pos = 0;
+        int left = 0, item = 0, len = 0, pos = 0, seen_by_all = 0;
+        uint32_t apart = 0;  // bit of a stream
         uint4 ahead = make_uint4(0, 0, 0, 0);
         uint32_t ahead_there = 0;
         auto ask = [&](int n) {
@@ -471,6 +493,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 if (!wait(item_full[(unsigned)item % kItems], (unsigned)item / kItems)) break;
                 const Item &at = items[(unsigned)item % kItems];
                 left = at.count, len = at.len, pos = at.chunk * kTokens + 4 * lane;
+                const int t_first = min(at.rt * ROWS / a.group, at.T - 1);
+                seen_by_all = a.mask ? at.len - at.T : min(at.len, at.len - at.T + t_first + 1);
+                apart = 0;
                 release(item_empty[(unsigned)item % kItems]);
                 ++item;
                 unit[0] = unit[1] = pow2i(-126);
@@ -486,16 +511,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 if (e >= valid) s[e] = 0.0f;
             }
             if (is_v) {
-                uint32_t top = __float_as_uint(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])));
-                top = __reduce_max_sync(0xffffffffu, top);
-                const float old = SPLIT && (n & 1) ? unit[1] : unit[0];
-                const float now = fmaxf(old, __uint_as_float((top + 0x7fffffu) & 0xff800000u));
-                const float per = __uint_as_float(0x7f000000u - __float_as_uint(now));
-                if (SPLIT && (n & 1)) unit[1] = now;
-                else unit[0] = now;
+                const int stream = SPLIT ? n & 1 : 0;
+                float top = 0.0f, common = 0.0f;  // the largest, and of those that all rows see
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[e] = s[e] * per * (float)(1 << kAttnRoom);
-                if (lane == 0) info.ratio = old * per, info.unit = now, info.present = there;
+                for (int e = 0; e < 4; ++e) top = fmaxf(top, s[e]), common = pos + e < seen_by_all ? fmaxf(common, s[e]) : common;
+                common = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(common)));
+                const float old = stream ? unit[1] : unit[0], now = fmaxf(old, pow2_above(common)), per = pow2_inverse(now);
+                if (stream) unit[1] = now;
+                else unit[0] = now;
+                if (__any_sync(0xffffffffu, top > now)) apart |= 1u << stream;
+                const bool each = apart >> stream & 1u;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] = each ? s[e] : s[e] * per * (float)(1 << kAttnRoom);
+                if (lane == 0) {
+                    info.ratio = old * per, info.unit = now, info.before = old;
+                    info.present = each ? there | kApart
+                                   : there == 0xffu && pos + kTokens <= seen_by_all ? kWhole : there;
+                }
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[e] *= a.scale_log2;
@@ -705,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
             // of rows q = 0, 1 of this thread, in both streams
             const int own = 32 * (warp & 3) + 16 * part + g, steps = PAIR ? 2 * count : count;
             float cr[2][2], m[2][2], l[2][2], unit[SPLIT ? 2 : 1];  // PAIR: the same of both
-            int seen_by_all[2];
+            uint32_t apart = 0;  // bit of a stream: its rows' units are in row_unit
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
 #pragma unroll
@@ -715,8 +747,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                     l[st][q] = 0.0f;
                 }
                 if (st == 0 || SPLIT) unit[st] = pow2i(-126);
-                const int t_first = min((at.rt * ROWS + (PAIR ? st * kRows : 0)) / a.group, at.T - 1);
-                seen_by_all[st] = (a.mask ? at.len - at.T : min(at.len, at.len - at.T + t_first + 1)) - kTokens;
             }
             const uint32_t down = (uint32_t)(16 * part) << 16;
             // a warp whose wait gave up goes on to the end of the item: the others wait for it there
@@ -726,7 +756,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 if (!PAIR || !stream) (void)wait(info_full[slot], (unsigned)x / kInfos);
                 (void)wait(s_full[stream], PAIR ? x : x >> 1);
                 tc_fence_after();
-                const int pos0 = (at.chunk + i) * kTokens;
                 const uint32_t there = infos[slot].present;
                 const float ratio = infos[slot].ratio;
                 uint32_t scales = smem_u32(infos[slot].scales[j]);
@@ -746,10 +775,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                     sc[q] = own_state ? cr[1][q] : cr[0][q], sm[q] = own_state ? m[1][q] : m[0][q];
                     sl[q] = own_state ? l[1][q] : l[0][q];
                 }
-                if (pos0 <= (stream ? seen_by_all[1] : seen_by_all[0]) && there == 0xffu) {
+                if (there == kWhole) {
                     const uint32_t none[4] = {};
-                    weights<false, DP>(s_at, o_at, scales, none, j, step < (ONE ? 1 : 2), ratio, sc, sm, sl, sums_still);
+                    weights<false, false, DP>(s_at, o_at, scales, none, j, step < (ONE ? 1 : 2), ratio, sc, sm, sl, nullptr,
+                                              sums_still);
                 } else {
+                    const int pos0 = (at.chunk + i) * kTokens;
                     uint32_t bits[4];
                     const int row = at.rt * ROWS + (PAIR ? stream * kRows : 0) + 32 * (warp & 3) + 16 * part + (lane & 15);
                     const int t = min(row / a.group, at.T - 1);
@@ -758,7 +789,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                         bits[w] = seen_bits(a, at, t, pos0 + 32 * w) &
                                   ((there >> (2 * w) & 1u ? 0xffffu : 0u) | (there >> (2 * w + 1) & 1u ? 0xffff0000u : 0u));
                     __syncwarp();
-                    weights<true, DP>(s_at, o_at, scales, bits, j, step < (ONE ? 1 : 2), ratio, sc, sm, sl, sums_still);
+                    if (!(there & kApart)) {
+                        weights<true, false, DP>(s_at, o_at, scales, bits, j, step < (ONE ? 1 : 2), ratio, sc, sm, sl, nullptr,
+                                                 sums_still);
+                    } else {
+                        float own_unit[2], *at_unit = &row_unit[own_state][own];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) own_unit[q] = apart >> own_state & 1u ? at_unit[8 * q] : infos[slot].before;
+                        weights<true, true, DP>(s_at, o_at, scales, bits, j, step < (ONE ? 1 : 2), ratio, sc, sm, sl, own_unit,
+                                                sums_still);
+                        apart |= 1u << own_state;
+                        if (j == 0) at_unit[0] = own_unit[0], at_unit[8] = own_unit[1];
+                    }
                 }
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -783,9 +825,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 for (int q = 0; q < 2; ++q) {
                     l[st][q] += __shfl_xor_sync(0xffffffffu, l[st][q], 1);
                     l[st][q] += __shfl_xor_sync(0xffffffffu, l[st][q], 2);
-                    if (j == 0) row_m[st][own + 8 * q] = m[st][q], row_l[st][own + 8 * q] = l[st][q];
+                    if (j == 0) {
+                        const int row = own + 8 * q;
+                        row_m[st][row] = m[st][q], row_l[st][row] = l[st][q];
+                        if (!(apart >> st & 1u)) row_unit[st][row] = unit[SPLIT ? st : 0];
+                    }
                 }
-            if (threadIdx.x == kRowWarp0 * 32) stream_unit[0] = unit[0], stream_unit[1] = unit[SPLIT ? 1 : 0];
             (void)wait(o_full, item);
             tc_fence_after();
             meet();
@@ -794,10 +839,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                 const float m0 = row_m[s0][r], m1 = row_m[s1][r], up = fmaxf(m0, m1);
                 const float f0 = m0 == up ? 1.0f : ex2(m0 - up), f1 = !SPLIT ? 0.0f : m1 == up ? 1.0f : ex2(m1 - up);
                 const float total = !SPLIT ? row_l[s0][r] : __fmaf_rn(row_l[0][r], f0, row_l[1][r] * f1);
-                const float top_unit = !SPLIT ? stream_unit[s0] : fmaxf(stream_unit[0], stream_unit[1]);
-                const float per = __uint_as_float(0x7f000000u - __float_as_uint(top_unit));
+                const float u0 = row_unit[s0][r], u1 = row_unit[s1][r], top_unit = fmaxf(u0, u1);  // (s1: s0 without SPLIT)
+                const float per = pow2_inverse(top_unit);
                 const bool has0 = !SPLIT || count > 1 || !(n & 1), has1 = SPLIT && (count > 1 || (n & 1));
-                const float g0 = !SPLIT ? 1.0f : f0 * (stream_unit[0] * per), g1 = !SPLIT ? 0.0f : f1 * (stream_unit[1] * per);
+                const float g0 = !SPLIT ? 1.0f : f0 * (u0 * per), g1 = !SPLIT ? 0.0f : f1 * (u1 * per);
                 const bool done = starts_here && ends_here;
                 const int part_row = PAIR ? part * kRows + r : r;
                 float *slot = attn_slot(a, blockIdx.x, starts_here ? 1 : 0, ROWS, DP);
@@ -835,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
                         if (a.lse) a.lse[out_row * a.heads_q + hq] = attn_lse(up, total);
                     } else {
                         slot[ROWS * DP + 2 * part_row] = up, slot[ROWS * DP + 2 * part_row + 1] = total;
-                        if (part_row == 0) slot[ROWS * (DP + 2)] = top_unit;
+                        slot[ROWS * (DP + 2) + part_row] = top_unit;
                     }
                 }
             }

@@ -353,3 +353,28 @@ def test_keys_and_queries_at_the_ends_of_the_range(tokens, D, size_q, size_k):
     q = rng.normal(0, 1, size=(c.rows, 4, D)) * size_q
     for scale in (D ** -0.5, -0.02, 3.0):
         check(c, Dev(c), 4, q=q, scale=scale)
+
+
+@pytest.mark.parametrize("power", [24, 40, 110])
+@pytest.mark.parametrize("tokens, heads, group, D, kv", [
+    (7, 2, 1, 64, "s8"), (4, 2, 4, 64, "u4"), (7, 1, 1, 128, "s8"), (2, 3, 4, 128, "u4"), (9, 1, 3, 256, "s8"),
+    (20, 2, 4, 64, "s8"), (40, 1, 4, 128, "u4"), (70, 2, 4, 128, "s8"), (20, 2, 4, 160, "s8"), (150, 1, 2, 256, "u4")])
+def test_hidden_tokens_have_no_part_in_a_row(tokens, heads, group, D, kv, power):
+    """Values of later tokens, and of other branches, 2^power times those that a row sees: its result is as exact
+    as without them.  A row that sees one of them is as exact as its largest value lets it be."""
+    rng = np.random.default_rng(tokens + D)
+    c = _kv.Cache(rng, [tokens + 2600, tokens + 100, tokens], [tokens] * 3, heads, D, 16, kv, "bf16")
+    sees = [_kv.random_tree(rng, tokens) for _ in range(3)]
+    sees[1][::3] = False
+    for b in range(3):
+        first = c.lens[b] - tokens
+        large = np.arange(1 + b, tokens, 3)
+        c.v[b][first + large] = _kv.bf16(c.v[b][first + large] * 2.0 ** power)
+    d = Dev(c)
+    check(c, d, heads * group)
+    check(c, d, heads * group, sees)
+    # the last token alone
+    for b in range(3):
+        first = c.lens[b] - tokens
+        c.v[b][first:-1] = _kv.bf16(rng.normal(0, 1, size=(tokens - 1, heads, D)))
+    check(c, Dev(c), heads * group)
