@@ -403,66 +403,69 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_rows_kernel(const __grid_
     } else if (warp == 1) {
         const uint32_t idesc_s = idesc_f32acc(0, 0, kRows, kTokens);
         const uint32_t idesc_o = idesc_f32acc(0, 0, kRows, 0) | (uint32_t)(c.D >> 3) << 17 | 1u << 16;  // B is N-major
-        // one thread, step by step: S of step t after O of step t - 2, which is of the same stream
+        // Step by step: S of step t after O of step t - 2, which is of the same stream.  One lane issues products and
+        // commits, always the same, but all lanes go through the loops: a product's descriptors are one value for the
+        // warp, and so no lane has another, however the compiler lays out the branches.  (Where one lane went through
+        // the loops alone, an unrolled loop with a condition inside read operands elsewhere.  With the lane chosen by
+        // its number, which does not tell the compiler that it is one, the prompt of the note above took 327 us.)
         const uint64_t kd0 = sdesc_sw128(tiles), vd0 = sdesc_n_major(tiles + TILES * TILE, PANEL), qd0 = sdesc_sw128(q_tile);
         int n = 0, item = 0;
-        auto wait1 = [&](uint64_t &bar, int use) {
-            ok = ok && mbar_wait_short(smem_u32(&bar), (uint32_t)use & 1u, nullptr);
-            return ok;
-        };
-        while (lane == 0 && n < chunks && ok) {
-            if (!wait1(item_full[(unsigned)item % kItems], (unsigned)item / kItems)) break;
+#pragma unroll 1
+        while (n < chunks && ok) {
+            if (!wait(item_full[(unsigned)item % kItems], (unsigned)item / kItems)) break;
             const int count = items[(unsigned)item % kItems].count, steps = PAIR ? 2 * count : count;
-            mbar_arrive(smem_u32(&item_empty[(unsigned)item % kItems]));
-            if (!wait1(q_full, item)) break;
+            release(item_empty[(unsigned)item % kItems]);
+            if (!wait(q_full, item)) break;
 #pragma unroll 1
             for (int t = 0; t < steps + 2; ++t) {
                 const int x = n + (PAIR ? t >> 1 : t), stream = PAIR ? t & 1 : x & 1;  // of S
                 const uint32_t s_at = tmem + stream * kTokens;
                 if (t >= 2) {
                     const int y = PAIR ? x - 1 : x - 2, tile = y & (TILES - 1);  // the chunk of O
-                    if (!wait1(tile_full[2 + tile], y / TILES) || !wait1(p_ready[stream], PAIR ? y : y >> 1)) break;
+                    if (!wait(tile_full[2 + tile], y / TILES) || !wait(p_ready[stream], PAIR ? y : y >> 1)) break;
                     tc_fence_after();
                     const uint64_t vd = vd0 + (uint64_t)(tile * (TILE >> 4));
                     const uint32_t o = tmem + kOCol + (ONE ? 0 : stream * 128);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int s = 0; s < kTokens / 16; ++s)
-                        mma_ts(o, s_at + 8 * s, vd + (uint64_t)s * (2048 >> 4), idesc_o, t >= (ONE ? 3 : 4) || s > 0);
-                    if (!PAIR || stream) mma_commit(smem_u32(&tile_empty[2 + tile]));
-                    if constexpr (ONE) mma_commit(smem_u32(&o_added));
+                        for (int s = 0; s < kTokens / 16; ++s)
+                            mma_ts(o, s_at + 8 * s, vd + (uint64_t)s * (2048 >> 4), idesc_o, t >= (ONE ? 3 : 4) || s > 0);
+                        if (!PAIR || stream) mma_commit(smem_u32(&tile_empty[2 + tile]));
+                        if constexpr (ONE) mma_commit(smem_u32(&o_added));
+                    }
                 }
                 if (t < steps) {
                     const int tile = x & (TILES - 1);
-                    if (!wait1(tile_full[tile], x / TILES)) break;
+                    if (!wait(tile_full[tile], x / TILES)) break;
                     tc_fence_after();
                     const uint64_t kd = kd0 + (uint64_t)(tile * (TILE >> 4)), qd = qd0 + (uint64_t)(PAIR ? stream * (TILE >> 4) : 0);
                     auto step = [&](int s) {
                         const uint64_t off = (uint64_t)((s >> 2) * (PANEL >> 4) + (s & 3) * 2);
                         mma_f16_ss(s_at, qd + off, kd + off, idesc_s, s > 0);
                     };
-                    // not an unrolled loop with a condition inside: what came of it read operands elsewhere
                     if (c.D == DP) {
+                        if (elect_one()) {
 #pragma unroll
-                        for (int s = 0; s < DP / 16; ++s) step(s);
+                            for (int s = 0; s < DP / 16; ++s) step(s);
+                        }
                     } else {
 #pragma unroll 1
-                        for (int s = 0; s < c.D / 16; ++s) step(s);
+                        for (int s = 0; s < c.D / 16; ++s)
+                            if (elect_one()) step(s);
                     }
-                    mma_commit(smem_u32(&s_full[stream]));
-                    if (!PAIR || stream) mma_commit(smem_u32(&tile_empty[tile]));
+                    if (elect_one()) {
+                        mma_commit(smem_u32(&s_full[stream]));
+                        if (!PAIR || stream) mma_commit(smem_u32(&tile_empty[tile]));
+                    }
                 }
             }
-            if (ok) mma_commit(smem_u32(&o_full));
+            if (ok && elect_one()) mma_commit(smem_u32(&o_full));
             n += count;
             ++item;
         }
-        __syncwarp();
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        // nothing of this thread's is in flight when the block ends
-        if (lane == 0) {
-            mma_commit(smem_u32(&mma_end));
-            (void)mbar_wait_short(smem_u32(&mma_end), 0, c.status);
-        }
+        // nothing of this warp's is in flight when the block ends
+        if (elect_one()) mma_commit(smem_u32(&mma_end));
+        (void)mbar_wait_short(smem_u32(&mma_end), 0, c.status);
         __syncwarp();
     } else {
         // warp 2: scales of K, 3: of V; four tokens a lane, their words asked for a chunk ahead

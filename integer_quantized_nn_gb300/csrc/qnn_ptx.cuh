@@ -142,6 +142,18 @@ __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, u
     return false;
 }
 
+// One lane of a converged warp, the same each time.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
 // ---- proxies / bulk copies ---------------------------------------------------
 __device__ __forceinline__ void fence_proxy_async_smem()
 {

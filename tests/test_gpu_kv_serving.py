@@ -378,3 +378,11 @@ def test_hidden_tokens_have_no_part_in_a_row(tokens, heads, group, D, kv, power)
         first = c.lens[b] - tokens
         c.v[b][first:-1] = _kv.bf16(rng.normal(0, 1, size=(tokens - 1, heads, D)))
     check(c, Dev(c), heads * group)
+
+
+@pytest.mark.parametrize("D", [32, 96, 160, 192, 224])
+@pytest.mark.parametrize("tokens, kv", [(24, "s8"), (70, "u4")])
+def test_channels_that_do_not_fill_the_operands(D, tokens, kv):
+    """Many rows of any number of channels, several chunks a block."""
+    c = _kv.Cache(np.random.default_rng(D + tokens), [1500, tokens + 1, tokens], [tokens] * 3, 20, D, 16, kv, "f16")
+    check(c, Dev(c), 40)

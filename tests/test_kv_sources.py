@@ -45,3 +45,15 @@ def test_waits_by_counting_end_within_seconds():
     probe, shift = re.search(r"kProbeNs = (\d+), kWaitLimitProbes = 1u << (\d+);", s).groups()
     assert 1e9 <= int(probe) * 2 ** int(shift) <= 4e9
     assert "uint32_t limit = kWaitLimitProbes" in s and "mbar_wait_short(b, 0, status, " in source("qnn_api.cu")
+
+
+def test_all_lanes_of_the_products_warp_go_the_same_way():
+    """Its descriptors are the warp's: what leads to a product or a commit is done by all lanes, and only they by one."""
+    s = source("qnn_kv_attn_rows.cu")
+    role = s[s.index("} else if (warp == 1) {"):]
+    role = role[:role.index("const bool is_v = warp == 3;")]
+    assert "lane == 0" not in role and "mbar_arrive" not in role
+    for call in re.finditer(r"(?:mma_commit|mma_ts|step)\((?!int)", role):
+        before = role[:call.start()]
+        block = before[before.rindex("elect_one())"):]
+        assert "wait(" not in block and block.count("{") - block.count("}") in (0, 1), block[-300:]
