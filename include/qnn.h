@@ -683,7 +683,7 @@ size_t qnn_kv_attn_workspace_bytes(const qnn_kv_geom *g, const qnn_kv_seqs *seqs
  *   x_j = scale * sum_d q_d k_jd,  out = sum_j e^(x_j - max x) v_j / sum_j e^(x_j - max x)
  * (k, v: the cache's values), lse = max x + ln sum_j e^(x_j - max x).  A row that sees nothing
  * gets zeros and -inf.  out: of x_dt, ld_out elements between rows (0: packed, for both); lse:
- * fp32 [rows][heads_q] or NULL.  scale finite.
+ * fp32 [rows][heads_q] or NULL.  scale log2(e) finite in fp32.
  * q enters the products as f16, each row scaled by a power of two that brings its largest value
  * near f16's, so that bf16 keeps its 8 bits (values below 2^-30 of the row's largest lose
  * some); |scale| max|k| and D |scale| max|q| max|k|, of a row and a token that it sees, must fit

@@ -216,7 +216,8 @@ extern "C" qnn_status q_kv_attn(const void *q, qnn_dtype x_dt, int64_t ld_q, int
     KvAttnArgs a = {};
     const qnn_status st = kv_args(g, seqs, &a.c);
     if (st != QNN_OK) return st;
-    if (!heads_ok(g, heads_q) || !(scale - scale == 0.0f) || mask_words < 0 || (mask && mask_words == 0))
+    const float scale_log2 = (float)(scale * 1.4426950408889634);
+    if (!heads_ok(g, heads_q) || !(scale_log2 - scale_log2 == 0.0f) || mask_words < 0 || (mask && mask_words == 0))
         return QNN_ERR_INVALID_ARG;
     if (x_dt != QNN_F16 && x_dt != QNN_BF16) return QNN_ERR_UNSUPPORTED;
     const int64_t width = (int64_t)heads_q * g->D, most = INT64_MAX / 8 / std::max<int64_t>(1, a.c.rows);
@@ -235,7 +236,7 @@ extern "C" qnn_status q_kv_attn(const void *q, qnn_dtype x_dt, int64_t ld_q, int
     a.lse = lse;
     a.mask = mask;
     a.mask_words = mask_words;
-    a.scale_log2 = (float)(scale * 1.4426950408889634);
+    a.scale_log2 = scale_log2;
     a.heads_q = heads_q;
     a.group = heads_q / g->heads;
     if (!(a.c.status = status_word())) return QNN_ERR_CUDA;

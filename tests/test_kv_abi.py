@@ -123,6 +123,17 @@ def test_attention_refusals(lib):
     assert call(tokens=0, rows=0, q=None, out=None, ws=None) == qnn.QNN_OK
 
 
+def test_scales_that_fit_fp32_but_not_in_units_of_log2(lib):
+    """2.4e38 log2(e) is beyond fp32: such a scale would make NaN of a score of zero."""
+    def call(scale):
+        return lib.q_kv_attn(None, qnn.DTYPES["bf16"], 0, 4, ctypes.byref(geom()), ctypes.byref(seqs(batch=0, rows=0)),
+                             scale, None, 0, None, 0, None, None, 0, None)
+    for scale in (0.0, 0.1, -0.1, 1e-45, 2.35e38, -2.35e38):
+        assert call(scale) == qnn.QNN_OK, scale
+    for scale in (2.4e38, -2.4e38, 3.4e38, float("inf"), float("nan")):
+        assert call(scale) == INVALID, scale
+
+
 def test_workspace_sizes(lib):
     size = lambda heads_q=4, **bad: qnn.qnn_kv_attn_workspace_bytes(*split(bad)[:2], heads_q)  # noqa: E731
     assert size() > 0
