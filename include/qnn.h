@@ -678,8 +678,8 @@ size_t qnn_kv_attn_workspace_bytes(const qnn_kv_geom *g, const qnn_kv_seqs *seqs
  * h / (heads_q / heads) of the cache.  Row t of sequence b sees every position before the newest
  * tokens, and of those the newest token j if bit j % 32 of mask[row * mask_words + j / 32] is
  * set (a tree of drafted tokens: itself and its ancestors), or without a mask if j <= t.  Bits
- * beyond T[b] do not count; newest tokens beyond 32 * mask_words are not seen.  Over the
- * visible positions j
+ * beyond T[b] do not count; newest tokens beyond 32 * mask_words are not seen.  (A row without a
+ * token sees what its bits say of those that there are.)  Over the visible positions j
  *   x_j = scale * sum_d q_d k_jd,  out = sum_j e^(x_j - max x) v_j / sum_j e^(x_j - max x)
  * (k, v: the cache's values), lse = max x + ln sum_j e^(x_j - max x).  A row that sees nothing
  * gets zeros and -inf.  out: of x_dt, ld_out elements between rows (0: packed, for both); lse:

@@ -145,11 +145,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_attn_join_kernel(const __g
     if (a.lse && lane == 0) a.lse[(first + tok) * a.heads_q + hq] = attn_lse(top, total);
 }
 
-// Where the tensor memory's kernel takes over.  Few against many rows, in 8 bits, 32 heads of q on 8, us:
-//   16 sequences of 4096, D = 128:  8 rows 43 / 56, 16 rows 60 / 57, 32 rows 77 / 58
-//   1 of 512, D = 128:             16 rows 12.9 / 12.9, 32 rows 15.5 / 12.9
-//   16 of 4096, D = 64:            16 rows 47 / 46, 32 rows 57 / 47; 32 heads on 32 over 1024, 16 rows 53 / 74
-//   16 of 4096, D = 256:           32 rows 117 / 129; 8 of 8192: 256 rows 744 / 244
+// Where the tensor memory's kernel takes over.  Few against many rows, in 8 bits, 32 heads of q on 8 (D = 256: 64), us:
+//   16 sequences of 4096, D = 128:  8 rows 43 / 58, and 16 and 32 rows of the second 58 and 59
+//   1 of 512, D = 128:              8 rows 10.9 / 13.1
+//   16 of 4096, D = 64:             8 rows 30 / 47, 16 rows 40 / 47, 32 rows 58 / 49; 32 heads on 32 over 1024, 16 rows
+//                                   49 / 67
+//   16 of 4096, D = 256:            8 rows 65 / 107, 16 rows 71 / 109, 32 rows 122 / 112, 64 rows 222 / 118; 1 of 512,
+//                                   32 rows 16.0 / 17.4
+// For D > 128 the two cross below 32 rows where sequences are long, and above where they are short.
 int most_few_rows(const KvArgs &c) { return c.D <= 64 ? 16 : c.D <= 128 ? 8 : 32; }
 
 bool many_rows(const KvArgs &c, int group)
@@ -161,7 +164,7 @@ bool many_rows(const KvArgs &c, int group)
 // A batch in which most sequences have far fewer newest tokens than the longest (prompts beside sequences that
 // decode) goes through both kernels, each with the sequences that suit it.  The host knows the tokens' number and
 // the most of one; where the mean is below a quarter of the most, two more launches (about 4 us) are worth it: 63
-// sequences of 4096 with one token beside one with 512, 32 heads on 8, D = 128, 8 bits: 192 us, 344 by one kernel.
+// sequences of 4096 with one token beside one with 512, 32 heads on 8, D = 128, 8 bits: 195 us, 344 by one kernel.
 struct AttnPlans {
     AttnPlan plan[2];
     int t_min[2], t_max[2], count;

@@ -11,8 +11,8 @@
 // bits; but a product's unit then is its number's exponent, 2^-14, and sums lose ten bits.)
 //
 // The stream of codes is what it cannot do without: 64 sequences of 8192 tokens, 8 of 64 heads, in 8 bits take
-// 140 us, 4.5 TB/s; the copies alone take 109, the rest alone 113, and a warp of each scheduler's four waits
-// for memory, another for its chain of products.  One sequence of 131072 tokens in 4 bits: 57 us, 2.5 TB/s, by
+// 141 us, 4.4 TB/s; the copies alone take 109, the rest alone 113, and a warp of each scheduler's four waits
+// for memory, another for its chain of products.  One sequence of 131072 tokens in 4 bits: 56 us, 2.5 TB/s, by
 // instructions (450 for a tile of 16 tokens).  Each warp has a ring of its own in shared memory, stages
 // of 16 tokens (their K and V rows and words), filled by asynchronous copies; warps meet only
 // where an item ends.  Maxima move only when a score passes the warp's by 2^8 (the

@@ -8,9 +8,9 @@
 // which meet where an item ends.  The rows' warps have the streams in turn: while they make P of one, the
 // tensor cores work on the other's.
 //
-// A chunk of 2048 tokens over 8192, 32 heads on 8, D = 128, in 8 bits takes 280 us, 860 TFLOP/s (45% of the
-// library's bf16 products); 8 trees of 64 tokens over 8192 take 104 us; with D = 256, 16 heads on 8, the chunk
-// takes 359 us, 669 TFLOP/s (a tile of K or V is then made while nothing multiplies by it).  Of the 2800 cycles
+// A chunk of 2048 tokens over 8192, 32 heads on 8, D = 128, in 8 bits takes 279 us, 862 TFLOP/s (45% of the
+// library's bf16 products); 8 trees of 64 tokens over 8192 take 106 us; with D = 256, 16 heads on 8, the chunk
+// takes 320 us, 751 TFLOP/s (a tile of K or V is then made while nothing multiplies by it).  Of the 2800 cycles
 // of a step (D = 128) the rows' warps work in 1850, the tensor cores in 1200; an item's start and end (q to f16, the
 // sums out) take 6 us in which the tensor cores wait.
 //
