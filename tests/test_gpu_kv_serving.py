@@ -358,7 +358,8 @@ def test_keys_and_queries_at_the_ends_of_the_range(tokens, D, size_q, size_k):
 @pytest.mark.parametrize("power", [24, 40, 110])
 @pytest.mark.parametrize("tokens, heads, group, D, kv", [
     (7, 2, 1, 64, "s8"), (4, 2, 4, 64, "u4"), (7, 1, 1, 128, "s8"), (2, 3, 4, 128, "u4"), (9, 1, 3, 256, "s8"),
-    (20, 2, 4, 64, "s8"), (40, 1, 4, 128, "u4"), (70, 2, 4, 128, "s8"), (20, 2, 4, 160, "s8"), (150, 1, 2, 256, "u4")])
+    (20, 2, 4, 64, "s8"), (40, 1, 4, 128, "u4"), (70, 2, 4, 128, "s8"), (20, 2, 4, 160, "s8"), (150, 1, 2, 256, "u4"),
+    (120, 2, 1, 128, "s8"), (300, 1, 1, 64, "u4")])
 def test_hidden_tokens_have_no_part_in_a_row(tokens, heads, group, D, kv, power):
     """Values of later tokens, and of other branches, 2^power times those that a row sees: its result is as exact
     as without them.  A row that sees one of them is as exact as its largest value lets it be."""
@@ -386,3 +387,20 @@ def test_channels_that_do_not_fill_the_operands(D, tokens, kv):
     """Many rows of any number of channels, several chunks a block."""
     c = _kv.Cache(np.random.default_rng(D + tokens), [1500, tokens + 1, tokens], [tokens] * 3, 20, D, 16, kv, "f16")
     check(c, Dev(c), 40)
+
+
+@pytest.mark.parametrize("masked", [False, True])
+def test_hidden_tokens_in_a_batch_for_few_rows(masked):
+    """Wide heads in more sequences than the kernel for many rows takes: tiles of 16 rows over newest tokens that
+    fill several of a warp's tiles, large values among them."""
+    rng = np.random.default_rng(17)
+    tokens = [0] * 2100
+    tokens[40], tokens[900], tokens[2099] = 280, 3, 130
+    lens = list(tokens)
+    lens[40], lens[900], lens[2099] = 900, 30, 130
+    c = _kv.Cache(rng, lens, tokens, 1, 160, 16, "s8", "bf16")
+    for b in (40, 900, 2099):
+        large = lens[b] - tokens[b] + np.arange(1, tokens[b], 5)
+        c.v[b][large] = _kv.bf16(c.v[b][large] * 2.0 ** rng.integers(20, 90, size=(len(large), 1, 1)))
+    sees = [_kv.random_tree(rng, n) for n in tokens] if masked else None
+    check(c, Dev(c), 2, sees)
