@@ -580,8 +580,10 @@ def q_kv_attn(q, x_dt: str, heads_q: int, g: KvGeom, seqs: KvSeqs, scale: float,
               ld_q: int = 0, ld_out: int = 0, stream=None):
     """Attention of q [rows, heads_q, D] over the cache into out; mask: int32 [rows, words], contiguous, bits
     of the newest tokens that a row sees (None: up to itself); workspace: uint8 device tensor of
-    qnn_kv_attn_workspace_bytes(g, seqs, heads_q) bytes; lse: fp32 [rows, heads_q] or None."""
+    qnn_kv_attn_workspace_bytes(g, seqs, heads_q) bytes; lse: fp32 [rows, heads_q], contiguous, or None."""
     load()
+    if lse is not None and not lse.is_contiguous():
+        raise QnnError(QNN_ERR_INVALID_ARG, "q_kv_attn: lse must be contiguous")
     _check(_SYMBOLS["q_kv_attn"](_ptr(q), DTYPES[x_dt], int(ld_q), int(heads_q), ctypes.byref(g), ctypes.byref(seqs),
                                  float(scale), _packed(mask, 4, "q_kv_attn: mask"),
                                  0 if mask is None else int(mask.shape[-1]), _ptr(out),

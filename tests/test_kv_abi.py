@@ -172,6 +172,7 @@ def test_binding_refuses_tensors_that_would_be_read_as_others(lib):
     x = t.zeros(4, dtype=t.bfloat16)
     for bad in (t.zeros((3, 4), dtype=t.int32)[:, :2], t.zeros((3, 4), dtype=t.int64), t.zeros((3, 4))):
         refused("mask", qnn.q_kv_attn, x, "bf16", 4, geom(), s, 0.1, x, x, mask=bad, stream=0)
+    refused("lse", qnn.q_kv_attn, x, "bf16", 4, geom(), s, 0.1, x, x, lse=t.zeros((3, 8))[:, :4], stream=0)
 
 
 @pytest.mark.parametrize("name, struct", [("qnn_kv_geom", qnn.KvGeom), ("qnn_kv_seqs", qnn.KvSeqs)])
